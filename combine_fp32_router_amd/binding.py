@@ -28,7 +28,12 @@ MOE_PACK_STREAM = 0x100  # OR into the quant of the pack calls: streaming row st
 EXPORTS = ("moe_route_topk", "moe_dispatch_layout", "moe_dispatch_layout_chunks",
            "moe_route_layout_chunks", "moe_route_layout_chunks_noalloc",
            "moe_dispatch_pack", "moe_combine", "moe_combine_pack", "moe_status_string",
-           "moe_row_bytes", "moe_recv_layout", "moe_recv_regroup", "moe_recv_ungroup")
+           "moe_row_bytes", "moe_recv_layout", "moe_recv_regroup", "moe_recv_ungroup",
+           "moe_balance_loss", "moe_route_grad", "moe_combine_grad", "moe_expert_matmul",
+           "moe_expert_matmul_dx", "moe_expert_matmul_dw")
+
+MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = range(5)
+MOE_GRAD_FP32, MOE_GRAD_BF16, MOE_GRAD_ACCUMULATE = 0, 1, 0x100
 
 _lib = None
 
@@ -63,6 +68,12 @@ def load() -> ctypes.CDLL:
     lib.moe_recv_layout.argtypes = [P, i32, i32, i64, P, P, P, P, P, P]
     lib.moe_recv_regroup.argtypes = [P, P, i64, i32, i32, P, P, P, P]
     lib.moe_recv_ungroup.argtypes = [P, P, i64, i32, i32, P, P, P, P]
+    lib.moe_balance_loss.argtypes = [P, P, P, i64, i64, i32, i32, P, P, P, P, P, P, P]
+    lib.moe_route_grad.argtypes = [P, P, P, P, P, P, P, P, i64, i64, i32, i32, P, P]
+    lib.moe_combine_grad.argtypes = [P, P, P, i32, P, P, i64, i32, i32, P, P, P]
+    lib.moe_expert_matmul.argtypes = [P, P, P, P, i32, P, i32, i64, i32, i32, P, P, P]
+    lib.moe_expert_matmul_dx.argtypes = [P, P, P, i32, P, i32, i64, i32, i32, P, P]
+    lib.moe_expert_matmul_dw.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P, P]
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_row_bytes.argtypes = [i32, i32]
@@ -449,3 +460,248 @@ def moe_recv_ungroup(grouped: torch.Tensor, grouped_scales: torch.Tensor | None,
            load().moe_recv_ungroup(_ptr(grouped), _ptr(grouped_scales), max_rows, H, quant,
                                    _ptr(group_pos), _ptr(recv), _ptr(recv_scales),
                                    _stream(stream)))
+
+
+def _stream_on(stream, *tensors) -> ctypes.c_void_p:
+    """The stream handle for a call over `tensors`, which must share one
+    device: `stream`, or that device's current stream."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+    if stream is None:
+        stream = torch.cuda.current_stream(devices.pop())
+    return _stream(stream)
+
+
+def _want_bf16(t: torch.Tensor, shape, name: str):
+    """bf16 values (or their int16/uint16 bits) of exactly `shape`."""
+    if t.element_size() != 2:
+        raise ValueError(f"{name} must hold bf16 bits")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+class Balance(NamedTuple):
+    """Outputs of moe_balance_loss for S segments of seg_tokens tokens."""
+    loss: torch.Tensor           # [S] fp32
+    expert_counts: torch.Tensor  # [S, E] int32
+    prob_sums: torch.Tensor      # [S, E] fp32
+    tokens: torch.Tensor         # [S] int32: live tokens
+    workspace: torch.Tensor      # uint8 scratch
+    seg_tokens: int
+
+
+def balance_workspace_bytes(T: int, seg_tokens: int, E: int, k: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_balance_loss",
+           load().moe_balance_loss(None, None, None, T, seg_tokens, E, k, None, None, None, None,
+                                   None, ctypes.byref(n), None))
+    return int(n.value)
+
+
+def alloc_balance(T: int, seg_tokens: int, E: int, k: int, device) -> Balance:
+    """Outputs and workspace for T tokens in segments of seg_tokens."""
+    seg_tokens = max(1, min(seg_tokens, max(T, 1)))
+    S = max(1, -(-T // seg_tokens))
+    f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+    ws = balance_workspace_bytes(T, seg_tokens, E, k)
+    return Balance(torch.empty(S, **f32), torch.empty((S, E), **i32), torch.empty((S, E), **f32),
+                   torch.empty(S, **i32), torch.empty(ws, dtype=torch.uint8, device=device),
+                   seg_tokens)
+
+
+def _want_mask(mask: torch.Tensor | None, T: int):
+    if mask is not None:
+        if mask.element_size() != 1:
+            raise ValueError("token_mask: expected one byte per token (uint8 or bool)")
+        if mask.numel() != T:
+            raise ValueError("token_mask must hold one byte per token")
+
+
+def _want_segments(b: Balance, T: int, E: int):
+    S = max(1, -(-T // b.seg_tokens))
+    _want(b.loss, torch.float32, "loss")
+    _want(b.expert_counts, torch.int32, "expert_counts")
+    _want(b.prob_sums, torch.float32, "prob_sums")
+    _want(b.tokens, torch.int32, "tokens")
+    if (b.loss.numel() < S or b.tokens.numel() < S or b.expert_counts.numel() < S * E or
+            b.prob_sums.numel() < S * E):
+        raise ValueError("Balance buffers too small")
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
+                     token_mask: torch.Tensor | None, out: Balance, stream=None) -> Balance:
+    """logits fp32 [T, E], topk_idx int32 [T, k], token_mask uint8 [T] or
+    None -> out.loss, expert_counts, prob_sums and tokens per segment."""
+    _want(logits, torch.float32, "logits")
+    _want(topk_idx, torch.int32, "topk_idx")
+    T, E = logits.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, k]")
+    _want_mask(token_mask, T)
+    _want_segments(out, T, E)
+    n = ctypes.c_size_t(out.workspace.numel())
+    st = _stream_on(stream, logits, topk_idx, token_mask, *out[:5])
+    _check("moe_balance_loss",
+           load().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(token_mask), T,
+                                   out.seg_tokens, E, topk_idx.shape[1], _ptr(out.loss),
+                                   _ptr(out.expert_counts), _ptr(out.prob_sums),
+                                   _ptr(out.tokens), _ptr(out.workspace), ctypes.byref(n), st))
+    return out
+
+
+def moe_route_grad(logits: torch.Tensor | None, topk_idx: torch.Tensor,
+                   topk_w: torch.Tensor | None, d_topk_w: torch.Tensor | None,
+                   token_mask: torch.Tensor | None, d_loss: torch.Tensor | None,
+                   balance: Balance | None, d_logits: torch.Tensor, stream=None) -> torch.Tensor:
+    """Gradient of the router's logits [T, E] from that of the gate weights
+    (d_topk_w [T, k] or None) and of the balance loss (d_loss [S] with the
+    forward call's Balance, or None for both)."""
+    _want(d_logits, torch.float32, "d_logits")
+    _want(topk_idx, torch.int32, "topk_idx")
+    T, E = d_logits.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    _want_mask(token_mask, T)
+    if d_topk_w is not None:
+        if topk_w is None:
+            raise ValueError("d_topk_w needs topk_w")
+        for t, name in ((topk_w, "topk_w"), (d_topk_w, "d_topk_w")):
+            _want(t, torch.float32, name)
+            if t.numel() != T * k:
+                raise ValueError(f"{name} must hold T*k elements")
+    if d_loss is not None:
+        if logits is None or balance is None:
+            raise ValueError("d_loss needs logits and the forward call's Balance")
+        _want(logits, torch.float32, "logits")
+        if tuple(logits.shape) != (T, E):
+            raise ValueError("logits and d_logits differ in shape")
+        _want_segments(balance, T, E)
+        _want(d_loss, torch.float32, "d_loss")
+        if d_loss.numel() < max(1, -(-T // balance.seg_tokens)):
+            raise ValueError("d_loss must hold one value per segment")
+    counts = balance.expert_counts if d_loss is not None else None
+    live = balance.tokens if d_loss is not None else None
+    seg = balance.seg_tokens if d_loss is not None else max(T, 1)
+    st = _stream_on(stream, logits, topk_idx, topk_w, d_topk_w, token_mask, d_loss, counts, live,
+                    d_logits)
+    _check("moe_route_grad",
+           load().moe_route_grad(_ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
+                                 _ptr(token_mask), _ptr(d_loss), _ptr(counts), _ptr(live), T, seg,
+                                 E, k, _ptr(d_logits), st))
+    return d_logits
+
+
+def moe_combine_grad(d_out: torch.Tensor, recv: torch.Tensor | None,
+                     recv_scales: torch.Tensor | None, quant: int, pos: torch.Tensor,
+                     topk_w: torch.Tensor, T: int, H: int, k: int, d_recv: torch.Tensor | None,
+                     d_topk_w: torch.Tensor | None, stream=None) -> None:
+    """Gradient of moe_combine: d_out bf16 [T, H] -> d_recv (bf16 rows) and
+    d_topk_w fp32 [T*k]; either output may be None."""
+    if d_out.element_size() != 2 or d_out.numel() < T * H:
+        raise ValueError("d_out must hold T*H bf16 values")
+    _want(pos, torch.int32, "pos")
+    _want(topk_w, torch.float32, "topk_w")
+    if pos.numel() < T * k or topk_w.numel() < T * k:
+        raise ValueError("pos / topk_w too small")
+    if d_topk_w is not None:
+        _want(d_topk_w, torch.float32, "d_topk_w")
+        if d_topk_w.numel() < T * k:
+            raise ValueError("d_topk_w must hold T*k values")
+        _want_scales(recv_scales, 0, quant, "recv_scales")
+    st = _stream_on(stream, d_out, recv, recv_scales, pos, topk_w, d_recv, d_topk_w)
+    _check("moe_combine_grad",
+           load().moe_combine_grad(_ptr(d_out), _ptr(recv), _ptr(recv_scales), quant, _ptr(pos),
+                                   _ptr(topk_w), T, H, k, _ptr(d_recv), _ptr(d_topk_w), st))
+
+
+def _want_weights(w: torch.Tensor, offsets: torch.Tensor):
+    if w.dim() != 3:
+        raise ValueError("weights must be [E, N, K]")
+    _want(offsets, torch.int32, "offsets")
+    if offsets.numel() != w.shape[0] + 1:
+        raise ValueError("offsets must hold E+1 int32")
+
+
+def moe_expert_matmul(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                      bias: torch.Tensor | None, act: int, residual: torch.Tensor | None,
+                      out: torch.Tensor, preact: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """x bf16 [rows, K] in runs of offsets int32 [E+1], w bf16 [E, N, K]
+    ([E, 2N, K] for MOE_ACT_SWIGLU) -> out bf16 [rows, N]; bias fp32 [E, N]
+    ([E, 2N]); preact bf16 [rows, N] ([rows, 2N]) keeps z for the gradient."""
+    _want_weights(w, offsets)
+    E, wide_n, K = w.shape
+    wide = 2 if act == MOE_ACT_SWIGLU else 1
+    if wide_n % wide:
+        raise ValueError("MOE_ACT_SWIGLU takes an even number of weight rows")
+    rows, N = x.shape[0], wide_n // wide
+    _want_bf16(w, (E, wide_n, K), "w")
+    _want_bf16(x, (rows, K), "x")
+    _want_bf16(out, (rows, N), "out")
+    if residual is not None:
+        _want_bf16(residual, (rows, N), "residual")
+    if preact is not None:
+        _want_bf16(preact, (rows, wide_n), "preact")
+    if bias is not None:
+        _want(bias, torch.float32, "bias")
+        if bias.numel() != E * wide_n:
+            raise ValueError("bias must hold one value per weight row")
+    st = _stream_on(stream, x, offsets, w, bias, residual, out, preact)
+    _check("moe_expert_matmul",
+           load().moe_expert_matmul(_ptr(x), _ptr(offsets), _ptr(w), _ptr(bias), act,
+                                    _ptr(residual), E, rows, K, N, _ptr(out), _ptr(preact), st))
+    return out
+
+
+def moe_expert_matmul_dx(dy: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor, act: int,
+                         preact: torch.Tensor | None, dx: torch.Tensor,
+                         stream=None) -> torch.Tensor:
+    """dy bf16 [rows, N], w bf16 [E, N, K] -> dx bf16 [rows, K], through the
+    activation before the product when act says so (preact and dx [rows, K],
+    or [rows, 2K] for MOE_ACT_SWIGLU)."""
+    _want_weights(w, offsets)
+    E, N, K = w.shape
+    rows, wide = dy.shape[0], 2 if act == MOE_ACT_SWIGLU else 1
+    _want_bf16(w, (E, N, K), "w")
+    _want_bf16(dy, (rows, N), "dy")
+    _want_bf16(dx, (rows, wide * K), "dx")
+    if act == MOE_ACT_NONE:
+        preact = None
+    elif preact is None:
+        raise ValueError("an activation's gradient needs preact")
+    else:
+        _want_bf16(preact, (rows, wide * K), "preact")
+    st = _stream_on(stream, dy, offsets, w, preact, dx)
+    _check("moe_expert_matmul_dx",
+           load().moe_expert_matmul_dx(_ptr(dy), _ptr(offsets), _ptr(w), act, _ptr(preact), E,
+                                       rows, K, N, _ptr(dx), st))
+    return dx
+
+
+def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                         dw: torch.Tensor, dbias: torch.Tensor | None = None,
+                         accumulate: bool = False, stream=None) -> torch.Tensor:
+    """dy bf16 [rows, N], x bf16 [rows, K] -> dw [E, N, K] (fp32, or bf16 by
+    its dtype) and dbias fp32 [E, N]; accumulate adds to what they hold
+    (fp32 dw only)."""
+    _want_weights(dw, offsets)
+    E, N, K = dw.shape
+    rows = dy.shape[0]
+    _want_bf16(dy, (rows, N), "dy")
+    _want_bf16(x, (rows, K), "x")
+    if dw.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dw: expected float32 or bfloat16, got {dw.dtype}")
+    if dbias is not None:
+        _want(dbias, torch.float32, "dbias")
+        if dbias.numel() != E * N:
+            raise ValueError("dbias must hold E*N values")
+    flags = MOE_GRAD_FP32 if dw.dtype == torch.float32 else MOE_GRAD_BF16
+    if accumulate:
+        flags |= MOE_GRAD_ACCUMULATE
+    st = _stream_on(stream, dy, x, offsets, dw, dbias)
+    _check("moe_expert_matmul_dw",
+           load().moe_expert_matmul_dw(_ptr(dy), _ptr(x), _ptr(offsets), E, rows, K, N, flags,
+                                       _ptr(dw), _ptr(dbias), st))
+    return dw

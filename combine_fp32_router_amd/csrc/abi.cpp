@@ -28,6 +28,28 @@ bool overlap(const Extent &a, const Extent &b)
     return a0 < b0 + static_cast<uintptr_t>(b.bytes) && b0 < a0 + static_cast<uintptr_t>(a.bytes);
 }
 
+// Segments of the balance loss: seg_tokens is clamped to T (one segment).
+int check_segments(int64_t T, int64_t &seg_tokens, int E, int k)
+{
+    if (T < 0 || check_ek(E, k) != MOE_OK || too_many_slots(T, k) || seg_tokens < 0 ||
+        (T > 0 && seg_tokens < 1))
+        return MOE_ERR_SHAPE;
+    if (seg_tokens > T)
+        seg_tokens = T;
+    return moe::layout_chunks(T, seg_tokens) > 65535 ? MOE_ERR_SHAPE : MOE_OK;  // grid y dimension
+}
+
+// Sizes of an experts' product: N may count both halves of a gated one.
+int check_product(int E, int64_t max_rows, int K, int N, int most)
+{
+    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows >= kMaxSlots || K < 16 ||
+        K > MOE_MAX_HIDDEN || (K % 16) != 0 || N < 16 || N > most || (N % 16) != 0)
+        return MOE_ERR_SHAPE;
+    return MOE_OK;
+}
+
+bool known_act(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_SWIGLU; }
+
 }  // namespace
 
 extern "C" {
@@ -372,6 +394,141 @@ int moe_recv_ungroup(const void *grouped, const float *grouped_scales, int64_t m
 {
     return gather_rows(grouped, grouped_scales, recv, recv_scales, max_rows, H, quant, group_pos,
                        stream);
+}
+
+int moe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t *token_mask,
+                     int64_t T, int64_t seg_tokens, int E, int k, float *loss,
+                     int32_t *expert_counts, float *prob_sums, int32_t *seg_live,
+                     void *workspace, size_t *workspace_bytes, hipStream_t stream)
+{
+    if (!workspace_bytes)
+        return MOE_ERR_NULL;
+    if (check_segments(T, seg_tokens, E, k) != MOE_OK)
+        return MOE_ERR_SHAPE;
+    const size_t need = moe::balance_workspace_bytes(T, seg_tokens, E);
+    if (!workspace) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
+    if (*workspace_bytes < need)
+        return MOE_ERR_WORKSPACE;
+    if (!loss || !expert_counts || !prob_sums || !seg_live || (T > 0 && (!logits || !topk_idx)))
+        return MOE_ERR_NULL;
+    if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(loss, 4) ||
+        !aligned(expert_counts, 4) || !aligned(prob_sums, 4) || !aligned(seg_live, 4) ||
+        !aligned(workspace, 256))
+        return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_balance_loss(logits, topk_idx, token_mask, T, seg_tokens, E, k,
+                                               loss, expert_counts, prob_sums, seg_live, workspace,
+                                               stream));
+}
+
+int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *topk_w,
+                   const float *d_topk_w, const uint8_t *token_mask, const float *d_loss,
+                   const int32_t *expert_counts, const int32_t *seg_live, int64_t T,
+                   int64_t seg_tokens, int E, int k, float *d_logits, hipStream_t stream)
+{
+    if (check_segments(T, seg_tokens, E, k) != MOE_OK ||
+        !grid_fits(route_grad_blocks(T, E), kRouteThreads))
+        return MOE_ERR_SHAPE;
+    if (T == 0)
+        return MOE_OK;
+    if (!d_logits || (!d_topk_w && !d_loss) || (d_topk_w && (!topk_idx || !topk_w)) ||
+        (d_loss && (!logits || !expert_counts || !seg_live)))
+        return MOE_ERR_NULL;
+    if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+        !aligned(d_topk_w, 4) || !aligned(d_loss, 4) || !aligned(expert_counts, 4) ||
+        !aligned(seg_live, 4) || !aligned(d_logits, 4))
+        return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_route_grad(logits, topk_idx, topk_w, d_topk_w, token_mask, d_loss,
+                                             expert_counts, seg_live, T, seg_tokens, E, k, d_logits,
+                                             stream));
+}
+
+int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv_scales, int quant,
+                     const int32_t *pos, const float *topk_w, int64_t T, int H, int k,
+                     void *d_recv, float *d_topk_w, hipStream_t stream)
+{
+    int s = check_rows(T, H, k, quant);
+    if (s != MOE_OK)
+        return s;
+    if (!grid_fits(T, token_threads(H, quant)))
+        return MOE_ERR_SHAPE;
+    if (T == 0)
+        return MOE_OK;
+    if (!d_out_bf16 || !pos || !topk_w || (!d_recv && !d_topk_w) || (d_topk_w && !recv))
+        return MOE_ERR_NULL;
+    if (!aligned(d_out_bf16, 16) || !aligned(pos, 4) || !aligned(topk_w, 4) ||
+        !aligned(d_recv, 16) || !aligned(d_topk_w, 4))
+        return MOE_ERR_ALIGN;
+    if (d_topk_w) {
+        if (!aligned(recv, 16))
+            return MOE_ERR_ALIGN;
+        if ((s = check_scales(recv_scales, quant)) != MOE_OK)
+            return s;
+    }
+    if (d_recv && (d_recv == d_out_bf16 || (d_topk_w && d_recv == recv)))
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_combine_grad(d_out_bf16, recv, recv_scales, quant, pos, topk_w, T,
+                                               H, k, d_recv, d_topk_w, stream));
+}
+
+int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, const float *bias,
+                      int act, const void *residual, int E, int64_t max_rows, int K, int N,
+                      void *out, void *preact, hipStream_t stream)
+{
+    if (check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK || !known_act(act))
+        return MOE_ERR_SHAPE;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!x || !offsets || !w || !out)
+        return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(offsets, 4) || !aligned(w, 16) || !aligned(bias, 16) ||
+        !aligned(residual, 16) || !aligned(out, 16) || !aligned(preact, 16))
+        return MOE_ERR_ALIGN;
+    if (out == x || out == w || out == preact ||
+        (preact && (preact == x || preact == w || preact == residual)))
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_expert_matmul(x, offsets, w, bias, act, residual, E, max_rows, K,
+                                                N, out, preact, stream));
+}
+
+int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
+                         const void *preact, int E, int64_t max_rows, int K, int N, void *dx,
+                         hipStream_t stream)
+{
+    if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK || !known_act(act))
+        return MOE_ERR_SHAPE;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!dy || !offsets || !w || !dx || (act != MOE_ACT_NONE && !preact))
+        return MOE_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(offsets, 4) || !aligned(w, 16) || !aligned(preact, 16) ||
+        !aligned(dx, 16))
+        return MOE_ERR_ALIGN;
+    if (dx == dy || dx == w)
+        return MOE_ERR_ALIAS;
+    return hip_status(
+        moe::launch_expert_matmul_dx(dy, offsets, w, act, preact, E, max_rows, K, N, dx, stream));
+}
+
+int moe_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
+                         int64_t max_rows, int K, int N, int flags, void *dw, float *dbias,
+                         hipStream_t stream)
+{
+    if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK ||
+        (flags != MOE_GRAD_FP32 && flags != MOE_GRAD_BF16 &&
+         flags != (MOE_GRAD_FP32 | MOE_GRAD_ACCUMULATE)))
+        return MOE_ERR_SHAPE;
+    if (!offsets || !dw || (max_rows > 0 && (!dy || !x)))
+        return MOE_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(dw, 16) ||
+        !aligned(dbias, 16))
+        return MOE_ERR_ALIGN;
+    if (dw == dy || dw == x)
+        return MOE_ERR_ALIAS;
+    return hip_status(
+        moe::launch_expert_matmul_dw(dy, x, offsets, E, max_rows, K, N, flags, dw, dbias, stream));
 }
 
 }  // extern "C"

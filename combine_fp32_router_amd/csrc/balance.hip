@@ -1,0 +1,446 @@
+// Balance loss of the router with per-expert counts, and the router's
+// gradient (through the gate weights and through the balance loss).
+//
+// With p = softmax(logits[t]) over the E experts, c_e the number of a
+// segment's slots routed to expert e, S_e = sum_t p_te and n the segment's
+// live (unmasked) tokens:
+//   loss        = E / (k n^2) * sum_e c_e S_e
+//   d loss/d l  = E / (k n^2) * p_te * (c_e - sum_e' c_e' p_te')
+// (the counts are constants of the gradient) and, for the gate weights
+// w = softmax of the k selected logits,
+//   d l_{idx_j} += w_j (dw_j - sum_i w_i dw_i).
+//
+// gfx950 mapping.  L lanes own one token (a 16-lane DPP row for E <= 256,
+// the wave above), each holding NE of its logits in registers, so a row is
+// read once and its maximum, sum and products reduce in the VALU.  The
+// forward pass keeps each lane's running sum of p over the tokens of its
+// block in registers, joins the block's waves through LDS in wave order and
+// leaves one row of partial sums and counts per block; a second launch adds
+// the rows of a segment in block order (in double), so no result depends on
+// the order in which blocks or atomics ran.  A segment that fits one block
+// needs no second launch.
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+template <int CTRL>
+__device__ __forceinline__ float dppf(float v)
+{
+    return __uint_as_float(dpp32<CTRL>(__float_as_uint(v)));
+}
+
+template <int L>
+__device__ __forceinline__ float group_max(float v)
+{
+    v = fmaxf(v, dppf<0xB1>(v));
+    v = fmaxf(v, dppf<0x4E>(v));
+    v = fmaxf(v, dppf<0x141>(v));
+    v = fmaxf(v, dppf<0x140>(v));
+    if (L == 64) {
+        v = fmaxf(v, __shfl_xor(v, 16));
+        v = fmaxf(v, __shfl_xor(v, 32));
+    }
+    return v;
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v)
+{
+    v += dppf<0xB1>(v);
+    v += dppf<0x4E>(v);
+    v += dppf<0x141>(v);
+    v += dppf<0x140>(v);
+    if (L == 64) {
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+    }
+    return v;
+}
+
+// Expert held as element q of lane `sub`: runs of four per lane when the row
+// is read as 16-byte vectors, else one expert per lane in turn.
+template <int L, bool VEC>
+__device__ __forceinline__ int expert_of(int q, int sub)
+{
+    return VEC ? (q / 4) * (4 * L) + 4 * sub + q % 4 : q * L + sub;
+}
+
+// A token's logits, -inf past E; all zero for a token that is not live
+// (whose memory is not read).
+template <int L, int NE, bool VEC>
+__device__ __forceinline__ void load_row(const float *__restrict__ row, int E, int sub, bool live,
+                                         float (&v)[NE])
+{
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NE / 4; ++i) {
+            const int e = expert_of<L, VEC>(4 * i, sub);
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (live && e < E)
+                x = *reinterpret_cast<const float4 *>(row + e);
+            const bool past = e >= E;
+            v[4 * i + 0] = past ? -INFINITY : x.x;
+            v[4 * i + 1] = past ? -INFINITY : x.y;
+            v[4 * i + 2] = past ? -INFINITY : x.z;
+            v[4 * i + 3] = past ? -INFINITY : x.w;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < NE; ++q) {
+            const int e = expert_of<L, VEC>(q, sub);
+            v[q] = e >= E ? -INFINITY : (live ? row[e] : 0.0f);
+        }
+    }
+}
+
+// p of the token in place of its logits; 0 everywhere if it is not live.
+template <int L, int NE>
+__device__ __forceinline__ void softmax_row(float (&v)[NE], bool live)
+{
+    float m = v[0];
+#pragma unroll
+    for (int q = 1; q < NE; ++q)
+        m = fmaxf(m, v[q]);
+    m = group_max<L>(m);
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < NE; ++q) {
+        v[q] = expf(v[q] - m);
+        s += v[q];
+    }
+    s = group_sum<L>(s);
+    const float inv = live ? 1.0f / s : 0.0f;
+#pragma unroll
+    for (int q = 0; q < NE; ++q)
+        v[q] *= inv;
+}
+
+struct BalanceOut {
+    float *loss;
+    int32_t *counts;
+    float *prob_sums;
+    int32_t *live;
+};
+
+// loss of one segment from its sums; called by every thread of a block.
+__device__ void write_loss(const float *sums, const int32_t *counts, int live, int E, int k,
+                           float *loss)
+{
+    __shared__ double red[16];
+    double acc = 0.0;
+    for (int e = threadIdx.x; e < E; e += blockDim.x)
+        acc += static_cast<double>(counts[e]) * static_cast<double>(sums[e]);
+    for (int o = kWave / 2; o > 0; o >>= 1)
+        acc += __shfl_xor(acc, o);
+    if (lane_id() == 0)
+        red[threadIdx.x / kWave] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int w = 0; w < static_cast<int>(blockDim.x) / kWave; ++w)
+            total += red[w];
+        const double n = static_cast<double>(live);
+        *loss = live > 0 ? static_cast<float>(total * E / (n * n * k)) : 0.0f;
+    }
+}
+
+// One block: tokens [b*tpb, (b+1)*tpb) of segment blockIdx.y.  ONE: the
+// block covers its whole segment and writes the results itself.
+template <int L, int NE, bool VEC, bool ONE>
+__global__ __launch_bounds__(1024) void balance_partial_kernel(
+    const float *__restrict__ logits, const int32_t *__restrict__ idx,
+    const uint8_t *__restrict__ mask, int64_t T, int64_t seg, int tpb, int E, int k, float *psum,
+    int32_t *pcount, int32_t *plive, unsigned *done, BalanceOut out)
+{
+    extern __shared__ float lds[];  // [waves][E] sums, then [E] counts, then the live count
+    const int nw = blockDim.x / kWave, w = threadIdx.x / kWave, lane = lane_id();
+    int32_t *hist = reinterpret_cast<int32_t *>(lds + nw * E);
+    for (int e = threadIdx.x; e <= E; e += blockDim.x)
+        hist[e] = 0;
+    __syncthreads();
+    const int64_t s = blockIdx.y;
+    const int64_t t0 = s * seg + static_cast<int64_t>(blockIdx.x) * tpb;
+    const int64_t end = min(T, (s + 1) * seg);
+    const int n = static_cast<int>(max(int64_t(0), min(static_cast<int64_t>(tpb), end - t0)));
+
+    // counts of the live tokens' slots
+    for (int i = threadIdx.x; i < n; i += blockDim.x)
+        if (!mask || mask[t0 + i])
+            atomicAdd(&hist[E], 1);
+    for (int i = threadIdx.x; i < n * k; i += blockDim.x) {
+        const int e = idx[t0 * k + i];
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(E) && (!mask || mask[t0 + i / k]))
+            atomicAdd(&hist[e], 1);
+    }
+
+    constexpr int G = kWave / L;  // tokens of a wave at a time
+    const int sub = lane % L;
+    float acc[NE];
+#pragma unroll
+    for (int q = 0; q < NE; ++q)
+        acc[q] = 0.0f;
+    for (int i = w * G; i < n; i += nw * G) {
+        const int64_t t = t0 + i + lane / L;
+        const bool live = i + lane / L < n && (!mask || mask[t]);
+        float v[NE];
+        load_row<L, NE, VEC>(logits + t * E, E, sub, live, v);
+        softmax_row<L, NE>(v, live);
+#pragma unroll
+        for (int q = 0; q < NE; ++q)
+            acc[q] += v[q];
+    }
+#pragma unroll
+    for (int q = 0; q < NE; ++q) {
+        if (L == 16) {
+            acc[q] += __shfl_xor(acc[q], 16);
+            acc[q] += __shfl_xor(acc[q], 32);
+        }
+        const int e = expert_of<L, VEC>(q, sub);
+        if (lane < L && e < E)
+            lds[w * E + e] = acc[q];
+    }
+    __syncthreads();
+    const int64_t row = s * gridDim.x + blockIdx.x;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+        double sum = 0.0;
+        for (int i = 0; i < nw; ++i)
+            sum += static_cast<double>(lds[i * E + e]);
+        if (ONE) {
+            lds[e] = static_cast<float>(sum);  // row 0: this thread alone reads and writes entry e
+            out.prob_sums[s * E + e] = static_cast<float>(sum);
+            out.counts[s * E + e] = hist[e];
+        } else {
+            psum[row * E + e] = static_cast<float>(sum);
+            pcount[row * E + e] = hist[e];
+        }
+    }
+    if (ONE) {
+        __syncthreads();
+        write_loss(lds, hist, hist[E], E, k, out.loss + s);
+        if (threadIdx.x == 0)
+            out.live[s] = hist[E];
+    } else if (threadIdx.x == 0) {
+        plive[row] = hist[E];
+        if (blockIdx.x == 0)
+            done[s] = 0;
+    }
+}
+
+// Adds a segment's partial rows: block (x, s) takes 64 experts, its waves
+// every fourth row each; the segment's last block to finish forms the loss.
+__global__ __launch_bounds__(256) void balance_join_kernel(const float *__restrict__ psum,
+                                                           const int32_t *__restrict__ pcount,
+                                                           const int32_t *__restrict__ plive,
+                                                           int rows, int E, int k, unsigned *done,
+                                                           BalanceOut out)
+{
+    __shared__ double sums[4][kWave];
+    __shared__ int32_t counts[4][kWave], lives[4];
+    __shared__ unsigned last;
+    const int64_t s = blockIdx.y;
+    const int w = threadIdx.x / kWave, lane = lane_id(), e = blockIdx.x * kWave + lane;
+    double sum = 0.0;
+    int32_t count = 0, live = 0;
+    if (e < E)
+        for (int r = w; r < rows; r += 4) {
+            sum += static_cast<double>(psum[(s * rows + r) * E + e]);
+            count += pcount[(s * rows + r) * E + e];
+        }
+    for (int r = threadIdx.x; r < rows; r += blockDim.x)
+        live += plive[s * rows + r];
+    for (int o = kWave / 2; o > 0; o >>= 1)
+        live += __shfl_xor(live, o);
+    sums[w][lane] = sum;
+    counts[w][lane] = count;
+    if (lane == 0)
+        lives[w] = live;
+    __syncthreads();
+    live = lives[0] + lives[1] + lives[2] + lives[3];
+    if (w == 0 && e < E) {
+        out.prob_sums[s * E + e] =
+            static_cast<float>(sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
+        out.counts[s * E + e] = counts[0][lane] + counts[1][lane] + counts[2][lane] + counts[3][lane];
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = atomicAdd(&done[s], 1u) == gridDim.x - 1 ? 1u : 0u;
+    __syncthreads();
+    if (!last)
+        return;
+    __threadfence();
+    write_loss(out.prob_sums + s * E, out.counts + s * E, live, E, k, out.loss + s);
+    if (threadIdx.x == 0)
+        out.live[s] = live;
+}
+
+template <int L, int NE, bool VEC>
+__global__ __launch_bounds__(256) void route_grad_kernel(
+    const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
+    const float *__restrict__ dw, const uint8_t *__restrict__ mask, const float *__restrict__ dloss,
+    const int32_t *__restrict__ counts, const int32_t *__restrict__ live_tokens, int64_t T,
+    int64_t seg, int E, int k, float *__restrict__ dlogits)
+{
+    constexpr int G = kWave / L;
+    const int lane = lane_id(), sub = lane % L;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / kWave) +
+                           threadIdx.x / kWave) * G + lane / L;
+    if (first - lane / L >= T)
+        return;  // whole wave
+    const int64_t t = min(first, T - 1);
+    const bool live = first < T && (!mask || mask[t]);
+    float d[NE];
+    if (dloss) {
+        float c[NE];
+        load_row<L, NE, VEC>(logits + t * E, E, sub, live, d);
+        softmax_row<L, NE>(d, live);
+        const int64_t s = t / seg;
+        float dot = 0.0f;
+#pragma unroll
+        for (int q = 0; q < NE; ++q) {
+            const int e = expert_of<L, VEC>(q, sub);
+            c[q] = e < E ? static_cast<float>(counts[s * E + e]) : 0.0f;
+            dot = fmaf(c[q], d[q], dot);
+        }
+        dot = group_sum<L>(dot);
+        const float n = fmaxf(static_cast<float>(live_tokens[s]), 1.0f);
+        const float scale = live ? dloss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n : 0.0f;
+#pragma unroll
+        for (int q = 0; q < NE; ++q)
+            d[q] = d[q] * (c[q] - dot) * scale;
+    } else {
+#pragma unroll
+        for (int q = 0; q < NE; ++q)
+            d[q] = 0.0f;
+    }
+    if (dw) {
+        // lane j of the token holds slot j
+        const bool slot = sub < k && live;
+        const int e = slot ? idx[t * k + sub] : -1;
+        const float wj = slot ? w[t * k + sub] : 0.0f, dwj = slot ? dw[t * k + sub] : 0.0f;
+        const float g = wj * (dwj - group_sum<L>(wj * dwj));
+        for (int j = 0; j < k; ++j) {
+            const int ej = __shfl(e, j, L);
+            const float gj = __shfl(g, j, L);
+#pragma unroll
+            for (int q = 0; q < NE; ++q)
+                d[q] += ej == expert_of<L, VEC>(q, sub) ? gj : 0.0f;
+        }
+    }
+    if (first >= T)
+        return;
+    float *out = dlogits + t * E;
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < NE / 4; ++i) {
+            const int e = expert_of<L, VEC>(4 * i, sub);
+            if (e < E)
+                *reinterpret_cast<float4 *>(out + e) =
+                    make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < NE; ++q) {
+            const int e = expert_of<L, VEC>(q, sub);
+            if (e < E)
+                out[e] = d[q];
+        }
+    }
+}
+
+// Blocks of a segment and their tokens: about 1024 blocks over the batch,
+// none under 64 tokens.
+struct BalanceTiling {
+    int tpb, blocks;
+};
+BalanceTiling balance_tiling(int64_t T, int64_t seg)
+{
+    int64_t tpb = (T + 1023) / 1024;
+    tpb = tpb < 64 ? 64 : (tpb + 15) / 16 * 16;
+    if (tpb > seg || seg <= 256)
+        tpb = seg > 0 ? seg : 1;
+    return {static_cast<int>(tpb), static_cast<int>(seg > 0 ? (seg + tpb - 1) / tpb : 1)};
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t balance_workspace_bytes(int64_t T, int64_t seg, int E)
+{
+    const size_t S = layout_chunks(T, seg), rows = S * balance_tiling(T, seg).blocks;
+    return round256(rows * E * 4) * 2 + round256(rows * 4) + round256(S * 4);
+}
+
+// Calls F with the lanes per token, elements per lane and vector flag of a
+// router over E experts.
+#define MOE_ROUTER_SHAPE(E, VEC, F)                                                            \
+    if (E <= 16) { F(16, 1, false); }                                                          \
+    else if (E <= 32) { F(16, 2, false); }                                                     \
+    else if (E <= 64) { if (VEC) { F(16, 4, true); } else { F(16, 4, false); } }               \
+    else if (E <= 128) { if (VEC) { F(16, 8, true); } else { F(16, 8, false); } }              \
+    else if (E <= 256) { if (VEC) { F(16, 16, true); } else { F(16, 16, false); } }            \
+    else if (E <= 512) { if (VEC) { F(64, 8, true); } else { F(64, 8, false); } }              \
+    else { if (VEC) { F(64, 16, true); } else { F(64, 16, false); } }
+
+hipError_t launch_balance_loss(const float *logits, const int32_t *idx, const uint8_t *mask,
+                               int64_t T, int64_t seg, int E, int k, float *loss, int32_t *counts,
+                               float *prob_sums, int32_t *live, void *workspace,
+                               hipStream_t stream)
+{
+    const int S = layout_chunks(T, seg);
+    const BalanceTiling bt = balance_tiling(T, seg);
+    const size_t rows = static_cast<size_t>(S) * bt.blocks;
+    char *ws = static_cast<char *>(workspace);
+    float *psum = reinterpret_cast<float *>(ws);
+    int32_t *pcount = reinterpret_cast<int32_t *>(ws + round256(rows * E * 4));
+    int32_t *plive = reinterpret_cast<int32_t *>(ws + 2 * round256(rows * E * 4));
+    unsigned *done = reinterpret_cast<unsigned *>(ws + 2 * round256(rows * E * 4) + round256(rows * 4));
+    const BalanceOut out{loss, counts, prob_sums, live};
+    const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+    const bool one = bt.blocks == 1;
+    const int threads = one && E <= 256 ? 1024 : 256;
+    const size_t lds = (static_cast<size_t>(threads / kWave) * E + E + 1) * 4;
+    const dim3 grid(bt.blocks, S);
+#define MOE_BALANCE(L, NE, V)                                                                  \
+    if (one)                                                                                   \
+        balance_partial_kernel<L, NE, V, true><<<grid, threads, lds, stream>>>(                \
+            logits, idx, mask, T, seg, bt.tpb, E, k, psum, pcount, plive, done, out);          \
+    else                                                                                       \
+        balance_partial_kernel<L, NE, V, false><<<grid, threads, lds, stream>>>(               \
+            logits, idx, mask, T, seg, bt.tpb, E, k, psum, pcount, plive, done, out)
+    MOE_ROUTER_SHAPE(E, vec, MOE_BALANCE)
+#undef MOE_BALANCE
+    hipError_t err = hipGetLastError();
+    if (err != hipSuccess || one)
+        return err;
+    balance_join_kernel<<<dim3((E + kWave - 1) / kWave, S), 256, 0, stream>>>(
+        psum, pcount, plive, bt.blocks, E, k, done, out);
+    return hipGetLastError();
+}
+
+int64_t route_grad_blocks(int64_t T, int E)
+{
+    const int per = E <= 256 ? 16 : 4;
+    return (T + per - 1) / per;
+}
+
+hipError_t launch_route_grad(const float *logits, const int32_t *idx, const float *w,
+                             const float *dw, const uint8_t *mask, const float *dloss,
+                             const int32_t *counts, const int32_t *live, int64_t T, int64_t seg,
+                             int E, int k, float *dlogits, hipStream_t stream)
+{
+    const bool vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) |
+                                     reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
+    const dim3 grid(static_cast<unsigned>(route_grad_blocks(T, E)));
+#define MOE_ROUTE_GRAD(L, NE, V)                                                               \
+    route_grad_kernel<L, NE, V><<<grid, 256, 0, stream>>>(logits, idx, w, dw, mask, dloss,     \
+                                                          counts, live, T, seg, E, k, dlogits)
+    MOE_ROUTER_SHAPE(E, vec, MOE_ROUTE_GRAD)
+#undef MOE_ROUTE_GRAD
+    return hipGetLastError();
+}
+
+}  // namespace moe

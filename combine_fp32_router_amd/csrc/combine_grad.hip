@@ -1,0 +1,204 @@
+// Gradient of the combine: out[t] = sum_j w_tj * deq(row[pos_tj]) gives, for
+// the gradient d of out[t],
+//   d_row[pos_tj, h] = bf16_rne(w_tj * d_h)
+//   d_w_tj           = sum_h d_h * deq(row[pos_tj])_h    (0 for a dropped slot)
+// A quantised row's scale is taken out of the sum: sum_h d_h * code_h, times
+// the scale once.
+//
+// gfx950 design.  One block per token; each thread holds its 16-byte vectors
+// of d in registers as fp32 (VPT groups of 8 elements for bf16 rows, of 16
+// for the quantised ones), so d is read once for all k slots.  Per slot a
+// thread reads its part of the row, adds its products to one fp32 partial
+// and writes its part of w * d.  The partials of a group of slots reduce over
+// the wave, then over the block through LDS in wave order: the same bits
+// every time.
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+constexpr int kSlotGroup = 4;  // slots whose row loads are in flight together
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1)
+        v += __shfl_xor(v, o);
+    return v;
+}
+
+// Codes of one thread's group as fp32, without the scale.
+template <int Q>
+struct RowVec;
+template <>
+struct RowVec<0> {  // 8 bf16
+    static constexpr int n = 8;
+    typedef u32x4 vec;
+    static __device__ __forceinline__ void get(const vec &v, float *f) { unpack8(v, f); }
+};
+template <>
+struct RowVec<1> {  // 16 int8
+    static constexpr int n = 16;
+    typedef u32x4 vec;
+    static __device__ __forceinline__ void get(const vec &v, float *f)
+    {
+        dequant8(u32x2{v.x, v.y}, 1.0f, f);
+        dequant8(u32x2{v.z, v.w}, 1.0f, f + 8);
+    }
+};
+template <>
+struct RowVec<2> {  // 16 int4
+    static constexpr int n = 16;
+    typedef u32x2 vec;
+    static __device__ __forceinline__ void get(const vec &v, float *f)
+    {
+        dequant4x8(v.x, 1.0f, f);
+        dequant4x8(v.y, 1.0f, f + 8);
+    }
+};
+template <>
+struct RowVec<3> {  // 16 E4M3
+    static constexpr int n = 16;
+    typedef u32x4 vec;
+    static __device__ __forceinline__ void get(const vec &v, float *f)
+    {
+        dequant_fp8x8(u32x2{v.x, v.y}, 1.0f, f);
+        dequant_fp8x8(u32x2{v.z, v.w}, 1.0f, f + 8);
+    }
+};
+
+// ROWS: write d_row; GATES: read the rows and write d_w.
+template <int Q, int VPT, bool ROWS, bool GATES>
+__global__ __launch_bounds__(1024) void combine_grad_kernel(
+    const u32x4 *__restrict__ d_out, const void *__restrict__ rows_,
+    const float *__restrict__ scales, const int32_t *__restrict__ pos,
+    const float *__restrict__ w, int G, int k, u32x4 *__restrict__ d_rows, float *__restrict__ d_w)
+{
+    typedef RowVec<Q> RV;
+    constexpr int N = RV::n, NV = N / 8;
+    __shared__ float red[16][MOE_MAX_TOPK];  // [wave][slot]
+    const typename RV::vec *rows = static_cast<const typename RV::vec *>(rows_);
+    const int64_t t = blockIdx.x;
+    const int nthr = blockDim.x, wv = threadIdx.x / kWave;
+    const int32_t at = load_per_lane(pos + t * k, k);
+    const float wts = load_per_lane(w + t * k, k);
+    float d[VPT][N];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int g = threadIdx.x + i * nthr;
+#pragma unroll
+        for (int h = 0; h < NV; ++h)
+            unpack8(g < G ? d_out[(t * G + g) * NV + h] : u32x4{0, 0, 0, 0}, d[i] + 8 * h);
+    }
+    for (int j0 = 0; j0 < k; j0 += kSlotGroup) {
+        typename RV::vec v[kSlotGroup][VPT];
+        if (GATES) {
+#pragma unroll
+            for (int q = 0; q < kSlotGroup; ++q) {
+                const int32_t p = j0 + q < k ? lane_value(at, j0 + q) : -1;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int g = threadIdx.x + i * nthr;
+                    v[q][i] = typename RV::vec{};
+                    if (p >= 0 && g < G)
+                        v[q][i] = __builtin_nontemporal_load(rows + static_cast<int64_t>(p) * G + g);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kSlotGroup; ++q) {
+            const int j = j0 + q;
+            if (j >= k)
+                break;
+            const int32_t p = lane_value(at, j);
+            if (ROWS && p >= 0) {
+                const float wj = lane_value(wts, j);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int g = threadIdx.x + i * nthr;
+                    float f[N];
+#pragma unroll
+                    for (int c = 0; c < N; ++c)
+                        f[c] = wj * d[i][c];
+                    if (g < G)
+#pragma unroll
+                        for (int h = 0; h < NV; ++h)
+                            __builtin_nontemporal_store(
+                                pack8(f + 8 * h), d_rows + (static_cast<int64_t>(p) * G + g) * NV + h);
+                }
+            }
+            if (GATES) {
+                float dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    float f[N];
+                    RV::get(v[q][i], f);
+#pragma unroll
+                    for (int c = 0; c < N; ++c)
+                        dot = fmaf(d[i][c], f[c], dot);
+                }
+                dot = wave_sum(dot);
+                if (lane_id() == 0)
+                    red[wv][j] = dot;
+            }
+        }
+    }
+    if (GATES) {
+        __syncthreads();
+        if (static_cast<int>(threadIdx.x) < k) {
+            const int32_t p = pos[t * k + threadIdx.x];
+            float sum = 0.0f;
+            for (int i = 0; i < nthr / kWave; ++i)
+                sum += red[i][threadIdx.x];
+            if (Q != 0 && p >= 0)
+                sum *= scales[p];
+            d_w[t * k + threadIdx.x] = p >= 0 ? sum : 0.0f;
+        }
+    }
+}
+
+template <int Q>
+void launch_format(const void *d_out, const void *rows, const float *scales, const int32_t *pos,
+                   const float *w, int64_t T, int H, int k, void *d_rows, float *d_w,
+                   hipStream_t stream)
+{
+    const int G = H / RowVec<Q>::n;
+    const RowTiling rt = row_tiling(G);
+    const dim3 grid(static_cast<unsigned>(T)), block(rt.threads);
+#define MOE_CG(V, R, W)                                                                        \
+    combine_grad_kernel<Q, V, R, W><<<grid, block, 0, stream>>>(                               \
+        static_cast<const u32x4 *>(d_out), rows, scales, pos, w, G, k,                         \
+        static_cast<u32x4 *>(d_rows), d_w)
+#define MOE_CG_PARTS(V)                                                                        \
+    if (d_rows && d_w) { MOE_CG(V, true, true); }                                              \
+    else if (d_rows) { MOE_CG(V, true, false); }                                               \
+    else { MOE_CG(V, false, true); }
+    switch (rt.vpt) {
+    case 1: MOE_CG_PARTS(1); break;
+    case 2: MOE_CG_PARTS(2); break;
+    case 4: MOE_CG_PARTS(4); break;
+    default:
+        if constexpr (Q == 0) { MOE_CG_PARTS(8); }
+        break;
+    }
+#undef MOE_CG_PARTS
+#undef MOE_CG
+}
+
+}  // namespace
+
+hipError_t launch_combine_grad(const void *d_out, const void *rows, const float *scales, int quant,
+                               const int32_t *pos, const float *w, int64_t T, int H, int k,
+                               void *d_rows, float *d_w, hipStream_t stream)
+{
+    switch (quant) {
+    case 0: launch_format<0>(d_out, rows, scales, pos, w, T, H, k, d_rows, d_w, stream); break;
+    case 1: launch_format<1>(d_out, rows, scales, pos, w, T, H, k, d_rows, d_w, stream); break;
+    case 2: launch_format<2>(d_out, rows, scales, pos, w, T, H, k, d_rows, d_w, stream); break;
+    default: launch_format<3>(d_out, rows, scales, pos, w, T, H, k, d_rows, d_w, stream); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -96,6 +96,35 @@ hipError_t launch_gather_rows(const void *in, const float *in_scales, void *out,
                               int64_t max_rows, int H, int quant, const int32_t *map,
                               hipStream_t stream);
 
+// Balance loss over segments of `seg` tokens, and the router's gradient.
+size_t balance_workspace_bytes(int64_t T, int64_t seg, int E);
+hipError_t launch_balance_loss(const float *logits, const int32_t *idx, const uint8_t *mask,
+                               int64_t T, int64_t seg, int E, int k, float *loss, int32_t *counts,
+                               float *prob_sums, int32_t *live, void *workspace,
+                               hipStream_t stream);
+int64_t route_grad_blocks(int64_t T, int E);  // of kRouteThreads threads
+hipError_t launch_route_grad(const float *logits, const int32_t *idx, const float *w,
+                             const float *dw, const uint8_t *mask, const float *dloss,
+                             const int32_t *counts, const int32_t *live, int64_t T, int64_t seg,
+                             int E, int k, float *dlogits, hipStream_t stream);
+
+// Gradient of the combine; d_rows or d_w may be null.
+hipError_t launch_combine_grad(const void *d_out, const void *rows, const float *scales, int quant,
+                               const int32_t *pos, const float *w, int64_t T, int H, int k,
+                               void *d_rows, float *d_w, hipStream_t stream);
+
+// The experts' products over their runs of rows, and their gradients.
+hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const void *w,
+                                const float *bias, int act, const void *residual, int E,
+                                int64_t max_rows, int K, int N, void *out, void *preact,
+                                hipStream_t stream);
+hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
+                                   const void *z, int E, int64_t max_rows, int K, int N, void *dx,
+                                   hipStream_t stream);
+hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
+                                   int64_t max_rows, int K, int N, int flags, void *dw, float *db,
+                                   hipStream_t stream);
+
 // Threads per block and 16-byte vectors per thread covering one row of
 // `vecs` 16-byte vectors with one block (<= 1024 threads, a whole number of
 // 64-lane waves): one vector per thread up to 1024 vectors, then 2, 4, 8.

@@ -2,7 +2,8 @@
  * moe_recv.h -- the receiver side of the expert-parallel exchange: where
  * each source's segment lands in a rank's receive buffer, and the regroup of
  * the received rows into one contiguous run per expert, ready for the
- * experts, with its inverse for the return trip.  Exported by the same
+ * experts, with its inverse for the return trip; and the experts' matrix
+ * products over those runs, with their gradients.  Exported by the same
  * library as moe_route.h; conventions (device pointers, caller-owned,
  * asynchronous on `stream`, host-side validation, status codes) are those of
  * moe_route.h.
@@ -113,6 +114,107 @@ int moe_recv_regroup(const void *recv, const float *recv_scales, int64_t max_row
 int moe_recv_ungroup(const void *grouped, const float *grouped_scales, int64_t max_rows, int H,
                      int quant, const int32_t *group_pos, void *recv, float *recv_scales,
                      hipStream_t stream);
+
+/* Activations of the experts' products. */
+#define MOE_ACT_NONE 0   /* z                                                */
+#define MOE_ACT_RELU 1   /* max(z, 0); slope 0 at 0                          */
+#define MOE_ACT_SILU 2   /* z / (1 + exp(-z))                                */
+#define MOE_ACT_GELU 3   /* z (1 + erf(z / sqrt 2)) / 2                      */
+#define MOE_ACT_SWIGLU 4 /* silu(z_gate) * z_up: two columns of z per output */
+
+/*
+ * moe_expert_matmul -- every expert's product with its own run of rows:
+ *     z[p, :]   = x[p, :] W_e^T + bias_e
+ *     out[p, :] = bf16_rne( act(z[p, :]) + residual[p, :] )
+ * for the rows p of expert e, offsets[e] <= p + offsets[0] < offsets[e+1]:
+ * row 0 of the buffers is row offsets[0] of the flat numbering, so a rank
+ * holding only its own grouped buffer passes group_offsets + r*E/R and its
+ * E/R experts, and the flat buffer of all ranks passes group_offsets and E.
+ * E = 1 is a plain product.  bf16 inputs, fp32 sums (matrix cores); bias,
+ * activation and residual are applied to the fp32 sum, which is rounded once.
+ *
+ *   x          [max_rows, K] bf16 bits.                               (in)
+ *   offsets    [E+1] int32, device, non-decreasing: group_offsets.  (in)
+ *   w          [E, N, K] bf16 bits; MOE_ACT_SWIGLU: [E, 2N, K], an expert's
+ *              N gate rows, then its N up rows.                       (in)
+ *   bias       [E, N] fp32 (MOE_ACT_SWIGLU: [E, 2N]), or NULL.        (in)
+ *   act        MOE_ACT_*.
+ *   residual   [max_rows, N] bf16 bits, or NULL; may be out itself.   (in)
+ *   E, max_rows, K, N   1 <= E <= MOE_MAX_EXPERTS; 0 <= max_rows < 2^31, at
+ *              least the rows of all runs (a run is cut at max_rows: nothing
+ *              is read or written past it); K and N multiples of 16 in [16,
+ *              MOE_MAX_HIDDEN].
+ *   out        [max_rows, N] bf16 bits; rows of no run are not written. (out)
+ *   preact     [max_rows, N] (MOE_ACT_SWIGLU: [max_rows, 2N]) bf16 bits of z
+ *              rounded once, for the gradient; or NULL.               (out)
+ *
+ * Every array 16-byte aligned (offsets 4).  out and preact must not overlap
+ * each other or the inputs (but for out == residual).
+ * Errors: MOE_ERR_NULL; MOE_ERR_SHAPE; MOE_ERR_ALIGN; MOE_ERR_ALIAS (out or
+ * preact starts where x or w does, or both at one place, or preact where
+ * residual does).  max_rows == 0: MOE_OK, nothing launched.
+ */
+int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, const float *bias,
+                      int act, const void *residual, int E, int64_t max_rows, int K, int N,
+                      void *out, void *preact, hipStream_t stream);
+
+/*
+ * moe_expert_matmul_dx -- gradient of a product's input rows, carried through
+ * the activation that produced them.  For z = x W_e^T and the gradient dy of
+ * z:
+ *     g[p, :]  = dy[p, :] W_e
+ *     dx[p, :] = bf16_rne( g )                          (act MOE_ACT_NONE)
+ *              = bf16_rne( act'(preact[p, :]) * g )     (x = act(preact))
+ * MOE_ACT_SWIGLU: dx has 2K columns, the gate's gradient g * z_up *
+ * silu'(z_gate), then the up projection's g * silu(z_gate).  preact is what
+ * the forward call of the product before kept, so an expert of two products
+ * takes two calls and rounds twice.  (A residual's gradient is dy itself.)
+ *
+ *   dy      [max_rows, N] bf16 bits.                                  (in)
+ *   offsets, E, max_rows   as moe_expert_matmul.                      (in)
+ *   w       [E, N, K] bf16 bits, the forward product's weights (for a
+ *           product with MOE_ACT_SWIGLU, N here counts both halves).  (in)
+ *   act     activation between the two products.
+ *   preact  [max_rows, K] (MOE_ACT_SWIGLU: [max_rows, 2K]) bf16 bits; not
+ *           used for MOE_ACT_NONE.                                    (in)
+ *   dx      as preact; may be preact itself; rows of no run are not
+ *           written.                                                  (out)
+ *   K, N    multiples of 16 in [16, 2 * MOE_MAX_HIDDEN] (N) and [16,
+ *           MOE_MAX_HIDDEN] (K).
+ *
+ * Every array 16-byte aligned (offsets 4).  Errors: as moe_expert_matmul;
+ * MOE_ERR_ALIAS when dx starts where dy or w does.
+ */
+int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
+                         const void *preact, int E, int64_t max_rows, int K, int N, void *dx,
+                         hipStream_t stream);
+
+/* Flags of moe_expert_matmul_dw. */
+#define MOE_GRAD_FP32 0           /* dw and dbias fp32                       */
+#define MOE_GRAD_BF16 1           /* dw bf16 bits (dbias stays fp32)         */
+#define MOE_GRAD_ACCUMULATE 0x100 /* add to dw and dbias (fp32 dw only)      */
+
+/*
+ * moe_expert_matmul_dw -- gradient of every expert's weights and bias:
+ *     dw[e]    = sum over its rows p of dy[p, :]^T x[p, :]      [N, K]
+ *     dbias[e] = sum over its rows p of dy[p, :]                [N]
+ * in fp32, in a fixed order.  An expert without rows gets zeros (with
+ * MOE_GRAD_ACCUMULATE: keeps what is there).
+ *
+ *   dy, x    [max_rows, N], [max_rows, K] bf16 bits.                  (in)
+ *   offsets, E, max_rows, K, N   as moe_expert_matmul_dx.
+ *   flags    MOE_GRAD_FP32 or MOE_GRAD_BF16; MOE_GRAD_FP32 |
+ *            MOE_GRAD_ACCUMULATE.
+ *   dw       [E, N, K] fp32 or bf16 bits.                             (out)
+ *   dbias    [E, N] fp32, or NULL.                                    (out)
+ *
+ * Every array 16-byte aligned (offsets 4).  Errors: MOE_ERR_NULL (dy and x
+ * may be NULL when max_rows == 0), MOE_ERR_SHAPE (also unknown flags),
+ * MOE_ERR_ALIGN, MOE_ERR_ALIAS when dw starts where dy or x does.
+ */
+int moe_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
+                         int64_t max_rows, int K, int N, int flags, void *dw, float *dbias,
+                         hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -24,7 +24,13 @@
  * fused with the layout's counting pass; moe_route_layout_chunks_noalloc
  * for callers that cannot allocate), moe_combine_pack (the combine of one
  * chunk and the pack of the next in one launch).  The receiver side of the
- * exchange is declared in moe_recv.h.
+ * exchange and the experts' products are declared in moe_recv.h.
+ *
+ * Training: moe_balance_loss (the router's balance loss and per-expert
+ * counts), moe_route_grad (the gradient of the logits, through the gate
+ * weights and the balance loss) and moe_combine_grad (the gradient of the
+ * combine for the rows and the gate weights).  The pack's gradient is
+ * moe_combine with weights of 1: a token's gradient is the sum of its rows'.
  *
  * Conventions shared by every call
  *   - All array arguments are DEVICE pointers owned by the caller; the
@@ -388,6 +394,97 @@ int moe_combine_pack(const void *recv, const float *recv_scales, const int32_t *
                      const float *topk_w, int64_t Tc, void *out_bf16, const void *x_bf16,
                      const int32_t *pos_p, int64_t Tp, void *send, float *send_scales, int H,
                      int k, int quant, hipStream_t stream);
+
+/*
+ * moe_balance_loss -- the router's load-balance loss and per-expert counts.
+ * The batch is cut into segments of `seg_tokens` tokens (a sequence, or the
+ * whole batch), S = ceil(T / seg_tokens), at least 1; a segment with n live
+ * tokens, c_e slots routed to expert e and S_e = sum over its live tokens of
+ * softmax(logits[t])_e has
+ *     loss[s] = E / (k * n^2) * sum_e c_e * S_e        (0 when n == 0)
+ * that is E * sum_e f_e * P_e with the share of slots f_e = c_e / (k n) and
+ * the mean probability P_e = S_e / n: 1 when both are uniform.  The caller
+ * weighs the segments (moe_route_grad's d_loss).
+ *
+ *   logits        [T, E] fp32; -inf is allowed (probability 0) while a
+ *                 live token has a finite logit.                      (in)
+ *   topk_idx      [T, k] int32 ids; an id outside [0, E) is not counted. (in)
+ *   token_mask    NULL, or [T] bytes: tokens with 0 (padding) take no part,
+ *                 their logits and ids are not used.                   (in)
+ *   seg_tokens    >= 1 when T > 0; values >= T mean one segment.
+ *   loss          [S] fp32.                                           (out)
+ *   expert_counts [S][E] int32 c_e.                                   (out)
+ *   prob_sums     [S][E] fp32 S_e.                                    (out)
+ *   seg_live      [S] int32 n.                                        (out)
+ *   workspace     device scratch as for moe_dispatch_layout (query with
+ *                 NULL); its size depends on T, seg_tokens and E.
+ *
+ * Sums are taken in a fixed order: the same inputs give the same bits.
+ * Errors: MOE_ERR_NULL; MOE_ERR_SHAPE (T, E, k as moe_route_topk,
+ * seg_tokens < 1 with T > 0, more than 65535 segments); MOE_ERR_ALIGN
+ * (arrays not 4-byte aligned, workspace not 256-byte aligned);
+ * MOE_ERR_WORKSPACE.  T == 0 writes one segment of zeros.
+ */
+int moe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t *token_mask,
+                     int64_t T, int64_t seg_tokens, int E, int k, float *loss,
+                     int32_t *expert_counts, float *prob_sums, int32_t *seg_live,
+                     void *workspace, size_t *workspace_bytes, hipStream_t stream);
+
+/*
+ * moe_route_grad -- gradient of the router's logits.
+ *     d_logits[t, e] =  sum_{j: topk_idx[t, j] = e} w_j (d_j - sum_i w_i d_i)
+ *                     + d_loss[s] * E / (k n^2) * p_e (c_e - sum_e' c_e' p_e')
+ * with w = topk_w[t], d = d_topk_w[t], p = softmax(logits[t]) and s, n, c the
+ * token's segment, its live tokens and its counts: the first line through
+ * the renormalised gate weights of moe_route_topk, the second through
+ * moe_balance_loss (whose counts are constants).  Either part may be left
+ * out.  The whole row is written; a masked token's row is zero.
+ *
+ *   logits, token_mask, T, seg_tokens, E, k   as moe_balance_loss; logits,
+ *                 expert_counts and seg_live are not used when d_loss is
+ *                 NULL.                                                (in)
+ *   topk_idx, topk_w  [T, k] as moe_route_topk wrote them; an id that
+ *                 occurs twice gets both contributions, one outside [0, E)
+ *                 none.  Not used when d_topk_w is NULL.               (in)
+ *   d_topk_w      [T, k] fp32 gradient of the gate weights, or NULL.   (in)
+ *   d_loss        [S] fp32 gradient of each segment's loss, or NULL.   (in)
+ *   expert_counts, seg_live   from moe_balance_loss.                   (in)
+ *   d_logits      [T, E] fp32; may be logits itself.                  (out)
+ *
+ * Errors: MOE_ERR_NULL (also when both d_topk_w and d_loss are NULL),
+ * MOE_ERR_SHAPE as moe_balance_loss, MOE_ERR_ALIGN.  T == 0: MOE_OK, nothing
+ * launched.
+ */
+int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *topk_w,
+                   const float *d_topk_w, const uint8_t *token_mask, const float *d_loss,
+                   const int32_t *expert_counts, const int32_t *seg_live, int64_t T,
+                   int64_t seg_tokens, int E, int k, float *d_logits, hipStream_t stream);
+
+/*
+ * moe_combine_grad -- gradient of moe_combine.  For the gradient d_out of its
+ * output and every slot s = t*k + j with pos[s] >= 0:
+ *     d_recv[pos[s], h] = bf16_rne( topk_w[s] * d_out[t, h] )
+ *     d_topk_w[s]       = sum_h d_out[t, h] * deq(recv[pos[s]])[h]
+ * (fp32 sums in a fixed order; a quantised row's scale multiplies the sum of
+ * d_out * code once), and d_topk_w[s] = 0 for a dropped slot.  Rows of d_recv
+ * that no slot points to are not written.  The gradient rows are bf16
+ * whatever the payload of the forward rows; they go back to their experts as
+ * a bf16 payload does.
+ *
+ *   d_out        [T, H] bf16 bits, 16-byte aligned.                    (in)
+ *   recv, recv_scales, quant, pos, topk_w, T, H, k   as moe_combine;
+ *                recv and recv_scales are not used when d_topk_w is NULL. (in)
+ *   d_recv       bf16 row buffer (rows of 2*H bytes), 16-byte aligned, not
+ *                overlapping d_out or recv; or NULL.                  (out)
+ *   d_topk_w     [T*k] fp32, or NULL.                                 (out)
+ *
+ * Errors: as moe_combine; MOE_ERR_NULL also when both outputs are NULL;
+ * MOE_ERR_ALIAS when d_recv starts where d_out or a recv in use does.
+ * T == 0: MOE_OK, nothing launched.
+ */
+int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv_scales, int quant,
+                     const int32_t *pos, const float *topk_w, int64_t T, int H, int k,
+                     void *d_recv, float *d_topk_w, hipStream_t stream);
 
 #ifdef __cplusplus
 }
