@@ -23,34 +23,27 @@ __device__ __forceinline__ ExpertRun expert_run(const int32_t *__restrict__ offs
     return {a, b - a};
 }
 
-// A tile of rows of one expert: rows [first, first + n), n <= the tile's
-// height; n == 0 past the last tile.
-struct RowTile {
-    int e, first, n;
+// Workgroup j of a round runs on XCD j % 8, each with an L2 of its own: give
+// every XCD a contiguous range of the n entries.  -1 for spare workgroups.
+__device__ __forceinline__ int64_t xcd_order(int64_t j, int64_t n)
+{
+    const int64_t x = j % 8, i = j / 8, each = n / 8, more = n % 8;
+    if (i >= each + (x < more))
+        return -1;
+    return x * each + min(x, more) + i;
+}
+
+struct TileAt {
+    int row, col;
 };
 
-// The index-th tile of `height` rows over all experts' runs in expert order
-// (a run's last tile is short).  Every lane of the wave calls it; index is
-// uniform.  64 experts' tile counts are scanned at a time.
-__device__ __forceinline__ RowTile find_row_tile(const int32_t *__restrict__ offsets, int E,
-                                                 int max_rows, int height, int index)
+// Groups of eight row tiles, all columns of a group before the next: tiles
+// that run side by side share both operands' pieces in L2.
+__device__ __forceinline__ TileAt grouped_order(int64_t id, int row_tiles, int col_tiles)
 {
-    int before = 0;  // tiles of the experts below `e0`
-    for (int e0 = 0; e0 < E; e0 += kWave) {
-        const int e = e0 + lane_id();
-        const ExpertRun run = e < E ? expert_run(offsets, e, max_rows) : ExpertRun{0, 0};
-        const int tiles = (run.n + height - 1) / height;
-        const int upto = before + wave_inclusive_scan(tiles);
-        const uint64_t hit = __ballot(upto > index);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            const int in_run = (index - (lane_value(upto, l) - lane_value(tiles, l))) * height;
-            return {e0 + l, lane_value(run.first, l) + in_run,
-                    min(height, lane_value(run.n, l) - in_run)};
-        }
-        before = lane_value(upto, kWave - 1);
-    }
-    return {0, 0, 0};
+    const int group = static_cast<int>(id / (8 * col_tiles)), in = static_cast<int>(id % (8 * col_tiles));
+    const int height = min(8, row_tiles - 8 * group);
+    return {8 * group + in % height, in / height};
 }
 
 // Most tiles that E runs of together max_rows rows can have.
@@ -60,33 +53,57 @@ inline int64_t max_row_tiles(int64_t max_rows, int E, int height)
     return (max_rows - live) / height + live;
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
-
-// act(z) for the activations of one value (SwiGLU: act_pair).
-__device__ __forceinline__ float act_value(float z, int act)
+// exp and the reciprocal in single instructions, good to 1 ulp each, behind a
+// rounded product: off by about (|z| + 2) 2^-24 of the result, against the
+// 2^-9 of the bf16 that is stored.  Past +-88 they give 0 and 1.
+__device__ __forceinline__ float sigmoid(float z)
 {
-    if (act == MOE_ACT_RELU)
-        return fmaxf(z, 0.0f);
-    if (act == MOE_ACT_SILU)
-        return z * sigmoid(z);
-    if (act == MOE_ACT_GELU)
-        return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    return z;
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
 
-// d act / d z.
-__device__ __forceinline__ float act_slope(float z, int act)
+// v[i][j] = act(v[i][j]) for the activations of one value.
+template <int N, typename V>
+__device__ __forceinline__ void apply_act(V (&v)[N], int act)
 {
-    if (act == MOE_ACT_RELU)
-        return z > 0.0f ? 1.0f : 0.0f;
-    if (act == MOE_ACT_SILU) {
-        const float s = sigmoid(z);
-        return s * (1.0f + z * (1.0f - s));
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i)
+            v[i / 4][i % 4] = fmaxf(v[i / 4][i % 4], 0.0f);
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i)
+            v[i / 4][i % 4] *= sigmoid(v[i / 4][i % 4]);
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) {
+            const float z = v[i / 4][i % 4];
+            v[i / 4][i % 4] = 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        }
     }
-    if (act == MOE_ACT_GELU)
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-               z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    return 1.0f;
+}
+
+// v[i][j] *= act'(z[i][j]).
+template <int N, typename V>
+__device__ __forceinline__ void apply_slope(V (&v)[N], const V (&z)[N], int act)
+{
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i)
+            v[i / 4][i % 4] = z[i / 4][i % 4] > 0.0f ? v[i / 4][i % 4] : 0.0f;
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) {
+            const float x = z[i / 4][i % 4], s = sigmoid(x);
+            v[i / 4][i % 4] *= s * (1.0f + x * (1.0f - s));
+        }
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 4 * N; ++i) {
+            const float x = z[i / 4][i % 4];
+            v[i / 4][i % 4] *= 0.5f * (1.0f + erff(x * 0.70710678118654752f)) +
+                               x * __expf(-0.5f * x * x) * 0.39894228040143268f;
+        }
+    }
 }
 
 }  // namespace moe

@@ -1,20 +1,27 @@
 // One output tile of the experts' products on the matrix cores.
 //
-// C[row, col] = sum over r < R of Q[row, r] * P[col, r], BR rows and BC
-// columns, by WR x WC waves of (BR/WR) x (BC/WC) each, in 32x32x16 bf16
-// MFMAs whose first operand is P: lane l then holds row l%32 and, in
-// registers 4g..4g+3, columns 8g + 4(l/32).. of a 32x32 block.
+// C[row, col] = sum over r < R of Q[row, r] * P[col, r]: 256 rows by 256
+// columns a workgroup of four waves, one on each SIMD, 128 x 128 a wave in
+// 16x16x32 bf16 MFMAs.  Their first operand is P, so lane l holds columns
+// 4 (l/16) .. + 3 of a block's row l%16.  The wave's 256 accumulator
+// registers are the AGPR half of its 512: the MFMAs are written as inline
+// assembly on "a" registers, because the compiler, given the builtin, copies
+// accumulators between the two halves in the loop.
+//
+// Four waves of 128 x 128 read 128 KiB of LDS for 64 r, eight of 128 x 64
+// would read 192; with real data, where the card's power limits the clock,
+// that is worth 10% (8192 x 8192, r 7168, time of 64 r: 1.33 against 1.45 us).
 //
 // r is walked 64 at a time through two LDS stages, filled by loads that go
 // from memory to LDS without passing registers.  Such a load writes 16 bytes
 // a lane to consecutive LDS addresses, so the LDS image cannot be padded;
 // instead a lane fetches a permuted 16-byte piece of its row, chosen so that
-// the reads below fall on different banks:
-//   r contiguous in memory:  image [index][64 r], piece c of row i at c ^ (i/2)%8;
-//     a lane reads its eight r values with one 16-byte read.
-//   index contiguous:        image [64 r][index], piece c of row r at c ^ 4(r%4);
-//     two transposing 8-byte reads of four r rows give the same eight values.
-// Out of range reads of the buffer descriptor return zeros, so short tiles
+// the reads fall on different banks:
+//   r contiguous in memory: image [index][64 r]; a lane reads its eight r
+//     values with one 16-byte read.
+//   index contiguous:       image [64 r][index]; two transposing 8-byte reads
+//     of four r rows give the same eight values.
+// Reads of a buffer descriptor outside its range return zeros, so short tiles
 // and the end of r need no other care.
 #pragma once
 
@@ -24,125 +31,96 @@ namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 #define MOE_LDS __attribute__((address_space(3)))
 
 constexpr int kOutside = static_cast<int>(0x80000000u);  // an offset past every descriptor
+constexpr int kStep = 64;       // r of a stage
+constexpr int kTileWaves = 4;
 
-// ---- order of the tiles
-
-// Total tiles of `height` rows over all runs.
-__device__ __forceinline__ int count_row_tiles(const int32_t *__restrict__ offsets, int E,
-                                               int max_rows, int height)
-{
-    int n = 0;
-    for (int e = lane_id(); e < E; e += kWave)
-        n += (expert_run(offsets, e, max_rows).n + height - 1) / height;
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1)
-        n += __shfl_xor(n, o);
-    return static_cast<int>(uniform(n));
-}
-
-// Workgroup b runs on XCD b % 8, each with an L2 of its own: give every XCD a
-// contiguous range of the n tiles.  -1 for the grid's spare workgroups.
-__device__ __forceinline__ int xcd_order(int b, int n)
-{
-    const int x = b % 8, i = b / 8, each = n / 8, more = n % 8;
-    if (i >= each + (x < more))
-        return -1;
-    return x * each + min(x, more) + i;
-}
-
-struct TileAt {
-    int row, col;
-};
-
-// Groups of eight row tiles, all columns of a group before the next: tiles
-// that run side by side share both operands' pieces in L2.
-__device__ __forceinline__ TileAt grouped_order(int id, int row_tiles, int col_tiles)
-{
-    const int group = id / (8 * col_tiles), in = id % (8 * col_tiles);
-    const int height = min(8, row_tiles - 8 * group);
-    return {8 * group + in % height, in / height};
-}
-
-// ---- operands
-
-// Tile of W indices of an operand, 64 r a stage, staged by NW waves.
+// Image of W indices of an operand, kStep r a stage, staged by four waves.
 // CONTIG: memory [index][r], else [r][index].  PAIR: indices come in blocks
 // of 32 from two places in turn (gate and up weights).
-template <int W, int NW, bool CONTIG, bool PAIR>
+template <int W, bool CONTIG, bool PAIR>
 struct Operand {
-    static constexpr int kBytes = W * 128;
-    static constexpr int kLoads = W * 128 / 1024 / NW;  // of 1 KiB, per wave and stage
-    static constexpr int kRowsLoad = CONTIG ? 8 : 512 / W;  // memory rows a load covers
-    static_assert(W * 128 % (1024 * NW) == 0 && (CONTIG || !PAIR), "whole loads");
-    static_assert(CONTIG || (kRowsLoad * NW) % 4 == 0, "a wave's loads permute alike");
-    const char *base;
-    int pitch, n;  // bytes a memory row, indices inside
-    int off;       // this lane's offset in the wave's first load
-    int piece;     // CONTIG: its first r within the stage, the same in each of its loads
+    static constexpr int kBytes = W * kStep * 2;
+    static constexpr int kLoads = kBytes / 1024 / kTileWaves;   // of 1 KiB, per wave and stage
+    static constexpr int kPieces = CONTIG ? kStep / 8 : W / 8;  // 16-byte pieces of an image row
+    static constexpr int kRowsLoad = 64 / kPieces;              // image rows a load covers
+    static constexpr bool kSwap = !CONTIG && W == 256;          // a wave's loads lie 8 r apart
+    static_assert((CONTIG || !PAIR) && (CONTIG || W == 64 || W == 256), "the permutations below");
+    const char *base[PAIR ? 2 : 1];
+    int pitch, n;            // bytes of a memory row, indices inside
+    int off[kSwap ? 2 : 1];  // this lane's offset in its wave's even loads, and odd ones
+    int piece;               // CONTIG: its first r within the stage
 
+    // Where piece c of image row i is kept.  The 64 lanes of a read fall on
+    // 16 rows (CONTIG: 16 indices at one piece; else r = 0..3, 8..11, 16..19,
+    // 24..27 at two neighbouring pieces); LDS has 256 bytes of banks.
+    static __device__ __forceinline__ int place_of(int c, int i)
+    {
+        return CONTIG ? c ^ (i / 2 % 8)
+                      : W == 64 ? c ^ (i / 2 % 2 * 2 + i / 8 % 2 * 4) : c ^ (i % 4 * 2 + i / 8 % 2 * 8);
+    }
+
+    // Index 0 and r = 0 at p (PAIR: up weights at p2), `pitch_` elements a
+    // memory row, n_ indices inside.
     __device__ __forceinline__ void init(const uint16_t *p, const uint16_t *p2, int pitch_, int n_)
     {
-        // PAIR: each of a wave's loads covers 8 indices of a block of the same kind
-        static_assert(!PAIR || NW % 8 == 0, "whole pairs of blocks");
-        base = reinterpret_cast<const char *>(PAIR && uniform(threadIdx.x / kWave) / 4 % 2 ? p2 : p);
         pitch = pitch_ * 2;
         n = n_;
         const int w = threadIdx.x / kWave, lane = lane_id();
-        if (CONTIG) {
-            const int i = w * 8 + lane / 8;
-            const int row = PAIR ? i / 64 * 32 + i % 32 : i;
-            static_assert(!CONTIG || NW % 2 == 0, "a wave's loads permute alike");
-            piece = ((lane % 8) ^ (i / 2 % 8)) * 8;
-            off = row * pitch + piece * 2;
-        } else {
-            constexpr int kPieces = W / 8;
-            const int r = w * kRowsLoad + lane / kPieces;
-            off = r * pitch + ((lane % kPieces) ^ (r % 4 * 4)) * 16;
-        }
+        const int i = w * kRowsLoad + lane / kPieces;
+        const int c = place_of(lane % kPieces, i);
+        base[0] = reinterpret_cast<const char *>(p);
+        if (PAIR)
+            base[PAIR] = reinterpret_cast<const char *>(p2);
+        piece = c * 8;
+        off[0] = i * pitch + c * 16;
+        if (kSwap)
+            off[kSwap] = i * pitch + place_of(lane % kPieces, i + 8) * 16;
     }
 
-    // Starts this wave's j-th load of r0 .. r0 + 63 into `image`.
-    __device__ __forceinline__ void fetch(MOE_LDS char *__restrict__ image, int r0, int R, int j) const
+    // Starts this wave's j-th load of r0 .. r0 + kStep - 1 into `image`; the
+    // image's indices start at `first`.
+    __device__ __forceinline__ void fetch(MOE_LDS char *__restrict__ image, int r0, int R, int j,
+                                          int first = 0) const
     {
-        const int load = static_cast<int>(uniform(threadIdx.x / kWave)) + j * NW;
+        const int load = static_cast<int>(uniform(threadIdx.x / kWave)) + j * kTileWaves;
         MOE_LDS void *to = (MOE_LDS void *)(image + load * 1024);
+        // memory rows after those of the wave's first load; PAIR: four loads
+        // cover a block of 32 indices, all gate or all up
+        const int rows = PAIR ? j / 2 * 32 : j * kTileWaves * kRowsLoad;
+        const char *src = base[PAIR ? j % 2 : 0];
         if (CONTIG) {
-            // the row's pieces past R; adding rows to kOutside stays outside
-            const int at = (r0 + piece < R ? off : kOutside) + j * (PAIR ? NW * 4 : NW * 8) * pitch;
+            // pieces past R are outside, whatever row is added
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                row_rsrc(const_cast<char *>(base) + static_cast<int64_t>(r0) * 2, max(0, n * pitch - r0 * 2)), to, 16, at, 0, 0, 0);
+                row_rsrc(const_cast<char *>(src) + static_cast<int64_t>(r0) * 2, max(0, n * pitch - r0 * 2)),
+                to, 16, (r0 + piece < R ? off[0] : kOutside) + (first + rows) * pitch, 0, 0, 0);
         } else {
-            const int rows = min(64, R - r0);  // <= 0 past the end: nothing is read
+            const int live = min(kStep, R - r0);  // <= 0 past the end: nothing is read
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                row_rsrc(const_cast<char *>(base) + static_cast<int64_t>(r0) * pitch, rows > 0 ? (rows - 1) * pitch + n * 2 : 0), to, 16,
-                off + j * NW * kRowsLoad * pitch, 0, 0, 0);
+                row_rsrc(const_cast<char *>(src) + static_cast<int64_t>(r0) * pitch,
+                         live > 0 ? (live - 1) * pitch + n * 2 : 0),
+                to, 16, off[kSwap ? j % 2 : 0] + rows * pitch + first * 2, 0, 0, 0);
         }
     }
 
-    // This lane's place in the image for the fragments that start at index 0
-    // and r = s.
-    static __device__ __forceinline__ int lane_place(int s)
+    // The fragment of indices i0 .. i0 + 15 (i0 a multiple of 16) and r = s ..
+    // s + 31: lane l gets index l%16 and r = 8 (l/16) .. + 7.
+    static __device__ __forceinline__ bf16x8 frag(const MOE_LDS char *__restrict__ image, int i0, int s)
     {
         const int lane = lane_id();
-        if (CONTIG)
-            return lane % 32 * 128 + ((s / 8 + lane / 32) ^ (lane % 32 / 2 % 8)) * 16;
-        const int r = s + lane / 32 * 8 + lane % 16 / 4, i = lane / 16 % 2 * 16 + lane % 4 * 4;
-        return r * (2 * W) + ((i / 8) ^ (r % 4 * 4)) * 16 + i % 8 * 2;
-    }
-
-    // The fragment of indices i0 .. i0 + 31 (i0 a multiple of 32) and r = s ..
-    // s + 15; `place` is lane_place(s).
-    static __device__ __forceinline__ bf16x8 frag(const MOE_LDS char *__restrict__ image, int i0, int place)
-    {
         if constexpr (CONTIG) {
-            return *reinterpret_cast<const MOE_LDS bf16x8 *>(image + i0 * 128 + place);
+            const int place = lane % 16 * (kStep * 2) + place_of(s / 8 + lane / 16, lane % 16) * 16;
+            return *reinterpret_cast<const MOE_LDS bf16x8 *>(image + i0 * (kStep * 2) + place);
         } else {
-            // i0 adds 4 pieces a block of 32, under the same permutation
+            // lane l of 16 points at r = l/4, indices 4 (l%4) .. of the 4 x 16
+            // block it is to get column l of; i0 adds 2 pieces a block of 16
+            // under the same permutation, which is the same again 4 r later
+            const int r = s + lane / 16 * 8 + lane % 16 / 4, i = lane % 4 * 4;
+            const int place = r * (2 * W) + place_of(i / 8, r) * 16 + i % 8 * 2;
             const MOE_LDS char *p = image + (place ^ (i0 * 2));
             const bf16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((MOE_LDS bf16x4 *)(p));
             const bf16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((MOE_LDS bf16x4 *)(p + 4 * 2 * W));
@@ -151,158 +129,333 @@ struct Operand {
     }
 };
 
-template <int BR, int BC, int WR, int WC, bool P_CONTIG, bool Q_CONTIG, bool GATED>
+// Wave w has columns 128 (w%2) .. + 127 and, of every block of 64 rows, the 32
+// from 32 (w/2), so that a short tile's rows are shared evenly.
+template <bool P_CONTIG, bool Q_CONTIG, bool GATED>
 struct Tile {
-    static constexpr int NW = WR * WC;
-    static constexpr int kRowFrags = BR / WR / 32, kColFrags = BC / WC / 32;
-    typedef Operand<BC, NW, P_CONTIG, GATED> P;
-    typedef Operand<BR, NW, Q_CONTIG, false> Q;
-    static constexpr int kStageBytes = P::kBytes + Q::kBytes;
+    static constexpr int kRows = 256, kCols = 256;
+    static constexpr int kBlocks = 4;  // of 64 rows
+    static constexpr int kFrags = 8;   // blocks of 16 columns of a wave
+    typedef Operand<kCols, P_CONTIG, GATED> P;
+    typedef Operand<64, Q_CONTIG, false> Q;  // an image for each block of 64 rows
+    static constexpr int kStageBytes = P::kBytes + kBlocks * Q::kBytes;
+    static constexpr int kThinBytes = P::kBytes + 2 * Q::kBytes;  // of a stage of at most 128 rows
+    static constexpr int kLdsBytes = 3 * kThinBytes;
+    static_assert(kLdsBytes >= 2 * kStageBytes, "two whole stages or three thin ones");
     P p;
     Q q;
     int R;
-    f32x16 acc[kColFrags][kRowFrags];
-    f32x16 sums;  // SUMS: sums of Q over r, of the row block that this wave keeps
+    f32x4 acc[kFrags][kBlocks][2];
+    float sum[2][2];  // SUMS: this lane's parts of the sums of Q over r, of row blocks 2 (w%2), + 1
 
     __device__ __forceinline__ int wave() const { return static_cast<int>(uniform(threadIdx.x / kWave)); }
-    __device__ __forceinline__ int col0() const { return wave() % WC * (BC / WC); }
-    __device__ __forceinline__ int row0() const { return wave() / WC * (BR / WR); }
+    __device__ __forceinline__ int col0() const { return wave() % 2 * 128; }
+    __device__ __forceinline__ int row0(int block) const { return block * 64 + wave() / 2 * 32; }
 
-    __device__ __forceinline__ void init(const uint16_t *pp, const uint16_t *pp2, int ppitch, int pn,
-                                         const uint16_t *qp, int qpitch, int qn, int R_)
+    __device__ __forceinline__ void clear()
     {
-        p.init(pp, pp2, ppitch, pn);
-        q.init(qp, nullptr, qpitch, qn);
-        R = R_;
-        sums = f32x16{};
+        sum[0][0] = sum[0][1] = sum[1][0] = sum[1][1] = 0.0f;
 #pragma unroll
-        for (int r = 0; r < kRowFrags; ++r)
+        for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-            for (int c = 0; c < kColFrags; ++c)
-                acc[c][r] = f32x16{};
+            for (int c = 0; c < kFrags; ++c)
+                acc[c][b][0] = acc[c][b][1] = f32x4{};
     }
 
+    // Waits until at most LEFT of this wave's loads are in flight and its LDS
+    // reads are done, then for the other waves.  Nothing moves across.
+    template <int LEFT>
+    static __device__ __forceinline__ void join()
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070 | (LEFT & 15) | (LEFT >> 4) << 14);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    typedef bf16x8 Slice[2][2];  // 32 indices (two of 16), 64 r (two of 32)
     struct Frags {
-        bf16x8 p[kColFrags], q[kRowFrags];
+        bf16x8 p[kFrags][2];
+        Slice q[2];
     };
-    __device__ __forceinline__ void read(Frags &f, const MOE_LDS char *__restrict__ cur, int s) const
+    __device__ __forceinline__ void read_p(Frags &f, int c, int s, const MOE_LDS char *__restrict__ stage) const
     {
-        const int pl = P::lane_place(s), ql = Q::lane_place(s);
-#pragma unroll
-        for (int c = 0; c < kColFrags; ++c)
-            f.p[c] = P::frag(cur, col0() + c * 32, pl);
-#pragma unroll
-        for (int r = 0; r < kRowFrags; ++r)
-            f.q[r] = Q::frag(cur + P::kBytes, row0() + r * 32, ql);
+        f.p[c][s] = P::frag(stage, col0() + c * 16, 32 * s);
+    }
+    __device__ __forceinline__ void read_q(Slice &q, int b, int h, int s, const MOE_LDS char *__restrict__ stage) const
+    {
+        q[h][s] = Q::frag(stage + P::kBytes + b * Q::kBytes, wave() / 2 * 32 + h * 16, 32 * s);
+    }
+    __device__ __forceinline__ void load_p(MOE_LDS char *__restrict__ stage, int r0, int j) const
+    {
+        p.fetch(stage, r0, R, j);
+    }
+    __device__ __forceinline__ void load_q(MOE_LDS char *__restrict__ stage, int r0, int b, int j) const
+    {
+        q.fetch(stage + P::kBytes + b * Q::kBytes, r0, R, j, 64 * b);
     }
 
-    // SUMS: wave column c also multiplies its row block c by ones.
-    static_assert(kRowFrags <= WC, "a wave column for each row block");
-
-    // Multiplies the stage at `cur` while the loads of the next one, at r0,
-    // run into `nxt`.
-    template <bool SUMS>
-    __device__ __forceinline__ void step(const MOE_LDS char *__restrict__ cur, MOE_LDS char *__restrict__ nxt, int r0)
+    // Multiplies row block b, half s of the stage; after each column block's
+    // products, beside(c) issues what is to run beside the next ones.
+    template <typename F>
+    __device__ __forceinline__ void group(const Frags &f, const Slice &q, int b, int s, F beside)
     {
-        Frags f[2];
-        read(f[0], cur, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int c = 0; c < kFrags; ++c) {
 #pragma unroll
-            for (int j = i * P::kLoads / 4; j < (i + 1) * P::kLoads / 4; ++j)
-                p.fetch(nxt, r0, R, j);
-#pragma unroll
-            for (int j = i * Q::kLoads / 4; j < (i + 1) * Q::kLoads / 4; ++j)
-                q.fetch(nxt + P::kBytes, r0, R, j);
-            if (i < 3)
-                read(f[(i + 1) % 2], cur, 16 * (i + 1));
-#pragma unroll
-            for (int c = 0; c < kColFrags; ++c)
-#pragma unroll
-                for (int r = 0; r < kRowFrags; ++r)
-                    acc[c][r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[i % 2].p[c], f[i % 2].q[r], acc[c][r], 0, 0, 0);
-            if (SUMS) {
-                const __bf16 one = static_cast<__bf16>(1.0f);
-                const bf16x8 ones = {one, one, one, one, one, one, one, one};
-                bf16x8 mine = f[i % 2].q[0];
-#pragma unroll
-                for (int r = 1; r < kRowFrags; ++r)
-                    mine = wave() % WC == r ? f[i % 2].q[r] : mine;
-                sums = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ones, mine, sums, 0, 0, 0);
-            }
+            for (int h = 0; h < 2; ++h)
+                if (c == 0 && h == 0)  // two wait states behind whatever vector instruction wrote an operand
+                    asm("s_nop 1\nv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[c][b][h]) : "v"(f.p[c][s]), "v"(q[h][s]));
+                else
+                    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[c][b][h]) : "v"(f.p[c][s]), "v"(q[h][s]));
+            __builtin_amdgcn_sched_barrier(0);
+            beside(c);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-
-    // Waits for the loads in flight and for the other waves.
-    static __device__ __forceinline__ void join()
+    template <bool SUMS>
+    __device__ __forceinline__ void add_up(const Slice &q, int b)
     {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        if (SUMS && wave() % 2 == b / 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+                unpack8(__builtin_bit_cast(u32x4, q[i / 2][i % 2]), v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sum[b % 2][i / 2] += v[j];
+            }
     }
 
-    template <bool SUMS = false>
-    __device__ __forceinline__ void run(char (&lds)[2][kStageBytes])
+    // The loads that a tile's first steps expect to be in flight.
+    __device__ __forceinline__ void start(MOE_LDS char *lds) const
     {
-        MOE_LDS char *cur = (MOE_LDS char *)lds[0], *nxt = (MOE_LDS char *)lds[1];
-        if (R <= 0)
-            return;
 #pragma unroll
         for (int j = 0; j < P::kLoads; ++j)
-            p.fetch(cur, 0, R, j);
+            load_p(lds, 0, j);
+        load_pair(lds, 0, 0);
+        load_pair(lds, 0, 1);
+        load_pair(lds, 0, 2);
+#pragma unroll
+        for (int j = 0; j < P::kLoads; ++j)
+            load_p(lds + kStageBytes, kStep, j);
+        load_pair(lds, 0, 3);
+        load_pair(lds + kStageBytes, kStep, 0);
+        load_pair(lds + kStageBytes, kStep, 1);
+    }
+    __device__ __forceinline__ void load_pair(MOE_LDS char *__restrict__ stage, int r0, int b) const
+    {
 #pragma unroll
         for (int j = 0; j < Q::kLoads; ++j)
-            q.fetch(cur + P::kBytes, 0, R, j);
+            load_q(stage, r0, b, j);
+    }
+
+    // Stage k, at offset `cur` of LDS, in four phases, one for each block of
+    // 64 rows; its P and first Q block are in f.  Each phase multiplies what
+    // the phase before it read, and an image is refilled (for stage k + 2, Q
+    // block 3 and the end of block 2: k + 1) as soon as a join has shown that
+    // every wave has read it: one to one and a half stages ahead of its use,
+    // two loads for every 16 MFMAs.  Issued together the loads stall their
+    // waves: a step took 17% longer.  `rd` and `wr` are the same LDS, apart
+    // for the compiler, which would else wait for every load before a read.
+    template <bool SUMS>
+    __device__ __forceinline__ void step(Frags &f, const MOE_LDS char *__restrict__ rd,
+                                         MOE_LDS char *__restrict__ wr, int cur, int nxt, int r0)
+    {
+        group(f, f.q[0], 0, 0, [&](int c) {
+            if (c == 2 || c == 5)
+                load_q(wr + nxt, r0 + kStep, 2, c / 3);
+        });
+        join<16>();  // Q blocks 1 and 2 of this stage are here; all P and Q block 0 were read
+        add_up<SUMS>(f.q[0], 0);
+        group(f, f.q[0], 0, 1, [&](int c) {
+            if (c < 4)
+                read_q(f.q[1], 1, c % 2, c / 2, rd + cur);
+            if (c == 4 || c == 6)
+                load_p(wr + cur, r0 + 2 * kStep, c / 2 - 2);
+        });
+        group(f, f.q[1], 1, 0, [&](int c) {
+            if (c == 1 || c == 3)
+                read_q(f.q[0], 2, c / 2, 0, rd + cur);
+            if (c == 4 || c == 6)
+                load_p(wr + cur, r0 + 2 * kStep, c / 2);
+        });
+        add_up<SUMS>(f.q[1], 1);
+        group(f, f.q[1], 1, 1, [&](int c) {
+            if (c == 1 || c == 3)
+                read_q(f.q[0], 2, c / 2, 1, rd + cur);
+            if (c == 4 || c == 6)
+                load_p(wr + cur, r0 + 2 * kStep, c / 2 + 2);
+        });
+        group(f, f.q[0], 2, 0, [&](int c) {
+            if (c == 2 || c == 5)
+                load_p(wr + cur, r0 + 2 * kStep, c / 3 + 6);
+        });
+        join<12>();  // Q block 3 of this stage, P and Q block 0 of the next are here; blocks 1 and 2 were read
+        add_up<SUMS>(f.q[0], 2);
+        group(f, f.q[0], 2, 1, [&](int c) {
+            if (c < 4)
+                read_q(f.q[1], 3, c % 2, c / 2, rd + cur);
+            if (c == 4 || c == 6)
+                load_q(wr + nxt, r0 + kStep, 3, c / 2 - 2);
+        });
+        add_up<SUMS>(f.q[1], 3);
+        group(f, f.q[1], 3, 0, [&](int c) {
+            if (c < 4)
+                read_q(f.q[0], 0, c % 2, c / 2, rd + nxt);
+            read_p(f, c, 0, rd + nxt);
+            if (c == 4 || c == 6)
+                load_q(wr + cur, r0 + 2 * kStep, 0, c / 2 - 2);
+        });
+        group(f, f.q[1], 3, 1, [&](int c) {
+            read_p(f, c, 1, rd + nxt);
+            if (c == 4 || c == 6)
+                load_q(wr + cur, r0 + 2 * kStep, 1, c / 2 - 2);
+        });
+    }
+
+    // The product of a tile whose start() is under way.  (Memory operations
+    // issued since only make the joins wait for more than they need.)
+    template <bool SUMS>
+    __device__ __forceinline__ void run(MOE_LDS char *lds)
+    {
+        int cur = 0, nxt = kStageBytes;
+        Frags f;
+        join<18>();  // P and Q block 0 of the first stage
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            read_q(f.q[0], 0, 0, s, lds);
+            read_q(f.q[0], 0, 1, s, lds);
+#pragma unroll
+            for (int c = 0; c < kFrags; ++c)
+                read_p(f, c, s, lds);
+        }
 #pragma unroll 1
-        for (int r0 = 0; r0 < R; r0 += 64) {
-            join();
-            step<SUMS>(cur, nxt, r0 + 64);
-            MOE_LDS char *t = cur;
+        for (int r0 = 0; r0 < R; r0 += kStep) {
+            step<SUMS>(f, lds, lds, cur, nxt, r0);
+            const int t = cur;
             cur = nxt;
             nxt = t;
         }
+        settle();
     }
 
-    // Calls f(row, column, values, up values) for eight columns of one row at
-    // a time: 32 rows of a wave's columns go through its part of LDS, so that
-    // lanes take neighbouring columns and memory sees whole lines.  GATED:
-    // `column` counts output columns, the gate's values and the up values.
-    static constexpr int kWaveCols = BC / WC, kOutPitch = kWaveCols + 4;  // floats; rows 4 banks apart
-    static_assert(NW * 32 * kOutPitch * 4 <= 2 * kStageBytes, "fits the stages");
-    template <typename F>
-    __device__ __forceinline__ void finish(char (&lds)[2][kStageBytes], F f)
+    // A tile of at most NB blocks of 64 rows: three stages, whole stages in
+    // flight; P's reading bounds it, not the products.
+    __device__ __forceinline__ void load_thin(MOE_LDS char *__restrict__ stage, int r0, int nb) const
     {
-        join();
-        const int lane = lane_id();
-        float *mine = reinterpret_cast<float *>(lds[0]) + wave() * (32 * kOutPitch);
 #pragma unroll
-        for (int r = 0; r < kRowFrags; ++r) {
+        for (int j = 0; j < P::kLoads; ++j)
+            load_p(stage, r0, j);
 #pragma unroll
-            for (int c = 0; c < kColFrags; ++c)
+        for (int b = 0; b < 2; ++b)
+            if (b < nb)
+                load_pair(stage, r0, b);
+    }
+    __device__ __forceinline__ void start_thin(MOE_LDS char *lds, int nb) const
+    {
+        load_thin(lds, 0, nb);
+        load_thin(lds + kThinBytes, kStep, nb);
+    }
+    template <int NB, bool SUMS>
+    __device__ __forceinline__ void step_thin(const MOE_LDS char *__restrict__ rd, MOE_LDS char *__restrict__ wr,
+                                              int r0)
+    {
+        join<P::kLoads + NB * Q::kLoads>();  // this stage is here, and the third was read
+        load_thin(wr, r0 + 2 * kStep, NB);
+        Frags f;
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *reinterpret_cast<float4 *>(mine + lane % 32 * kOutPitch + c * 32 + g * 8 + lane / 32 * 4) =
-                        make_float4(acc[c][r][4 * g], acc[c][r][4 * g + 1], acc[c][r][4 * g + 2], acc[c][r][4 * g + 3]);
-            constexpr int kOuts = kWaveCols / (GATED ? 2 : 1) / 8;  // of a row
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i)
+                read_q(f.q[i / 2], i / 2, i % 2, s, rd);
+#pragma unroll
+            for (int c = 0; c < kFrags; ++c)
+                read_p(f, c, s, rd);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            add_up<SUMS>(f.q[b], b);
+            group(f, f.q[b], b, 0, [](int) {});
+            group(f, f.q[b], b, 1, [](int) {});
+        }
+    }
+    template <int NB, bool SUMS>
+    __device__ __forceinline__ void run_thin(MOE_LDS char *lds)
+    {
+        int cur = 0, into = 2 * kThinBytes;
 #pragma unroll 1
-            for (int i = lane; i < 32 * kOuts; i += kWave) {
-                const int row = i / kOuts, o = i % kOuts * 8;
-                // gated: blocks of 32 gate and 32 up columns in turn
-                const float *src = mine + row * kOutPitch + (GATED ? o / 32 * 64 + o % 32 : o);
-                float v[8], u[8];
+        for (int r0 = 0; r0 < R; r0 += kStep) {
+            step_thin<NB, SUMS>(lds + cur, lds + into, r0);
+            into = cur;
+            cur = cur == 2 * kThinBytes ? 0 : cur + kThinBytes;
+        }
+        settle();
+    }
+
+    // The same for a tile of `rows` rows (start_rows: its first loads).
+    __device__ __forceinline__ void start_rows(int rows, MOE_LDS char *lds) const
+    {
+        if (rows > 128)
+            start(lds);
+        else if (rows > 64)
+            start_thin(lds, 2);
+        else
+            start_thin(lds, 1);
+    }
+    template <bool SUMS>
+    __device__ __forceinline__ void run_rows(int rows, MOE_LDS char *lds)
+    {
+        if (rows > 128)
+            run<SUMS>(lds);
+        else if (rows > 64)
+            run_thin<2, SUMS>(lds);
+        else
+            run_thin<1, SUMS>(lds);
+    }
+
+    // The last products written, all loads and reads done, in all waves.
+    static __device__ __forceinline__ void settle()
+    {
+        asm volatile("s_nop 15\ns_nop 15" ::: "memory");  // MFMA results, before they are read
+        join<0>();
+    }
+
+    // Calls f(row, column, v) for this lane's part of each of its rows: v[c]
+    // has columns column + 16 c .. + 3.  The row's accumulators are picked by a
+    // switch, so that the code behind them is there once.
+    template <typename F>
+    __device__ __forceinline__ void finish(int rows, F f) const
+    {
+        const int lane = lane_id();
+#pragma unroll 1
+        for (int i = 0; i < 2 * kBlocks; ++i) {
+            const int row = row0(i / 2) + i % 2 * 16 + lane % 16;
+            if (row0(i / 2) + i % 2 * 16 >= rows)
+                break;
+            f32x4 v[kFrags];
+#define MOE_PICK(I)                                                                            \
+    case I:                                                                                    \
+        _Pragma("unroll") for (int c = 0; c < kFrags; ++c) v[c] = acc[c][I / 2][I % 2];        \
+        break
+            switch (i) {
+                MOE_PICK(0);
+                MOE_PICK(1);
+                MOE_PICK(2);
+                MOE_PICK(3);
+                MOE_PICK(4);
+                MOE_PICK(5);
+                MOE_PICK(6);
+            default:
 #pragma unroll
-                for (int h = 0; h < 8; h += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src + h);
-                    v[h] = x.x, v[h + 1] = x.y, v[h + 2] = x.z, v[h + 3] = x.w;
-                    if (GATED) {
-                        const float4 y = *reinterpret_cast<const float4 *>(src + 32 + h);
-                        u[h] = y.x, u[h + 1] = y.y, u[h + 2] = y.z, u[h + 3] = y.w;
-                    }
-                }
-                f(row0() + r * 32 + row, col0() / (GATED ? 2 : 1) + o, v, u);
+                for (int c = 0; c < kFrags; ++c)
+                    v[c] = acc[c][3][1];
             }
+#undef MOE_PICK
+            if (row < rows)
+                f(row, col0() + lane / 16 * 4, v);
         }
     }
 };
