@@ -33,128 +33,280 @@ struct Args {
     int rows;               // dw: rows of the output (N)
 };
 
-constexpr int kFrags = 8;  // column blocks of 16 that a wave finishes of a row, four columns a lane
+// Results leave 16 rows of a wave's 128 columns at a time.  A lane's share is
+// four columns of each of eight blocks of 16 (the MFMA's layout); memory is
+// read and written in 16-byte pieces of whole rows.  The two meet in 4 KiB of
+// LDS a wave, rows of 256 bytes, piece p of row r kept at p ^ r: stored
+// straight from the MFMA's layout, in pieces of 8 bytes, a tile's results cost
+// L2 four requests a line, and took 17000 clocks instead of 10000.
+// Rows and columns outside a tile are given offsets outside the buffer
+// descriptors, whose reads return 0 and whose writes are dropped, so that the
+// number of memory operations in flight is always known.
+constexpr int kFrags = 8;
 
-__device__ __forceinline__ f32x4 load4(const uint16_t *p)
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ f32x4 widen4(u32x2 v)
 {
-    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
     return f32x4{bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
 }
-__device__ __forceinline__ void store4(uint16_t *p, f32x4 f)
+__device__ __forceinline__ u32x2 round4(f32x4 f)
 {
-    *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w)};
+    const bf16x2 a = __builtin_convertvector((f32x2{f.x, f.y}), bf16x2);
+    const bf16x2 b = __builtin_convertvector((f32x2{f.z, f.w}), bf16x2);
+    return u32x2{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b)};
 }
 
-// One row of the forward product: v[i] has columns c + 16 i .. + 3 (i < n
-// inside), GATED: v[4 i + j] of the gate and v[4 i + 2 + j] of the up half
-// columns c + 32 i + 16 j.
+// The wave's LDS: 16 rows of up to sixteen 16-byte pieces.
+struct Place {
+    MOE_LDS char *base;
+    // MFMA layout: four columns of block c, as bf16 or fp32 (c < 4)
+    static __device__ __forceinline__ int half(int c)
+    {
+        const int lane = lane_id();
+        return lane % 16 * 256 + ((c * 2 + lane / 32) ^ (lane % 16)) * 16 + lane / 16 % 2 * 8;
+    }
+    static __device__ __forceinline__ int whole(int c)
+    {
+        const int lane = lane_id();
+        return lane % 16 * 256 + ((c * 4 + lane / 16) ^ (lane % 16)) * 16;
+    }
+    // row layout: piece lane%P of row (64 / P) j + lane/P
+    template <int P>
+    static __device__ __forceinline__ int piece(int j)
+    {
+        const int lane = lane_id(), row = 64 / P * j + lane / P;
+        return row * 256 + ((lane % P) ^ row) * 16;
+    }
+};
+
+// A row-major array in memory, from a tile's first row on: 16-byte pieces of
+// its rows, P of them a wave's columns.
+template <int P>
+struct Pieces {
+    __amdgpu_buffer_rsrc_t rsrc;
+    int pitch, col, n;  // bytes of a row, this lane's offset in a row (kOutside past the columns), rows
+
+    // Rows first .. first + n - 1 of `cols` columns of `size` bytes; the wave's
+    // pieces start at column c, `inside` of its columns are the array's.
+    __device__ __forceinline__ Pieces(const void *p, int64_t first, int n_, int cols, int size, int c, int inside)
+        : rsrc(row_rsrc(const_cast<char *>(static_cast<const char *>(p)) + first * cols * size, n_ * cols * size)),
+          pitch(cols * size), n(n_)
+    {
+        const int in_wave = lane_id() % P * (16 / size);
+        col = in_wave < inside ? (c + in_wave) * size : kOutside;
+    }
+    static constexpr int kCount = P / 4;  // loads or stores for 16 rows
+    // offset of the j-th of them, for the 16 rows from `row`
+    __device__ __forceinline__ int at(int row, int j) const
+    {
+        const int r = row + 64 / P * j + lane_id() / P;
+        return r < n && col != kOutside ? r * pitch + col : kOutside;
+    }
+    __device__ __forceinline__ u32x4 load(int row, int j) const
+    {
+        return __builtin_amdgcn_raw_buffer_load_b128(rsrc, at(row, j), 0, 0);
+    }
+    __device__ __forceinline__ void store(int row, int j, u32x4 v) const
+    {
+        __builtin_amdgcn_raw_buffer_store_b128(v, rsrc, at(row, j), 0, 0);
+    }
+};
+
+// Loaded pieces of 16 rows -> the MFMA layout (blocks first, first + step, ...
+// of v), and back.
+template <int P, int BLOCKS>
+__device__ __forceinline__ void to_blocks(MOE_LDS char *__restrict__ lds, const u32x4 (&in)[P / 4], f32x4 (&v)[BLOCKS])
+{
+#pragma unroll
+    for (int j = 0; j < P / 4; ++j)
+        *reinterpret_cast<MOE_LDS u32x4 *>(lds + Place::piece<P>(j)) = in[j];
+#pragma unroll
+    for (int c = 0; c < BLOCKS; ++c)
+        v[c] = widen4(*reinterpret_cast<const MOE_LDS u32x2 *>(lds + Place::half(c)));
+}
+template <int P, int BLOCKS>
+__device__ __forceinline__ void store_blocks(MOE_LDS char *__restrict__ lds, const f32x4 (&v)[BLOCKS],
+                                             const Pieces<P> &out, int row)
+{
+#pragma unroll
+    for (int c = 0; c < BLOCKS; ++c)
+        *reinterpret_cast<MOE_LDS u32x2 *>(lds + Place::half(c)) = round4(v[c]);
+#pragma unroll
+    for (int j = 0; j < P / 4; ++j)
+        out.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<P>(j)));
+}
+
+// Forward: bias, pre-activations, activation, residual.  GATED: v[0, 1, 4, 5]
+// are the gate's four blocks of 16 columns, v[2, 3, 6, 7] the up half's.
 template <bool GATED>
-__device__ __forceinline__ void finish_forward(const Args &a, int e, int64_t row, int c, int n,
-                                               f32x4 (&v)[kFrags])
-{
-    constexpr int wide = GATED ? 2 : 1;
-    if (a.bias) {
-        const float *b = a.bias + static_cast<int64_t>(e) * wide * a.C + c;
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i) {
-            const int o = GATED ? i / 4 * 32 + i % 2 * 16 : i * 16;
-            if (o < n)
-                v[i] += *reinterpret_cast<const f32x4 *>(b + o + (GATED ? i / 2 % 2 * a.C : 0));
-        }
-    }
-    if (a.preact) {
-        uint16_t *z = a.preact + row * wide * a.C + c;
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i) {
-            const int o = GATED ? i / 4 * 32 + i % 2 * 16 : i * 16;
-            if (o < n)
-                store4(z + o + (GATED ? i / 2 % 2 * a.C : 0), v[i]);
-        }
-    }
-    if (GATED) {
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-            if (i / 2 % 2 == 0)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[i][j] = v[i][j] * sigmoid(v[i][j]) * v[i + 2][j];
-    } else {
-        apply_act(v, a.act);
-    }
-    uint16_t *out = static_cast<uint16_t *>(a.out) + row * a.C + c;
-    if (a.residual) {
-        const uint16_t *res = a.residual + row * a.C + c;
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i) {
-            const int o = GATED ? i / 4 * 32 + i % 2 * 16 : i * 16;
-            if ((!GATED || i / 2 % 2 == 0) && o < n)
-                v[i] += load4(res + o);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kFrags; ++i) {
-        const int o = GATED ? i / 4 * 32 + i % 2 * 16 : i * 16;
-        if ((!GATED || i / 2 % 2 == 0) && o < n)
-            store4(out + o, v[i]);
-    }
-}
+struct FinishForward {
+    static constexpr int kBlocks = GATED ? 4 : 8, P = GATED ? 8 : 16;
+    const Args &a;
+    MOE_LDS char *lds;
+    Pieces<P> out, res, pre, pre_up;
+    f32x4 bias[kFrags];
+    u32x4 ahead[P / 4];  // the residual's next 16 rows
 
-__device__ __forceinline__ void finish_dx(const Args &a, int64_t row, int c, int n, f32x4 (&v)[kFrags])
-{
-    uint16_t *out = static_cast<uint16_t *>(a.out);
-    if (a.act == MOE_ACT_SWIGLU) {
-        const int64_t at = row * 2 * a.C + c;
+    __device__ __forceinline__ FinishForward(const Args &a_, MOE_LDS char *lds_, int e, int first, int n, int c, int inside, int row)
+        : a(a_), lds(lds_), out(a.out, first, n, a.C, 2, c, inside), res(a.residual ? a.residual : a.q, first, n, a.C, 2, c, inside),
+          pre(a.preact ? a.preact : a.q, first, n, GATED ? 2 * a.C : a.C, 2, c, inside),
+          pre_up(a.preact ? a.preact : a.q, first, n, GATED ? 2 * a.C : a.C, 2, GATED ? c + a.C : c, inside)
+    {
+        if (a.bias) {
+            const float *b = a.bias + static_cast<int64_t>(e) * (GATED ? 2 : 1) * a.C + c + lane_id() / 16 * 4;
 #pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-            if (i * 16 < n) {
-                const f32x4 g = load4(a.z + at + i * 16), u = load4(a.z + at + a.C + i * 16);
-                f32x4 dg, du;
+            for (int i = 0; i < kFrags; ++i) {
+                const int o = GATED ? i / 4 * 32 + i % 2 * 16 : i * 16;
+                bias[i] = f32x4{};
+                if (o < inside)
+                    bias[i] = *reinterpret_cast<const f32x4 *>(b + o + (GATED && i / 2 % 2 ? a.C : 0));
+            }
+        }
+        if (a.residual)
+            load(row);
+    }
+    __device__ __forceinline__ void load(int row)
+    {
+#pragma unroll
+        for (int j = 0; j < P / 4; ++j)
+            ahead[j] = res.load(row, j);
+    }
+    __device__ __forceinline__ void operator()(int row, int next, f32x4 (&v)[kFrags])
+    {
+        f32x4 y[kBlocks], add[kBlocks];
+        if (a.residual) {
+            to_blocks<P>(lds, ahead, add);
+            load(next);  // in front of this block's stores: waiting for it is then not waiting for them
+        }
+        if (a.bias)
+#pragma unroll
+            for (int i = 0; i < kFrags; ++i)
+                v[i] += bias[i];
+        if (GATED) {
+            if (a.preact) {
+                const f32x4 g[4] = {v[0], v[1], v[4], v[5]}, u[4] = {v[2], v[3], v[6], v[7]};
+                store_blocks<8>(lds, g, reinterpret_cast<const Pieces<8> &>(pre), row);
+                store_blocks<8>(lds, u, reinterpret_cast<const Pieces<8> &>(pre_up), row);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float s = sigmoid(g[j]);
-                    dg[j] = v[i][j] * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
-                    du[j] = v[i][j] * (g[j] * s);
+                    const float g = v[i / 2 * 4 + i % 2][j];
+                    y[i][j] = g * sigmoid(g) * v[i / 2 * 4 + i % 2 + 2][j];
                 }
-                store4(out + at + i * 16, dg);
-                store4(out + at + a.C + i * 16, du);
-            }
-        return;
-    }
-    const int64_t at = row * a.C + c;
-    if (a.act != MOE_ACT_NONE) {
-        f32x4 z[kFrags];
+        } else {
+            if (a.preact)
+                store_blocks<16>(lds, v, reinterpret_cast<const Pieces<16> &>(pre), row);
+            apply_act(v, a.act);
 #pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-            z[i] = i * 16 < n ? load4(a.z + at + i * 16) : f32x4{};
-        apply_slope(v, z, a.act);
-    }
+            for (int i = 0; i < kBlocks; ++i)
+                y[i] = v[i];
+        }
+        if (a.residual)
 #pragma unroll
-    for (int i = 0; i < kFrags; ++i)
-        if (i * 16 < n)
-            store4(out + at + i * 16, v[i]);
-}
+            for (int i = 0; i < kBlocks; ++i)
+                y[i] += add[i];
+        store_blocks<P>(lds, y, out, row);
+    }
+};
 
-__device__ __forceinline__ void finish_dw(const Args &a, int e, int64_t row, int c, int n, f32x4 (&v)[kFrags])
-{
-    const int64_t at = (static_cast<int64_t>(e) * a.rows + row) * a.C + c;
-    if (a.flags & MOE_GRAD_BF16) {
-#pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-            if (i * 16 < n)
-                store4(static_cast<uint16_t *>(a.out) + at + i * 16, v[i]);
-        return;
+// dx: through the activation that made the product's input.
+struct FinishDx {
+    const Args &a;
+    MOE_LDS char *lds;
+    const bool gated;
+    Pieces<16> out, out_up, pre, pre_up;
+    u32x4 ahead[4], ahead_up[4];
+
+    __device__ __forceinline__ FinishDx(const Args &a_, MOE_LDS char *lds_, int first, int n, int c, int inside, int row)
+        : a(a_), lds(lds_), gated(a_.act == MOE_ACT_SWIGLU), out(a.out, first, n, gated ? 2 * a.C : a.C, 2, c, inside),
+          out_up(a.out, first, n, gated ? 2 * a.C : a.C, 2, gated ? c + a.C : c, inside),
+          pre(a.z ? a.z : a.q, first, n, gated ? 2 * a.C : a.C, 2, c, inside),
+          pre_up(a.z ? a.z : a.q, first, n, gated ? 2 * a.C : a.C, 2, gated ? c + a.C : c, inside)
+    {
+        load(row);
     }
-    f32x4 *o = reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at);
-    if (a.flags & MOE_GRAD_ACCUMULATE)
+    __device__ __forceinline__ void load(int row)
+    {
+        if (a.act == MOE_ACT_NONE)
+            return;
 #pragma unroll
-        for (int i = 0; i < kFrags; ++i)
-            if (i * 16 < n)
-                v[i] += o[i * 4];
+        for (int j = 0; j < 4; ++j)
+            ahead[j] = pre.load(row, j);
+        if (gated)
 #pragma unroll
-    for (int i = 0; i < kFrags; ++i)
-        if (i * 16 < n)
-            o[i * 4] = v[i];
-}
+            for (int j = 0; j < 4; ++j)
+                ahead_up[j] = pre_up.load(row, j);
+    }
+    __device__ __forceinline__ void operator()(int row, int next, f32x4 (&v)[kFrags])
+    {
+        if (a.act != MOE_ACT_NONE) {
+            f32x4 z[kFrags];
+            to_blocks<16>(lds, ahead, z);
+            if (gated) {
+                f32x4 u[kFrags];
+                to_blocks<16>(lds, ahead_up, u);
+                load(next);
+#pragma unroll
+                for (int i = 0; i < 4 * kFrags; ++i) {
+                    const float g = z[i / 4][i % 4], up = u[i / 4][i % 4], x = v[i / 4][i % 4], s = sigmoid(g);
+                    v[i / 4][i % 4] = x * up * (s * (1.0f + g * (1.0f - s)));
+                    u[i / 4][i % 4] = x * (g * s);
+                }
+                store_blocks<16>(lds, u, out_up, row);
+            } else {
+                load(next);
+                apply_slope(v, z, a.act);
+            }
+        }
+        store_blocks<16>(lds, v, out, row);
+    }
+};
+
+struct FinishDw {
+    const Args &a;
+    MOE_LDS char *lds;
+    const bool half;
+    Pieces<16> out, out2;  // bf16: all columns; fp32: 64 columns each
+
+    __device__ __forceinline__ FinishDw(const Args &a_, MOE_LDS char *lds_, int64_t first, int n, int c, int inside)
+        : a(a_), lds(lds_), half((a_.flags & MOE_GRAD_BF16) != 0), out(a.out, first, n, a.C, half ? 2 : 4, c, inside),
+          out2(a.out, first, n, a.C, half ? 2 : 4, c + 64, inside - 64)
+    {
+    }
+    __device__ __forceinline__ void operator()(int row, int, f32x4 (&v)[kFrags])
+    {
+        if (half) {
+            store_blocks<16>(lds, v, out, row);
+            return;
+        }
+        fp32_half(lds, out, row, v[0], v[1], v[2], v[3]);
+        fp32_half(lds, out2, row, v[4], v[5], v[6], v[7]);
+    }
+    __device__ __forceinline__ void fp32_half(MOE_LDS char *__restrict__ place, const Pieces<16> &to, int row,
+                                              f32x4 v0, f32x4 v1, f32x4 v2, f32x4 v3) const
+    {
+        const f32x4 v[4] = {v0, v1, v2, v3};
+        u32x4 old[4];
+        if (a.flags & MOE_GRAD_ACCUMULATE)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                old[j] = to.load(row, j);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<MOE_LDS f32x4 *>(place + Place::whole(c)) = v[c];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4 x = *reinterpret_cast<const MOE_LDS f32x4 *>(place + Place::piece<16>(j));
+            if (a.flags & MOE_GRAD_ACCUMULATE)
+                x += __builtin_bit_cast(f32x4, old[j]);
+            to.store(row, j, __builtin_bit_cast(u32x4, x));
+        }
+    }
+};
 
 // One tile of a workgroup's list.
 struct Work {
@@ -168,40 +320,48 @@ struct Work {
 // takes entries b, b + gridDim.x, ...  Entry j runs on XCD j % 8, so every
 // list is dealt out in eight contiguous parts (xcd_order).  forward, dx: the
 // whole tiles of all runs, then the runs' short ends, which fill up the last
-// round.  dw: expert after expert, the longest runs first.
+// round.  dw: expert after expert, the longest runs first (of up to 64
+// experts).  Runs and list are worked out once, into LDS.
 template <Op OP, int ROWS, int COLS>
 struct TileList {
-    int32_t *table;  // LDS: [E] upto of the whole tiles, [E] of the ends (dw: [E] experts in order)
-    int whole, ends, col_tiles, row_tiles;
+    static constexpr int kBytes = 4 * (3 * MOE_MAX_EXPERTS + 1);
+    int32_t *starts;  // [E + 1] first rows of the runs
+    int32_t *table;   // [E] upto of the whole tiles, [E] of the ends (dw: [E] experts in order)
+    int E, whole, ends, col_tiles, row_tiles;
+    int nw, nw8, ne, end;  // entries: whole tiles (dw: an expert's), rounded up, ends, all
 
     __device__ __forceinline__ void build(const Args &a, int32_t *lds)
     {
-        table = lds;
+        E = a.E;
+        starts = lds;
+        table = lds + E + 1;
         col_tiles = (a.C + COLS - 1) / COLS;
         row_tiles = (a.rows + ROWS - 1) / ROWS;  // dw
         const int w = threadIdx.x / kWave, lane = lane_id();
+        for (int e = threadIdx.x; e <= E; e += blockDim.x)
+            starts[e] = run_start(a.offsets, e, a.max_rows);
+        __syncthreads();
         if (OP == kDw) {
-            if (a.E <= kWave && w == 0) {
-                const int n = lane < a.E ? expert_run(a.offsets, lane, a.max_rows).n : -1;
+            if (E <= kWave && w == 0) {
+                const int n = lane < E ? run(lane).n : -1;
                 int rank = 0;
-                for (int j = 0; j < a.E; ++j) {
+                for (int j = 0; j < E; ++j) {
                     const int m = lane_value(n, j);
                     rank += m > n || (m == n && j < lane);
                 }
-                if (lane < a.E)
+                if (lane < E)
                     table[rank] = lane;
-            } else if (a.E > kWave) {
-                for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+            } else if (E > kWave) {
+                for (int e = threadIdx.x; e < E; e += blockDim.x)
                     table[e] = e;
             }
         } else if (w < 2) {
-            int32_t *upto = table + w * a.E;
+            int32_t *upto = table + w * E;
             int before = 0;
-            for (int e0 = 0; e0 < a.E; e0 += kWave) {
-                const int e = e0 + lane;
-                const int n = e < a.E ? expert_run(a.offsets, e, a.max_rows).n : 0;
+            for (int e0 = 0; e0 < E; e0 += kWave) {
+                const int e = e0 + lane, n = e < E ? run(e).n : 0;
                 const int sum = before + wave_inclusive_scan(w == 0 ? n / ROWS : (n % ROWS != 0));
-                if (e < a.E)
+                if (e < E)
                     upto[e] = sum;
                 before = lane_value(sum, kWave - 1);
             }
@@ -209,14 +369,28 @@ struct TileList {
         __syncthreads();
         if (OP == kDw) {
             whole = ends = 0;
+            nw = row_tiles * col_tiles;
+            nw8 = (nw + 7) / 8 * 8;
+            ne = 0;
+            end = nw8 * E;
         } else {
-            whole = static_cast<int>(uniform(table[a.E - 1]));
-            ends = static_cast<int>(uniform(table[2 * a.E - 1]));
+            whole = static_cast<int>(uniform(table[E - 1]));
+            ends = static_cast<int>(uniform(table[2 * E - 1]));
+            nw = whole * col_tiles;
+            nw8 = (nw + 7) / 8 * 8;
+            ne = ends * col_tiles;
+            end = nw8 + (ne + 7) / 8 * 8;
         }
     }
 
+    __device__ __forceinline__ ExpertRun run(int e) const
+    {
+        const int first = starts[e];
+        return {first, max(starts[e + 1] - first, 0)};
+    }
+
     // Expert of entry k of a list whose counts add up to upto[].
-    __device__ __forceinline__ int expert_of(const int32_t *upto, int E, int k) const
+    __device__ __forceinline__ int expert_of(const int32_t *upto, int k) const
     {
         int e = 0;
         for (int e0 = 0; e0 < E; e0 += kWave) {
@@ -227,37 +401,34 @@ struct TileList {
     }
 
     // Moves j to the next entry with work; false at the end of the list.
-    __device__ __forceinline__ bool next(const Args &a, int64_t &j, Work &t) const
+    __device__ __forceinline__ bool next(const Args &a, int &j, Work &t) const
     {
-        const int64_t per = static_cast<int64_t>(row_tiles) * col_tiles, per8 = (per + 7) / 8 * 8;
-        const int64_t nw = static_cast<int64_t>(whole) * col_tiles, ne = static_cast<int64_t>(ends) * col_tiles;
-        const int64_t nw8 = (nw + 7) / 8 * 8, end = OP == kDw ? per8 * a.E : nw8 + (ne + 7) / 8 * 8;
         for (; j < end; j += gridDim.x) {
             if (OP == kDw) {
-                const int64_t id = xcd_order(j % per8, per);
+                const int id = xcd_order(j % nw8, nw);
                 if (id < 0)
                     continue;
-                t.e = static_cast<int>(uniform(table[j / per8]));
+                t.e = static_cast<int>(uniform(table[j / nw8]));
                 const TileAt at = grouped_order(id, row_tiles, col_tiles);
-                const ExpertRun run = expert_run(a.offsets, t.e, a.max_rows);
+                const ExpertRun r = run(t.e);
                 t.first = at.row * ROWS;
                 t.n = min(ROWS, a.rows - t.first);
                 t.c0 = at.col * COLS;
-                t.r_first = run.first;
-                t.R = run.n;
+                t.r_first = static_cast<int>(uniform(r.first));
+                t.R = static_cast<int>(uniform(r.n));
             } else {
                 const bool end_tile = j >= nw8;
-                const int64_t id = end_tile ? xcd_order(j - nw8, ne) : xcd_order(j, nw);
+                const int id = end_tile ? xcd_order(j - nw8, ne) : xcd_order(j, nw);
                 if (id < 0)
                     continue;
                 const TileAt at = grouped_order(id, end_tile ? ends : whole, col_tiles);
-                const int32_t *upto = table + (end_tile ? a.E : 0);
-                t.e = expert_of(upto, a.E, at.row);
-                const ExpertRun run = expert_run(a.offsets, t.e, a.max_rows);
-                const int before = t.e ? static_cast<int>(uniform(upto[t.e - 1])) : 0;
-                const int in_run = end_tile ? run.n / ROWS * ROWS : (at.row - before) * ROWS;
-                t.first = run.first + in_run;
-                t.n = min(ROWS, run.n - in_run);
+                const int32_t *upto = table + (end_tile ? E : 0);
+                t.e = expert_of(upto, at.row);
+                const ExpertRun r = run(t.e);
+                const int before = t.e ? upto[t.e - 1] : 0;
+                const int in_run = end_tile ? r.n / ROWS * ROWS : (at.row - before) * ROWS;
+                t.first = static_cast<int>(uniform(r.first + in_run));
+                t.n = static_cast<int>(uniform(min(ROWS, r.n - in_run)));
                 t.c0 = at.col * COLS;
                 t.R = a.R;
             }
@@ -273,9 +444,10 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
     typedef Tile<OP == kForward, OP != kDw, GATED> T;
     constexpr int kCols = GATED ? T::kCols / 2 : T::kCols;  // output columns of a tile
     // one array: for two the compiler would wait for all loads before a read
-    __shared__ __align__(1024) char shared[T::kLdsBytes + 8 * MOE_MAX_EXPERTS];
+    typedef TileList<OP, T::kRows, kCols> List;
+    __shared__ __align__(1024) char shared[T::kLdsBytes + List::kBytes];
     MOE_LDS char *lds = (MOE_LDS char *)shared;
-    TileList<OP, T::kRows, kCols> list;
+    List list;
     list.build(a, reinterpret_cast<int32_t *>(shared + T::kLdsBytes));
 
     T t;
@@ -296,7 +468,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
         t.start_rows(k.n, lds);
     };
 
-    int64_t j = blockIdx.x;
+    int j = blockIdx.x;
     Work k;
     if (!list.next(a, j, k))
         return;
@@ -331,16 +503,18 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
                 }
             }
         }
-        t.finish(k.n, [&](int row, int col, f32x4 (&v)[kFrags]) {
-            const int c = GATED ? k.c0 + (col - col % 16) / 2 + col % 16 : k.c0 + col;
-            const int n = a.C - (c - col % 16);  // columns inside, from the wave's first
-            if (OP == kForward)
-                finish_forward<GATED>(a, k.e, k.first + row, c, n, v);
-            else if (OP == kDx)
-                finish_dx(a, k.first + row, c, n, v);
-            else
-                finish_dw(a, k.e, k.first + row, c, n, v);
-        });
+        const int c = k.c0 + t.col0() / (GATED ? 2 : 1), inside = a.C - c;
+        MOE_LDS char *place = t.out_place(lds);
+        if constexpr (OP == kForward) {
+            FinishForward<GATED> f(a, place, k.e, k.first, k.n, c, inside, t.row0(0));
+            t.finish(k.n, f);
+        } else if constexpr (OP == kDx) {
+            FinishDx f(a, place, k.first, k.n, c, inside, t.row0(0));
+            t.finish(k.n, f);
+        } else {
+            FinishDw f(a, place, static_cast<int64_t>(k.e) * a.rows + k.first, k.n, c, inside);
+            t.finish(k.n, f);
+        }
         if (!more)
             return;
         k = after;

@@ -140,8 +140,15 @@ struct Tile {
     typedef Operand<64, Q_CONTIG, false> Q;  // an image for each block of 64 rows
     static constexpr int kStageBytes = P::kBytes + kBlocks * Q::kBytes;
     static constexpr int kThinBytes = P::kBytes + 2 * Q::kBytes;  // of a stage of at most 128 rows
-    static constexpr int kLdsBytes = 3 * kThinBytes;
-    static_assert(kLdsBytes >= 2 * kStageBytes, "two whole stages or three thin ones");
+    // two whole stages or three thin ones; the results pass through what the
+    // first stages of the next tile leave free
+    static constexpr int kLdsBytes = 3 * kThinBytes, kOutBytes = 4096;
+    static_assert(kLdsBytes >= 2 * kStageBytes + kTileWaves * kOutBytes, "whole stages and results");
+    static_assert(kLdsBytes >= 2 * kThinBytes + kTileWaves * kOutBytes, "thin stages and results");
+    __device__ __forceinline__ MOE_LDS char *out_place(MOE_LDS char *lds) const
+    {
+        return lds + kLdsBytes - (kTileWaves - wave()) * kOutBytes;
+    }
     P p;
     Q q;
     int R;
@@ -423,22 +430,32 @@ struct Tile {
         join<0>();
     }
 
-    // Calls f(row, column, v) for this lane's part of each of its rows: v[c]
-    // has columns column + 16 c .. + 3.  The row's accumulators are picked by a
-    // switch, so that the code behind them is there once.
-    template <typename F>
-    __device__ __forceinline__ void finish(int rows, F f) const
+    // (written out, so that the accumulators stay in the AGPRs up to here)
+    static __device__ __forceinline__ f32x4 read_acc(const f32x4 &a)
     {
-        const int lane = lane_id();
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x;
+            asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(a[i]));
+            v[i] = x;
+        }
+        return v;
+    }
+
+    // Calls f(row, v) for each 16 of this wave's rows of the tile, from `row`
+    // on: v[c] has of row + lane%16 the columns col0() + 16 c + 4 (lane/16) ..
+    // + 3.  Rows from `rows` on may be among them.  The accumulators are picked
+    // by a switch, so that the code behind them is there once.
+    template <typename F>
+    __device__ __forceinline__ void finish(int rows, F &f) const
+    {
 #pragma unroll 1
-        for (int i = 0; i < 2 * kBlocks; ++i) {
-            const int row = row0(i / 2) + i % 2 * 16 + lane % 16;
-            if (row0(i / 2) + i % 2 * 16 >= rows)
-                break;
+        for (int i = 0; i < 2 * kBlocks && row0(i / 2) + i % 2 * 16 < rows; ++i) {
             f32x4 v[kFrags];
 #define MOE_PICK(I)                                                                            \
     case I:                                                                                    \
-        _Pragma("unroll") for (int c = 0; c < kFrags; ++c) v[c] = acc[c][I / 2][I % 2];        \
+        _Pragma("unroll") for (int c = 0; c < kFrags; ++c) v[c] = read_acc(acc[c][I / 2][I % 2]); \
         break
             switch (i) {
                 MOE_PICK(0);
@@ -448,14 +465,12 @@ struct Tile {
                 MOE_PICK(4);
                 MOE_PICK(5);
                 MOE_PICK(6);
-            default:
-#pragma unroll
-                for (int c = 0; c < kFrags; ++c)
-                    v[c] = acc[c][3][1];
+                MOE_PICK(7);
             }
 #undef MOE_PICK
-            if (row < rows)
-                f(row, col0() + lane / 16 * 4, v);
+            // (past the last rows the next ones are again these: loads ahead of them are not used)
+            const int next = min(i + 1, 2 * kBlocks - 1);
+            f(row0(i / 2) + i % 2 * 16, row0(next / 2) + next % 2 * 16, v);
         }
     }
 };
