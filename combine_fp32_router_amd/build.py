@@ -31,7 +31,7 @@ HARNESS_PATH = os.path.join(HERE, "libmoe_harness.so")
 
 SOURCES = ["route_topk.hip", "dispatch_layout.hip", "dispatch_pack.hip", "combine.hip",
            "recv_regroup.hip", "combine_pack.hip", "combine_grad.hip", "balance.hip",
-           "expert_matmul.hip", "static_scratch.hip", "abi.cpp"]
+           "expert_matmul.hip", "expert_few.hip", "static_scratch.hip", "abi.cpp"]
 HARNESS_SOURCES = ["harness.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -477,7 +477,8 @@ int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, cons
                       int act, const void *residual, int E, int64_t max_rows, int K, int N,
                       void *out, void *preact, hipStream_t stream)
 {
-    if (check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK || !known_act(act))
+    if (check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK || !known_act(act) ||
+        !product_tiles_fit(max_row_tiles(max_rows, E, 256), act == MOE_ACT_SWIGLU ? 2 * N : N))
         return MOE_ERR_SHAPE;
     if (max_rows == 0)
         return MOE_OK;
@@ -497,7 +498,8 @@ int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, 
                          const void *preact, int E, int64_t max_rows, int K, int N, void *dx,
                          hipStream_t stream)
 {
-    if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK || !known_act(act))
+    if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK || !known_act(act) ||
+        !product_tiles_fit(max_row_tiles(max_rows, E, 256), K))
         return MOE_ERR_SHAPE;
     if (max_rows == 0)
         return MOE_OK;

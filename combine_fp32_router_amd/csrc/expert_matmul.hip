@@ -33,8 +33,8 @@ struct Args {
     int rows;               // dw: rows of the output (N)
 };
 
-// Results leave 16 rows of a wave's 128 columns at a time.  A lane's share is
-// four columns of each of eight blocks of 16 (the MFMA's layout); memory is
+// Results leave 16 rows of a wave's columns at a time.  A lane's share is
+// four columns of each of FR blocks of 16 (the MFMA's layout); memory is
 // read and written in 16-byte pieces of whole rows.  The two meet in 4 KiB of
 // LDS a wave, rows of 256 bytes, piece p of row r kept at p ^ r: stored
 // straight from the MFMA's layout, in pieces of 8 bytes, a tile's results cost
@@ -42,8 +42,6 @@ struct Args {
 // Rows and columns outside a tile are given offsets outside the buffer
 // descriptors, whose reads return 0 and whose writes are dropped, so that the
 // number of memory operations in flight is always known.
-constexpr int kFrags = 8;
-
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
@@ -138,15 +136,15 @@ __device__ __forceinline__ void store_blocks(MOE_LDS char *__restrict__ lds, con
         out.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<P>(j)));
 }
 
-// Forward: bias, pre-activations, activation, residual.  GATED: v[0, 1, 4, 5]
-// are the gate's four blocks of 16 columns, v[2, 3, 6, 7] the up half's.
-template <bool GATED>
+// Forward: bias, pre-activations, activation, residual.  GATED: blocks 0, 1, 4,
+// 5 of v are the gate's, 2, 3, 6, 7 the up half's.
+template <int FR, bool GATED>
 struct FinishForward {
-    static constexpr int kBlocks = GATED ? 4 : 8, P = GATED ? 8 : 16;
+    static constexpr int kBlocks = GATED ? FR / 2 : FR, P = 2 * kBlocks;
     const Args &a;
     MOE_LDS char *lds;
     Pieces<P> out, res, pre, pre_up;
-    f32x4 bias[kFrags];
+    f32x4 bias[FR];
     u32x4 ahead[P / 4];  // the residual's next 16 rows
 
     __device__ __forceinline__ FinishForward(const Args &a_, MOE_LDS char *lds_, int e, int first, int n, int c, int inside, int row)
@@ -157,7 +155,7 @@ struct FinishForward {
         if (a.bias) {
             const float *b = a.bias + static_cast<int64_t>(e) * (GATED ? 2 : 1) * a.C + c + lane_id() / 16 * 4;
 #pragma unroll
-            for (int i = 0; i < kFrags; ++i) {
+            for (int i = 0; i < FR; ++i) {
                 const int o = GATED ? i / 4 * 32 + i % 2 * 16 : i * 16;
                 bias[i] = f32x4{};
                 if (o < inside)
@@ -173,7 +171,7 @@ struct FinishForward {
         for (int j = 0; j < P / 4; ++j)
             ahead[j] = res.load(row, j);
     }
-    __device__ __forceinline__ void operator()(int row, int next, f32x4 (&v)[kFrags])
+    __device__ __forceinline__ void operator()(int row, int next, f32x4 (&v)[FR])
     {
         f32x4 y[kBlocks], add[kBlocks];
         if (a.residual) {
@@ -182,24 +180,27 @@ struct FinishForward {
         }
         if (a.bias)
 #pragma unroll
-            for (int i = 0; i < kFrags; ++i)
+            for (int i = 0; i < FR; ++i)
                 v[i] += bias[i];
-        if (GATED) {
+        if constexpr (GATED) {
+            f32x4 g[kBlocks], u[kBlocks];
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                g[i] = v[i / 2 * 4 + i % 2];
+                u[i] = v[i / 2 * 4 + i % 2 + 2];
+            }
             if (a.preact) {
-                const f32x4 g[4] = {v[0], v[1], v[4], v[5]}, u[4] = {v[2], v[3], v[6], v[7]};
-                store_blocks<8>(lds, g, reinterpret_cast<const Pieces<8> &>(pre), row);
-                store_blocks<8>(lds, u, reinterpret_cast<const Pieces<8> &>(pre_up), row);
+                store_blocks<P>(lds, g, pre, row);
+                store_blocks<P>(lds, u, pre_up, row);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float g = v[i / 2 * 4 + i % 2][j];
-                    y[i][j] = g * sigmoid(g) * v[i / 2 * 4 + i % 2 + 2][j];
-                }
+            for (int i = 0; i < 4 * kBlocks; ++i) {
+                const float x = g[i / 4][i % 4];
+                y[i / 4][i % 4] = x * sigmoid(x) * u[i / 4][i % 4];
+            }
         } else {
             if (a.preact)
-                store_blocks<16>(lds, v, reinterpret_cast<const Pieces<16> &>(pre), row);
+                store_blocks<P>(lds, v, pre, row);
             apply_act(v, a.act);
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i)
@@ -214,12 +215,14 @@ struct FinishForward {
 };
 
 // dx: through the activation that made the product's input.
+template <int FR>
 struct FinishDx {
+    static constexpr int P = 2 * FR;
     const Args &a;
     MOE_LDS char *lds;
     const bool gated;
-    Pieces<16> out, out_up, pre, pre_up;
-    u32x4 ahead[4], ahead_up[4];
+    Pieces<P> out, out_up, pre, pre_up;
+    u32x4 ahead[P / 4], ahead_up[P / 4];
 
     __device__ __forceinline__ FinishDx(const Args &a_, MOE_LDS char *lds_, int first, int n, int c, int inside, int row)
         : a(a_), lds(lds_), gated(a_.act == MOE_ACT_SWIGLU), out(a.out, first, n, gated ? 2 * a.C : a.C, 2, c, inside),
@@ -234,57 +237,60 @@ struct FinishDx {
         if (a.act == MOE_ACT_NONE)
             return;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < P / 4; ++j)
             ahead[j] = pre.load(row, j);
         if (gated)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < P / 4; ++j)
                 ahead_up[j] = pre_up.load(row, j);
     }
-    __device__ __forceinline__ void operator()(int row, int next, f32x4 (&v)[kFrags])
+    __device__ __forceinline__ void operator()(int row, int next, f32x4 (&v)[FR])
     {
         if (a.act != MOE_ACT_NONE) {
-            f32x4 z[kFrags];
-            to_blocks<16>(lds, ahead, z);
+            f32x4 z[FR];
+            to_blocks<P>(lds, ahead, z);
             if (gated) {
-                f32x4 u[kFrags];
-                to_blocks<16>(lds, ahead_up, u);
+                f32x4 u[FR];
+                to_blocks<P>(lds, ahead_up, u);
                 load(next);
 #pragma unroll
-                for (int i = 0; i < 4 * kFrags; ++i) {
+                for (int i = 0; i < 4 * FR; ++i) {
                     const float g = z[i / 4][i % 4], up = u[i / 4][i % 4], x = v[i / 4][i % 4], s = sigmoid(g);
                     v[i / 4][i % 4] = x * up * (s * (1.0f + g * (1.0f - s)));
                     u[i / 4][i % 4] = x * (g * s);
                 }
-                store_blocks<16>(lds, u, out_up, row);
+                store_blocks<P>(lds, u, out_up, row);
             } else {
                 load(next);
                 apply_slope(v, z, a.act);
             }
         }
-        store_blocks<16>(lds, v, out, row);
+        store_blocks<P>(lds, v, out, row);
     }
 };
 
+template <int FR>
 struct FinishDw {
     const Args &a;
     MOE_LDS char *lds;
     const bool half;
-    Pieces<16> out, out2;  // bf16: all columns; fp32: 64 columns each
+    Pieces<2 * FR> out;      // bf16: all columns
+    Pieces<16> lower, upper;  // fp32: 64 columns each
 
     __device__ __forceinline__ FinishDw(const Args &a_, MOE_LDS char *lds_, int64_t first, int n, int c, int inside)
-        : a(a_), lds(lds_), half((a_.flags & MOE_GRAD_BF16) != 0), out(a.out, first, n, a.C, half ? 2 : 4, c, inside),
-          out2(a.out, first, n, a.C, half ? 2 : 4, c + 64, inside - 64)
+        : a(a_), lds(lds_), half((a_.flags & MOE_GRAD_BF16) != 0), out(a.out, first, n, a.C, 2, c, inside),
+          lower(a.out, first, n, a.C, 4, c, inside), upper(a.out, first, n, a.C, 4, c + 64, inside - 64)
     {
     }
-    __device__ __forceinline__ void operator()(int row, int, f32x4 (&v)[kFrags])
+    __device__ __forceinline__ void operator()(int row, int, f32x4 (&v)[FR])
     {
         if (half) {
-            store_blocks<16>(lds, v, out, row);
+            store_blocks<2 * FR>(lds, v, out, row);
             return;
         }
-        fp32_half(lds, out, row, v[0], v[1], v[2], v[3]);
-        fp32_half(lds, out2, row, v[4], v[5], v[6], v[7]);
+        fp32_half(lds, lower, row, v[0], v[1], v[2], v[3]);
+        if constexpr (FR == 8)
+            fp32_half(lds, upper, row, v[4], v[5], v[6], v[7]);
     }
     __device__ __forceinline__ void fp32_half(MOE_LDS char *__restrict__ place, const Pieces<16> &to, int row,
                                               f32x4 v0, f32x4 v1, f32x4 v2, f32x4 v3) const
@@ -319,8 +325,9 @@ struct Work {
 // The tiles of a call, in the order in which they are handed out: workgroup b
 // takes entries b, b + gridDim.x, ...  Entry j runs on XCD j % 8, so every
 // list is dealt out in eight contiguous parts (xcd_order).  forward, dx: the
-// whole tiles of all runs, then the runs' short ends, which fill up the last
-// round.  dw: expert after expert, the longest runs first (of up to 64
+// tiles of more than half their rows, which all cost the same, then the runs'
+// shorter ends; these go, two at a time, to the workgroups that the others'
+// last round leaves idle.  dw: expert after expert, the longest runs first (of up to 64
 // experts).  Runs and list are worked out once, into LDS.
 template <Op OP, int ROWS, int COLS>
 struct TileList {
@@ -360,7 +367,7 @@ struct TileList {
             int before = 0;
             for (int e0 = 0; e0 < E; e0 += kWave) {
                 const int e = e0 + lane, n = e < E ? run(e).n : 0;
-                const int sum = before + wave_inclusive_scan(w == 0 ? n / ROWS : (n % ROWS != 0));
+                const int sum = before + wave_inclusive_scan(w == 0 ? (n + ROWS / 2 - 1) / ROWS : short_end(n));
                 if (e < E)
                     upto[e] = sum;
                 before = lane_value(sum, kWave - 1);
@@ -389,6 +396,8 @@ struct TileList {
         return {first, max(starts[e + 1] - first, 0)};
     }
 
+    static __device__ __forceinline__ int short_end(int n) { return n % ROWS > 0 && n % ROWS <= ROWS / 2; }
+
     // Expert of entry k of a list whose counts add up to upto[].
     __device__ __forceinline__ int expert_of(const int32_t *upto, int k) const
     {
@@ -400,10 +409,26 @@ struct TileList {
         return static_cast<int>(uniform(e));
     }
 
-    // Moves j to the next entry with work; false at the end of the list.
-    __device__ __forceinline__ bool next(const Args &a, int &j, Work &t) const
+    // Moves this workgroup's count i to its next entry with work; false at the
+    // end of its list.
+    __device__ __forceinline__ bool next(const Args &a, int &i, Work &t) const
     {
-        for (; j < end; j += gridDim.x) {
+        const int groups = gridDim.x, b = blockIdx.x;
+        for (;; ++i) {
+            int j = i * groups + b;
+            if (OP == kDw) {
+                if (j >= end)
+                    return false;
+            } else if (j >= nw8) {
+                // the short ends: i0 whole tiles of this workgroup lie behind it
+                const int idle = groups - nw8 % groups, i0 = nw8 / groups + (b < nw8 % groups);
+                const int turn = i - i0;  // of this workgroup's ends
+                j = nw8 + (b < groups - idle ? 2 * idle + turn * groups + b
+                           : turn < 2        ? turn * idle + b - (groups - idle)
+                                             : 2 * idle + (turn - 2) * groups + b);
+                if (j >= end)
+                    return false;
+            }
             if (OP == kDw) {
                 const int id = xcd_order(j % nw8, nw);
                 if (id < 0)
@@ -438,10 +463,10 @@ struct TileList {
     }
 };
 
-template <Op OP, bool GATED>
+template <Op OP, bool GATED, int TILE_COLS>
 __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
 {
-    typedef Tile<OP == kForward, OP != kDw, GATED> T;
+    typedef Tile<TILE_COLS, OP == kForward, OP != kDw, GATED> T;
     constexpr int kCols = GATED ? T::kCols / 2 : T::kCols;  // output columns of a tile
     // one array: for two the compiler would wait for all loads before a read
     typedef TileList<OP, T::kRows, kCols> List;
@@ -468,9 +493,9 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
         t.start_rows(k.n, lds);
     };
 
-    int j = blockIdx.x;
+    int i = 0;
     Work k;
-    if (!list.next(a, j, k))
+    if (!list.next(a, i, k))
         return;
     start(k);
     for (;;) {
@@ -481,8 +506,8 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
         else
             t.template run_rows<false>(k.n, lds);
         Work after = k;
-        j += gridDim.x;
-        const bool more = list.next(a, j, after);
+        ++i;
+        const bool more = list.next(a, i, after);
         if (more)
             start(after);  // runs beside the rest of this tile
         if (sums) {
@@ -506,13 +531,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
         const int c = k.c0 + t.col0() / (GATED ? 2 : 1), inside = a.C - c;
         MOE_LDS char *place = t.out_place(lds);
         if constexpr (OP == kForward) {
-            FinishForward<GATED> f(a, place, k.e, k.first, k.n, c, inside, t.row0(0));
+            FinishForward<T::kFrags, GATED> f(a, place, k.e, k.first, k.n, c, inside, t.row0(0));
             t.finish(k.n, f);
         } else if constexpr (OP == kDx) {
-            FinishDx f(a, place, k.first, k.n, c, inside, t.row0(0));
+            FinishDx<T::kFrags> f(a, place, k.first, k.n, c, inside, t.row0(0));
             t.finish(k.n, f);
         } else {
-            FinishDw f(a, place, static_cast<int64_t>(k.e) * a.rows + k.first, k.n, c, inside);
+            FinishDw<T::kFrags> f(a, place, static_cast<int64_t>(k.e) * a.rows + k.first, k.n, c, inside);
             t.finish(k.n, f);
         }
         if (!more)
@@ -524,8 +549,23 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
 int64_t tiles(int64_t n, int t) { return (n + t - 1) / t; }
 
 // Workgroups of a call of at most n tiles: one for each of the card's 256
-// CUs, whose LDS it fills, each with a list of tiles.
-unsigned grid_for(int64_t n) { return static_cast<unsigned>(n < 256 ? n : 256); }
+// CUs, whose LDS it fills, each with a list of tiles.  (Each of the two lists
+// is a whole number for each XCD: spare entries.)
+dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < 256 ? n + 14 : 256)); }
+
+// Whether tiles of 128 columns serve a call of at most `n` tiles of 256
+// better: they cost 0.72 of one (K = N = 2048: 38 us against 51), so they do
+// while all of them fit the card at once (4096 rows, 128 tiles: 38 us against
+// 51; 4352 rows, 136 tiles: 64 against 51).
+bool narrow(int64_t n) { return n <= 128; }
+
+#define MOE_EXPERT(OP, GATED, ROW_TILES, COLS)                                                 \
+    if (narrow((ROW_TILES) * tiles(COLS, GATED ? 128 : 256)))                                   \
+        expert_kernel<OP, GATED, 128><<<grid_for((ROW_TILES) * tiles(COLS, GATED ? 64 : 128)),  \
+                                        64 * kTileWaves, 0, stream>>>(a);                       \
+    else                                                                                       \
+        expert_kernel<OP, GATED, 256><<<grid_for((ROW_TILES) * tiles(COLS, GATED ? 128 : 256)), \
+                                        64 * kTileWaves, 0, stream>>>(a)
 
 }  // namespace
 
@@ -540,12 +580,14 @@ hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const voi
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = K, a.C = N;
     a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
     a.out = out, a.preact = static_cast<uint16_t *>(preact);
-    // spare entries: each of the two lists is a whole number for each XCD
+    if (few_rows_pay(act, E, max_rows, K, N))
+        return launch_expert_few(x, offsets, w, bias, act, residual, E, max_rows, K, N, out, preact, stream);
     const int64_t rt = max_row_tiles(max_rows, E, 256);
-    if (act == MOE_ACT_SWIGLU)
-        expert_kernel<kForward, true><<<grid_for(rt * tiles(N, 128) + 14), 64 * kTileWaves, 0, stream>>>(a);
-    else
-        expert_kernel<kForward, false><<<grid_for(rt * tiles(N, 256) + 14), 64 * kTileWaves, 0, stream>>>(a);
+    if (act == MOE_ACT_SWIGLU) {
+        MOE_EXPERT(kForward, true, rt, N);
+    } else {
+        MOE_EXPERT(kForward, false, rt, N);
+    }
     return hipGetLastError();
 }
 
@@ -559,7 +601,7 @@ hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = N, a.C = K;
     a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
     const int64_t rt = max_row_tiles(max_rows, E, 256);
-    expert_kernel<kDx, false><<<grid_for(rt * tiles(K, 256) + 14), 64 * kTileWaves, 0, stream>>>(a);
+    MOE_EXPERT(kDx, false, rt, K);
     return hipGetLastError();
 }
 
@@ -572,8 +614,7 @@ hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t 
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.C = K, a.rows = N;
     a.out = dw, a.db = db, a.flags = flags;
-    const int64_t n = E * ((tiles(K, 256) * tiles(N, 256) + 7) / 8 * 8);
-    expert_kernel<kDw, false><<<grid_for(n), 64 * kTileWaves, 0, stream>>>(a);
+    MOE_EXPERT(kDw, false, E * tiles(N, 256), K);
     return hipGetLastError();
 }
 

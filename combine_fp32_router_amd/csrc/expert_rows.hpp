@@ -43,13 +43,6 @@ __device__ __forceinline__ TileAt grouped_order(int id, int row_tiles, int col_t
     return {8 * group + in % height, in / height};
 }
 
-// Most tiles that E runs of together max_rows rows can have.
-inline int64_t max_row_tiles(int64_t max_rows, int E, int height)
-{
-    const int64_t live = max_rows < E ? max_rows : E;
-    return (max_rows - live) / height + live;
-}
-
 // exp and the reciprocal in single instructions, good to 1 ulp each, behind a
 // rounded product: off by about (|z| + 2) 2^-24 of the result, against the
 // 2^-9 of the bf16 that is stored.  Past +-88 they give 0 and 1.

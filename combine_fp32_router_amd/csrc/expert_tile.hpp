@@ -1,8 +1,8 @@
 // One output tile of the experts' products on the matrix cores.
 //
 // C[row, col] = sum over r < R of Q[row, r] * P[col, r]: 256 rows by 256
-// columns a workgroup of four waves, one on each SIMD, 128 x 128 a wave in
-// 16x16x32 bf16 MFMAs.  Their first operand is P, so lane l holds columns
+// columns (or 128, for calls of few tiles) a workgroup of four waves, one on
+// each SIMD, 128 x 128 (64) a wave in 16x16x32 bf16 MFMAs.  Their first operand is P, so lane l holds columns
 // 4 (l/16) .. + 3 of a block's row l%16.  The wave's 256 accumulator
 // registers are the AGPR half of its 512: the MFMAs are written as inline
 // assembly on "a" registers, because the compiler, given the builtin, copies
@@ -49,7 +49,7 @@ struct Operand {
     static constexpr int kPieces = CONTIG ? kStep / 8 : W / 8;  // 16-byte pieces of an image row
     static constexpr int kRowsLoad = 64 / kPieces;              // image rows a load covers
     static constexpr bool kSwap = !CONTIG && W == 256;          // a wave's loads lie 8 r apart
-    static_assert((CONTIG || !PAIR) && (CONTIG || W == 64 || W == 256), "the permutations below");
+    static_assert((CONTIG || !PAIR) && (CONTIG || W == 64 || W == 128 || W == 256), "the permutations below");
     const char *base[PAIR ? 2 : 1];
     int pitch, n;            // bytes of a memory row, indices inside
     int off[kSwap ? 2 : 1];  // this lane's offset in its wave's even loads, and odd ones
@@ -129,21 +129,21 @@ struct Operand {
     }
 };
 
-// Wave w has columns 128 (w%2) .. + 127 and, of every block of 64 rows, the 32
-// from 32 (w/2), so that a short tile's rows are shared evenly.
-template <bool P_CONTIG, bool Q_CONTIG, bool GATED>
+// Wave w has the columns' half w%2 and, of every block of 64 rows, the 32 from
+// 32 (w/2), so that a short tile's rows are shared evenly.
+template <int COLS, bool P_CONTIG, bool Q_CONTIG, bool GATED>
 struct Tile {
-    static constexpr int kRows = 256, kCols = 256;
-    static constexpr int kBlocks = 4;  // of 64 rows
-    static constexpr int kFrags = 8;   // blocks of 16 columns of a wave
+    static constexpr int kRows = 256, kCols = COLS;
+    static constexpr int kBlocks = 4;           // of 64 rows
+    static constexpr int kFrags = kCols / 32;   // blocks of 16 columns of a wave
     typedef Operand<kCols, P_CONTIG, GATED> P;
     typedef Operand<64, Q_CONTIG, false> Q;  // an image for each block of 64 rows
     static constexpr int kStageBytes = P::kBytes + kBlocks * Q::kBytes;
     static constexpr int kThinBytes = P::kBytes + 2 * Q::kBytes;  // of a stage of at most 128 rows
     // two whole stages or three thin ones; the results pass through what the
     // first stages of the next tile leave free
-    static constexpr int kLdsBytes = 3 * kThinBytes, kOutBytes = 4096;
-    static_assert(kLdsBytes >= 2 * kStageBytes + kTileWaves * kOutBytes, "whole stages and results");
+    static constexpr int kOutBytes = 4096, kWhole = 2 * kStageBytes + kTileWaves * kOutBytes;
+    static constexpr int kLdsBytes = kWhole > 3 * kThinBytes ? kWhole : 3 * kThinBytes;
     static_assert(kLdsBytes >= 2 * kThinBytes + kTileWaves * kOutBytes, "thin stages and results");
     __device__ __forceinline__ MOE_LDS char *out_place(MOE_LDS char *lds) const
     {
@@ -156,7 +156,7 @@ struct Tile {
     float sum[2][2];  // SUMS: this lane's parts of the sums of Q over r, of row blocks 2 (w%2), + 1
 
     __device__ __forceinline__ int wave() const { return static_cast<int>(uniform(threadIdx.x / kWave)); }
-    __device__ __forceinline__ int col0() const { return wave() % 2 * 128; }
+    __device__ __forceinline__ int col0() const { return wave() % 2 * (kCols / 2); }
     __device__ __forceinline__ int row0(int block) const { return block * 64 + wave() / 2 * 32; }
 
     __device__ __forceinline__ void clear()
@@ -271,55 +271,54 @@ struct Tile {
     __device__ __forceinline__ void step(Frags &f, const MOE_LDS char *__restrict__ rd,
                                          MOE_LDS char *__restrict__ wr, int cur, int nxt, int r0)
     {
-        group(f, f.q[0], 0, 0, [&](int c) {
-            if (c == 2 || c == 5)
-                load_q(wr + nxt, r0 + kStep, 2, c / 3);
-        });
-        join<16>();  // Q blocks 1 and 2 of this stage are here; all P and Q block 0 were read
+        // loads go behind the second half of a group's columns, fragments behind
+        // the first ones
+        constexpr int H = kFrags / 2, NP = P::kLoads / 4;
+        auto p_share = [&](int c, int i) {
+            if (c >= H && (c - H) % (H / NP) == 0)
+                load_p(wr + cur, r0 + 2 * kStep, i * NP + (c - H) / (H / NP));
+        };
+        auto q_pair = [&](int c, int to, int r, int b) {
+            if (c >= H && (c - H) % (H / 2) == 0)
+                load_q(wr + to, r, b, (c - H) / (H / 2));
+        };
+        group(f, f.q[0], 0, 0, [&](int c) { q_pair(c, nxt, r0 + kStep, 2); });
+        join<P::kLoads + 8>();  // Q blocks 1 and 2 of this stage are here; all P and Q block 0 were read
         add_up<SUMS>(f.q[0], 0);
         group(f, f.q[0], 0, 1, [&](int c) {
             if (c < 4)
                 read_q(f.q[1], 1, c % 2, c / 2, rd + cur);
-            if (c == 4 || c == 6)
-                load_p(wr + cur, r0 + 2 * kStep, c / 2 - 2);
+            p_share(c, 0);
         });
         group(f, f.q[1], 1, 0, [&](int c) {
             if (c == 1 || c == 3)
                 read_q(f.q[0], 2, c / 2, 0, rd + cur);
-            if (c == 4 || c == 6)
-                load_p(wr + cur, r0 + 2 * kStep, c / 2);
+            p_share(c, 1);
         });
         add_up<SUMS>(f.q[1], 1);
         group(f, f.q[1], 1, 1, [&](int c) {
             if (c == 1 || c == 3)
                 read_q(f.q[0], 2, c / 2, 1, rd + cur);
-            if (c == 4 || c == 6)
-                load_p(wr + cur, r0 + 2 * kStep, c / 2 + 2);
+            p_share(c, 2);
         });
-        group(f, f.q[0], 2, 0, [&](int c) {
-            if (c == 2 || c == 5)
-                load_p(wr + cur, r0 + 2 * kStep, c / 3 + 6);
-        });
-        join<12>();  // Q block 3 of this stage, P and Q block 0 of the next are here; blocks 1 and 2 were read
+        group(f, f.q[0], 2, 0, [&](int c) { p_share(c, 3); });
+        join<P::kLoads + 4>();  // Q block 3 of this stage, P and Q block 0 of the next are here; blocks 1 and 2 were read
         add_up<SUMS>(f.q[0], 2);
         group(f, f.q[0], 2, 1, [&](int c) {
             if (c < 4)
                 read_q(f.q[1], 3, c % 2, c / 2, rd + cur);
-            if (c == 4 || c == 6)
-                load_q(wr + nxt, r0 + kStep, 3, c / 2 - 2);
+            q_pair(c, nxt, r0 + kStep, 3);
         });
         add_up<SUMS>(f.q[1], 3);
         group(f, f.q[1], 3, 0, [&](int c) {
             if (c < 4)
                 read_q(f.q[0], 0, c % 2, c / 2, rd + nxt);
             read_p(f, c, 0, rd + nxt);
-            if (c == 4 || c == 6)
-                load_q(wr + cur, r0 + 2 * kStep, 0, c / 2 - 2);
+            q_pair(c, cur, r0 + 2 * kStep, 0);
         });
         group(f, f.q[1], 3, 1, [&](int c) {
             read_p(f, c, 1, rd + nxt);
-            if (c == 4 || c == 6)
-                load_q(wr + cur, r0 + 2 * kStep, 1, c / 2 - 2);
+            q_pair(c, cur, r0 + 2 * kStep, 1);
         });
     }
 
@@ -330,7 +329,7 @@ struct Tile {
     {
         int cur = 0, nxt = kStageBytes;
         Frags f;
-        join<18>();  // P and Q block 0 of the first stage
+        join<P::kLoads + 10>();  // P and Q block 0 of the first stage
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             read_q(f.q[0], 0, 0, s, lds);

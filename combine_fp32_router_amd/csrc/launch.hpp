@@ -118,12 +118,26 @@ hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const voi
                                 const float *bias, int act, const void *residual, int E,
                                 int64_t max_rows, int K, int N, void *out, void *preact,
                                 hipStream_t stream);
+// The same for few rows an expert, and whether it pays.
+bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N);
+hipError_t launch_expert_few(const void *x, const int32_t *offsets, const void *w, const float *bias,
+                             int act, const void *residual, int E, int64_t max_rows, int K, int N,
+                             void *out, void *preact, hipStream_t stream);
 hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
                                    const void *z, int E, int64_t max_rows, int K, int N, void *dx,
                                    hipStream_t stream);
+// The products walk lists of 256 x 256 tiles counted in 32 bits.
+inline bool product_tiles_fit(int64_t row_tiles, int cols) { return row_tiles * ((cols + 127) / 128) < (int64_t(1) << 30); }
 hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
                                    int64_t max_rows, int K, int N, int flags, void *dw, float *db,
                                    hipStream_t stream);
+
+// Most tiles of `height` rows that E runs of together max_rows rows can have.
+inline int64_t max_row_tiles(int64_t max_rows, int E, int height)
+{
+    const int64_t live = max_rows < E ? max_rows : E;
+    return (max_rows - live) / height + live;
+}
 
 // Threads per block and 16-byte vectors per thread covering one row of
 // `vecs` 16-byte vectors with one block (<= 1024 threads, a whole number of

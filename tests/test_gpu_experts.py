@@ -64,6 +64,41 @@ def test_run_lengths(n, act):
     check_product([0, n], 144, 80, act, True, True, True, seed=n)
 
 
+# Runs around the tiles' edges, with enough rows for the 256- and (MANY) the
+# 128-column tiles rather than the kernel for few rows.
+EDGES = [127, 128, 129, 1, 255, 256, 257, 0, 64, 65, 2, 3000]
+MANY = [130, 1, 0, 64, 1200, 105]
+TILED = [(EDGES, 80, 2064, NONE, True, True, True), (EDGES, 272, 1040, SWIGLU, True, True, True),
+         (EDGES, 144, 2064, GELU, False, False, True), (EDGES, 528, 1040, SWIGLU, False, False, False),
+         (MANY, 528, 2064, SILU, True, True, True), (MANY, 1040, 1040, SWIGLU, True, False, True),
+         (MANY, 1040, 1200, RELU, False, True, False), ([0, 1500, 0], 1040, 1040, SWIGLU, True, True, True)]
+
+
+@pytest.mark.parametrize("case", TILED, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}a{c[3]}" for c in TILED])
+def test_tiled_product(case):
+    check_product(*case, base=7)
+
+
+@pytest.mark.parametrize("K", [48, 64, 80, 112, 128, 144, 192, 272])
+def test_tiled_reduced_lengths(K):
+    check_product(EDGES, K, 2064, NONE, False, False, False, seed=K)
+
+
+def test_tiled_runs_are_cut_and_nan_stays():
+    check_product(EDGES, 144, 2064, SILU, True, True, True, rows=3333)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = normal(g, 4000, 144), normal(g, 3, 2064, 144)
+    x[1777], x[3990:] = float("nan"), float("nan")
+    out = torch.zeros(4000, 2064, dtype=torch.bfloat16, device="cuda")
+    B.moe_expert_matmul(x, offsets_of([1777, 1, 2212]), w, None, NONE, None, out)
+    assert torch.isnan(out).any(1).nonzero()[:, 0].tolist() == [1777]
+    y, dy, *_ = R.product(x, [0, 1777, 1778, 3990], w, None, NONE, out)
+    x[1777] = 0
+    B.moe_expert_matmul(x, offsets_of([1777, 1, 2212]), w, None, NONE, out, out)  # residual in place
+    keep = torch.arange(3990, device="cuda") != 1777
+    R.inside(out[:3990][keep], y[:3990][keep], dy[:3990][keep], "in place")
+
+
 @pytest.mark.parametrize("K", [16, 32, 48, 64, 80, 112, 128, 144, 272, 528, 1040])
 def test_reduced_lengths(K):
     check_product([70, 6], K, 112, SILU, False, True, False, seed=K)
@@ -115,7 +150,7 @@ def test_residual_in_place_and_alias_refusals():
 GRADIENTS = [
     ([1], 16, 16, NONE), ([5, 0, 2], 64, 128, GELU), ([127, 128, 129], 272, 144, SWIGLU), ([256, 0, 257, 31], 512, 272, SILU),
     ([300], 1040, 528, RELU), ([0, 0], 64, 64, SWIGLU), ([33] * 9, 768, 2048, SWIGLU), ([700, 1, 500], 256, 1024, SWIGLU),
-    ([3, 1, 0, 4], 2048, 512, NONE)]
+    ([3, 1, 0, 4], 2048, 512, NONE), ([2100, 0, 129, 1, 64], 2064, 272, SWIGLU), ([700, 900], 1040, 4112, GELU)]
 
 
 @pytest.mark.parametrize("lengths,K,N,act", GRADIENTS, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}a{c[3]}" for c in GRADIENTS])
