@@ -429,7 +429,7 @@ int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *to
                    int64_t seg_tokens, int E, int k, float *d_logits, hipStream_t stream)
 {
     if (check_segments(T, seg_tokens, E, k) != MOE_OK ||
-        !grid_fits(route_grad_blocks(T, E), kRouteThreads))
+        !grid_fits(route_grad_blocks(seg_tokens, E), kRouteThreads))
         return MOE_ERR_SHAPE;
     if (T == 0)
         return MOE_OK;
@@ -452,7 +452,7 @@ int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv
     int s = check_rows(T, H, k, quant);
     if (s != MOE_OK)
         return s;
-    if (!grid_fits(T, token_threads(H, quant)))
+    if (!grid_fits(T, token_threads(H, MOE_QUANT_BF16)))
         return MOE_ERR_SHAPE;
     if (T == 0)
         return MOE_OK;

@@ -95,10 +95,13 @@ __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, i
     }
 }
 
-// p of the token in place of its logits; 0 everywhere if it is not live.
+// p of the token in place of its logits; 0 everywhere if it is not live.  The
+// exponential is the base-2 instruction behind a rounded product: off by about
+// (max - z) 2^-23 of the result.
 template <int L, int NE>
 __device__ __forceinline__ void softmax_row(float (&v)[NE], bool live)
 {
+    constexpr float kLog2e = 1.44269504088896341f;
     float m = v[0];
 #pragma unroll
     for (int q = 1; q < NE; ++q)
@@ -107,7 +110,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[NE], bool live)
     float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < NE; ++q) {
-        v[q] = expf(v[q] - m);
+        v[q] = __builtin_amdgcn_exp2f((v[q] - m) * kLog2e);
         s += v[q];
     }
     s = group_sum<L>(s);
@@ -181,15 +184,22 @@ __global__ __launch_bounds__(1024) void balance_partial_kernel(
 #pragma unroll
     for (int q = 0; q < NE; ++q)
         acc[q] = 0.0f;
-    for (int i = w * G; i < n; i += nw * G) {
-        const int64_t t = t0 + i + lane / L;
-        const bool live = i + lane / L < n && (!mask || mask[t]);
-        float v[NE];
-        load_row<L, NE, VEC>(logits + t * E, E, sub, live, v);
-        softmax_row<L, NE>(v, live);
+    for (int i = w * G; i < n; i += 2 * nw * G) {
+        float v[2][NE];  // two tokens at a time: their loads and their sums run side by side
+        bool live[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int in = i + u * nw * G + lane / L;
+            const int64_t t = t0 + in;
+            live[u] = in < n && (!mask || mask[t]);
+            load_row<L, NE, VEC>(logits + t * E, E, sub, live[u], v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            softmax_row<L, NE>(v[u], live[u]);
 #pragma unroll
         for (int q = 0; q < NE; ++q)
-            acc[q] += v[q];
+            acc[q] += v[0][q] + v[1][q];
     }
 #pragma unroll
     for (int q = 0; q < NE; ++q) {
@@ -228,53 +238,90 @@ __global__ __launch_bounds__(1024) void balance_partial_kernel(
     }
 }
 
-// Adds a segment's partial rows: block (x, s) takes 64 experts, its waves
-// every fourth row each; the segment's last block to finish forms the loss.
-__global__ __launch_bounds__(256) void balance_join_kernel(const float *__restrict__ psum,
-                                                           const int32_t *__restrict__ pcount,
-                                                           const int32_t *__restrict__ plive,
-                                                           int rows, int E, int k, unsigned *done,
-                                                           BalanceOut out)
+// Adds a segment's partial rows: a group of COLS threads for each of 1024 /
+// COLS rows at a time, eight of them in flight, the groups' sums added in
+// order.  ALL: block (0, s) takes every expert of its segment and forms the
+// loss.  Else block (x, s) takes COLS experts, and the segment's last block to
+// finish forms the loss: its first wave alone has written results, so only
+// that one makes them visible to the other XCDs (a fence of every wave of
+// 1024 blocks took 370 us).
+template <int COLS, bool ALL>
+__global__ __launch_bounds__(1024) void balance_join_kernel(const float *__restrict__ psum,
+                                                            const int32_t *__restrict__ pcount,
+                                                            const int32_t *__restrict__ plive,
+                                                            int rows, int E, int k, unsigned *done,
+                                                            BalanceOut out)
 {
-    __shared__ double sums[4][kWave];
-    __shared__ int32_t counts[4][kWave], lives[4];
+    constexpr int kGroups = 1024 / COLS;
+    __shared__ double sums[kGroups][COLS];
+    __shared__ int32_t counts[kGroups][COLS], lives[16];
     __shared__ unsigned last;
     const int64_t s = blockIdx.y;
-    const int w = threadIdx.x / kWave, lane = lane_id(), e = blockIdx.x * kWave + lane;
-    double sum = 0.0;
-    int32_t count = 0, live = 0;
-    if (e < E)
-        for (int r = w; r < rows; r += 4) {
-            sum += static_cast<double>(psum[(s * rows + r) * E + e]);
-            count += pcount[(s * rows + r) * E + e];
-        }
-    for (int r = threadIdx.x; r < rows; r += blockDim.x)
+    const int col = threadIdx.x % COLS, g = threadIdx.x / COLS;
+    int32_t live = 0;
+    for (int r = threadIdx.x; r < rows; r += 1024)
         live += plive[s * rows + r];
     for (int o = kWave / 2; o > 0; o >>= 1)
         live += __shfl_xor(live, o);
-    sums[w][lane] = sum;
-    counts[w][lane] = count;
-    if (lane == 0)
-        lives[w] = live;
-    __syncthreads();
-    live = lives[0] + lives[1] + lives[2] + lives[3];
-    if (w == 0 && e < E) {
-        out.prob_sums[s * E + e] =
-            static_cast<float>(sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane]);
-        out.counts[s * E + e] = counts[0][lane] + counts[1][lane] + counts[2][lane] + counts[3][lane];
+    if (lane_id() == 0)
+        lives[threadIdx.x / kWave] = live;
+    for (int e0 = ALL ? 0 : blockIdx.x * COLS; e0 < (ALL ? E : (static_cast<int>(blockIdx.x) + 1) * COLS); e0 += COLS) {
+        const int e = e0 + col;
+        const int64_t at = s * rows * E + e;
+        double sum = 0.0;
+        int32_t count = 0;
+        if (e < E)
+            for (int r0 = g; r0 < rows; r0 += 8 * kGroups) {
+                float v[8];
+                int32_t c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + i * kGroups;
+                    v[i] = r < rows ? psum[at + static_cast<int64_t>(r) * E] : 0.0f;
+                    c[i] = r < rows ? pcount[at + static_cast<int64_t>(r) * E] : 0;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    sum += static_cast<double>(v[i]);
+                    count += c[i];
+                }
+            }
+        __syncthreads();  // the last experts' sums were read
+        sums[g][col] = sum;
+        counts[g][col] = count;
+        __syncthreads();
+        if (g == 0 && e < E) {
+            for (int i = 1; i < min(kGroups, rows); ++i) {
+                sum += sums[i][col];
+                count += counts[i][col];
+            }
+            out.prob_sums[s * E + e] = static_cast<float>(sum);
+            out.counts[s * E + e] = count;
+        }
     }
-    __threadfence();
+    live = 0;
+    for (int i = 0; i < 16; ++i)
+        live += lives[i];
+    if (!ALL) {
+        static_assert(ALL || COLS <= kWave, "the first wave writes all results");
+        if (threadIdx.x < kWave)
+            __threadfence();
+        if (threadIdx.x == 0)
+            last = atomicAdd(&done[s], 1u) == gridDim.x - 1 ? 1u : 0u;
+        __syncthreads();
+        if (!last)
+            return;
+        __threadfence();
+    }
     __syncthreads();
-    if (threadIdx.x == 0)
-        last = atomicAdd(&done[s], 1u) == gridDim.x - 1 ? 1u : 0u;
-    __syncthreads();
-    if (!last)
-        return;
-    __threadfence();
     write_loss(out.prob_sums + s * E, out.counts + s * E, live, E, k, out.loss + s);
     if (threadIdx.x == 0)
         out.live[s] = live;
 }
+
+// Block (x, s): tokens of segment s, two a group of lanes, whose loads and
+// sums run side by side.
+constexpr int kGradTokens = 2;
 
 template <int L, int NE, bool VEC>
 __global__ __launch_bounds__(256) void route_grad_kernel(
@@ -283,69 +330,97 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
     const int32_t *__restrict__ counts, const int32_t *__restrict__ live_tokens, int64_t T,
     int64_t seg, int E, int k, float *__restrict__ dlogits)
 {
-    constexpr int G = kWave / L;
-    const int lane = lane_id(), sub = lane % L;
-    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (blockDim.x / kWave) +
-                           threadIdx.x / kWave) * G + lane / L;
-    if (first - lane / L >= T)
-        return;  // whole wave
-    const int64_t t = min(first, T - 1);
-    const bool live = first < T && (!mask || mask[t]);
-    float d[NE];
+    constexpr int G = 256 / L, kRow = L * NE;  // tokens at a time; experts a row has room for
+    __shared__ __align__(16) float rows[G * kRow];
+    const int sub = threadIdx.x % L, group = threadIdx.x / L;
+    const int64_t s = blockIdx.y, end = min(T, (s + 1) * seg);
+    const int64_t first = s * seg + static_cast<int64_t>(blockIdx.x) * (G * kGradTokens) + group;
+    float d[kGradTokens][NE];
+    bool live[kGradTokens];
+    int e[kGradTokens];
+    float wj[kGradTokens], dwj[kGradTokens];
+#pragma unroll
+    for (int u = 0; u < kGradTokens; ++u) {
+        const int64_t t = first + u * G;
+        live[u] = t < end && (!mask || mask[t]);
+        if (dloss)
+            load_row<L, NE, VEC>(logits + t * E, E, sub, live[u], d[u]);
+        // lane j of the token holds slot j
+        const bool slot = dw && sub < k && live[u];
+        e[u] = slot ? idx[t * k + sub] : -1;
+        wj[u] = slot ? w[t * k + sub] : 0.0f;
+        dwj[u] = slot ? dw[t * k + sub] : 0.0f;
+    }
     if (dloss) {
         float c[NE];
-        load_row<L, NE, VEC>(logits + t * E, E, sub, live, d);
-        softmax_row<L, NE>(d, live);
-        const int64_t s = t / seg;
-        float dot = 0.0f;
 #pragma unroll
         for (int q = 0; q < NE; ++q) {
-            const int e = expert_of<L, VEC>(q, sub);
-            c[q] = e < E ? static_cast<float>(counts[s * E + e]) : 0.0f;
-            dot = fmaf(c[q], d[q], dot);
+            const int ee = expert_of<L, VEC>(q, sub);
+            c[q] = ee < E ? static_cast<float>(counts[s * E + ee]) : 0.0f;
         }
-        dot = group_sum<L>(dot);
         const float n = fmaxf(static_cast<float>(live_tokens[s]), 1.0f);
-        const float scale = live ? dloss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n : 0.0f;
+        const float scale = dloss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
 #pragma unroll
-        for (int q = 0; q < NE; ++q)
-            d[q] = d[q] * (c[q] - dot) * scale;
-    } else {
-#pragma unroll
-        for (int q = 0; q < NE; ++q)
-            d[q] = 0.0f;
-    }
-    if (dw) {
-        // lane j of the token holds slot j
-        const bool slot = sub < k && live;
-        const int e = slot ? idx[t * k + sub] : -1;
-        const float wj = slot ? w[t * k + sub] : 0.0f, dwj = slot ? dw[t * k + sub] : 0.0f;
-        const float g = wj * (dwj - group_sum<L>(wj * dwj));
-        for (int j = 0; j < k; ++j) {
-            const int ej = __shfl(e, j, L);
-            const float gj = __shfl(g, j, L);
+        for (int u = 0; u < kGradTokens; ++u) {
+            softmax_row<L, NE>(d[u], live[u]);
+            float dot = 0.0f;
 #pragma unroll
             for (int q = 0; q < NE; ++q)
-                d[q] += ej == expert_of<L, VEC>(q, sub) ? gj : 0.0f;
-        }
-    }
-    if (first >= T)
-        return;
-    float *out = dlogits + t * E;
-    if constexpr (VEC) {
+                dot = fmaf(c[q], d[u][q], dot);
+            dot = group_sum<L>(dot);
 #pragma unroll
-        for (int i = 0; i < NE / 4; ++i) {
-            const int e = expert_of<L, VEC>(4 * i, sub);
-            if (e < E)
-                *reinterpret_cast<float4 *>(out + e) =
-                    make_float4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+            for (int q = 0; q < NE; ++q)
+                d[u][q] = d[u][q] * (c[q] - dot) * scale;
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < NE; ++q) {
-            const int e = expert_of<L, VEC>(q, sub);
-            if (e < E)
-                out[e] = d[q];
+        for (int u = 0; u < kGradTokens; ++u)
+#pragma unroll
+            for (int q = 0; q < NE; ++q)
+                d[u][q] = 0.0f;
+    }
+    // The gradients of the slots' logits reach the lanes that hold them through
+    // a row of LDS, where an id that occurs twice adds up.
+    float *row = rows + group * kRow;
+#pragma unroll
+    for (int u = 0; u < kGradTokens; ++u) {
+        const int64_t t = first + u * G;
+        if (dw) {
+            const float g = wj[u] * (dwj[u] - group_sum<L>(wj[u] * dwj[u]));
+#pragma unroll
+            for (int q = 0; q < NE; q += NE >= 4 ? 4 : 1) {
+                if (NE >= 4)
+                    *reinterpret_cast<float4 *>(row + q * L + 4 * sub) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                else
+                    row[q * L + sub] = 0.0f;
+            }
+            asm volatile("" ::: "memory");  // one wave's LDS operations run in order
+            if (static_cast<unsigned>(e[u]) < static_cast<unsigned>(E))
+                atomicAdd(row + e[u], g);
+            asm volatile("" ::: "memory");
+#pragma unroll
+            for (int q = 0; q < NE; ++q)
+                d[u][q] += row[expert_of<L, VEC>(q, sub)];
+            asm volatile("" ::: "memory");
+        }
+        if (t >= end)
+            continue;
+        float *out = dlogits + t * E;
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < NE / 4; ++i) {
+                const int ee = expert_of<L, VEC>(4 * i, sub);
+                if (ee < E)
+                    *reinterpret_cast<float4 *>(out + ee) =
+                        make_float4(d[u][4 * i], d[u][4 * i + 1], d[u][4 * i + 2], d[u][4 * i + 3]);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < NE; ++q) {
+                const int ee = expert_of<L, VEC>(q, sub);
+                if (ee < E)
+                    out[ee] = d[u][q];
+            }
         }
     }
 }
@@ -416,15 +491,19 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *idx, const ui
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || one)
         return err;
-    balance_join_kernel<<<dim3((E + kWave - 1) / kWave, S), 256, 0, stream>>>(
-        psum, pcount, plive, bt.blocks, E, k, done, out);
+    // many segments fill the card with a block each
+    if (S >= 16)
+        balance_join_kernel<64, true><<<dim3(1, S), 1024, 0, stream>>>(psum, pcount, plive, bt.blocks, E, k, done, out);
+    else
+        balance_join_kernel<16, false><<<dim3((E + 15) / 16, S), 1024, 0, stream>>>(psum, pcount, plive, bt.blocks, E,
+                                                                                    k, done, out);
     return hipGetLastError();
 }
 
-int64_t route_grad_blocks(int64_t T, int E)
+int64_t route_grad_blocks(int64_t seg, int E)
 {
-    const int per = E <= 256 ? 16 : 4;
-    return (T + per - 1) / per;
+    const int per = (E <= 256 ? 16 : 4) * kGradTokens;
+    return (seg + per - 1) / per;
 }
 
 hipError_t launch_route_grad(const float *logits, const int32_t *idx, const float *w,
@@ -434,7 +513,7 @@ hipError_t launch_route_grad(const float *logits, const int32_t *idx, const floa
 {
     const bool vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) |
                                      reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
-    const dim3 grid(static_cast<unsigned>(route_grad_blocks(T, E)));
+    const dim3 grid(static_cast<unsigned>(route_grad_blocks(seg, E)), layout_chunks(T, seg));
 #define MOE_ROUTE_GRAD(L, NE, V)                                                               \
     route_grad_kernel<L, NE, V><<<grid, 256, 0, stream>>>(logits, idx, w, dw, mask, dloss,     \
                                                           counts, live, T, seg, E, k, dlogits)

@@ -5,9 +5,8 @@
 // A quantised row's scale is taken out of the sum: sum_h d_h * code_h, times
 // the scale once.
 //
-// gfx950 design.  One block per token; each thread holds its 16-byte vectors
-// of d in registers as fp32 (VPT groups of 8 elements for bf16 rows, of 16
-// for the quantised ones), so d is read once for all k slots.  Per slot a
+// gfx950 design.  One block per token; each thread holds VPT 16-byte vectors
+// of d in registers as fp32, so d is read once for all k slots.  Per slot a
 // thread reads its part of the row, adds its products to one fp32 partial
 // and writes its part of w * d.  The partials of a group of slots reduce over
 // the wave, then over the block through LDS in wave order: the same bits
@@ -28,44 +27,28 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// Codes of one thread's group as fp32, without the scale.
+// Eight elements of a row as fp32, without the scale.
 template <int Q>
 struct RowVec;
 template <>
-struct RowVec<0> {  // 8 bf16
-    static constexpr int n = 8;
+struct RowVec<0> {  // bf16
     typedef u32x4 vec;
-    static __device__ __forceinline__ void get(const vec &v, float *f) { unpack8(v, f); }
+    static __device__ __forceinline__ void get(vec v, float *f) { unpack8(v, f); }
 };
 template <>
-struct RowVec<1> {  // 16 int8
-    static constexpr int n = 16;
-    typedef u32x4 vec;
-    static __device__ __forceinline__ void get(const vec &v, float *f)
-    {
-        dequant8(u32x2{v.x, v.y}, 1.0f, f);
-        dequant8(u32x2{v.z, v.w}, 1.0f, f + 8);
-    }
-};
-template <>
-struct RowVec<2> {  // 16 int4
-    static constexpr int n = 16;
+struct RowVec<1> {  // int8
     typedef u32x2 vec;
-    static __device__ __forceinline__ void get(const vec &v, float *f)
-    {
-        dequant4x8(v.x, 1.0f, f);
-        dequant4x8(v.y, 1.0f, f + 8);
-    }
+    static __device__ __forceinline__ void get(vec v, float *f) { dequant8(v, 1.0f, f); }
 };
 template <>
-struct RowVec<3> {  // 16 E4M3
-    static constexpr int n = 16;
-    typedef u32x4 vec;
-    static __device__ __forceinline__ void get(const vec &v, float *f)
-    {
-        dequant_fp8x8(u32x2{v.x, v.y}, 1.0f, f);
-        dequant_fp8x8(u32x2{v.z, v.w}, 1.0f, f + 8);
-    }
+struct RowVec<2> {  // int4
+    typedef uint32_t vec;
+    static __device__ __forceinline__ void get(vec v, float *f) { dequant4x8(v, 1.0f, f); }
+};
+template <>
+struct RowVec<3> {  // E4M3
+    typedef u32x2 vec;
+    static __device__ __forceinline__ void get(vec v, float *f) { dequant_fp8x8(v, 1.0f, f); }
 };
 
 // ROWS: write d_row; GATES: read the rows and write d_w.
@@ -76,20 +59,17 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
     const float *__restrict__ w, int G, int k, u32x4 *__restrict__ d_rows, float *__restrict__ d_w)
 {
     typedef RowVec<Q> RV;
-    constexpr int N = RV::n, NV = N / 8;
     __shared__ float red[16][MOE_MAX_TOPK];  // [wave][slot]
     const typename RV::vec *rows = static_cast<const typename RV::vec *>(rows_);
     const int64_t t = blockIdx.x;
     const int nthr = blockDim.x, wv = threadIdx.x / kWave;
     const int32_t at = load_per_lane(pos + t * k, k);
     const float wts = load_per_lane(w + t * k, k);
-    float d[VPT][N];
+    float d[VPT][8];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int g = threadIdx.x + i * nthr;
-#pragma unroll
-        for (int h = 0; h < NV; ++h)
-            unpack8(g < G ? d_out[(t * G + g) * NV + h] : u32x4{0, 0, 0, 0}, d[i] + 8 * h);
+        unpack8(g < G ? d_out[t * G + g] : u32x4{0, 0, 0, 0}, d[i]);
     }
     for (int j0 = 0; j0 < k; j0 += kSlotGroup) {
         typename RV::vec v[kSlotGroup][VPT];
@@ -117,25 +97,22 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     const int g = threadIdx.x + i * nthr;
-                    float f[N];
+                    float f[8];
 #pragma unroll
-                    for (int c = 0; c < N; ++c)
+                    for (int c = 0; c < 8; ++c)
                         f[c] = wj * d[i][c];
                     if (g < G)
-#pragma unroll
-                        for (int h = 0; h < NV; ++h)
-                            __builtin_nontemporal_store(
-                                pack8(f + 8 * h), d_rows + (static_cast<int64_t>(p) * G + g) * NV + h);
+                        __builtin_nontemporal_store(pack8(f), d_rows + static_cast<int64_t>(p) * G + g);
                 }
             }
             if (GATES) {
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    float f[N];
+                    float f[8];
                     RV::get(v[q][i], f);
 #pragma unroll
-                    for (int c = 0; c < N; ++c)
+                    for (int c = 0; c < 8; ++c)
                         dot = fmaf(d[i][c], f[c], dot);
                 }
                 dot = wave_sum(dot);
@@ -163,7 +140,7 @@ void launch_format(const void *d_out, const void *rows, const float *scales, con
                    const float *w, int64_t T, int H, int k, void *d_rows, float *d_w,
                    hipStream_t stream)
 {
-    const int G = H / RowVec<Q>::n;
+    const int G = H / 8;
     const RowTiling rt = row_tiling(G);
     const dim3 grid(static_cast<unsigned>(T)), block(rt.threads);
 #define MOE_CG(V, R, W)                                                                        \
@@ -178,9 +155,7 @@ void launch_format(const void *d_out, const void *rows, const float *scales, con
     case 1: MOE_CG_PARTS(1); break;
     case 2: MOE_CG_PARTS(2); break;
     case 4: MOE_CG_PARTS(4); break;
-    default:
-        if constexpr (Q == 0) { MOE_CG_PARTS(8); }
-        break;
+    default: MOE_CG_PARTS(8); break;
     }
 #undef MOE_CG_PARTS
 #undef MOE_CG

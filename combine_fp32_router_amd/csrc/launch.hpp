@@ -102,7 +102,7 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *idx, const ui
                                int64_t T, int64_t seg, int E, int k, float *loss, int32_t *counts,
                                float *prob_sums, int32_t *live, void *workspace,
                                hipStream_t stream);
-int64_t route_grad_blocks(int64_t T, int E);  // of kRouteThreads threads
+int64_t route_grad_blocks(int64_t seg, int E);  // of a segment, of kRouteThreads threads
 hipError_t launch_route_grad(const float *logits, const int32_t *idx, const float *w,
                              const float *dw, const uint8_t *mask, const float *dloss,
                              const int32_t *counts, const int32_t *live, int64_t T, int64_t seg,
