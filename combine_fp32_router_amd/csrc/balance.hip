@@ -114,7 +114,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[NE], bool live)
         s += v[q];
     }
     s = group_sum<L>(s);
-    const float inv = live ? 1.0f / s : 0.0f;
+    const float inv = live ? __builtin_amdgcn_rcpf(s) : 0.0f;  // 1 ulp
 #pragma unroll
     for (int q = 0; q < NE; ++q)
         v[q] *= inv;
@@ -127,14 +127,29 @@ struct BalanceOut {
     int32_t *live;
 };
 
+// A value that another block stored, and the store, past the XCD's L2.
+template <typename V>
+__device__ __forceinline__ V load_shared(const V *p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename V>
+__device__ __forceinline__ void store_shared(V *p, V v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // loss of one segment from its sums; called by every thread of a block.
+// SHARED: they are other blocks'.
+template <bool SHARED>
 __device__ void write_loss(const float *sums, const int32_t *counts, int live, int E, int k,
                            float *loss)
 {
     __shared__ double red[16];
     double acc = 0.0;
     for (int e = threadIdx.x; e < E; e += blockDim.x)
-        acc += static_cast<double>(counts[e]) * static_cast<double>(sums[e]);
+        acc += static_cast<double>(SHARED ? load_shared(counts + e) : counts[e]) *
+               static_cast<double>(SHARED ? load_shared(sums + e) : sums[e]);
     for (int o = kWave / 2; o > 0; o >>= 1)
         acc += __shfl_xor(acc, o);
     if (lane_id() == 0)
@@ -228,7 +243,7 @@ __global__ __launch_bounds__(1024) void balance_partial_kernel(
     }
     if (ONE) {
         __syncthreads();
-        write_loss(lds, hist, hist[E], E, k, out.loss + s);
+        write_loss<false>(lds, hist, hist[E], E, k, out.loss + s);
         if (threadIdx.x == 0)
             out.live[s] = hist[E];
     } else if (threadIdx.x == 0) {
@@ -242,9 +257,10 @@ __global__ __launch_bounds__(1024) void balance_partial_kernel(
 // COLS rows at a time, eight of them in flight, the groups' sums added in
 // order.  ALL: block (0, s) takes every expert of its segment and forms the
 // loss.  Else block (x, s) takes COLS experts, and the segment's last block to
-// finish forms the loss: its first wave alone has written results, so only
-// that one makes them visible to the other XCDs (a fence of every wave of
-// 1024 blocks took 370 us).
+// finish forms the loss.  Its results pass the L2 by themselves (store_shared)
+// and are waited for before it counts itself done: a release fence would
+// write back all of the L2, full of the partial rows (13 us instead of 5; by
+// every wave of 1024 blocks, 370).
 template <int COLS, bool ALL>
 __global__ __launch_bounds__(1024) void balance_join_kernel(const float *__restrict__ psum,
                                                             const int32_t *__restrict__ pcount,
@@ -295,8 +311,13 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float *__restr
                 sum += sums[i][col];
                 count += counts[i][col];
             }
-            out.prob_sums[s * E + e] = static_cast<float>(sum);
-            out.counts[s * E + e] = count;
+            if (ALL) {
+                out.prob_sums[s * E + e] = static_cast<float>(sum);
+                out.counts[s * E + e] = count;
+            } else {
+                store_shared(&out.prob_sums[s * E + e], static_cast<float>(sum));
+                store_shared(&out.counts[s * E + e], count);
+            }
         }
     }
     live = 0;
@@ -304,17 +325,15 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float *__restr
         live += lives[i];
     if (!ALL) {
         static_assert(ALL || COLS <= kWave, "the first wave writes all results");
-        if (threadIdx.x < kWave)
-            __threadfence();
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the first wave's results are there
         if (threadIdx.x == 0)
             last = atomicAdd(&done[s], 1u) == gridDim.x - 1 ? 1u : 0u;
         __syncthreads();
         if (!last)
             return;
-        __threadfence();
     }
     __syncthreads();
-    write_loss(out.prob_sums + s * E, out.counts + s * E, live, E, k, out.loss + s);
+    write_loss<!ALL>(out.prob_sums + s * E, out.counts + s * E, live, E, k, out.loss + s);
     if (threadIdx.x == 0)
         out.live[s] = live;
 }
@@ -426,14 +445,14 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
 }
 
 // Blocks of a segment and their tokens: about 1024 blocks over the batch,
-// none under 64 tokens.
+// none under 32 tokens.
 struct BalanceTiling {
     int tpb, blocks;
 };
 BalanceTiling balance_tiling(int64_t T, int64_t seg)
 {
     int64_t tpb = (T + 1023) / 1024;
-    tpb = tpb < 64 ? 64 : (tpb + 15) / 16 * 16;
+    tpb = tpb < 32 ? 32 : (tpb + 15) / 16 * 16;
     if (tpb > seg || seg <= 256)
         tpb = seg > 0 ? seg : 1;
     return {static_cast<int>(tpb), static_cast<int>(seg > 0 ? (seg + tpb - 1) / tpb : 1)};
