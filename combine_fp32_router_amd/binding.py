@@ -462,15 +462,39 @@ def moe_recv_ungroup(grouped: torch.Tensor, grouped_scales: torch.Tensor | None,
                                    _stream(stream)))
 
 
-def _stream_on(stream, *tensors) -> ctypes.c_void_p:
-    """The stream handle for a call over `tensors`, which must share one
-    device: `stream`, or that device's current stream."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+def _call(name: str, stream, *args) -> None:
+    """Entry point `name` on `args`, its tensors as their addresses, and the
+    stream: `stream`, or the current stream of the tensors' device.  The
+    tensors must be contiguous and share one device, which is current during
+    the call (a null stream is the current device's).  Plain ints and the
+    argtypes rather than c_void_p objects: half the cost of a call."""
+    device, raw = -1, []
+    for a in args:
+        if isinstance(a, torch.Tensor):
+            d = a.get_device()
+            if d < 0:
+                raise ValueError("expected a device tensor")
+            if d != device:
+                if device >= 0:
+                    raise ValueError(f"tensors on different devices: cuda:{device}, cuda:{d}")
+                device = d
+            if not a.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+            a = a.data_ptr()
+        raw.append(a)
     if stream is None:
-        stream = torch.cuda.current_stream(devices.pop())
-    return _stream(stream)
+        stream = torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != device:
+            raise ValueError(f"a stream of cuda:{stream.device_index}, tensors on cuda:{device}")
+        stream = stream.cuda_stream
+    entry = getattr(load(), name)
+    if device == torch.cuda.current_device():
+        status = entry(*raw, int(stream))
+    else:
+        with torch.cuda.device(device):
+            status = entry(*raw, int(stream))
+    _check(name, status)
 
 
 def _want_bf16(t: torch.Tensor, shape, name: str):
@@ -541,12 +565,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
     _want_mask(token_mask, T)
     _want_segments(out, T, E)
     n = ctypes.c_size_t(out.workspace.numel())
-    st = _stream_on(stream, logits, topk_idx, token_mask, *out[:5])
-    _check("moe_balance_loss",
-           load().moe_balance_loss(_ptr(logits), _ptr(topk_idx), _ptr(token_mask), T,
-                                   out.seg_tokens, E, topk_idx.shape[1], _ptr(out.loss),
-                                   _ptr(out.expert_counts), _ptr(out.prob_sums),
-                                   _ptr(out.tokens), _ptr(out.workspace), ctypes.byref(n), st))
+    _call("moe_balance_loss", stream, logits, topk_idx, token_mask, T, out.seg_tokens, E,
+          topk_idx.shape[1], out.loss, out.expert_counts, out.prob_sums, out.tokens,
+          out.workspace, ctypes.byref(n))
     return out
 
 
@@ -584,12 +605,8 @@ def moe_route_grad(logits: torch.Tensor | None, topk_idx: torch.Tensor,
     counts = balance.expert_counts if d_loss is not None else None
     live = balance.tokens if d_loss is not None else None
     seg = balance.seg_tokens if d_loss is not None else max(T, 1)
-    st = _stream_on(stream, logits, topk_idx, topk_w, d_topk_w, token_mask, d_loss, counts, live,
-                    d_logits)
-    _check("moe_route_grad",
-           load().moe_route_grad(_ptr(logits), _ptr(topk_idx), _ptr(topk_w), _ptr(d_topk_w),
-                                 _ptr(token_mask), _ptr(d_loss), _ptr(counts), _ptr(live), T, seg,
-                                 E, k, _ptr(d_logits), st))
+    _call("moe_route_grad", stream, logits, topk_idx, topk_w, d_topk_w, token_mask, d_loss, counts,
+          live, T, seg, E, k, d_logits)
     return d_logits
 
 
@@ -610,10 +627,8 @@ def moe_combine_grad(d_out: torch.Tensor, recv: torch.Tensor | None,
         if d_topk_w.numel() < T * k:
             raise ValueError("d_topk_w must hold T*k values")
         _want_scales(recv_scales, 0, quant, "recv_scales")
-    st = _stream_on(stream, d_out, recv, recv_scales, pos, topk_w, d_recv, d_topk_w)
-    _check("moe_combine_grad",
-           load().moe_combine_grad(_ptr(d_out), _ptr(recv), _ptr(recv_scales), quant, _ptr(pos),
-                                   _ptr(topk_w), T, H, k, _ptr(d_recv), _ptr(d_topk_w), st))
+    _call("moe_combine_grad", stream, d_out, recv, recv_scales, quant, pos, topk_w, T, H, k, d_recv,
+          d_topk_w)
 
 
 def _want_weights(w: torch.Tensor, offsets: torch.Tensor):
@@ -648,10 +663,8 @@ def moe_expert_matmul(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
         _want(bias, torch.float32, "bias")
         if bias.numel() != E * wide_n:
             raise ValueError("bias must hold one value per weight row")
-    st = _stream_on(stream, x, offsets, w, bias, residual, out, preact)
-    _check("moe_expert_matmul",
-           load().moe_expert_matmul(_ptr(x), _ptr(offsets), _ptr(w), _ptr(bias), act,
-                                    _ptr(residual), E, rows, K, N, _ptr(out), _ptr(preact), st))
+    _call("moe_expert_matmul", stream, x, offsets, w, bias, act, residual, E, rows, K, N, out,
+          preact)
     return out
 
 
@@ -673,10 +686,7 @@ def moe_expert_matmul_dx(dy: torch.Tensor, offsets: torch.Tensor, w: torch.Tenso
         raise ValueError("an activation's gradient needs preact")
     else:
         _want_bf16(preact, (rows, wide * K), "preact")
-    st = _stream_on(stream, dy, offsets, w, preact, dx)
-    _check("moe_expert_matmul_dx",
-           load().moe_expert_matmul_dx(_ptr(dy), _ptr(offsets), _ptr(w), act, _ptr(preact), E,
-                                       rows, K, N, _ptr(dx), st))
+    _call("moe_expert_matmul_dx", stream, dy, offsets, w, act, preact, E, rows, K, N, dx)
     return dx
 
 
@@ -700,8 +710,5 @@ def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     flags = MOE_GRAD_FP32 if dw.dtype == torch.float32 else MOE_GRAD_BF16
     if accumulate:
         flags |= MOE_GRAD_ACCUMULATE
-    st = _stream_on(stream, dy, x, offsets, dw, dbias)
-    _check("moe_expert_matmul_dw",
-           load().moe_expert_matmul_dw(_ptr(dy), _ptr(x), _ptr(offsets), E, rows, K, N, flags,
-                                       _ptr(dw), _ptr(dbias), st))
+    _call("moe_expert_matmul_dw", stream, dy, x, offsets, E, rows, K, N, flags, dw, dbias)
     return dw
