@@ -11,6 +11,15 @@
 // and writes its part of w * d.  The partials of a group of slots reduce over
 // the wave, then over the block through LDS in wave order: the same bits
 // every time.
+//
+// HBM-bound: bf16 writes a row for every row it reads.  8192 tokens of 7168,
+// 8 slots: gates alone (read) 149 us, 7.1 TB/s; rows alone (write) 183, 5.8;
+// both in one kernel 376, since reads and writes then take turns in HBM
+// throughout, and in two launches, first all reads, 332.  With rows of one
+// byte or less that saves nothing (int8: 286 against 289).  Rows that the
+// last-level cache holds are written with ordinary stores (2048 tokens: 81 us
+// against 97; 4096 of 2048 int8: 36 against 43) and in one launch (81 against
+// 84); past it streaming stores are faster (376 against 405).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -18,6 +27,7 @@ namespace moe {
 namespace {
 
 constexpr int kSlotGroup = 4;  // slots whose row loads are in flight together
+constexpr int64_t kLastLevelBytes = 256 << 20;  // the cache behind the eight L2s
 
 __device__ __forceinline__ float wave_sum(float v)
 {
@@ -51,8 +61,9 @@ struct RowVec<3> {  // E4M3
     static __device__ __forceinline__ void get(vec v, float *f) { dequant_fp8x8(v, 1.0f, f); }
 };
 
-// ROWS: write d_row; GATES: read the rows and write d_w.
-template <int Q, int VPT, bool ROWS, bool GATES>
+// ROWS: write d_row, with streaming stores if STREAM; GATES: read the rows and
+// write d_w.
+template <int Q, int VPT, bool ROWS, bool GATES, bool STREAM>
 __global__ __launch_bounds__(1024) void combine_grad_kernel(
     const u32x4 *__restrict__ d_out, const void *__restrict__ rows_,
     const float *__restrict__ scales, const int32_t *__restrict__ pos,
@@ -101,8 +112,11 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
 #pragma unroll
                     for (int c = 0; c < 8; ++c)
                         f[c] = wj * d[i][c];
-                    if (g < G)
-                        __builtin_nontemporal_store(pack8(f), d_rows + static_cast<int64_t>(p) * G + g);
+                    u32x4 *at_row = d_rows + static_cast<int64_t>(p) * G + g;
+                    if (g < G && STREAM)
+                        __builtin_nontemporal_store(pack8(f), at_row);
+                    else if (g < G)
+                        *at_row = pack8(f);
                 }
             }
             if (GATES) {
@@ -143,14 +157,21 @@ void launch_format(const void *d_out, const void *rows, const float *scales, con
     const int G = H / 8;
     const RowTiling rt = row_tiling(G);
     const dim3 grid(static_cast<unsigned>(T)), block(rt.threads);
-#define MOE_CG(V, R, W)                                                                        \
-    combine_grad_kernel<Q, V, R, W><<<grid, block, 0, stream>>>(                               \
+    const bool large = T * k * H * 2 > kLastLevelBytes;
+#define MOE_CG(V, R, W, S)                                                                     \
+    combine_grad_kernel<Q, V, R, W, S><<<grid, block, 0, stream>>>(                            \
         static_cast<const u32x4 *>(d_out), rows, scales, pos, w, G, k,                         \
         static_cast<u32x4 *>(d_rows), d_w)
 #define MOE_CG_PARTS(V)                                                                        \
-    if (d_rows && d_w) { MOE_CG(V, true, true); }                                              \
-    else if (d_rows) { MOE_CG(V, true, false); }                                               \
-    else { MOE_CG(V, false, true); }
+    if (d_w && (!d_rows || (Q == 0 && large))) { MOE_CG(V, false, true, false); }              \
+    if (!d_rows) { return; }                                                                   \
+    if (!large) {                                                                              \
+        if (d_w) { MOE_CG(V, true, true, false); } else { MOE_CG(V, true, false, false); }     \
+    } else if (Q != 0 && d_w) {                                                                \
+        MOE_CG(V, true, true, Q != 0);                                                         \
+    } else {                                                                                   \
+        MOE_CG(V, true, false, true);                                                          \
+    }
     switch (rt.vpt) {
     case 1: MOE_CG_PARTS(1); break;
     case 2: MOE_CG_PARTS(2); break;

@@ -76,6 +76,13 @@ def test_combine_grad(T, H, k, quant, dropped, parts):
         assert not d_w[pos.view(T, k) < 0].any()
 
 
+@pytest.mark.parametrize("parts", ["both", "rows", "gates"])
+@pytest.mark.parametrize("quant", range(4))
+def test_rows_past_the_last_level_cache(quant, parts):
+    """More than 256 MiB of gradient rows."""
+    test_combine_grad(2060, 8192, 8, quant, 0.01, parts)
+
+
 def test_dropped_rows_are_not_read():
     """NaN in rows that no slot points to reaches nothing."""
     T, H, k = 40, 256, 4
