@@ -349,7 +349,7 @@ struct Tile {
     }
 
     // A tile of at most NB blocks of 64 rows: three stages, whole stages in
-    // flight; P's reading bounds it, not the products.
+    // flight.
     __device__ __forceinline__ void load_thin(MOE_LDS char *__restrict__ stage, int r0, int nb) const
     {
 #pragma unroll
@@ -365,38 +365,63 @@ struct Tile {
         load_thin(lds, 0, nb);
         load_thin(lds + kThinBytes, kStep, nb);
     }
+    // Stage k at offset `cur`; its first half's fragments are in f.  The second
+    // half's are read, and stage k + 2 is loaded over k - 1, beside the first
+    // half's products; the next stage's first half beside the second's.
     template <int NB, bool SUMS>
-    __device__ __forceinline__ void step_thin(const MOE_LDS char *__restrict__ rd, MOE_LDS char *__restrict__ wr,
-                                              int r0)
+    __device__ __forceinline__ void step_thin(Frags &f, const MOE_LDS char *__restrict__ rd,
+                                              MOE_LDS char *__restrict__ wr, int cur, int nxt, int into, int r0)
     {
-        join<P::kLoads + NB * Q::kLoads>();  // this stage is here, and the third was read
-        load_thin(wr, r0 + 2 * kStep, NB);
-        Frags f;
+        constexpr int NP = P::kLoads, NL = NP + NB * Q::kLoads;  // loads of a stage
+        constexpr int NG = NB * kFrags;                          // places beside products
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int b = 0; b < NB; ++b)
+            group(f, f.q[b], b, 0, [&](int c) {
+                const int at = b * kFrags + c;
+                if (at < kFrags)
+                    read_p(f, at, 1, rd + cur);
+                if (at < 2 * NB)
+                    read_q(f.q[at / 2], at / 2, at % 2, 1, rd + cur);
 #pragma unroll
-            for (int i = 0; i < 2 * NB; ++i)
-                read_q(f.q[i / 2], i / 2, i % 2, s, rd);
+                for (int i = at * NL / NG; i < (at + 1) * NL / NG; ++i)
+                    if (i < NP)
+                        load_p(wr + into, r0 + 2 * kStep, i);
+                    else
+                        load_q(wr + into, r0 + 2 * kStep, (i - NP) / Q::kLoads, (i - NP) % Q::kLoads);
+            });
+        join<NL>();  // the next stage is here; this one was read
 #pragma unroll
-            for (int c = 0; c < kFrags; ++c)
-                read_p(f, c, s, rd);
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < NB; ++b)
             add_up<SUMS>(f.q[b], b);
-            group(f, f.q[b], b, 0, [](int) {});
-            group(f, f.q[b], b, 1, [](int) {});
-        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            group(f, f.q[b], b, 1, [&](int c) {
+                const int at = b * kFrags + c;
+                if (at < kFrags)
+                    read_p(f, at, 0, rd + nxt);
+                if (at < 2 * NB)
+                    read_q(f.q[at / 2], at / 2, at % 2, 0, rd + nxt);
+            });
     }
     template <int NB, bool SUMS>
     __device__ __forceinline__ void run_thin(MOE_LDS char *lds)
     {
-        int cur = 0, into = 2 * kThinBytes;
+        int cur = 0, nxt = kThinBytes, into = 2 * kThinBytes;
+        Frags f;
+        join<P::kLoads + NB * Q::kLoads>();  // the first stage
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i)
+            read_q(f.q[i / 2], i / 2, i % 2, 0, lds);
+#pragma unroll
+        for (int c = 0; c < kFrags; ++c)
+            read_p(f, c, 0, lds);
 #pragma unroll 1
         for (int r0 = 0; r0 < R; r0 += kStep) {
-            step_thin<NB, SUMS>(lds + cur, lds + into, r0);
-            into = cur;
-            cur = cur == 2 * kThinBytes ? 0 : cur + kThinBytes;
+            step_thin<NB, SUMS>(f, lds, lds, cur, nxt, into, r0);
+            const int t = cur;
+            cur = nxt;
+            nxt = into;
+            into = t;
         }
         settle();
     }
