@@ -18,6 +18,9 @@ namespace {
 
 enum Op { kForward, kDx, kDw };
 
+constexpr int kCus = 256;           // of the card
+constexpr float kCutAbove = 1.4f;  // (TileList)
+
 struct Args {
     const uint16_t *p, *q;  // operands as above
     const int32_t *offsets;
@@ -31,6 +34,7 @@ struct Args {
     float *db;
     int flags;
     int rows;               // dw: rows of the output (N)
+    int height;             // forward, dx: rows of a tile
 };
 
 // Results leave 16 rows of a wave's columns at a time.  A lane's share is
@@ -324,65 +328,61 @@ struct Work {
 
 // The tiles of a call, in the order in which they are handed out: workgroup b
 // takes entries b, b + gridDim.x, ...  Entry j runs on XCD j % 8, so every
-// list is dealt out in eight contiguous parts (xcd_order).  forward, dx: the
-// tiles of more than half their rows, which all cost the same, then the runs'
+// list is dealt out in eight contiguous parts (xcd_order).  Runs and list are
+// worked out once, into LDS.
+//
+// forward, dx: tiles of `height` rows (256, 128 or 64, the host's choice), at
+// first those of more than half of it, which all cost the same, then the runs'
 // shorter ends; these go, two at a time, to the workgroups that the others'
-// last round leaves idle.  dw: expert after expert, the longest runs first (of up to 64
-// experts).  Runs and list are worked out once, into LDS.
-template <Op OP, int ROWS, int COLS>
+// last round leaves idle.
+//
+// dw (TileList<kDw>): an expert's tiles cost what its run is long, and the
+// longest run's could outlast all others: up to 64 experts' are cut to 128 or 64
+// rows where one of 256 would take too much of the whole call, ordered by
+// their cost, and every second round is dealt out backwards.
+template <Op OP, int COLS>
 struct TileList {
     static constexpr int kBytes = 4 * (3 * MOE_MAX_EXPERTS + 1);
     int32_t *starts;  // [E + 1] first rows of the runs
-    int32_t *table;   // [E] upto of the whole tiles, [E] of the ends (dw: [E] experts in order)
-    int E, whole, ends, col_tiles, row_tiles;
-    int nw, nw8, ne, end;  // entries: whole tiles (dw: an expert's), rounded up, ends, all
+    int32_t *upto;    // [E] entries up to an expert's last (of whole tiles; dw: in the order of `experts`)
+    int32_t *second;  // [E] the same of the ends; dw: experts, those to come first first
+    int E, height, whole, ends, col_tiles;
+    int nw, nw8, ne, end;  // entries: whole tiles, rounded up, ends, all
 
     __device__ __forceinline__ void build(const Args &a, int32_t *lds)
     {
         E = a.E;
+        height = a.height;
         starts = lds;
-        table = lds + E + 1;
+        upto = lds + E + 1;
+        second = upto + E;
         col_tiles = (a.C + COLS - 1) / COLS;
-        row_tiles = (a.rows + ROWS - 1) / ROWS;  // dw
-        const int w = threadIdx.x / kWave, lane = lane_id();
         for (int e = threadIdx.x; e <= E; e += blockDim.x)
             starts[e] = run_start(a.offsets, e, a.max_rows);
         __syncthreads();
+        // (a branch on it that is not known to be a wave's makes the compiler take the
+        // tiles' addresses for lanes' own, in loops around every load)
+        const int w = static_cast<int>(uniform(threadIdx.x / kWave)), lane = lane_id();
         if (OP == kDw) {
-            if (E <= kWave && w == 0) {
-                const int n = lane < E ? run(lane).n : -1;
-                int rank = 0;
-                for (int j = 0; j < E; ++j) {
-                    const int m = lane_value(n, j);
-                    rank += m > n || (m == n && j < lane);
-                }
-                if (lane < E)
-                    table[rank] = lane;
-            } else if (E > kWave) {
-                for (int e = threadIdx.x; e < E; e += blockDim.x)
-                    table[e] = e;
-            }
+            if (w == 0)
+                order(a);
         } else if (w < 2) {
-            int32_t *upto = table + w * E;
             int before = 0;
             for (int e0 = 0; e0 < E; e0 += kWave) {
                 const int e = e0 + lane, n = e < E ? run(e).n : 0;
-                const int sum = before + wave_inclusive_scan(w == 0 ? (n + ROWS / 2 - 1) / ROWS : short_end(n));
+                const int end_rows = short_end(n);
+                const int sum = before + wave_inclusive_scan(w == 0 ? (n + height - 1) / height - end_rows : end_rows);
                 if (e < E)
-                    upto[e] = sum;
+                    (w == 0 ? upto : second)[e] = sum;
                 before = lane_value(sum, kWave - 1);
             }
         }
         __syncthreads();
         if (OP == kDw) {
-            whole = ends = 0;
-            nw = row_tiles * col_tiles;
-            nw8 = (nw + 7) / 8 * 8;
-            ne = 0;
-            end = nw8 * E;
+            end = static_cast<int>(uniform(upto[E - 1]));
         } else {
-            whole = static_cast<int>(uniform(table[E - 1]));
-            ends = static_cast<int>(uniform(table[2 * E - 1]));
+            whole = static_cast<int>(uniform(upto[E - 1]));
+            ends = static_cast<int>(uniform(second[E - 1]));
             nw = whole * col_tiles;
             nw8 = (nw + 7) / 8 * 8;
             ne = ends * col_tiles;
@@ -396,17 +396,62 @@ struct TileList {
         return {first, max(starts[e + 1] - first, 0)};
     }
 
-    static __device__ __forceinline__ int short_end(int n) { return n % ROWS > 0 && n % ROWS <= ROWS / 2; }
-
-    // Expert of entry k of a list whose counts add up to upto[].
-    __device__ __forceinline__ int expert_of(const int32_t *upto, int k) const
+    // Whether the run's last tile is one of the ends.
+    __device__ __forceinline__ int short_end(int n) const
     {
-        int e = 0;
+        return height > 64 && n % height > 0 && n % height <= height / 2;
+    }
+
+    // dw.  Cost of a tile of 256 >> cut rows, in 1/16 of 64 r of a tile of 256:
+    // the products' and the results'.
+    static __device__ __forceinline__ int cost(int n, int cut)
+    {
+        const int steps = (n + kStep - 1) / kStep;
+        return cut == 0 ? 16 * steps + 64 : cut == 1 ? 10 * steps + 40 : 7 * steps + 28;
+    }
+    __device__ __forceinline__ void order(const Args &a)
+    {
+        const int lane = lane_id();
+        int before = 0;
+        for (int e0 = 0; e0 < E; e0 += kWave) {
+            const int e = e0 + lane, n = e < E ? run(e).n : 0;
+            int cut = 0, at = e;
+            if (E <= kWave) {
+                const int tiles = ((a.rows + 255) / 256) * col_tiles;
+                float share = e < E ? static_cast<float>(cost(n, 0)) * tiles / kCus : 0.0f;
+#pragma unroll
+                for (int o = 1; o < kWave; o <<= 1)
+                    share += __shfl_xor(share, o);
+                while (cut < 2 && cost(n, cut) > kCutAbove * share)
+                    ++cut;
+                const int c = e < E ? cost(n, cut) : -1;
+                at = 0;
+                for (int j = 0; j < E; ++j) {
+                    const int other = lane_value(c, j);
+                    at += other > c || (other == c && j < lane);
+                }
+            }
+            if (e < E) {
+                second[at] = e | cut << 16;
+                upto[at] = (((a.rows + (256 >> cut) - 1) >> (8 - cut)) * col_tiles + 7) / 8 * 8;
+            }
+            // (this wave's own writes)
+            const int sum = before + wave_inclusive_scan(e < E ? upto[e] : 0);
+            if (e < E)
+                upto[e] = sum;
+            before = lane_value(sum, kWave - 1);
+        }
+    }
+
+    // First i whose upto[i] is past entry j.
+    __device__ __forceinline__ int holder(const int32_t *list, int j) const
+    {
+        int i = 0;
         for (int e0 = 0; e0 < E; e0 += kWave) {
             const int at = e0 + lane_id();
-            e += __builtin_popcountll(__ballot(at < E && upto[at] <= k));
+            i += __builtin_popcountll(__ballot(at < E && list[at] <= j));
         }
-        return static_cast<int>(uniform(e));
+        return static_cast<int>(uniform(i));
     }
 
     // Moves this workgroup's count i to its next entry with work; false at the
@@ -415,45 +460,49 @@ struct TileList {
     {
         const int groups = gridDim.x, b = blockIdx.x;
         for (;; ++i) {
-            int j = i * groups + b;
+            int j = i * groups + (OP == kDw && i % 2 ? (groups / 8 - 1 - b / 8) * 8 + b % 8 : b);
             if (OP == kDw) {
-                if (j >= end)
+                if (i * groups >= end)
                     return false;
-            } else if (j >= nw8) {
-                // the short ends: i0 whole tiles of this workgroup lie behind it
-                const int idle = groups - nw8 % groups, i0 = nw8 / groups + (b < nw8 % groups);
-                const int turn = i - i0;  // of this workgroup's ends
-                j = nw8 + (b < groups - idle ? 2 * idle + turn * groups + b
-                           : turn < 2        ? turn * idle + b - (groups - idle)
-                                             : 2 * idle + (turn - 2) * groups + b);
                 if (j >= end)
-                    return false;
-            }
-            if (OP == kDw) {
-                const int id = xcd_order(j % nw8, nw);
+                    continue;
+                const int at = holder(upto, j), entry = static_cast<int>(uniform(second[at]));
+                const int before = at ? static_cast<int>(uniform(upto[at - 1])) : 0;
+                const int shift = 8 - (entry >> 16), h = 1 << shift, row_tiles = (a.rows + h - 1) >> shift;
+                const int id = xcd_order(j - before, row_tiles * col_tiles);
                 if (id < 0)
                     continue;
-                t.e = static_cast<int>(uniform(table[j / nw8]));
-                const TileAt at = grouped_order(id, row_tiles, col_tiles);
+                t.e = entry & 0xffff;
+                const TileAt tile = grouped_order(id, row_tiles, col_tiles);
                 const ExpertRun r = run(t.e);
-                t.first = at.row * ROWS;
-                t.n = min(ROWS, a.rows - t.first);
-                t.c0 = at.col * COLS;
+                t.first = static_cast<int>(uniform(tile.row * h));
+                t.n = min(h, a.rows - t.first);
+                t.c0 = static_cast<int>(uniform(tile.col * COLS));
                 t.r_first = static_cast<int>(uniform(r.first));
                 t.R = static_cast<int>(uniform(r.n));
             } else {
+                if (j >= nw8) {
+                    // the short ends: i0 whole tiles of this workgroup lie behind it
+                    const int idle = groups - nw8 % groups, i0 = nw8 / groups + (b < nw8 % groups);
+                    const int turn = i - i0;  // of this workgroup's ends
+                    j = nw8 + (b < groups - idle ? 2 * idle + turn * groups + b
+                               : turn < 2        ? turn * idle + b - (groups - idle)
+                                                 : 2 * idle + (turn - 2) * groups + b);
+                    if (j >= end)
+                        return false;
+                }
                 const bool end_tile = j >= nw8;
                 const int id = end_tile ? xcd_order(j - nw8, ne) : xcd_order(j, nw);
                 if (id < 0)
                     continue;
                 const TileAt at = grouped_order(id, end_tile ? ends : whole, col_tiles);
-                const int32_t *upto = table + (end_tile ? E : 0);
-                t.e = expert_of(upto, at.row);
+                const int32_t *list = end_tile ? second : upto;
+                t.e = holder(list, at.row);
                 const ExpertRun r = run(t.e);
-                const int before = t.e ? upto[t.e - 1] : 0;
-                const int in_run = end_tile ? r.n / ROWS * ROWS : (at.row - before) * ROWS;
+                const int before = t.e ? list[t.e - 1] : 0;
+                const int in_run = end_tile ? r.n / height * height : (at.row - before) * height;
                 t.first = static_cast<int>(uniform(r.first + in_run));
-                t.n = static_cast<int>(uniform(min(ROWS, r.n - in_run)));
+                t.n = static_cast<int>(uniform(min(height, r.n - in_run)));
                 t.c0 = at.col * COLS;
                 t.R = a.R;
             }
@@ -469,7 +518,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
     typedef Tile<TILE_COLS, OP == kForward, OP != kDw, GATED> T;
     constexpr int kCols = GATED ? T::kCols / 2 : T::kCols;  // output columns of a tile
     // one array: for two the compiler would wait for all loads before a read
-    typedef TileList<OP, T::kRows, kCols> List;
+    typedef TileList<OP, kCols> List;
     __shared__ __align__(1024) char shared[T::kLdsBytes + List::kBytes];
     MOE_LDS char *lds = (MOE_LDS char *)shared;
     List list;
@@ -551,7 +600,7 @@ int64_t tiles(int64_t n, int t) { return (n + t - 1) / t; }
 // Workgroups of a call of at most n tiles: one for each of the card's 256
 // CUs, whose LDS it fills, each with a list of tiles.  (Each of the two lists
 // is a whole number for each XCD: spare entries.)
-dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < 256 ? n + 14 : 256)); }
+dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < kCus ? (n + 14) / 8 * 8 : kCus)); }
 
 // Whether tiles of 128 columns serve a call of at most `n` tiles of 256
 // better: they cost 0.72 of one (K = N = 2048: 38 us against 51), so they do
@@ -559,12 +608,13 @@ dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < 256 ? n + 
 // 51; 4352 rows, 136 tiles: 64 against 51).
 bool narrow(int64_t n) { return n <= 128; }
 
-#define MOE_EXPERT(OP, GATED, ROW_TILES, COLS)                                                 \
+// CUT: the most tiles that a row tile may become.
+#define MOE_EXPERT(OP, GATED, ROW_TILES, CUT, COLS)                                            \
     if (narrow((ROW_TILES) * tiles(COLS, GATED ? 128 : 256)))                                   \
-        expert_kernel<OP, GATED, 128><<<grid_for((ROW_TILES) * tiles(COLS, GATED ? 64 : 128)),  \
+        expert_kernel<OP, GATED, 128><<<grid_for((ROW_TILES) * CUT * tiles(COLS, GATED ? 64 : 128)),  \
                                         64 * kTileWaves, 0, stream>>>(a);                       \
     else                                                                                       \
-        expert_kernel<OP, GATED, 256><<<grid_for((ROW_TILES) * tiles(COLS, GATED ? 128 : 256)), \
+        expert_kernel<OP, GATED, 256><<<grid_for((ROW_TILES) * CUT * tiles(COLS, GATED ? 128 : 256)), \
                                         64 * kTileWaves, 0, stream>>>(a)
 
 }  // namespace
@@ -578,15 +628,15 @@ hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const voi
     a.p = static_cast<const uint16_t *>(w);
     a.q = static_cast<const uint16_t *>(x);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = K, a.C = N;
-    a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
+    a.height = 256, a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
     a.out = out, a.preact = static_cast<uint16_t *>(preact);
     if (few_rows_pay(act, E, max_rows, K, N))
         return launch_expert_few(x, offsets, w, bias, act, residual, E, max_rows, K, N, out, preact, stream);
     const int64_t rt = max_row_tiles(max_rows, E, 256);
     if (act == MOE_ACT_SWIGLU) {
-        MOE_EXPERT(kForward, true, rt, N);
+        MOE_EXPERT(kForward, true, rt, 1, N);
     } else {
-        MOE_EXPERT(kForward, false, rt, N);
+        MOE_EXPERT(kForward, false, rt, 1, N);
     }
     return hipGetLastError();
 }
@@ -599,9 +649,9 @@ hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const
     a.p = static_cast<const uint16_t *>(w);
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = N, a.C = K;
-    a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
+    a.height = 256, a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
     const int64_t rt = max_row_tiles(max_rows, E, 256);
-    MOE_EXPERT(kDx, false, rt, K);
+    MOE_EXPERT(kDx, false, rt, 1, K);
     return hipGetLastError();
 }
 
@@ -614,7 +664,7 @@ hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t 
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.C = K, a.rows = N;
     a.out = dw, a.db = db, a.flags = flags;
-    MOE_EXPERT(kDw, false, E * tiles(N, 256), K);
+    MOE_EXPERT(kDw, false, E * tiles(N, 256), 4, K);
     return hipGetLastError();
 }
 
