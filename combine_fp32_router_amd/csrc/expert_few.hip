@@ -225,22 +225,23 @@ static int few_height(int E, int64_t max_rows)
 }
 
 // Estimates in us.  Here: the weights from memory at 6.2 TB/s, the rows once
-// for every 16 columns from L2 at 17 TB/s, and 5.  The tiles of 256 x 256: 8
-// for each round of 256 of them and 0.75 for 64 of K, or the weights if that is
-// longer.  Measured (here / tiles): 1 token of 8 experts above 78 / 101; 64
-// rows of 1 expert, K = N = 4096 11 / 47; 256 rows of it 38 / 78; 128 rows of
-// each of 8, K = 2048, N = 768 gated 28 / 40; 64 rows of each of 8, K = 7168,
-// N = 2048 gated 124 / 112; 2 rows of each of 64, K = 1024, N = 4096 107 / 94.
+// for every 16 columns at 17 TB/s, or 6.2 where they are more than the L2s hold,
+// and 5.  The tiles: 8 for each round of them and 0.75 for 64 of K, or the
+// weights if that is longer.  Measured (here / tiles): 1 token of 8 experts above
+// 78 / 101; 64 rows of 1 expert, K = N = 4096 11 / 47; 256 rows of it 38 / 78;
+// 128 rows of each of 8, K = 2048, N = 768 gated 28 / 40; 64 rows of each of 8,
+// K = 7168, N = 2048 gated 124 / 112; 2 rows of each of 64, K = 1024, N = 4096
+// 107 / 94.
 bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N)
 {
     const int wide = act == MOE_ACT_SWIGLU ? 2 : 1;
     const int64_t live = max_rows < E ? max_rows : E;
     if (!grid_fits(max_row_tiles(max_rows, E, few_height(E, max_rows)) * (N / 16), 64 * kWaves))
         return false;
-    const double weights = 2.0 * live * wide * N * K / 6.2e6;
-    const double here = weights + (N / 16) * 2.0 * max_rows * K / 17e6 + 5;
-    const int64_t tiles = max_row_tiles(max_rows, E, 256) * ((wide * N + 255) / 256);
-    const double there = ((tiles + 255) / 256) * (8 + K / 64 * 0.75);
+    const double weights = 2.0 * live * wide * N * K / 6.2e6, rows = 2.0 * max_rows * K;
+    const double here = weights + (N / 16) * rows / (rows > 32e6 ? 6.2e6 : 17e6) + 5;
+    const TileShape shape = tile_shape(E, max_rows, N, 128 / wide);
+    const double there = ((shape.tiles + kCus - 1) / kCus) * (8 + K / 64 * 0.0075 * shape.percent);
     return here < (there > weights ? there : weights);
 }
 

@@ -18,8 +18,7 @@ namespace {
 
 enum Op { kForward, kDx, kDw };
 
-constexpr int kCus = 256;           // of the card
-constexpr float kCutAbove = 1.4f;  // (TileList)
+constexpr float kCutAbove = 1.7f;  // (TileList)
 
 struct Args {
     const uint16_t *p, *q;  // operands as above
@@ -595,27 +594,16 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
     }
 }
 
-int64_t tiles(int64_t n, int t) { return (n + t - 1) / t; }
-
 // Workgroups of a call of at most n tiles: one for each of the card's 256
 // CUs, whose LDS it fills, each with a list of tiles.  (Each of the two lists
 // is a whole number for each XCD: spare entries.)
 dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < kCus ? (n + 14) / 8 * 8 : kCus)); }
 
-// Whether tiles of 128 columns serve a call of at most `n` tiles of 256
-// better: they cost 0.72 of one (K = N = 2048: 38 us against 51), so they do
-// while all of them fit the card at once (4096 rows, 128 tiles: 38 us against
-// 51; 4352 rows, 136 tiles: 64 against 51).
-bool narrow(int64_t n) { return n <= 128; }
-
-// CUT: the most tiles that a row tile may become.
-#define MOE_EXPERT(OP, GATED, ROW_TILES, CUT, COLS)                                            \
-    if (narrow((ROW_TILES) * tiles(COLS, GATED ? 128 : 256)))                                   \
-        expert_kernel<OP, GATED, 128><<<grid_for((ROW_TILES) * CUT * tiles(COLS, GATED ? 64 : 128)),  \
-                                        64 * kTileWaves, 0, stream>>>(a);                       \
+#define MOE_EXPERT(OP, GATED, COLS, TILES)                                                     \
+    if ((COLS) == 128)                                                                         \
+        expert_kernel<OP, GATED, 128><<<grid_for(TILES), 64 * kTileWaves, 0, stream>>>(a);     \
     else                                                                                       \
-        expert_kernel<OP, GATED, 256><<<grid_for((ROW_TILES) * CUT * tiles(COLS, GATED ? 128 : 256)), \
-                                        64 * kTileWaves, 0, stream>>>(a)
+        expert_kernel<OP, GATED, 256><<<grid_for(TILES), 64 * kTileWaves, 0, stream>>>(a)
 
 }  // namespace
 
@@ -628,15 +616,16 @@ hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const voi
     a.p = static_cast<const uint16_t *>(w);
     a.q = static_cast<const uint16_t *>(x);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = K, a.C = N;
-    a.height = 256, a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
+    a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
     a.out = out, a.preact = static_cast<uint16_t *>(preact);
     if (few_rows_pay(act, E, max_rows, K, N))
         return launch_expert_few(x, offsets, w, bias, act, residual, E, max_rows, K, N, out, preact, stream);
-    const int64_t rt = max_row_tiles(max_rows, E, 256);
+    const TileShape shape = tile_shape(E, max_rows, N, act == MOE_ACT_SWIGLU ? 64 : 128);
+    a.height = shape.rows;
     if (act == MOE_ACT_SWIGLU) {
-        MOE_EXPERT(kForward, true, rt, 1, N);
+        MOE_EXPERT(kForward, true, shape.cols, shape.tiles);
     } else {
-        MOE_EXPERT(kForward, false, rt, 1, N);
+        MOE_EXPERT(kForward, false, shape.cols, shape.tiles);
     }
     return hipGetLastError();
 }
@@ -649,9 +638,10 @@ hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const
     a.p = static_cast<const uint16_t *>(w);
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = N, a.C = K;
-    a.height = 256, a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
-    const int64_t rt = max_row_tiles(max_rows, E, 256);
-    MOE_EXPERT(kDx, false, rt, 1, K);
+    a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
+    const TileShape shape = tile_shape(E, max_rows, K, 128);
+    a.height = shape.rows;
+    MOE_EXPERT(kDx, false, shape.cols, shape.tiles);
     return hipGetLastError();
 }
 
@@ -664,7 +654,8 @@ hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t 
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.C = K, a.rows = N;
     a.out = dw, a.db = db, a.flags = flags;
-    MOE_EXPERT(kDw, false, E * tiles(N, 256), 4, K);
+    const int64_t n = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);  // cut into up to 4 each
+    MOE_EXPERT(kDw, false, 2 * n <= kCus ? 128 : 256, 8 * n);
     return hipGetLastError();
 }
 

@@ -139,6 +139,35 @@ inline int64_t max_row_tiles(int64_t max_rows, int E, int height)
     return (max_rows - live) / height + live;
 }
 
+constexpr int kCus = 256;  // of the card
+
+// Rows and columns of the tiles of a product whose outputs have C columns,
+// `unit` of which make 128 of a tile.  256 x 256 has the best rate; smaller ones
+// serve a call that all of them fit the card at once, where larger ones would
+// leave more of it idle.  Cost in percent of 256 x 256's, as measured: 72 with
+// half the columns (K = N = 2048, 4096 rows: 38 us against 51; 4352 rows, more
+// than fit: 64 against 51), 49 and 38 with half or a quarter of the rows too
+// (K = N = 1024, 2048 rows: 11.9 us against 20.7; 8192 rows, K = 16384, N =
+// 256: 121 against 218).
+struct TileShape {
+    int rows, cols, percent;
+    int64_t tiles;
+};
+inline TileShape tile_shape(int E, int64_t max_rows, int C, int unit)
+{
+    const TileShape shapes[6] = {{64, 128, 38, 0},  {64, 256, 44, 0},  {128, 128, 49, 0},
+                                 {128, 256, 63, 0}, {256, 128, 72, 0}, {256, 256, 100, 0}};
+    TileShape s{};
+    for (const TileShape &each : shapes) {
+        s = each;
+        const int cols = s.cols / 128 * unit;
+        s.tiles = max_row_tiles(max_rows, E, s.rows) * ((C + cols - 1) / cols);
+        if (s.tiles <= kCus)
+            break;
+    }
+    return s;
+}
+
 // Threads per block and 16-byte vectors per thread covering one row of
 // `vecs` 16-byte vectors with one block (<= 1024 threads, a whole number of
 // 64-lane waves): one vector per thread up to 1024 vectors, then 2, 4, 8.

@@ -84,6 +84,42 @@ def test_tiled_reduced_lengths(K):
     check_product(EDGES, K, 2064, NONE, False, False, False, seed=K)
 
 
+def tile_shape(lengths, rows, columns):
+    """The tiles (rows, columns) that a call of these outputs takes: the smallest
+    of which at most 256 come out."""
+    live = min(rows, len(lengths))
+    for h, c in ((64, 128), (64, 256), (128, 128), (128, 256), (256, 128)):
+        if ((rows - live) // h + live) * -(-columns // c) <= 256:
+            return h, c
+    return 256, 256
+
+
+# runs, columns (gate and up ones both), the tiles they take
+SHAPES = [(EDGES, 368, (64, 128)), (EDGES, 752, (64, 256)), ([5000, 0, 130, 140], 640, (128, 128)),
+          (EDGES, 1248, (128, 256)), ([12000, 0, 65, 1], 640, (256, 128)), (EDGES, 2064, (256, 256)),
+          ([5000, 1, 129, 128], 640, (128, 128)), ([77] * 40, 256, (64, 128)), ([0, 8000, 1, 200, 63], 1152, (256, 256))]
+
+
+@pytest.mark.parametrize("lengths,columns,shape", SHAPES, ids=[f"r{sum(s[0])}N{s[1]}" for s in SHAPES])
+def test_every_tile_shape(lengths, columns, shape):
+    rows = sum(lengths)
+    assert tile_shape(lengths, rows, columns) == shape
+    check_product(lengths, 1040, columns, SILU, True, True, True, spare=0)
+    check_product(lengths, 1040, columns // 32 * 16, SWIGLU, True, False, True, spare=0)
+    check_dx(lengths, columns, 528, GELU, spare=0)
+    check_dx(lengths, columns, 272, SWIGLU, spare=0)
+
+
+# few tiles (cut to 64 rows), some (to 128), many; and more runs than are ordered
+CUTS = [([900], 272, 528), ([1500], 2560, 2560), ([0, 40, 1700, 3, 64], 1040, 1296), ([200, 300, 1000], 2064, 1040),
+        ([65] * 70, 144, 272), ([700], 4112, 4112)]
+
+
+@pytest.mark.parametrize("lengths,K,N", CUTS, ids=[f"E{len(s[0])}r{sum(s[0])}K{s[1]}N{s[2]}" for s in CUTS])
+def test_cut_tiles_of_dw(lengths, K, N):
+    test_dw(lengths, K, N, NONE)
+
+
 def test_tiled_runs_are_cut_and_nan_stays():
     check_product(EDGES, 144, 2064, SILU, True, True, True, rows=3333)
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -155,8 +191,12 @@ GRADIENTS = [
 
 @pytest.mark.parametrize("lengths,K,N,act", GRADIENTS, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}a{c[3]}" for c in GRADIENTS])
 def test_dx(lengths, K, N, act):
+    check_dx(lengths, K, N, act)
+
+
+def check_dx(lengths, K, N, act, spare=2):
     g = torch.Generator(device="cuda").manual_seed(7)
-    E, wide, rows = len(lengths), 2 if act == SWIGLU else 1, sum(lengths) + 2
+    E, wide, rows = len(lengths), 2 if act == SWIGLU else 1, sum(lengths) + spare
     dy, w = normal(g, rows, N), normal(g, E, N, K, scale=K ** -0.5)
     z = normal(g, rows, wide * K, scale=2.0) if act else None
     dx = torch.full((rows, wide * K), CANARY, dtype=torch.bfloat16, device="cuda")
