@@ -332,8 +332,11 @@ struct Work {
 //
 // forward, dx: tiles of `height` rows (256, 128 or 64, the host's choice), at
 // first those of more than half of it, which all cost the same, then the runs'
-// shorter ends; these go, two at a time, to the workgroups that the others'
-// last round leaves idle.
+// shorter ends.  The last round of whole tiles leaves workgroups idle: the
+// ends go to them, two at a time, or the round's tiles are cut to a half or a
+// quarter of their rows and dealt out together with the ends, if by the
+// tiles' costs that ends sooner (5000 rows, K = N = 4096, 320 tiles: 131 us
+// against 171; 10000 rows, K = N = 2048, also 320: 76 against 97).
 //
 // dw (TileList<kDw>): an expert's tiles cost what its run is long, and the
 // longest run's could outlast all others: up to 64 experts' are cut to 128 or 64
@@ -347,6 +350,7 @@ struct TileList {
     int32_t *second;  // [E] the same of the ends; dw: experts, those to come first first
     int E, height, whole, ends, col_tiles;
     int nw, nw8, ne, end;  // entries: whole tiles, rounded up, ends, all
+    int cut, full, parts;  // pieces that the last round's tiles are cut to, tiles before them, pieces
 
     __device__ __forceinline__ void build(const Args &a, int32_t *lds)
     {
@@ -383,8 +387,20 @@ struct TileList {
             whole = static_cast<int>(uniform(upto[E - 1]));
             ends = static_cast<int>(uniform(second[E - 1]));
             nw = whole * col_tiles;
-            nw8 = (nw + 7) / 8 * 8;
             ne = ends * col_tiles;
+            const int groups = gridDim.x, left = nw % groups;
+            full = nw - left;
+            cut = 1;
+            if (height == 256 && groups == kCus && left) {
+                auto rounds = [&](int n) { return (n + kCus - 1) / kCus; };
+                int least = 100 + rounds(max(ne - 2 * (groups - left), 0)) * 63;
+                if (rounds(2 * left + ne) * 63 < least)
+                    least = rounds(2 * left + ne) * 63, cut = 2;
+                if (rounds(4 * left + ne) * 50 < least)
+                    cut = 4;
+            }
+            parts = cut > 1 ? left * cut : 0;
+            nw8 = cut > 1 ? full + (parts + 7) / 8 * 8 : (nw + 7) / 8 * 8;
             end = nw8 + (ne + 7) / 8 * 8;
         }
     }
@@ -480,28 +496,39 @@ struct TileList {
                 t.r_first = static_cast<int>(uniform(r.first));
                 t.R = static_cast<int>(uniform(r.n));
             } else {
-                if (j >= nw8) {
+                if (j >= nw8 && cut == 1) {
                     // the short ends: i0 whole tiles of this workgroup lie behind it
                     const int idle = groups - nw8 % groups, i0 = nw8 / groups + (b < nw8 % groups);
                     const int turn = i - i0;  // of this workgroup's ends
                     j = nw8 + (b < groups - idle ? 2 * idle + turn * groups + b
                                : turn < 2        ? turn * idle + b - (groups - idle)
                                                  : 2 * idle + (turn - 2) * groups + b);
-                    if (j >= end)
-                        return false;
                 }
-                const bool end_tile = j >= nw8;
-                const int id = end_tile ? xcd_order(j - nw8, ne) : xcd_order(j, nw);
+                if (j >= end)
+                    return false;
+                const bool end_tile = j >= nw8, part = cut > 1 && j >= full && !end_tile;
+                int id = end_tile ? xcd_order(j - nw8, ne)
+                         : part   ? xcd_order(j - full, parts)
+                                  : xcd_order(j, cut > 1 ? full : nw);
                 if (id < 0)
                     continue;
+                int rows = height, skip = 0;  // of the tile, and in front of a piece of it
+                if (part) {
+                    rows = height / cut;
+                    skip = id % cut * rows;
+                    id = full + id / cut;
+                }
                 const TileAt at = grouped_order(id, end_tile ? ends : whole, col_tiles);
                 const int32_t *list = end_tile ? second : upto;
                 t.e = holder(list, at.row);
                 const ExpertRun r = run(t.e);
                 const int before = t.e ? list[t.e - 1] : 0;
-                const int in_run = end_tile ? r.n / height * height : (at.row - before) * height;
-                t.first = static_cast<int>(uniform(r.first + in_run));
-                t.n = static_cast<int>(uniform(min(height, r.n - in_run)));
+                const int in_run = static_cast<int>(
+                    uniform((end_tile ? r.n / height * height : (at.row - before) * height) + skip));
+                t.n = min(rows, static_cast<int>(uniform(r.n)) - in_run);
+                if (t.n <= 0)  // a piece behind its run
+                    continue;
+                t.first = static_cast<int>(uniform(r.first)) + in_run;
                 t.c0 = at.col * COLS;
                 t.R = a.R;
             }

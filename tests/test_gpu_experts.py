@@ -110,6 +110,16 @@ def test_every_tile_shape(lengths, columns, shape):
     check_dx(lengths, columns, 272, SWIGLU, spare=0)
 
 
+# 17 tiles of 256 columns: of 21 or 16 whole ones of 256 rows, 101 or 16 are the
+# last round's, which are cut to a half or a quarter; some pieces lie behind
+# their run's end
+@pytest.mark.parametrize("lengths", [[5000, 0, 200, 1], [3900, 150], [260, 3584, 140, 70]], ids=["halves", "quarters", "odd"])
+def test_last_round_in_pieces(lengths):
+    check_product(lengths, 144, 4112, SILU, True, True, True)
+    check_product(lengths, 144, 2064, SWIGLU, True, False, True)
+    check_dx(lengths, 4112, 144, GELU)
+
+
 # few tiles (cut to 64 rows), some (to 128), many; and more runs than are ordered
 CUTS = [([900], 272, 528), ([1500], 2560, 2560), ([0, 40, 1700, 3, 64], 1040, 1296), ([200, 300, 1000], 2064, 1040),
         ([65] * 70, 144, 272), ([700], 4112, 4112)]
