@@ -25,6 +25,8 @@
 namespace moe {
 namespace {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 template <int CTRL>
 __device__ __forceinline__ float dppf(float v)
 {
@@ -69,7 +71,7 @@ __device__ __forceinline__ int expert_of(int q, int sub)
 
 // A token's logits, -inf past E; all zero for a token that is not live
 // (whose memory is not read).
-template <int L, int NE, bool VEC>
+template <int L, int NE, bool VEC, bool LAST = false>
 __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, int sub, bool live,
                                          float (&v)[NE])
 {
@@ -77,9 +79,11 @@ __device__ __forceinline__ void load_row(const float *__restrict__ row, int E, i
 #pragma unroll
         for (int i = 0; i < NE / 4; ++i) {
             const int e = expert_of<L, VEC>(4 * i, sub);
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (live && e < E)
-                x = *reinterpret_cast<const float4 *>(row + e);
+            f32x4 x{};
+            if (live && e < E) {
+                const f32x4 *at = reinterpret_cast<const f32x4 *>(row + e);
+                x = LAST ? __builtin_nontemporal_load(at) : *at;
+            }
             const bool past = e >= E;
             v[4 * i + 0] = past ? -INFINITY : x.x;
             v[4 * i + 1] = past ? -INFINITY : x.y;
@@ -338,8 +342,12 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float *__restr
         out.live[s] = live;
 }
 
-// Block (x, s): tokens of segment s, two a group of lanes, whose loads and
-// sums run side by side.
+// Tokens of a segment, two a group of lanes, whose loads and sums run side by
+// side; the last ones first, for if the balance loss has just read the logits,
+// what the last-level cache still has of them is their end.  So that it stays
+// there, the gradient is written past it, and the logits are read for the last
+// time.  131072 tokens of 512 experts, both calls: 170 us, 192 front to back
+// with ordinary loads and stores; 131072 of 256: 97 and 112.
 constexpr int kGradTokens = 2;
 
 template <int L, int NE, bool VEC>
@@ -352,8 +360,8 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
     constexpr int G = 256 / L, kRow = L * NE;  // tokens at a time; experts a row has room for
     __shared__ __align__(16) float rows[G * kRow];
     const int sub = threadIdx.x % L, group = threadIdx.x / L;
-    const int64_t s = blockIdx.y, end = min(T, (s + 1) * seg);
-    const int64_t first = s * seg + static_cast<int64_t>(blockIdx.x) * (G * kGradTokens) + group;
+    const int64_t s = gridDim.y - 1 - blockIdx.y, end = min(T, (s + 1) * seg);
+    const int64_t first = s * seg + static_cast<int64_t>(gridDim.x - 1 - blockIdx.x) * (G * kGradTokens) + group;
     float d[kGradTokens][NE];
     bool live[kGradTokens];
     int e[kGradTokens];
@@ -363,7 +371,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
         const int64_t t = first + u * G;
         live[u] = t < end && (!mask || mask[t]);
         if (dloss)
-            load_row<L, NE, VEC>(logits + t * E, E, sub, live[u], d[u]);
+            load_row<L, NE, VEC, true>(logits + t * E, E, sub, live[u], d[u]);
         // lane j of the token holds slot j
         const bool slot = dw && sub < k && live[u];
         e[u] = slot ? idx[t * k + sub] : -1;
@@ -430,8 +438,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
             for (int i = 0; i < NE / 4; ++i) {
                 const int ee = expert_of<L, VEC>(4 * i, sub);
                 if (ee < E)
-                    *reinterpret_cast<float4 *>(out + ee) =
-                        make_float4(d[u][4 * i], d[u][4 * i + 1], d[u][4 * i + 2], d[u][4 * i + 3]);
+                    __builtin_nontemporal_store(
+                        f32x4{d[u][4 * i], d[u][4 * i + 1], d[u][4 * i + 2], d[u][4 * i + 3]},
+                        reinterpret_cast<f32x4 *>(out + ee));
             }
         } else {
 #pragma unroll
