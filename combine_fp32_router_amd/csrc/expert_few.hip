@@ -9,9 +9,9 @@
 // LDS, 16 weight rows by 128 bytes each two loads of eight whole lines, and
 // it waits for its oldest ones only; no barrier before the sums.
 // One token at 8 of 32 experts, K = 7168, N = 2048 gated (470 MB of weights):
-// 78 us, 6.0 TB/s, against 101 us of the 256-column tiles (128 of them for 256
-// CUs); loads straight into the MFMA's operands, each touching 16 lines of
-// which it uses half, took 89 us, rings of four and six chunks 80 and 82.
+// 78 us, 6.0 TB/s, against 80 us of the tiles of 64 x 128; loads straight into
+// the MFMA's operands, each touching 16 lines of which it uses half, took 89 us,
+// rings of four and six chunks 80 and 82.
 #include "expert_rows.hpp"
 #include "launch.hpp"
 
@@ -226,23 +226,27 @@ static int few_height(int E, int64_t max_rows)
 
 // Estimates in us.  Here: the weights from memory at 6.2 TB/s, the rows once
 // for every 16 columns at 17 TB/s, or 6.2 where they are more than the L2s hold,
-// and 5.  The tiles: 8 for each round of them and 0.75 for 64 of K, or the
-// weights if that is longer.  Measured (here / tiles): 1 token of 8 experts above
-// 78 / 101; 64 rows of 1 expert, K = N = 4096 11 / 47; 256 rows of it 38 / 78;
-// 128 rows of each of 8, K = 2048, N = 768 gated 28 / 40; 64 rows of each of 8,
-// K = 7168, N = 2048 gated 124 / 112; 2 rows of each of 64, K = 1024, N = 4096
-// 107 / 94.
+// 2, and 0.8 for each round of the workgroups that fit the card.  The tiles: 8
+// for each round of them and 0.75 for 64 of K, or the weights and 5 if that is
+// longer.  Measured (here / tiles): 1 token of 8 experts above 78 / 80; 64 rows
+// of 1 expert, K = N = 4096 11 / 30; 256 rows of it 37 / 28; 128 rows of each of
+// 8, K = 2048, N = 768 gated 27 / 23; 64 rows of each of 8, K = 7168, N = 2048
+// gated 126 / 113; 2 rows of each of 64, K = 1024, N = 4096 108 / 95; 1 row of each
+// of 8, K = 2048, N = 7168 52 / 37; 4 of each of 32, K = 2048, N = 1024 32 / 24.
 bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N)
 {
     const int wide = act == MOE_ACT_SWIGLU ? 2 : 1;
     const int64_t live = max_rows < E ? max_rows : E;
-    if (!grid_fits(max_row_tiles(max_rows, E, few_height(E, max_rows)) * (N / 16), 64 * kWaves))
+    const int height = few_height(E, max_rows);
+    const int64_t groups = max_row_tiles(max_rows, E, height) * (N / 16);
+    if (!grid_fits(groups, 64 * kWaves))
         return false;
+    const int fit = kCus * (163840 / (kWaves * kDepth * 2048 * (wide + height / 16)));  // by their LDS
     const double weights = 2.0 * live * wide * N * K / 6.2e6, rows = 2.0 * max_rows * K;
-    const double here = weights + (N / 16) * rows / (rows > 32e6 ? 6.2e6 : 17e6) + 5;
+    const double here = weights + (N / 16) * rows / (rows > 32e6 ? 6.2e6 : 17e6) + 2 + 0.8 * ((groups + fit - 1) / fit);
     const TileShape shape = tile_shape(E, max_rows, N, 128 / wide);
     const double there = ((shape.tiles + kCus - 1) / kCus) * (8 + K / 64 * 0.0075 * shape.percent);
-    return here < (there > weights ? there : weights);
+    return here < (there > weights + 5 ? there : weights + 5);
 }
 
 hipError_t launch_expert_few(const void *x, const int32_t *offsets, const void *w, const float *bias, int act,
