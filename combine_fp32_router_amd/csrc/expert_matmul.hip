@@ -333,10 +333,12 @@ struct Work {
 // forward, dx: tiles of `height` rows (256, 128 or 64, the host's choice), at
 // first those of more than half of it, which all cost the same, then the runs'
 // shorter ends.  The last round of whole tiles leaves workgroups idle: the
-// ends go to them, two at a time, or the round's tiles are cut to a half or a
+// ends go to them, 64 rows to each if they suffice, else whole and two at a
+// time, or the round's tiles are cut to a half or a
 // quarter of their rows and dealt out together with the ends, if by the
 // tiles' costs that ends sooner (5000 rows, K = N = 4096, 320 tiles: 131 us
-// against 171; 10000 rows, K = N = 2048, also 320: 76 against 97).
+// against 171; 10000 rows, K = N = 2048, also 320: 76 against 97.  Ends of 33, 109,
+// 25 and 52 rows behind 512 tiles: 432 us with the 109 cut, 455 without).
 //
 // dw (TileList<kDw>): an expert's tiles cost what its run is long, and the
 // longest run's could outlast all others: up to 64 experts' are cut to 128 or 64
@@ -344,11 +346,11 @@ struct Work {
 // their cost, and every second round is dealt out backwards.
 template <Op OP, int COLS>
 struct TileList {
-    static constexpr int kBytes = 4 * (3 * MOE_MAX_EXPERTS + 1);
+    static constexpr int kBytes = 4 * (3 * MOE_MAX_EXPERTS + 2);
     int32_t *starts;  // [E + 1] first rows of the runs
     int32_t *upto;    // [E] entries up to an expert's last (of whole tiles; dw: in the order of `experts`)
-    int32_t *second;  // [E] the same of the ends; dw: experts, those to come first first
-    int E, height, whole, ends, col_tiles;
+    int32_t *second;  // [E] the same of the ends, then their rows; dw: experts, those to come first first
+    int E, height, end_rows, whole, ends, col_tiles;
     int nw, nw8, ne, end;  // entries: whole tiles, rounded up, ends, all
     int cut, full, parts;  // pieces that the last round's tiles are cut to, tiles before them, pieces
 
@@ -369,16 +371,16 @@ struct TileList {
         if (OP == kDw) {
             if (w == 0)
                 order(a);
-        } else if (w < 2) {
-            int before = 0;
-            for (int e0 = 0; e0 < E; e0 += kWave) {
-                const int e = e0 + lane, n = e < E ? run(e).n : 0;
-                const int end_rows = short_end(n);
-                const int sum = before + wave_inclusive_scan(w == 0 ? (n + height - 1) / height - end_rows : end_rows);
-                if (e < E)
-                    (w == 0 ? upto : second)[e] = sum;
-                before = lane_value(sum, kWave - 1);
-            }
+        } else if (w == 0) {
+            const int all = count(upto, [&](int n) { return (n + height - 1) / height - short_end(n); });
+            const int idle = static_cast<int>(gridDim.x) - all * col_tiles % static_cast<int>(gridDim.x);
+            end_rows = height / 2;
+            if (count(second, [&](int n) { return end_tiles(n, 64); }) * col_tiles <= idle)
+                end_rows = 64;
+            else
+                count(second, [&](int n) { return short_end(n); });
+            if (lane == 0)
+                second[E] = end_rows;
         }
         __syncthreads();
         if (OP == kDw) {
@@ -386,6 +388,7 @@ struct TileList {
         } else {
             whole = static_cast<int>(uniform(upto[E - 1]));
             ends = static_cast<int>(uniform(second[E - 1]));
+            end_rows = static_cast<int>(uniform(second[E]));
             nw = whole * col_tiles;
             ne = ends * col_tiles;
             const int groups = gridDim.x, left = nw % groups;
@@ -411,10 +414,28 @@ struct TileList {
         return {first, max(starts[e + 1] - first, 0)};
     }
 
+    // Writes the experts' counts, added up; the sum of all.
+    template <typename F>
+    __device__ __forceinline__ int count(int32_t *list, F of) const
+    {
+        int before = 0;
+        for (int e0 = 0; e0 < E; e0 += kWave) {
+            const int e = e0 + lane_id(), sum = before + wave_inclusive_scan(e < E ? of(run(e).n) : 0);
+            if (e < E)
+                list[e] = sum;
+            before = static_cast<int>(lane_value(sum, kWave - 1));
+        }
+        return before;
+    }
+
     // Whether the run's last tile is one of the ends.
     __device__ __forceinline__ int short_end(int n) const
     {
         return height > 64 && n % height > 0 && n % height <= height / 2;
+    }
+    __device__ __forceinline__ int end_tiles(int n, int rows) const
+    {
+        return short_end(n) ? (n % height + rows - 1) / rows : 0;
     }
 
     // dw.  Cost of a tile of 256 >> cut rows, in 1/16 of 64 r of a tile of 256:
@@ -523,8 +544,9 @@ struct TileList {
                 t.e = holder(list, at.row);
                 const ExpertRun r = run(t.e);
                 const int before = t.e ? list[t.e - 1] : 0;
-                const int in_run = static_cast<int>(
-                    uniform((end_tile ? r.n / height * height : (at.row - before) * height) + skip));
+                if (end_tile)
+                    rows = end_rows, skip = r.n / height * height;
+                const int in_run = static_cast<int>(uniform((at.row - before) * (end_tile ? rows : height) + skip));
                 t.n = min(rows, static_cast<int>(uniform(r.n)) - in_run);
                 if (t.n <= 0)  // a piece behind its run
                     continue;
