@@ -32,12 +32,26 @@ library; this module allocates (torch) and orders launches.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import binding as B
 from . import harness as HN
 from .driver import KernelTimer, chunk_capacity, chunk_ranges
 from .experts import ExpertGrads, ExpertMLP
+
+
+def _group_device(call):
+    """`call` with the group's device current: a null stream is its own."""
+    @functools.wraps(call)
+    def on_device(self, *args, **kwargs):
+        if self.device.type != "cuda":  # refused further in
+            return call(self, *args, **kwargs)
+        with torch.cuda.device(self.device):
+            return call(self, *args, **kwargs)
+
+    return on_device
 
 
 class EPGroup:
@@ -110,6 +124,7 @@ class EPGroup:
                                self.max_rows, self.H, quant, self.src_offsets, self.E, self.R,
                                self.rl, reverse, st)
 
+    @_group_device
     def run(self, logits: torch.Tensor, x: torch.Tensor, out: torch.Tensor, quant: int = 0,
             capacity_factor=None, timer: KernelTimer | None = None,
             balance: B.Balance | None = None, token_mask: torch.Tensor | None = None):
@@ -122,7 +137,7 @@ class EPGroup:
         st = torch.cuda.current_stream(self.device)
         M = self.max_rows
         timed = self._timed(timer, st)
-        timed("route", lambda: B.moe_route_topk(logits, k, self.idx, self.w, st))
+        timed("route", lambda: B.moe_route_topk(logits, k, self.idx[:T], self.w[:T], st))
         if balance is not None:
             timed("balance", lambda: B.moe_balance_loss(logits, self.idx[:T], token_mask, balance,
                                                         st))
@@ -183,8 +198,6 @@ class EPGroup:
     def _run_experts(self, quant, timed, st):
         """Regroup to bf16, the experts, and ungroup to the payload's format."""
         H, M, rl = self.H, self.max_rows, self.rl
-        if M == 0:
-            return
         x, y = self.expert_in, self.expert_out
         if quant == B.MOE_QUANT_BF16:
             timed("regroup", lambda: B.moe_recv_regroup(self.recv, None, M, H, quant, rl.group_src,
@@ -200,6 +213,7 @@ class EPGroup:
             timed("ungroup", lambda: B.moe_dispatch_pack(y, M, H, 1, rl.group_src, quant,
                                                          self.recv, self.recv_scales, st))
 
+    @_group_device
     def backward(self, d_out: torch.Tensor, d_x: torch.Tensor | None, d_logits: torch.Tensor,
                  grads: ExpertGrads | None = None, d_loss: torch.Tensor | None = None,
                  accumulate: bool = False, timer: KernelTimer | None = None):
@@ -231,7 +245,7 @@ class EPGroup:
                     self.d_send[s * so:(s + 1) * so], self.d_w[t0:t1], st))
         timed("route_grad", lambda: B.moe_route_grad(
             logits, self.idx[:T], self.w[:T], self.d_w[:T], mask, d_loss, balance, d_logits, st))
-        if M == 0 or (d_x is None and grads is None):
+        if d_x is None and grads is None:
             return
         timed("exchange", lambda: self._exchange(self.d_send, None, self.d_recv, None, 0, False,
                                                  st))

@@ -135,7 +135,7 @@ def make(T, H, I, E, k, Rn, a, quant, biases, masked, seed=0):
     def rand(*s):
         return torch.randn(*s, generator=g, device="cuda")
 
-    x, size = exact_rows(T, H, quant, g)
+    x, size = exact_rows(T, H, quant, g) if T else (torch.empty(0, H, dtype=torch.bfloat16, device="cuda"), 1.0)
     wide = 2 if a == B.MOE_ACT_SWIGLU else 1
     w_up = (rand(E, wide * I, H) / (size * H ** 0.5)).bfloat16()
     w_down = (rand(E, H, I) / I ** 0.5).bfloat16()
@@ -287,3 +287,17 @@ def test_accumulating_and_partial_gradients():
     assert torch.equal(d_x, d_x2)
     for p, q in zip(one, two):
         assert torch.equal(2 * p, q)
+
+
+def test_no_tokens():
+    """Nothing to do but zero gradients."""
+    grp, mlp, x, logits, _, d_out = make(0, 32, 16, 4, 2, 2, B.MOE_ACT_SWIGLU, 0, True, 0.0)
+    bal = B.alloc_balance(0, 1, 4, 2, "cuda")
+    grads = mlp.alloc_grads()
+    for quant in (0, 1):
+        for g in grads:
+            g.fill_(3.0)
+        grp.run(logits, x, torch.empty_like(x), quant=quant, balance=bal)
+        grp.backward(d_out, torch.empty_like(x), torch.empty_like(logits), grads, torch.ones(1, device="cuda"))
+        torch.cuda.synchronize()
+        assert not any(g.any() for g in grads) and bal.loss.item() == 0 and not bal.expert_counts.any()
