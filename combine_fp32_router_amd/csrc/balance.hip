@@ -454,15 +454,18 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
 }
 
 // Blocks of a segment and their tokens: about 1024 blocks over the batch,
-// none under 32 tokens.
+// none under 32 tokens.  Short segments have one block each, and no join, if
+// they are many or of few logits (256 tokens of 8 experts: 4.4 us; 16 segments of
+// 256 tokens of 256: 10.3, 11.7 with a join; but five of 235 tokens of 995: 57, 19
+// with a join).
 struct BalanceTiling {
     int tpb, blocks;
 };
-BalanceTiling balance_tiling(int64_t T, int64_t seg)
+BalanceTiling balance_tiling(int64_t T, int64_t seg, int E)
 {
     int64_t tpb = (T + 1023) / 1024;
     tpb = tpb < 32 ? 32 : (tpb + 15) / 16 * 16;
-    if (tpb > seg || seg <= 256)
+    if (tpb > seg || (seg <= 256 && (T >= (E <= 256 ? 16 : 128) * seg || seg * E <= 32768)))
         tpb = seg > 0 ? seg : 1;
     return {static_cast<int>(tpb), static_cast<int>(seg > 0 ? (seg + tpb - 1) / tpb : 1)};
 }
@@ -473,7 +476,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t balance_workspace_bytes(int64_t T, int64_t seg, int E)
 {
-    const size_t S = layout_chunks(T, seg), rows = S * balance_tiling(T, seg).blocks;
+    const size_t S = layout_chunks(T, seg), rows = S * balance_tiling(T, seg, E).blocks;
     return round256(rows * E * 4) * 2 + round256(rows * 4) + round256(S * 4);
 }
 
@@ -494,7 +497,7 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *idx, const ui
                                hipStream_t stream)
 {
     const int S = layout_chunks(T, seg);
-    const BalanceTiling bt = balance_tiling(T, seg);
+    const BalanceTiling bt = balance_tiling(T, seg, E);
     const size_t rows = static_cast<size_t>(S) * bt.blocks;
     char *ws = static_cast<char *>(workspace);
     float *psum = reinterpret_cast<float *>(ws);

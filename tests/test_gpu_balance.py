@@ -14,7 +14,8 @@ CASES = [(1, 1, 1, 1, 0.0), (1, 8, 2, 1, 0.0), (1, 8, 2, 1, 1.0), (17, 7, 7, 5, 
          (300, 16, 4, 300, 0.2), (257, 17, 3, 64, 0.0), (1000, 33, 16, 999, 0.5), (4096, 64, 8, 4096, 0.1),
          (70, 66, 2, 7, 0.4), (2049, 128, 8, 700, 0.9), (5000, 256, 8, 5000, 0.0), (777, 255, 8, 400, 0.1),
          (3001, 260, 8, 1500, 0.1), (512, 512, 1, 512, 0.0), (1200, 513, 16, 601, 0.2), (999, 1024, 16, 999, 0.0),
-         (640, 1023, 5, 64, 1.0), (20000, 64, 4, 1, 0.1)]
+         (640, 1023, 5, 64, 1.0), (20000, 64, 4, 1, 0.1),
+         (1172, 995, 15, 235, 0.9), (700, 1024, 4, 140, 0.0), (4000, 256, 8, 250, 0.1)]
 
 
 def draw(T, E, k, masked, seed=0):
