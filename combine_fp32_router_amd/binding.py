@@ -11,6 +11,7 @@ PyTorch fallback, and a missing library is an error.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -72,8 +73,10 @@ def load() -> ctypes.CDLL:
     lib.moe_route_grad.argtypes = [P, P, P, P, P, P, P, P, i64, i64, i32, i32, P, P]
     lib.moe_combine_grad.argtypes = [P, P, P, i32, P, P, i64, i32, i32, P, P, P]
     lib.moe_expert_matmul.argtypes = [P, P, P, P, i32, P, i32, i64, i32, i32, P, P, P]
-    lib.moe_expert_matmul_dx.argtypes = [P, P, P, i32, P, i32, i64, i32, i32, P, P]
-    lib.moe_expert_matmul_dw.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P, P]
+    lib.moe_expert_matmul_dx.argtypes = [P, P, P, i32, P, i32, i64, i32, i32, P, P,
+                                         ctypes.POINTER(sz), P]
+    lib.moe_expert_matmul_dw.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P, P,
+                                         ctypes.POINTER(sz), P]
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_row_bytes.argtypes = [i32, i32]
@@ -668,12 +671,51 @@ def moe_expert_matmul(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def expert_grad_workspace_bytes(name: str, E: int, rows: int, K: int, N: int) -> int:
+    """Workspace of moe_expert_matmul_dx or _dw (`name`) for these sizes."""
+    n, i, none = ctypes.c_size_t(0), ctypes.byref, None
+    if name == "moe_expert_matmul_dx":
+        status = load().moe_expert_matmul_dx(none, none, none, 0, none, E, rows, K, N, none, none,
+                                             i(n), none)
+    else:
+        status = load().moe_expert_matmul_dw(none, none, none, E, rows, K, N, 0, none, none, none,
+                                             i(n), none)
+    _check(name, status)
+    return int(n.value)
+
+
+def _call_sharing(name: str, stream, workspace: torch.Tensor | None, E: int, rows: int, K: int,
+                  N: int, like: torch.Tensor, *args) -> None:
+    """A gradient call with its workspace: `workspace`, or one allocated for the
+    call (torch's allocator, in the stream's order) when the sizes want one."""
+    need = expert_grad_workspace_bytes(name, E, rows, K, N)
+    if not need:
+        _call(name, stream, *args, None, None)
+        return
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        if stream is not None and workspace.is_cuda:
+            # allocated in the current stream's order, used in this one's
+            current = torch.cuda.current_stream(like.device)
+            handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+            if handle != current.cuda_stream:
+                user = (stream if isinstance(stream, torch.cuda.Stream) else
+                        torch.cuda.ExternalStream(handle, device=like.device) if handle else
+                        torch.cuda.default_stream(like.device))
+                user.wait_stream(current)
+                workspace.record_stream(user)
+    n = ctypes.c_size_t(workspace.numel() * workspace.element_size())
+    _call(name, stream, *args, workspace, ctypes.byref(n))
+
+
 def moe_expert_matmul_dx(dy: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor, act: int,
-                         preact: torch.Tensor | None, dx: torch.Tensor,
-                         stream=None) -> torch.Tensor:
+                         preact: torch.Tensor | None, dx: torch.Tensor, stream=None,
+                         workspace: torch.Tensor | None = None) -> torch.Tensor:
     """dy bf16 [rows, N], w bf16 [E, N, K] -> dx bf16 [rows, K], through the
     activation before the product when act says so (preact and dx [rows, K],
-    or [rows, 2K] for MOE_ACT_SWIGLU)."""
+    or [rows, 2K] for MOE_ACT_SWIGLU).  workspace: scratch of
+    expert_grad_workspace_bytes, else allocated where wanted."""
     _want_weights(w, offsets)
     E, N, K = w.shape
     rows, wide = dy.shape[0], 2 if act == MOE_ACT_SWIGLU else 1
@@ -686,16 +728,18 @@ def moe_expert_matmul_dx(dy: torch.Tensor, offsets: torch.Tensor, w: torch.Tenso
         raise ValueError("an activation's gradient needs preact")
     else:
         _want_bf16(preact, (rows, wide * K), "preact")
-    _call("moe_expert_matmul_dx", stream, dy, offsets, w, act, preact, E, rows, K, N, dx)
+    _call_sharing("moe_expert_matmul_dx", stream, workspace, E, rows, K, N, dy, dy, offsets, w, act,
+                  preact, E, rows, K, N, dx)
     return dx
 
 
 def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
                          dw: torch.Tensor, dbias: torch.Tensor | None = None,
-                         accumulate: bool = False, stream=None) -> torch.Tensor:
+                         accumulate: bool = False, stream=None,
+                         workspace: torch.Tensor | None = None) -> torch.Tensor:
     """dy bf16 [rows, N], x bf16 [rows, K] -> dw [E, N, K] (fp32, or bf16 by
     its dtype) and dbias fp32 [E, N]; accumulate adds to what they hold
-    (fp32 dw only)."""
+    (fp32 dw only).  workspace: as moe_expert_matmul_dx."""
     _want_weights(dw, offsets)
     E, N, K = dw.shape
     rows = dy.shape[0]
@@ -710,5 +754,6 @@ def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     flags = MOE_GRAD_FP32 if dw.dtype == torch.float32 else MOE_GRAD_BF16
     if accumulate:
         flags |= MOE_GRAD_ACCUMULATE
-    _call("moe_expert_matmul_dw", stream, dy, x, offsets, E, rows, K, N, flags, dw, dbias)
+    _call_sharing("moe_expert_matmul_dw", stream, workspace, E, rows, K, N, dy, dy, x, offsets, E,
+                  rows, K, N, flags, dw, dbias)
     return dw

@@ -496,41 +496,57 @@ int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, cons
 
 int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
                          const void *preact, int E, int64_t max_rows, int K, int N, void *dx,
-                         hipStream_t stream)
+                         void *workspace, size_t *workspace_bytes, hipStream_t stream)
 {
     if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK || !known_act(act) ||
         !product_tiles_fit(max_row_tiles(max_rows, E, 256), K))
         return MOE_ERR_SHAPE;
+    const size_t need = moe::dx_parts(E, max_rows, K, N).bytes;
+    if (!workspace && workspace_bytes) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
     if (max_rows == 0)
         return MOE_OK;
+    if (workspace && (!workspace_bytes || *workspace_bytes < need))
+        return MOE_ERR_WORKSPACE;
     if (!dy || !offsets || !w || !dx || (act != MOE_ACT_NONE && !preact))
         return MOE_ERR_NULL;
     if (!aligned(dy, 16) || !aligned(offsets, 4) || !aligned(w, 16) || !aligned(preact, 16) ||
-        !aligned(dx, 16))
+        !aligned(dx, 16) || !aligned(workspace, 256))
         return MOE_ERR_ALIGN;
     if (dx == dy || dx == w)
         return MOE_ERR_ALIAS;
     return hip_status(
-        moe::launch_expert_matmul_dx(dy, offsets, w, act, preact, E, max_rows, K, N, dx, stream));
+        moe::launch_expert_matmul_dx(dy, offsets, w, act, preact, E, max_rows, K, N, dx,
+                                     workspace, stream));
 }
 
 int moe_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
                          int64_t max_rows, int K, int N, int flags, void *dw, float *dbias,
-                         hipStream_t stream)
+                         void *workspace, size_t *workspace_bytes, hipStream_t stream)
 {
     if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK ||
         (flags != MOE_GRAD_FP32 && flags != MOE_GRAD_BF16 &&
          flags != (MOE_GRAD_FP32 | MOE_GRAD_ACCUMULATE)))
         return MOE_ERR_SHAPE;
+    const size_t need = moe::dw_parts(E, max_rows, K, N).bytes;
+    if (!workspace && workspace_bytes) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
+    if (workspace && (!workspace_bytes || *workspace_bytes < need))
+        return MOE_ERR_WORKSPACE;
     if (!offsets || !dw || (max_rows > 0 && (!dy || !x)))
         return MOE_ERR_NULL;
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(dw, 16) ||
-        !aligned(dbias, 16))
+        !aligned(dbias, 16) || !aligned(workspace, 256))
         return MOE_ERR_ALIGN;
     if (dw == dy || dw == x)
         return MOE_ERR_ALIAS;
     return hip_status(
-        moe::launch_expert_matmul_dw(dy, x, offsets, E, max_rows, K, N, flags, dw, dbias, stream));
+        moe::launch_expert_matmul_dw(dy, x, offsets, E, max_rows, K, N, flags, dw, dbias, workspace,
+                                     stream));
 }
 
 }  // extern "C"

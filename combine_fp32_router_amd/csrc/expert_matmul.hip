@@ -19,6 +19,7 @@ namespace {
 enum Op { kForward, kDx, kDw };
 
 constexpr float kCutAbove = 1.7f;  // (TileList)
+constexpr int kPartExperts = 256;   // (PartList)
 
 struct Args {
     const uint16_t *p, *q;  // operands as above
@@ -34,6 +35,10 @@ struct Args {
     int flags;
     int rows;               // dw: rows of the output (N)
     int height;             // forward, dx: rows of a tile
+    // dx, dw in parts: how many, their sums in the MFMA's layout, those of db
+    int parts, tiles;       // (tiles: the most that the workspace is for)
+    f32x4 *part;
+    float *part_db;
 };
 
 // Results leave 16 rows of a wave's columns at a time.  A lane's share is
@@ -643,6 +648,198 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
     }
 }
 
+// dx and dw of few outputs and a long reduced length: every tile, of 64 x 128, is
+// shared by up to `parts` workgroups, each of which takes a piece of the
+// length and leaves its sums, as its accumulators hold them, in the workspace; a
+// second kernel adds them in order and finishes the tile.  Two workgroups
+// share a CU (THIN).  dw of 16384 rows, 512 x 512: 32 us, 100 in whole tiles;
+// 8192 rows, 128 x 2048: 28 and 54; dx of 200 rows, 4096 -> 256: 21 and 30.
+template <Op OP>
+struct PartList {
+    static constexpr int kBytes = 4 * (2 * kPartExperts + 1);
+    int32_t *starts, *upto;  // as in TileList; dx
+    int E, tiles, col_tiles, row_tiles;
+
+    __device__ __forceinline__ void build(const Args &a, int32_t *lds)
+    {
+        E = a.E;
+        starts = lds;
+        upto = lds + E + 1;
+        col_tiles = (a.C + 127) / 128;
+        row_tiles = (a.rows + 63) / 64;  // dw
+        for (int e = threadIdx.x; e <= E; e += blockDim.x)
+            starts[e] = run_start(a.offsets, e, a.max_rows);
+        __syncthreads();
+        tiles = E * row_tiles * col_tiles;
+        if (OP == kDx) {
+            if (uniform(threadIdx.x / kWave) == 0) {
+                int before = 0;
+                for (int e0 = 0; e0 < E; e0 += kWave) {
+                    const int e = e0 + lane_id();
+                    const int sum = before + wave_inclusive_scan(e < E ? (run(e).n + 63) / 64 : 0);
+                    if (e < E)
+                        upto[e] = sum;
+                    before = lane_value(sum, kWave - 1);
+                }
+            }
+            __syncthreads();
+            tiles = min(static_cast<int>(uniform(upto[E - 1])) * col_tiles, a.tiles);
+        }
+    }
+    __device__ __forceinline__ ExpertRun run(int e) const
+    {
+        const int first = starts[e];
+        return {first, max(starts[e + 1] - first, 0)};
+    }
+    __device__ __forceinline__ ExpertRun uniform_run(int e) const
+    {
+        const ExpertRun r = run(e);
+        return {static_cast<int>(uniform(r.first)), static_cast<int>(uniform(r.n))};
+    }
+    __device__ __forceinline__ Work at(const Args &a, int tile) const
+    {
+        Work t;
+        t.c0 = tile % col_tiles * 128;
+        const int row = tile / col_tiles;
+        if (OP == kDx) {
+            t.e = 0;
+            for (int e0 = 0; e0 < E; e0 += kWave) {
+                const int e = e0 + lane_id();
+                t.e += __builtin_popcountll(__ballot(e < E && upto[e] <= row));
+            }
+            t.e = static_cast<int>(uniform(t.e));
+            const ExpertRun r = uniform_run(t.e);
+            const int in_run = (row - (t.e ? static_cast<int>(uniform(upto[t.e - 1])) : 0)) * 64;
+            t.first = r.first + in_run;
+            t.n = min(64, r.n - in_run);
+            t.R = a.R;
+        } else {
+            t.e = row / row_tiles;
+            const ExpertRun r = uniform_run(t.e);
+            t.first = row % row_tiles * 64;
+            t.n = min(64, a.rows - t.first);
+            t.r_first = r.first;
+            t.R = r.n;
+        }
+        return t;
+    }
+    // r of a tile's part
+    static __device__ __forceinline__ int share(const Args &a, int R)
+    {
+        return ((R + kStep - 1) / kStep + a.parts - 1) / a.parts * kStep;
+    }
+};
+
+template <Op OP>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void expert_part_kernel(Args a)
+{
+    typedef Tile<128, false, OP != kDw, false, true> T;
+    typedef PartList<OP> List;
+    __shared__ __align__(1024) char shared[T::kLdsBytes + List::kBytes];
+    MOE_LDS char *lds = (MOE_LDS char *)shared;
+    List list;
+    list.build(a, reinterpret_cast<int32_t *>(shared + T::kLdsBytes));
+    T t;
+    for (int j = blockIdx.x; j < list.tiles * a.parts; j += gridDim.x) {
+        const int tile = j / a.parts, part = j % a.parts;
+        const Work k = list.at(a, tile);
+        const int share = List::share(a, k.R), r0 = part * share;
+        if (r0 >= k.R)
+            continue;
+        t.R = min(share, k.R - r0);
+        if (OP == kDx) {
+            t.p.init(a.p + (static_cast<int64_t>(k.e) * a.R + r0) * a.C + k.c0, nullptr, a.C, min(128, a.C - k.c0));
+            t.q.init(a.q + static_cast<int64_t>(k.first) * a.R + r0, nullptr, a.R, k.n);
+        } else {
+            t.p.init(a.p + (static_cast<int64_t>(k.r_first) + r0) * a.C + k.c0, nullptr, a.C, min(128, a.C - k.c0));
+            t.q.init(a.q + (static_cast<int64_t>(k.r_first) + r0) * a.rows + k.first, nullptr, a.rows, k.n);
+        }
+        t.start_rows(k.n, lds);
+        t.clear();
+        const bool sums = OP == kDw && a.db && k.c0 == 0;
+        if (sums)
+            t.template run_rows<OP == kDw>(k.n, lds);
+        else
+            t.template run_rows<false>(k.n, lds);
+        f32x4 *to = a.part + ((static_cast<int64_t>(tile) * a.parts + part) * kTileWaves + t.wave()) * (2 * T::kFrags * kWave) +
+                    lane_id();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < T::kFrags; ++c)
+                to[(i * T::kFrags + c) * kWave] = T::read_acc(t.acc[c][0][i]);
+        if (sums && t.wave() % 2 == 0) {  // (as in expert_kernel)
+            const int lane = lane_id();
+            float sum[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sum[h] = t.sum[0][h] + __shfl_xor(t.sum[0][h], 16);
+                sum[h] += __shfl_xor(sum[h], 32);
+            }
+            if (lane < 32)
+                a.part_db[(static_cast<int64_t>(tile / list.col_tiles) * a.parts + part) * 64 + t.row0(0) + lane] =
+                    sum[lane / 16];
+        }
+    }
+}
+
+template <Op OP>
+__global__ __launch_bounds__(64 * kTileWaves) void expert_join_kernel(Args a)
+{
+    typedef Tile<128, false, OP != kDw, false, true> T;
+    typedef PartList<OP> List;
+    __shared__ __align__(1024) char shared[kTileWaves * T::kOutBytes + List::kBytes];
+    List list;
+    list.build(a, reinterpret_cast<int32_t *>(shared + kTileWaves * T::kOutBytes));
+    const T t{};
+    MOE_LDS char *place = (MOE_LDS char *)shared + t.wave() * T::kOutBytes;
+    for (int tile = blockIdx.x; tile < list.tiles; tile += gridDim.x) {
+        const Work k = list.at(a, tile);
+        const int share = List::share(a, k.R), live = k.R > 0 ? (k.R + share - 1) / share : 0;
+        const f32x4 *from = a.part + (static_cast<int64_t>(tile) * a.parts * kTileWaves + t.wave()) * (2 * T::kFrags * kWave) +
+                            lane_id();
+        if (OP == kDw && a.db && k.c0 == 0 && static_cast<int>(threadIdx.x) < k.n) {
+            float sum = 0.0f;
+            for (int p = 0; p < live; ++p)
+                sum += a.part_db[(static_cast<int64_t>(tile / list.col_tiles) * a.parts + p) * 64 + threadIdx.x];
+            float *db = a.db + static_cast<int64_t>(k.e) * a.rows + k.first + threadIdx.x;
+            *db = ((a.flags & MOE_GRAD_ACCUMULATE) ? *db : 0.0f) + sum;
+        }
+        const int c = k.c0 + t.col0(), inside = a.C - c;
+        auto finish = [&](auto &f) {
+#pragma unroll 1
+            for (int i = 0; i < 2 && t.row0(0) + 16 * i < k.n; ++i) {
+                f32x4 v[T::kFrags] = {};
+                for (int p = 0; p < live; ++p)
+#pragma unroll
+                    for (int b = 0; b < T::kFrags; ++b)
+                        v[b] += from[(p * kTileWaves * 2 + i) * T::kFrags * kWave + b * kWave];
+                f(t.row0(0) + 16 * i, t.row0(0) + 16, v);
+            }
+        };
+        if constexpr (OP == kDx) {
+            FinishDx<T::kFrags> f(a, place, k.first, k.n, c, inside, t.row0(0));
+            finish(f);
+        } else {
+            FinishDw<T::kFrags> f(a, place, static_cast<int64_t>(k.e) * a.rows + k.first, k.n, c, inside);
+            finish(f);
+        }
+    }
+}
+
+// In how many parts a tile's reduced length R is best taken (1: not at all): as
+// many as fill the card, of at least four steps of 64 each, where they save 20
+// steps or more of about 0.45 us, against the 8 us of the second kernel.
+int parts_of(int64_t tiles, int E, int64_t R)
+{
+    const int64_t steps = R / kStep;
+    if (tiles < 1 || tiles > kCus / 2 || E > kPartExperts)
+        return 1;
+    const int64_t n = steps / 4 < 2 * kCus / tiles ? steps / 4 : 2 * kCus / tiles;
+    return n >= 2 && steps - steps / n >= 20 ? static_cast<int>(n) : 1;
+}
+constexpr int64_t kPartBytes = 64 * 128 * 4, kPartDbBytes = 64 * 4;  // of a part of a tile, and of a row of tiles
+
 // Workgroups of a call of at most n tiles: one for each of the card's 256
 // CUs, whose LDS it fills, each with a list of tiles.  (Each of the two lists
 // is a whole number for each XCD: spare entries.)
@@ -679,15 +876,52 @@ hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const voi
     return hipGetLastError();
 }
 
+GradParts dx_parts(int E, int64_t max_rows, int K, int N)
+{
+    GradParts g{};
+    g.tiles = max_row_tiles(max_rows, E, 64) * ((K + 127) / 128);
+    g.parts = parts_of(g.tiles, E, N);
+    g.bytes = g.parts > 1 ? g.tiles * g.parts * kPartBytes : 0;
+    return g;
+}
+
+GradParts dw_parts(int E, int64_t max_rows, int K, int N)
+{
+    GradParts g{};
+    const int64_t rows = static_cast<int64_t>(E) * ((N + 63) / 64);
+    g.tiles = rows * ((K + 127) / 128);
+    g.parts = parts_of(g.tiles, E, max_rows / E);
+    g.bytes = g.parts > 1 ? g.parts * (g.tiles * kPartBytes + rows * kPartDbBytes) : 0;
+    return g;
+}
+
+template <Op OP>
+static hipError_t launch_parts(Args &a, const GradParts &g, void *workspace, hipStream_t stream)
+{
+    a.parts = g.parts, a.tiles = static_cast<int>(g.tiles);
+    a.part = static_cast<f32x4 *>(workspace);
+    a.part_db = reinterpret_cast<float *>(static_cast<char *>(workspace) + g.tiles * g.parts * kPartBytes);
+    const int64_t n = g.tiles * g.parts;
+    expert_part_kernel<OP><<<dim3(static_cast<unsigned>(n < 2 * kCus ? n : 2 * kCus)), 64 * kTileWaves, 0, stream>>>(a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return err;
+    expert_join_kernel<OP><<<dim3(static_cast<unsigned>(g.tiles)), 64 * kTileWaves, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
                                    const void *z, int E, int64_t max_rows, int K, int N, void *dx,
-                                   hipStream_t stream)
+                                   void *workspace, hipStream_t stream)
 {
     Args a{};
     a.p = static_cast<const uint16_t *>(w);
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = N, a.C = K;
     a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
+    const GradParts parts = dx_parts(E, max_rows, K, N);
+    if (workspace && parts.parts > 1)
+        return launch_parts<kDx>(a, parts, workspace, stream);
     const TileShape shape = tile_shape(E, max_rows, K, 128);
     a.height = shape.rows;
     MOE_EXPERT(kDx, false, shape.cols, shape.tiles);
@@ -696,13 +930,16 @@ hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const
 
 hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
                                    int64_t max_rows, int K, int N, int flags, void *dw, float *db,
-                                   hipStream_t stream)
+                                   void *workspace, hipStream_t stream)
 {
     Args a{};
     a.p = static_cast<const uint16_t *>(x);
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.C = K, a.rows = N;
     a.out = dw, a.db = db, a.flags = flags;
+    const GradParts parts = dw_parts(E, max_rows, K, N);
+    if (workspace && parts.parts > 1)
+        return launch_parts<kDw>(a, parts, workspace, stream);
     const int64_t n = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);  // cut into up to 4 each
     MOE_EXPERT(kDw, false, 2 * n <= kCus ? 128 : 256, 8 * n);
     return hipGetLastError();

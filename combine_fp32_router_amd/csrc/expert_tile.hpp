@@ -131,19 +131,21 @@ struct Operand {
 
 // Wave w has the columns' half w%2 and, of every block of 64 rows, the 32 from
 // 32 (w/2), so that a short tile's rows are shared evenly.
-template <int COLS, bool P_CONTIG, bool Q_CONTIG, bool GATED>
+// THIN: tiles of at most 64 rows only, in half the LDS and registers, so that
+// two workgroups share a CU.
+template <int COLS, bool P_CONTIG, bool Q_CONTIG, bool GATED, bool THIN = false>
 struct Tile {
-    static constexpr int kRows = 256, kCols = COLS;
-    static constexpr int kBlocks = 4;           // of 64 rows
+    static constexpr int kCols = COLS;
+    static constexpr int kBlocks = THIN ? 1 : 4;  // of 64 rows
     static constexpr int kFrags = kCols / 32;   // blocks of 16 columns of a wave
     typedef Operand<kCols, P_CONTIG, GATED> P;
     typedef Operand<64, Q_CONTIG, false> Q;  // an image for each block of 64 rows
     static constexpr int kStageBytes = P::kBytes + kBlocks * Q::kBytes;
-    static constexpr int kThinBytes = P::kBytes + 2 * Q::kBytes;  // of a stage of at most 128 rows
+    static constexpr int kThinBytes = P::kBytes + (THIN ? 1 : 2) * Q::kBytes;  // of a stage of at most 128 rows
     // two whole stages or three thin ones; the results pass through what the
     // first stages of the next tile leave free
     static constexpr int kOutBytes = 4096, kWhole = 2 * kStageBytes + kTileWaves * kOutBytes;
-    static constexpr int kLdsBytes = kWhole > 3 * kThinBytes ? kWhole : 3 * kThinBytes;
+    static constexpr int kLdsBytes = !THIN && kWhole > 3 * kThinBytes ? kWhole : 3 * kThinBytes;
     static_assert(kLdsBytes >= 2 * kThinBytes + kTileWaves * kOutBytes, "thin stages and results");
     __device__ __forceinline__ MOE_LDS char *out_place(MOE_LDS char *lds) const
     {
@@ -429,22 +431,26 @@ struct Tile {
     // The same for a tile of `rows` rows (start_rows: its first loads).
     __device__ __forceinline__ void start_rows(int rows, MOE_LDS char *lds) const
     {
-        if (rows > 128)
-            start(lds);
-        else if (rows > 64)
+        if (THIN || rows <= 64)
+            start_thin(lds, 1);
+        else if (rows <= 128)
             start_thin(lds, 2);
         else
-            start_thin(lds, 1);
+            start(lds);
     }
     template <bool SUMS>
     __device__ __forceinline__ void run_rows(int rows, MOE_LDS char *lds)
     {
-        if (rows > 128)
-            run<SUMS>(lds);
-        else if (rows > 64)
-            run_thin<2, SUMS>(lds);
-        else
+        if constexpr (THIN) {
             run_thin<1, SUMS>(lds);
+        } else {
+            if (rows > 128)
+                run<SUMS>(lds);
+            else if (rows > 64)
+                run_thin<2, SUMS>(lds);
+            else
+                run_thin<1, SUMS>(lds);
+        }
     }
 
     // The last products written, all loads and reads done, in all waves.

@@ -125,12 +125,20 @@ hipError_t launch_expert_few(const void *x, const int32_t *offsets, const void *
                              void *out, void *preact, hipStream_t stream);
 hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
                                    const void *z, int E, int64_t max_rows, int K, int N, void *dx,
-                                   hipStream_t stream);
+                                   void *workspace, hipStream_t stream);
 // The products walk lists of 256 x 256 tiles counted in 32 bits.
 inline bool product_tiles_fit(int64_t row_tiles, int cols) { return row_tiles * ((cols + 127) / 128) < (int64_t(1) << 30); }
 hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
                                    int64_t max_rows, int K, int N, int flags, void *dw, float *db,
-                                   hipStream_t stream);
+                                   void *workspace, hipStream_t stream);
+// In how many parts a gradient's reduced length is taken (1: whole), its
+// tiles then, and the workspace for them.
+struct GradParts {
+    int parts;
+    int64_t tiles, bytes;
+};
+GradParts dx_parts(int E, int64_t max_rows, int K, int N);
+GradParts dw_parts(int E, int64_t max_rows, int K, int N);
 
 // Most tiles of `height` rows that E runs of together max_rows rows can have.
 inline int64_t max_row_tiles(int64_t max_rows, int E, int height)

@@ -243,6 +243,80 @@ def test_dw(lengths, K, N, act):
     R.inside(dbias, before_b.double() + 1.5 + db, tb + 4 * R.U32 * (before_b.abs() + db.abs() + 1.5), "dbias accumulated")
 
 
+# few outputs and long sums, which several workgroups share
+LONG_DX = [([130, 0, 70], 144, 8192, SWIGLU), ([1], 16, 4096, NONE), ([1200], 48, 6384, SILU), ([64, 1, 63, 65, 200], 272, 2064, GELU),
+           ([3] * 20, 384, 16400, RELU)]
+LONG_DW = [([15000, 707], 192, 544, NONE), ([9, 30000, 0], 16, 16, NONE), ([8192], 1040, 272, NONE), ([0, 0, 9000], 128, 80, NONE)]
+
+
+def workspace_of(name, lengths, spare, K, N):
+    return B.expert_grad_workspace_bytes("moe_expert_matmul_" + name, len(lengths), sum(lengths) + spare, K, N)
+
+
+@pytest.mark.parametrize("lengths,K,N,act", LONG_DX, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}a{c[3]}" for c in LONG_DX])
+def test_dx_in_parts(lengths, K, N, act):
+    assert workspace_of("dx", lengths, 2, K, N) > 0
+    check_dx(lengths, K, N, act)
+
+
+@pytest.mark.parametrize("lengths,K,N,act", LONG_DW, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}" for c in LONG_DW])
+def test_dw_in_parts(lengths, K, N, act):
+    assert workspace_of("dw", lengths, 2, K, N) > 0
+    test_dw(lengths, K, N, act)
+
+
+def test_parts_with_workspaces_streams_and_a_graph():
+    """The same bits with a workspace of the caller's (full of NaN, and nothing
+    written behind it), on another stream, and replayed."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    lengths, K, N = [9000, 0, 1000], 144, 80
+    E, rows, off = 3, 10000, offsets_of([9000, 0, 1000])
+    dy, x, w = normal(g, rows, N), normal(g, rows, K), normal(g, E, 8192, K)
+    long_dy = normal(g, 100, 8192)
+    short = offsets_of([60, 0, 40])
+
+    def outs():
+        return (torch.zeros(E, N, K, device="cuda"), torch.zeros(E, N, device="cuda"),
+                torch.zeros(100, K, dtype=torch.bfloat16, device="cuda"))
+
+    def call(o, stream=None, spaces=(None, None)):
+        B.moe_expert_matmul_dw(dy, x, off, o[0], o[1], stream=stream, workspace=spaces[0])
+        B.moe_expert_matmul_dx(long_dy, short, w, NONE, None, o[2], stream=stream, workspace=spaces[1])
+
+    first = outs()
+    call(first)
+    spaces = []
+    for need in (workspace_of("dw", lengths, 0, K, N), workspace_of("dx", [60, 0, 40], 0, K, 8192)):
+        assert need > 0 and need % 4 == 0
+        spaces.append(torch.full((need // 4 + 64,), float("nan"), device="cuda"))
+    used = [s[:-64].view(torch.uint8) for s in spaces]
+    second, third, fourth = outs(), outs(), outs()
+    call(second, None, used)
+    assert all(torch.isnan(s[-64:]).all() for s in spaces)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(third, side)
+    call(third, side.cuda_stream)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        call(fourth)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            call(fourth)
+    for s in range(3):
+        for t in fourth:
+            t.fill_(-7)
+        graphs[s % 2].replay()
+        torch.cuda.synchronize()
+        for got in (second, third, fourth):
+            assert all(torch.equal(p, q) for p, q in zip(first, got))
+        again = outs()
+        call(again)
+        assert all(torch.equal(p, q) for p, q in zip(first, again))
+
+
 def test_dw_without_rows():
     dw, db = torch.full((3, 32, 48), 2.0, device="cuda"), torch.full((3, 32), 2.0, device="cuda")
     none = torch.empty(0, 32, dtype=torch.bfloat16, device="cuda"), torch.empty(0, 48, dtype=torch.bfloat16, device="cuda")

@@ -93,8 +93,8 @@ def test_expert_matmul(lib):
 
 
 def test_expert_matmul_gradients(lib):
-    def dx(dy=F, off=F, w=G, act=0, z=None, E=2, rows=4, K=32, N=32, out=H):
-        return lib.moe_expert_matmul_dx(dy, off, w, act, z, E, rows, K, N, out, None)
+    def dx(dy=F, off=F, w=G, act=0, z=None, E=2, rows=4, K=32, N=32, out=H, ws=None, size=None):
+        return lib.moe_expert_matmul_dx(dy, off, w, act, z, E, rows, K, N, out, ws, size, None)
     for bad in (dict(E=0), dict(rows=-1), dict(rows=2 ** 31), dict(K=24), dict(K=65552), dict(N=24), dict(N=131088),
                 dict(act=7)):
         assert dx(**bad) == SHAPE, bad
@@ -106,8 +106,8 @@ def test_expert_matmul_gradients(lib):
     assert dx(off=ODD) == ALIGN and dx(out=F) == ALIAS and dx(out=G) == ALIAS
     assert dx(None, None, None, out=None, rows=0) == OK
 
-    def dw(dy=F, x=G, off=F, E=2, rows=4, K=32, N=32, flags=0, out=H, db=None):
-        return lib.moe_expert_matmul_dw(dy, x, off, E, rows, K, N, flags, out, db, None)
+    def dw(dy=F, x=G, off=F, E=2, rows=4, K=32, N=32, flags=0, out=H, db=None, ws=None, size=None):
+        return lib.moe_expert_matmul_dw(dy, x, off, E, rows, K, N, flags, out, db, ws, size, None)
     for bad in (dict(E=0), dict(rows=-1), dict(K=24), dict(K=65552), dict(N=0), dict(flags=2), dict(flags=0x101),
                 dict(flags=-1)):
         assert dw(**bad) == SHAPE, bad
@@ -116,6 +116,31 @@ def test_expert_matmul_gradients(lib):
     for p in ("dy", "x", "out", "db"):
         assert dw(**{p: EIGHT}) == ALIGN
     assert dw(off=ODD) == ALIGN and dw(out=F) == ALIAS and dw(out=G) == ALIAS
+
+
+def test_expert_gradient_workspaces(lib):
+    n = ctypes.c_size_t(7)
+    none = [None] * 3
+    q = {"moe_expert_matmul_dx": lambda E, rows, K, N, s=n: lib.moe_expert_matmul_dx(
+             *none, 0, None, E, rows, K, N, None, None, ctypes.byref(s), None),
+         "moe_expert_matmul_dw": lambda E, rows, K, N, s=n: lib.moe_expert_matmul_dw(
+             *none, E, rows, K, N, 0, None, None, None, ctypes.byref(s), None)}
+    for name, f in q.items():
+        assert f(1, 8192, 65552, 64) == SHAPE
+        for sizes in ((1, 0, 64, 64), (8, 8192, 7168, 7168), (300, 300, 16, 8192), (2, 64, 64, 64)):
+            assert f(*sizes) == OK and n.value == 0 == B.expert_grad_workspace_bytes(name, *sizes)
+    assert q["moe_expert_matmul_dx"](2, 200, 128, 8192) == OK and n.value > 0 and n.value % 256 == 0
+    few = ctypes.c_size_t(n.value - 1)
+    call = lambda ws, size: lib.moe_expert_matmul_dx(  # noqa: E731
+        F, F, G, 0, None, 2, 200, 128, 8192, H, ws, size, None)
+    assert call(F, ctypes.byref(few)) == WORKSPACE and call(F, None) == WORKSPACE
+    assert call(EIGHT, ctypes.byref(n)) == ALIGN
+    assert q["moe_expert_matmul_dw"](2, 20000, 128, 128) == OK and n.value > 0
+    few = ctypes.c_size_t(n.value - 1)
+    call = lambda ws, size: lib.moe_expert_matmul_dw(  # noqa: E731
+        F, G, F, 2, 20000, 128, 128, 0, H, None, ws, size, None)
+    assert call(F, ctypes.byref(few)) == WORKSPACE and call(F, None) == WORKSPACE
+    assert call(EIGHT, ctypes.byref(n)) == ALIGN
 
 
 def test_binding_refuses_host_tensors_and_wrong_shapes():
