@@ -72,7 +72,8 @@ def load() -> ctypes.CDLL:
     lib.moe_balance_loss.argtypes = [P, P, P, i64, i64, i32, i32, P, P, P, P, P, P, P]
     lib.moe_route_grad.argtypes = [P, P, P, P, P, P, P, P, i64, i64, i32, i32, P, P]
     lib.moe_combine_grad.argtypes = [P, P, P, i32, P, P, i64, i32, i32, P, P, P]
-    lib.moe_expert_matmul.argtypes = [P, P, P, P, i32, P, i32, i64, i32, i32, P, P, P]
+    lib.moe_expert_matmul.argtypes = [P, P, P, P, i32, P, i32, i64, i32, i32, P, P, P,
+                                      ctypes.POINTER(sz), P]
     lib.moe_expert_matmul_dx.argtypes = [P, P, P, i32, P, i32, i64, i32, i32, P, P,
                                          ctypes.POINTER(sz), P]
     lib.moe_expert_matmul_dw.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P, P,
@@ -642,40 +643,15 @@ def _want_weights(w: torch.Tensor, offsets: torch.Tensor):
         raise ValueError("offsets must hold E+1 int32")
 
 
-def moe_expert_matmul(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
-                      bias: torch.Tensor | None, act: int, residual: torch.Tensor | None,
-                      out: torch.Tensor, preact: torch.Tensor | None = None,
-                      stream=None) -> torch.Tensor:
-    """x bf16 [rows, K] in runs of offsets int32 [E+1], w bf16 [E, N, K]
-    ([E, 2N, K] for MOE_ACT_SWIGLU) -> out bf16 [rows, N]; bias fp32 [E, N]
-    ([E, 2N]); preact bf16 [rows, N] ([rows, 2N]) keeps z for the gradient."""
-    _want_weights(w, offsets)
-    E, wide_n, K = w.shape
-    wide = 2 if act == MOE_ACT_SWIGLU else 1
-    if wide_n % wide:
-        raise ValueError("MOE_ACT_SWIGLU takes an even number of weight rows")
-    rows, N = x.shape[0], wide_n // wide
-    _want_bf16(w, (E, wide_n, K), "w")
-    _want_bf16(x, (rows, K), "x")
-    _want_bf16(out, (rows, N), "out")
-    if residual is not None:
-        _want_bf16(residual, (rows, N), "residual")
-    if preact is not None:
-        _want_bf16(preact, (rows, wide_n), "preact")
-    if bias is not None:
-        _want(bias, torch.float32, "bias")
-        if bias.numel() != E * wide_n:
-            raise ValueError("bias must hold one value per weight row")
-    _call("moe_expert_matmul", stream, x, offsets, w, bias, act, residual, E, rows, K, N, out,
-          preact)
-    return out
-
-
 @functools.lru_cache(maxsize=4096)
-def expert_grad_workspace_bytes(name: str, E: int, rows: int, K: int, N: int) -> int:
-    """Workspace of moe_expert_matmul_dx or _dw (`name`) for these sizes."""
+def expert_workspace_bytes(name: str, E: int, rows: int, K: int, N: int,
+                           act: int = MOE_ACT_NONE) -> int:
+    """Workspace of moe_expert_matmul, _dx or _dw (`name`) for these sizes."""
     n, i, none = ctypes.c_size_t(0), ctypes.byref, None
-    if name == "moe_expert_matmul_dx":
+    if name == "moe_expert_matmul":
+        status = load().moe_expert_matmul(none, none, none, none, act, none, E, rows, K, N, none,
+                                          none, none, i(n), none)
+    elif name == "moe_expert_matmul_dx":
         status = load().moe_expert_matmul_dx(none, none, none, 0, none, E, rows, K, N, none, none,
                                              i(n), none)
     else:
@@ -685,11 +661,11 @@ def expert_grad_workspace_bytes(name: str, E: int, rows: int, K: int, N: int) ->
     return int(n.value)
 
 
-def _call_sharing(name: str, stream, workspace: torch.Tensor | None, E: int, rows: int, K: int,
-                  N: int, like: torch.Tensor, *args) -> None:
-    """A gradient call with its workspace: `workspace`, or one allocated for the
+def _call_sharing(name: str, stream, workspace: torch.Tensor | None, sizes: tuple,
+                  like: torch.Tensor, *args) -> None:
+    """A product's call with its workspace: `workspace`, or one allocated for the
     call (torch's allocator, in the stream's order) when the sizes want one."""
-    need = expert_grad_workspace_bytes(name, E, rows, K, N)
+    need = expert_workspace_bytes(name, *sizes)
     if not need:
         _call(name, stream, *args, None, None)
         return
@@ -709,13 +685,42 @@ def _call_sharing(name: str, stream, workspace: torch.Tensor | None, E: int, row
     _call(name, stream, *args, workspace, ctypes.byref(n))
 
 
+def moe_expert_matmul(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                      bias: torch.Tensor | None, act: int, residual: torch.Tensor | None,
+                      out: torch.Tensor, preact: torch.Tensor | None = None, stream=None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """x bf16 [rows, K] in runs of offsets int32 [E+1], w bf16 [E, N, K]
+    ([E, 2N, K] for MOE_ACT_SWIGLU) -> out bf16 [rows, N]; bias fp32 [E, N]
+    ([E, 2N]); preact bf16 [rows, N] ([rows, 2N]) keeps z for the gradient;
+    workspace: scratch of expert_workspace_bytes, else allocated where wanted."""
+    _want_weights(w, offsets)
+    E, wide_n, K = w.shape
+    wide = 2 if act == MOE_ACT_SWIGLU else 1
+    if wide_n % wide:
+        raise ValueError("MOE_ACT_SWIGLU takes an even number of weight rows")
+    rows, N = x.shape[0], wide_n // wide
+    _want_bf16(w, (E, wide_n, K), "w")
+    _want_bf16(x, (rows, K), "x")
+    _want_bf16(out, (rows, N), "out")
+    if residual is not None:
+        _want_bf16(residual, (rows, N), "residual")
+    if preact is not None:
+        _want_bf16(preact, (rows, wide_n), "preact")
+    if bias is not None:
+        _want(bias, torch.float32, "bias")
+        if bias.numel() != E * wide_n:
+            raise ValueError("bias must hold one value per weight row")
+    _call_sharing("moe_expert_matmul", stream, workspace, (E, rows, K, N, act), x, x, offsets, w,
+                  bias, act, residual, E, rows, K, N, out, preact)
+    return out
+
+
 def moe_expert_matmul_dx(dy: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor, act: int,
                          preact: torch.Tensor | None, dx: torch.Tensor, stream=None,
                          workspace: torch.Tensor | None = None) -> torch.Tensor:
     """dy bf16 [rows, N], w bf16 [E, N, K] -> dx bf16 [rows, K], through the
     activation before the product when act says so (preact and dx [rows, K],
-    or [rows, 2K] for MOE_ACT_SWIGLU).  workspace: scratch of
-    expert_grad_workspace_bytes, else allocated where wanted."""
+    or [rows, 2K] for MOE_ACT_SWIGLU).  workspace: as moe_expert_matmul."""
     _want_weights(w, offsets)
     E, N, K = w.shape
     rows, wide = dy.shape[0], 2 if act == MOE_ACT_SWIGLU else 1
@@ -728,8 +733,8 @@ def moe_expert_matmul_dx(dy: torch.Tensor, offsets: torch.Tensor, w: torch.Tenso
         raise ValueError("an activation's gradient needs preact")
     else:
         _want_bf16(preact, (rows, wide * K), "preact")
-    _call_sharing("moe_expert_matmul_dx", stream, workspace, E, rows, K, N, dy, dy, offsets, w, act,
-                  preact, E, rows, K, N, dx)
+    _call_sharing("moe_expert_matmul_dx", stream, workspace, (E, rows, K, N), dy, dy, offsets, w,
+                  act, preact, E, rows, K, N, dx)
     return dx
 
 
@@ -739,7 +744,7 @@ def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
                          workspace: torch.Tensor | None = None) -> torch.Tensor:
     """dy bf16 [rows, N], x bf16 [rows, K] -> dw [E, N, K] (fp32, or bf16 by
     its dtype) and dbias fp32 [E, N]; accumulate adds to what they hold
-    (fp32 dw only).  workspace: as moe_expert_matmul_dx."""
+    (fp32 dw only).  workspace: as moe_expert_matmul."""
     _want_weights(dw, offsets)
     E, N, K = dw.shape
     rows = dy.shape[0]
@@ -754,6 +759,6 @@ def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     flags = MOE_GRAD_FP32 if dw.dtype == torch.float32 else MOE_GRAD_BF16
     if accumulate:
         flags |= MOE_GRAD_ACCUMULATE
-    _call_sharing("moe_expert_matmul_dw", stream, workspace, E, rows, K, N, dy, dy, x, offsets, E,
-                  rows, K, N, flags, dw, dbias)
+    _call_sharing("moe_expert_matmul_dw", stream, workspace, (E, rows, K, N), dy, dy, x, offsets,
+                  E, rows, K, N, flags, dw, dbias)
     return dw

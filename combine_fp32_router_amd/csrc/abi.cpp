@@ -475,23 +475,32 @@ int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv
 
 int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, const float *bias,
                       int act, const void *residual, int E, int64_t max_rows, int K, int N,
-                      void *out, void *preact, hipStream_t stream)
+                      void *out, void *preact, void *workspace, size_t *workspace_bytes,
+                      hipStream_t stream)
 {
     if (check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK || !known_act(act) ||
         !product_tiles_fit(max_row_tiles(max_rows, E, 256), act == MOE_ACT_SWIGLU ? 2 * N : N))
         return MOE_ERR_SHAPE;
+    const size_t need = moe::forward_parts(act, E, max_rows, K, N).bytes;
+    if (!workspace && workspace_bytes) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
     if (max_rows == 0)
         return MOE_OK;
+    if (workspace && (!workspace_bytes || *workspace_bytes < need))
+        return MOE_ERR_WORKSPACE;
     if (!x || !offsets || !w || !out)
         return MOE_ERR_NULL;
     if (!aligned(x, 16) || !aligned(offsets, 4) || !aligned(w, 16) || !aligned(bias, 16) ||
-        !aligned(residual, 16) || !aligned(out, 16) || !aligned(preact, 16))
+        !aligned(residual, 16) || !aligned(out, 16) || !aligned(preact, 16) ||
+        !aligned(workspace, 256))
         return MOE_ERR_ALIGN;
     if (out == x || out == w || out == preact ||
         (preact && (preact == x || preact == w || preact == residual)))
         return MOE_ERR_ALIAS;
     return hip_status(moe::launch_expert_matmul(x, offsets, w, bias, act, residual, E, max_rows, K,
-                                                N, out, preact, stream));
+                                                N, out, preact, workspace, stream));
 }
 
 int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
@@ -501,7 +510,7 @@ int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, 
     if (check_product(E, max_rows, K, N, 2 * MOE_MAX_HIDDEN) != MOE_OK || !known_act(act) ||
         !product_tiles_fit(max_row_tiles(max_rows, E, 256), K))
         return MOE_ERR_SHAPE;
-    const size_t need = moe::dx_parts(E, max_rows, K, N).bytes;
+    const size_t need = moe::row_parts(E, max_rows, N, K, 128).bytes;
     if (!workspace && workspace_bytes) {
         *workspace_bytes = need;
         return MOE_OK;

@@ -227,13 +227,13 @@ static int few_height(int E, int64_t max_rows)
 // Estimates in us.  Here: the weights from memory at 6.2 TB/s, the rows once
 // for every 16 columns at 17 TB/s, or 6.2 where they are more than the L2s hold,
 // 2, and 0.8 for each round of the workgroups that fit the card.  The tiles: 8
-// for each round of them and 0.75 for 64 of K, or the weights and 5 if that is
-// longer.  Measured (here / tiles): 1 token of 8 experts above 78 / 80; 64 rows
+// for each round of them and 0.75 for 64 of K (in parts: 12, and 0.45 for 64 of
+// a part's), or the weights and 5 if that is longer.  Measured (here / tiles): 1 token of 8 experts above 78 / 80; 64 rows
 // of 1 expert, K = N = 4096 11 / 30; 256 rows of it 37 / 28; 128 rows of each of
 // 8, K = 2048, N = 768 gated 27 / 23; 64 rows of each of 8, K = 7168, N = 2048
 // gated 126 / 113; 2 rows of each of 64, K = 1024, N = 4096 108 / 95; 1 row of each
 // of 8, K = 2048, N = 7168 52 / 37; 4 of each of 32, K = 2048, N = 1024 32 / 24.
-bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N)
+bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N, int parts)
 {
     const int wide = act == MOE_ACT_SWIGLU ? 2 : 1;
     const int64_t live = max_rows < E ? max_rows : E;
@@ -245,7 +245,8 @@ bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N)
     const double weights = 2.0 * live * wide * N * K / 6.2e6, rows = 2.0 * max_rows * K;
     const double here = weights + (N / 16) * rows / (rows > 32e6 ? 6.2e6 : 17e6) + 2 + 0.8 * ((groups + fit - 1) / fit);
     const TileShape shape = tile_shape(E, max_rows, N, 128 / wide);
-    const double there = ((shape.tiles + kCus - 1) / kCus) * (8 + K / 64 * 0.0075 * shape.percent);
+    const double there = parts > 1 ? 12 + K / 64 * 0.45 / parts
+                                   : ((shape.tiles + kCus - 1) / kCus) * (8 + K / 64 * 0.0075 * shape.percent);
     return here < (there > weights + 5 ? there : weights + 5);
 }
 

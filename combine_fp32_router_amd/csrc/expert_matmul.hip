@@ -35,7 +35,7 @@ struct Args {
     int flags;
     int rows;               // dw: rows of the output (N)
     int height;             // forward, dx: rows of a tile
-    // dx, dw in parts: how many, their sums in the MFMA's layout, those of db
+    // in parts: how many, their sums in the MFMA's layout, those of db
     int parts, tiles;       // (tiles: the most that the workspace is for)
     f32x4 *part;
     float *part_db;
@@ -648,16 +648,17 @@ __global__ __launch_bounds__(64 * kTileWaves) void expert_kernel(Args a)
     }
 }
 
-// dx and dw of few outputs and a long reduced length: every tile, of 64 x 128, is
+// Few outputs of a long reduced length: every tile, of 64 x 128, is
 // shared by up to `parts` workgroups, each of which takes a piece of the
 // length and leaves its sums, as its accumulators hold them, in the workspace; a
 // second kernel adds them in order and finishes the tile.  Two workgroups
-// share a CU (THIN).  dw of 16384 rows, 512 x 512: 32 us, 100 in whole tiles;
-// 8192 rows, 128 x 2048: 28 and 54; dx of 200 rows, 4096 -> 256: 21 and 30.
-template <Op OP>
+// share a CU (THIN).  dw of 16384 rows, 512 x 512: 23 us, 100 in whole tiles;
+// 8192 rows, 128 x 2048: 19 and 54; dx of 512 rows, 8192 -> 256: 21 and 54.
+template <Op OP, bool GATED>
 struct PartList {
+    static constexpr int kCols = GATED ? 64 : 128;  // output columns of a tile
     static constexpr int kBytes = 4 * (2 * kPartExperts + 1);
-    int32_t *starts, *upto;  // as in TileList; dx
+    int32_t *starts, *upto;  // as in TileList; upto: not for dw
     int E, tiles, col_tiles, row_tiles;
 
     __device__ __forceinline__ void build(const Args &a, int32_t *lds)
@@ -665,13 +666,13 @@ struct PartList {
         E = a.E;
         starts = lds;
         upto = lds + E + 1;
-        col_tiles = (a.C + 127) / 128;
+        col_tiles = (a.C + kCols - 1) / kCols;
         row_tiles = (a.rows + 63) / 64;  // dw
         for (int e = threadIdx.x; e <= E; e += blockDim.x)
             starts[e] = run_start(a.offsets, e, a.max_rows);
         __syncthreads();
         tiles = E * row_tiles * col_tiles;
-        if (OP == kDx) {
+        if (OP != kDw) {
             if (uniform(threadIdx.x / kWave) == 0) {
                 int before = 0;
                 for (int e0 = 0; e0 < E; e0 += kWave) {
@@ -699,9 +700,9 @@ struct PartList {
     __device__ __forceinline__ Work at(const Args &a, int tile) const
     {
         Work t;
-        t.c0 = tile % col_tiles * 128;
+        t.c0 = tile % col_tiles * kCols;
         const int row = tile / col_tiles;
-        if (OP == kDx) {
+        if (OP != kDw) {
             t.e = 0;
             for (int e0 = 0; e0 < E; e0 += kWave) {
                 const int e = e0 + lane_id();
@@ -730,11 +731,11 @@ struct PartList {
     }
 };
 
-template <Op OP>
+template <Op OP, bool GATED>
 __global__ __launch_bounds__(64 * kTileWaves, 2) void expert_part_kernel(Args a)
 {
-    typedef Tile<128, false, OP != kDw, false, true> T;
-    typedef PartList<OP> List;
+    typedef Tile<128, OP == kForward, OP != kDw, GATED, true> T;
+    typedef PartList<OP, GATED> List;
     __shared__ __align__(1024) char shared[T::kLdsBytes + List::kBytes];
     MOE_LDS char *lds = (MOE_LDS char *)shared;
     List list;
@@ -747,8 +748,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void expert_part_kernel(Args a)
         if (r0 >= k.R)
             continue;
         t.R = min(share, k.R - r0);
-        if (OP == kDx) {
-            t.p.init(a.p + (static_cast<int64_t>(k.e) * a.R + r0) * a.C + k.c0, nullptr, a.C, min(128, a.C - k.c0));
+        if (OP != kDw) {
+            if (OP == kForward) {
+                const int64_t rows = static_cast<int64_t>(k.e) * (GATED ? 2 : 1) * a.C + k.c0;
+                t.p.init(a.p + rows * a.R + r0, a.p + (rows + a.C) * a.R + r0, a.R, min(List::kCols, a.C - k.c0));
+            } else {
+                t.p.init(a.p + (static_cast<int64_t>(k.e) * a.R + r0) * a.C + k.c0, nullptr, a.C, min(128, a.C - k.c0));
+            }
             t.q.init(a.q + static_cast<int64_t>(k.first) * a.R + r0, nullptr, a.R, k.n);
         } else {
             t.p.init(a.p + (static_cast<int64_t>(k.r_first) + r0) * a.C + k.c0, nullptr, a.C, min(128, a.C - k.c0));
@@ -783,60 +789,61 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void expert_part_kernel(Args a)
     }
 }
 
-template <Op OP>
-__global__ __launch_bounds__(64 * kTileWaves) void expert_join_kernel(Args a)
+// One wave for each 16 rows that a wave of the parts' kernel held: most of it
+// is waiting for the parts.
+template <Op OP, bool GATED>
+__global__ __launch_bounds__(kWave) void expert_join_kernel(Args a)
 {
-    typedef Tile<128, false, OP != kDw, false, true> T;
-    typedef PartList<OP> List;
-    __shared__ __align__(1024) char shared[kTileWaves * T::kOutBytes + List::kBytes];
+    constexpr int kFrags = 4, kUnits = 2 * kTileWaves, kUnit = kFrags * kWave;  // of a tile's part, in f32x4
+    typedef PartList<OP, GATED> List;
+    __shared__ __align__(1024) char shared[4096 + List::kBytes];
     List list;
-    list.build(a, reinterpret_cast<int32_t *>(shared + kTileWaves * T::kOutBytes));
-    const T t{};
-    MOE_LDS char *place = (MOE_LDS char *)shared + t.wave() * T::kOutBytes;
-    for (int tile = blockIdx.x; tile < list.tiles; tile += gridDim.x) {
-        const Work k = list.at(a, tile);
-        const int share = List::share(a, k.R), live = k.R > 0 ? (k.R + share - 1) / share : 0;
-        const f32x4 *from = a.part + (static_cast<int64_t>(tile) * a.parts * kTileWaves + t.wave()) * (2 * T::kFrags * kWave) +
-                            lane_id();
-        if (OP == kDw && a.db && k.c0 == 0 && static_cast<int>(threadIdx.x) < k.n) {
-            float sum = 0.0f;
-            for (int p = 0; p < live; ++p)
-                sum += a.part_db[(static_cast<int64_t>(tile / list.col_tiles) * a.parts + p) * 64 + threadIdx.x];
-            float *db = a.db + static_cast<int64_t>(k.e) * a.rows + k.first + threadIdx.x;
-            *db = ((a.flags & MOE_GRAD_ACCUMULATE) ? *db : 0.0f) + sum;
-        }
-        const int c = k.c0 + t.col0(), inside = a.C - c;
-        auto finish = [&](auto &f) {
-#pragma unroll 1
-            for (int i = 0; i < 2 && t.row0(0) + 16 * i < k.n; ++i) {
-                f32x4 v[T::kFrags] = {};
-                for (int p = 0; p < live; ++p)
+    list.build(a, reinterpret_cast<int32_t *>(shared + 4096));
+    const int tile = blockIdx.x / kUnits, unit = blockIdx.x % kUnits, wave = unit / 2, lane = lane_id();
+    if (tile >= list.tiles)
+        return;
+    const Work k = list.at(a, tile);
+    const int share = List::share(a, k.R), live = k.R > 0 ? (k.R + share - 1) / share : 0;
+    if (OP == kDw && a.db && k.c0 == 0 && unit == 0 && lane < k.n) {
+        float sum = 0.0f;
+        for (int p = 0; p < live; ++p)
+            sum += a.part_db[(static_cast<int64_t>(tile / list.col_tiles) * a.parts + p) * 64 + lane];
+        float *db = a.db + static_cast<int64_t>(k.e) * a.rows + k.first + lane;
+        *db = ((a.flags & MOE_GRAD_ACCUMULATE) ? *db : 0.0f) + sum;
+    }
+    const int row = wave / 2 * 32 + unit % 2 * 16, c = k.c0 + wave % 2 * (64 / (GATED ? 2 : 1)), inside = a.C - c;
+    if (row >= k.n)
+        return;
+    const f32x4 *from = a.part + (static_cast<int64_t>(tile) * a.parts * kUnits + unit) * kUnit + lane;
+    f32x4 v[kFrags] = {};
+#pragma unroll 4
+    for (int p = 0; p < live; ++p)
 #pragma unroll
-                    for (int b = 0; b < T::kFrags; ++b)
-                        v[b] += from[(p * kTileWaves * 2 + i) * T::kFrags * kWave + b * kWave];
-                f(t.row0(0) + 16 * i, t.row0(0) + 16, v);
-            }
-        };
-        if constexpr (OP == kDx) {
-            FinishDx<T::kFrags> f(a, place, k.first, k.n, c, inside, t.row0(0));
-            finish(f);
-        } else {
-            FinishDw<T::kFrags> f(a, place, static_cast<int64_t>(k.e) * a.rows + k.first, k.n, c, inside);
-            finish(f);
-        }
+        for (int b = 0; b < kFrags; ++b)
+            v[b] += from[p * (kUnits * kUnit) + b * kWave];
+    MOE_LDS char *place = (MOE_LDS char *)shared;
+    if constexpr (OP == kForward) {
+        FinishForward<kFrags, GATED> f(a, place, k.e, k.first, k.n, c, inside, row);
+        f(row, row, v);
+    } else if constexpr (OP == kDx) {
+        FinishDx<kFrags> f(a, place, k.first, k.n, c, inside, row);
+        f(row, row, v);
+    } else {
+        FinishDw<kFrags> f(a, place, static_cast<int64_t>(k.e) * a.rows + k.first, k.n, c, inside);
+        f(row, row, v);
     }
 }
 
 // In how many parts a tile's reduced length R is best taken (1: not at all): as
-// many as fill the card, of at least four steps of 64 each, where they save 20
-// steps or more of about 0.45 us, against the 8 us of the second kernel.
+// many as fill the card, of at least four steps of 64 each, where they save 16
+// steps or more, of about 0.45 us, against the 5 us of the second kernel.
 int parts_of(int64_t tiles, int E, int64_t R)
 {
     const int64_t steps = R / kStep;
     if (tiles < 1 || tiles > kCus / 2 || E > kPartExperts)
         return 1;
     const int64_t n = steps / 4 < 2 * kCus / tiles ? steps / 4 : 2 * kCus / tiles;
-    return n >= 2 && steps - steps / n >= 20 ? static_cast<int>(n) : 1;
+    return n >= 2 && steps - steps / n >= 16 ? static_cast<int>(n) : 1;
 }
 constexpr int64_t kPartBytes = 64 * 128 * 4, kPartDbBytes = 64 * 4;  // of a part of a tile, and of a row of tiles
 
@@ -853,41 +860,24 @@ dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < kCus ? (n 
 
 }  // namespace
 
-hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const void *w,
-                                const float *bias, int act, const void *residual, int E,
-                                int64_t max_rows, int K, int N, void *out, void *preact,
-                                hipStream_t stream)
+Parts row_parts(int E, int64_t max_rows, int R, int C, int unit)
 {
-    Args a{};
-    a.p = static_cast<const uint16_t *>(w);
-    a.q = static_cast<const uint16_t *>(x);
-    a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = K, a.C = N;
-    a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
-    a.out = out, a.preact = static_cast<uint16_t *>(preact);
-    if (few_rows_pay(act, E, max_rows, K, N))
-        return launch_expert_few(x, offsets, w, bias, act, residual, E, max_rows, K, N, out, preact, stream);
-    const TileShape shape = tile_shape(E, max_rows, N, act == MOE_ACT_SWIGLU ? 64 : 128);
-    a.height = shape.rows;
-    if (act == MOE_ACT_SWIGLU) {
-        MOE_EXPERT(kForward, true, shape.cols, shape.tiles);
-    } else {
-        MOE_EXPERT(kForward, false, shape.cols, shape.tiles);
-    }
-    return hipGetLastError();
-}
-
-GradParts dx_parts(int E, int64_t max_rows, int K, int N)
-{
-    GradParts g{};
-    g.tiles = max_row_tiles(max_rows, E, 64) * ((K + 127) / 128);
-    g.parts = parts_of(g.tiles, E, N);
+    Parts g{};
+    g.tiles = max_row_tiles(max_rows, E, 64) * ((C + unit - 1) / unit);
+    g.parts = parts_of(g.tiles, E, R);
     g.bytes = g.parts > 1 ? g.tiles * g.parts * kPartBytes : 0;
     return g;
 }
 
-GradParts dw_parts(int E, int64_t max_rows, int K, int N)
+Parts forward_parts(int act, int E, int64_t max_rows, int K, int N)
 {
-    GradParts g{};
+    const Parts g = row_parts(E, max_rows, K, N, act == MOE_ACT_SWIGLU ? 64 : 128);
+    return g.parts > 1 && !few_rows_pay(act, E, max_rows, K, N, g.parts) ? g : Parts{1, g.tiles, 0};
+}
+
+Parts dw_parts(int E, int64_t max_rows, int K, int N)
+{
+    Parts g{};
     const int64_t rows = static_cast<int64_t>(E) * ((N + 63) / 64);
     g.tiles = rows * ((K + 127) / 128);
     g.parts = parts_of(g.tiles, E, max_rows / E);
@@ -895,18 +885,47 @@ GradParts dw_parts(int E, int64_t max_rows, int K, int N)
     return g;
 }
 
-template <Op OP>
-static hipError_t launch_parts(Args &a, const GradParts &g, void *workspace, hipStream_t stream)
+template <Op OP, bool GATED>
+static hipError_t launch_parts(Args &a, const Parts &g, void *workspace, hipStream_t stream)
 {
     a.parts = g.parts, a.tiles = static_cast<int>(g.tiles);
     a.part = static_cast<f32x4 *>(workspace);
     a.part_db = reinterpret_cast<float *>(static_cast<char *>(workspace) + g.tiles * g.parts * kPartBytes);
     const int64_t n = g.tiles * g.parts;
-    expert_part_kernel<OP><<<dim3(static_cast<unsigned>(n < 2 * kCus ? n : 2 * kCus)), 64 * kTileWaves, 0, stream>>>(a);
+    expert_part_kernel<OP, GATED><<<dim3(static_cast<unsigned>(n < 2 * kCus ? n : 2 * kCus)), 64 * kTileWaves, 0, stream>>>(a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess)
         return err;
-    expert_join_kernel<OP><<<dim3(static_cast<unsigned>(g.tiles)), 64 * kTileWaves, 0, stream>>>(a);
+    expert_join_kernel<OP, GATED><<<dim3(static_cast<unsigned>(g.tiles * 2 * kTileWaves)), kWave, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const void *w,
+                                const float *bias, int act, const void *residual, int E,
+                                int64_t max_rows, int K, int N, void *out, void *preact,
+                                void *workspace, hipStream_t stream)
+{
+    Args a{};
+    a.p = static_cast<const uint16_t *>(w);
+    a.q = static_cast<const uint16_t *>(x);
+    a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = K, a.C = N;
+    a.act = act, a.bias = bias, a.residual = static_cast<const uint16_t *>(residual);
+    a.out = out, a.preact = static_cast<uint16_t *>(preact);
+    const bool gated = act == MOE_ACT_SWIGLU;
+    const Parts parts = forward_parts(act, E, max_rows, K, N);
+    const bool shared = workspace && parts.parts > 1;
+    if (!shared && few_rows_pay(act, E, max_rows, K, N, 1))
+        return launch_expert_few(x, offsets, w, bias, act, residual, E, max_rows, K, N, out, preact, stream);
+    if (shared)
+        return gated ? launch_parts<kForward, true>(a, parts, workspace, stream)
+                     : launch_parts<kForward, false>(a, parts, workspace, stream);
+    const TileShape shape = tile_shape(E, max_rows, N, gated ? 64 : 128);
+    a.height = shape.rows;
+    if (gated) {
+        MOE_EXPERT(kForward, true, shape.cols, shape.tiles);
+    } else {
+        MOE_EXPERT(kForward, false, shape.cols, shape.tiles);
+    }
     return hipGetLastError();
 }
 
@@ -919,9 +938,9 @@ hipError_t launch_expert_matmul_dx(const void *dy, const int32_t *offsets, const
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = N, a.C = K;
     a.act = act, a.z = static_cast<const uint16_t *>(z), a.out = dx;
-    const GradParts parts = dx_parts(E, max_rows, K, N);
+    const Parts parts = row_parts(E, max_rows, N, K, 128);
     if (workspace && parts.parts > 1)
-        return launch_parts<kDx>(a, parts, workspace, stream);
+        return launch_parts<kDx, false>(a, parts, workspace, stream);
     const TileShape shape = tile_shape(E, max_rows, K, 128);
     a.height = shape.rows;
     MOE_EXPERT(kDx, false, shape.cols, shape.tiles);
@@ -937,9 +956,9 @@ hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t 
     a.q = static_cast<const uint16_t *>(dy);
     a.offsets = offsets, a.E = E, a.max_rows = static_cast<int>(max_rows), a.C = K, a.rows = N;
     a.out = dw, a.db = db, a.flags = flags;
-    const GradParts parts = dw_parts(E, max_rows, K, N);
+    const Parts parts = dw_parts(E, max_rows, K, N);
     if (workspace && parts.parts > 1)
-        return launch_parts<kDw>(a, parts, workspace, stream);
+        return launch_parts<kDw, false>(a, parts, workspace, stream);
     const int64_t n = static_cast<int64_t>(E) * ((N + 255) / 256) * ((K + 255) / 256);  // cut into up to 4 each
     MOE_EXPERT(kDw, false, 2 * n <= kCus ? 128 : 256, 8 * n);
     return hipGetLastError();

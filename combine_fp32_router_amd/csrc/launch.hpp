@@ -117,9 +117,9 @@ hipError_t launch_combine_grad(const void *d_out, const void *rows, const float 
 hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const void *w,
                                 const float *bias, int act, const void *residual, int E,
                                 int64_t max_rows, int K, int N, void *out, void *preact,
-                                hipStream_t stream);
+                                void *workspace, hipStream_t stream);
 // The same for few rows an expert, and whether it pays.
-bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N);
+bool few_rows_pay(int act, int E, int64_t max_rows, int K, int N, int parts);
 hipError_t launch_expert_few(const void *x, const int32_t *offsets, const void *w, const float *bias,
                              int act, const void *residual, int E, int64_t max_rows, int K, int N,
                              void *out, void *preact, hipStream_t stream);
@@ -131,14 +131,16 @@ inline bool product_tiles_fit(int64_t row_tiles, int cols) { return row_tiles * 
 hipError_t launch_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, int E,
                                    int64_t max_rows, int K, int N, int flags, void *dw, float *db,
                                    void *workspace, hipStream_t stream);
-// In how many parts a gradient's reduced length is taken (1: whole), its
-// tiles then, and the workspace for them.
-struct GradParts {
+// In how many parts a product's reduced length is taken (1: whole), its tiles
+// then, and the workspace for them.  row_parts: products of rows with reduced
+// length R and C output columns, `unit` of which make 128 of a tile.
+struct Parts {
     int parts;
     int64_t tiles, bytes;
 };
-GradParts dx_parts(int E, int64_t max_rows, int K, int N);
-GradParts dw_parts(int E, int64_t max_rows, int K, int N);
+Parts row_parts(int E, int64_t max_rows, int R, int C, int unit);
+Parts forward_parts(int act, int E, int64_t max_rows, int K, int N);
+Parts dw_parts(int E, int64_t max_rows, int K, int N);
 
 // Most tiles of `height` rows that E runs of together max_rows rows can have.
 inline int64_t max_row_tiles(int64_t max_rows, int E, int height)

@@ -148,16 +148,25 @@ int moe_recv_ungroup(const void *grouped, const float *grouped_scales, int64_t m
  *   out        [max_rows, N] bf16 bits; rows of no run are not written. (out)
  *   preact     [max_rows, N] (MOE_ACT_SWIGLU: [max_rows, 2N]) bf16 bits of z
  *              rounded once, for the gradient; or NULL.               (out)
+ *   workspace  NULL, or device scratch of *workspace_bytes bytes, 256-byte
+ *              aligned, for calls of few outputs and a long sum, which share the
+ *              sum out (up to 8 times faster; the sums' order is then another,
+ *              and fixed too).  Its contents matter to no other call.
+ *   workspace_bytes  NULL, or a host pointer; with workspace NULL the size
+ *              needed (0: none) is written and nothing launched.  It depends on
+ *              E, max_rows, K, N and whether act is MOE_ACT_SWIGLU.
  *
  * Every array 16-byte aligned (offsets 4).  out and preact must not overlap
  * each other or the inputs (but for out == residual).
  * Errors: MOE_ERR_NULL; MOE_ERR_SHAPE; MOE_ERR_ALIGN; MOE_ERR_ALIAS (out or
  * preact starts where x or w does, or both at one place, or preact where
- * residual does).  max_rows == 0: MOE_OK, nothing launched.
+ * residual does); MOE_ERR_WORKSPACE when the workspace is too small or comes
+ * without a size.  max_rows == 0: MOE_OK, nothing launched.
  */
 int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, const float *bias,
                       int act, const void *residual, int E, int64_t max_rows, int K, int N,
-                      void *out, void *preact, hipStream_t stream);
+                      void *out, void *preact, void *workspace, size_t *workspace_bytes,
+                      hipStream_t stream);
 
 /*
  * moe_expert_matmul_dx -- gradient of a product's input rows, carried through
@@ -182,17 +191,10 @@ int moe_expert_matmul(const void *x, const int32_t *offsets, const void *w, cons
  *           written.                                                  (out)
  *   K, N    multiples of 16 in [16, 2 * MOE_MAX_HIDDEN] (N) and [16,
  *           MOE_MAX_HIDDEN] (K).
- *   workspace  NULL, or device scratch of *workspace_bytes bytes, 256-byte
- *           aligned, for calls of few outputs and a long sum, which share the
- *           sum out (up to 8 times faster; the sums' order is then another,
- *           and fixed too).  Its contents matter to no other call.
- *   workspace_bytes  NULL, or a host pointer; with workspace NULL the size
- *           needed (0: none) is written and nothing launched.  It depends on
- *           E, max_rows, K and N alone.
+ *   workspace, workspace_bytes   as moe_expert_matmul.
  *
  * Every array 16-byte aligned (offsets 4).  Errors: as moe_expert_matmul;
- * MOE_ERR_ALIAS when dx starts where dy or w does; MOE_ERR_WORKSPACE when the
- * workspace is too small or comes without a size.
+ * MOE_ERR_ALIAS when dx starts where dy or w does.
  */
 int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, int act,
                          const void *preact, int E, int64_t max_rows, int K, int N, void *dx,
@@ -216,7 +218,7 @@ int moe_expert_matmul_dx(const void *dy, const int32_t *offsets, const void *w, 
  *            MOE_GRAD_ACCUMULATE.
  *   dw       [E, N, K] fp32 or bf16 bits.                             (out)
  *   dbias    [E, N] fp32, or NULL.                                    (out)
- *   workspace, workspace_bytes   as moe_expert_matmul_dx.
+ *   workspace, workspace_bytes   as moe_expert_matmul.
  *
  * Every array 16-byte aligned (offsets 4).  Errors: MOE_ERR_NULL (dy and x
  * may be NULL when max_rows == 0), MOE_ERR_SHAPE (also unknown flags),

@@ -246,11 +246,24 @@ def test_dw(lengths, K, N, act):
 # few outputs and long sums, which several workgroups share
 LONG_DX = [([130, 0, 70], 144, 8192, SWIGLU), ([1], 16, 4096, NONE), ([1200], 48, 6384, SILU), ([64, 1, 63, 65, 200], 272, 2064, GELU),
            ([3] * 20, 384, 16400, RELU)]
+LONG = [([2000, 0, 100], 4096, 384, SILU, True, True, True), ([1900, 70, 1], 8192, 192, SWIGLU, True, True, True),
+        ([8000], 8192, 48, NONE, False, False, False), ([900, 1100, 64], 6160, 368, GELU, True, False, True)]
 LONG_DW = [([15000, 707], 192, 544, NONE), ([9, 30000, 0], 16, 16, NONE), ([8192], 1040, 272, NONE), ([0, 0, 9000], 128, 80, NONE)]
 
 
 def workspace_of(name, lengths, spare, K, N):
-    return B.expert_grad_workspace_bytes("moe_expert_matmul_" + name, len(lengths), sum(lengths) + spare, K, N)
+    return B.expert_workspace_bytes("moe_expert_matmul_" + name, len(lengths), sum(lengths) + spare, K, N)
+
+
+@pytest.mark.parametrize("case", LONG, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}a{c[3]}" for c in LONG])
+def test_product_in_parts(case):
+    lengths, K, N, act = case[:4]
+    assert B.expert_workspace_bytes("moe_expert_matmul", len(lengths), sum(lengths) + 3, K, N, act) > 0
+    x, w, b, res, off, out, pre = check_product(*case)
+    space = torch.full((1 << 22,), float("nan"), device="cuda")
+    again = torch.full_like(out, CANARY)
+    B.moe_expert_matmul(x, off, w, b, act, res, again, pre, workspace=space)
+    assert torch.equal(out, again)
 
 
 @pytest.mark.parametrize("lengths,K,N,act", LONG_DX, ids=[f"E{len(c[0])}r{sum(c[0])}K{c[1]}N{c[2]}a{c[3]}" for c in LONG_DX])

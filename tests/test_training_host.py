@@ -77,8 +77,8 @@ def test_combine_grad(lib):
 
 
 def test_expert_matmul(lib):
-    def f(x=F, off=F, w=G, b=None, act=0, res=None, E=2, rows=4, K=32, N=32, out=H, pre=None):
-        return lib.moe_expert_matmul(x, off, w, b, act, res, E, rows, K, N, out, pre, None)
+    def f(x=F, off=F, w=G, b=None, act=0, res=None, E=2, rows=4, K=32, N=32, out=H, pre=None, ws=None, size=None):
+        return lib.moe_expert_matmul(x, off, w, b, act, res, E, rows, K, N, out, pre, ws, size, None)
     for bad in (dict(E=0), dict(E=1025), dict(rows=-1), dict(rows=2 ** 31), dict(K=0), dict(K=24), dict(K=65552),
                 dict(N=8), dict(N=40), dict(N=65552), dict(act=-1), dict(act=5)):
         assert f(**bad) == SHAPE, bad
@@ -121,15 +121,25 @@ def test_expert_matmul_gradients(lib):
 def test_expert_gradient_workspaces(lib):
     n = ctypes.c_size_t(7)
     none = [None] * 3
-    q = {"moe_expert_matmul_dx": lambda E, rows, K, N, s=n: lib.moe_expert_matmul_dx(
+    q = {"moe_expert_matmul": lambda E, rows, K, N, s=n: lib.moe_expert_matmul(
+             *none, None, 0, None, E, rows, K, N, None, None, None, ctypes.byref(s), None),
+         "moe_expert_matmul_dx": lambda E, rows, K, N, s=n: lib.moe_expert_matmul_dx(
              *none, 0, None, E, rows, K, N, None, None, ctypes.byref(s), None),
          "moe_expert_matmul_dw": lambda E, rows, K, N, s=n: lib.moe_expert_matmul_dw(
              *none, E, rows, K, N, 0, None, None, None, ctypes.byref(s), None)}
     for name, f in q.items():
-        assert f(1, 8192, 65552, 64) == SHAPE
+        assert f(1, 8192, 65552, 65552) == SHAPE
         for sizes in ((1, 0, 64, 64), (8, 8192, 7168, 7168), (300, 300, 16, 8192), (2, 64, 64, 64)):
-            assert f(*sizes) == OK and n.value == 0 == B.expert_grad_workspace_bytes(name, *sizes)
+            assert f(*sizes) == OK and n.value == 0 == B.expert_workspace_bytes(name, *sizes)
     assert q["moe_expert_matmul_dx"](2, 200, 128, 8192) == OK and n.value > 0 and n.value % 256 == 0
+    few = ctypes.c_size_t(n.value - 1)
+    assert q["moe_expert_matmul"](2, 4000, 8192, 128) == OK and n.value > 0
+    few = ctypes.c_size_t(n.value - 1)
+    call = lambda ws, size: lib.moe_expert_matmul(  # noqa: E731
+        F, F, G, None, 0, None, 2, 4000, 8192, 128, H, None, ws, size, None)
+    assert call(F, ctypes.byref(few)) == WORKSPACE and call(F, None) == WORKSPACE
+    assert call(EIGHT, ctypes.byref(n)) == ALIGN
+    assert q["moe_expert_matmul_dx"](2, 200, 128, 8192) == OK
     few = ctypes.c_size_t(n.value - 1)
     call = lambda ws, size: lib.moe_expert_matmul_dx(  # noqa: E731
         F, F, G, 0, None, 2, 200, 128, 8192, H, ws, size, None)
