@@ -19,6 +19,11 @@
 // the rows of a segment in block order (in double), so no result depends on
 // the order in which blocks or atomics ran.  A segment that fits one block
 // needs no second launch.
+//
+// HBM-bound from about 10^7 logits on: 131072 tokens of 512 experts take 51 us
+// (5.3 TB/s) and 11 for the join, the gradient 107 (5.0 TB/s, half of it
+// written); 16384 of 256 in four segments 7 + 6 and 10.5, latency; 256 of 8
+// 4.5 and 3.6.
 #include "common.hpp"
 #include "launch.hpp"
 
