@@ -151,7 +151,7 @@ int moe_recv_ungroup(const void *grouped, const float *grouped_scales, int64_t m
  *   workspace  NULL, or device scratch of *workspace_bytes bytes, 256-byte
  *              aligned, for calls of few outputs and a long sum, which share the
  *              sum out (up to 8 times faster; the sums' order is then another,
- *              and fixed too).  Its contents matter to no other call.
+ *              and fixed too).  Calls that may run at once need one each.
  *   workspace_bytes  NULL, or a host pointer; with workspace NULL the size
  *              needed (0: none) is written and nothing launched.  It depends on
  *              E, max_rows, K, N and whether act is MOE_ACT_SWIGLU.
