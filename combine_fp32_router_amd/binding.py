@@ -466,20 +466,27 @@ def moe_recv_ungroup(grouped: torch.Tensor, grouped_scales: torch.Tensor | None,
                                    _stream(stream)))
 
 
+# torch's own calls behind current_stream() and current_device(), without the
+# Stream object and the check for a first use: 1.3 us less a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _call(name: str, stream, *args) -> None:
     """Entry point `name` on `args`, its tensors as their addresses, and the
     stream: `stream`, or the current stream of the tensors' device.  The
     tensors must be contiguous and share one device, which is current during
     the call (a null stream is the current device's).  Plain ints and the
     argtypes rather than c_void_p objects: half the cost of a call."""
-    device, raw = -1, []
+    device, raw, tensor = None, [], torch.Tensor
     for a in args:
-        if isinstance(a, torch.Tensor):
+        if isinstance(a, tensor):
             d = a.get_device()
-            if d < 0:
-                raise ValueError("expected a device tensor")
             if d != device:
-                if device >= 0:
+                if d < 0:
+                    raise ValueError("expected a device tensor")
+                if device is not None:
                     raise ValueError(f"tensors on different devices: cuda:{device}, cuda:{d}")
                 device = d
             if not a.is_contiguous():
@@ -487,26 +494,29 @@ def _call(name: str, stream, *args) -> None:
             a = a.data_ptr()
         raw.append(a)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if isinstance(stream, torch.cuda.Stream):
+        stream = _raw_stream(device)
+    elif isinstance(stream, torch.cuda.Stream):
         if stream.device_index != device:
             raise ValueError(f"a stream of cuda:{stream.device_index}, tensors on cuda:{device}")
         stream = stream.cuda_stream
-    entry = getattr(load(), name)
-    if device == torch.cuda.current_device():
-        status = entry(*raw, int(stream))
+    else:
+        stream = int(stream)
+    entry = getattr(_lib or load(), name)
+    if device == _raw_device():
+        status = entry(*raw, stream)
     else:
         with torch.cuda.device(device):
-            status = entry(*raw, int(stream))
-    _check(name, status)
+            status = entry(*raw, stream)
+    if status:
+        _check(name, status)
 
 
 def _want_bf16(t: torch.Tensor, shape, name: str):
     """bf16 values (or their int16/uint16 bits) of exactly `shape`."""
     if t.element_size() != 2:
         raise ValueError(f"{name} must hold bf16 bits")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
 
 
 class Balance(NamedTuple):
@@ -547,13 +557,14 @@ def _want_mask(mask: torch.Tensor | None, T: int):
 
 
 def _want_segments(b: Balance, T: int, E: int):
-    S = max(1, -(-T // b.seg_tokens))
-    _want(b.loss, torch.float32, "loss")
-    _want(b.expert_counts, torch.int32, "expert_counts")
-    _want(b.prob_sums, torch.float32, "prob_sums")
-    _want(b.tokens, torch.int32, "tokens")
-    if (b.loss.numel() < S or b.tokens.numel() < S or b.expert_counts.numel() < S * E or
-            b.prob_sums.numel() < S * E):
+    loss, counts, sums, tokens, _, seg_tokens = b
+    S = max(1, -(-T // seg_tokens))
+    _want(loss, torch.float32, "loss")
+    _want(counts, torch.int32, "expert_counts")
+    _want(sums, torch.float32, "prob_sums")
+    _want(tokens, torch.int32, "tokens")
+    if (loss.numel() < S or tokens.numel() < S or counts.numel() < S * E or
+            sums.numel() < S * E):
         raise ValueError("Balance buffers too small")
 
 
