@@ -31,6 +31,7 @@ namespace moe {
 namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 template <int CTRL>
 __device__ __forceinline__ float dppf(float v)
@@ -385,10 +386,23 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
     }
     if (dloss) {
         float c[NE];
+        if constexpr (VEC) {
 #pragma unroll
-        for (int q = 0; q < NE; ++q) {
-            const int ee = expert_of<L, VEC>(q, sub);
-            c[q] = ee < E ? static_cast<float>(counts[s * E + ee]) : 0.0f;
+            for (int i = 0; i < NE / 4; ++i) {
+                const int ee = expert_of<L, VEC>(4 * i, sub);
+                i32x4 x{};
+                if (ee < E)
+                    x = *reinterpret_cast<const i32x4 *>(counts + s * E + ee);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    c[4 * i + q] = static_cast<float>(x[q]);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < NE; ++q) {
+                const int ee = expert_of<L, VEC>(q, sub);
+                c[q] = ee < E ? static_cast<float>(counts[s * E + ee]) : 0.0f;
+            }
         }
         const float n = fmaxf(static_cast<float>(live_tokens[s]), 1.0f);
         const float scale = dloss[s] * (static_cast<float>(E) / static_cast<float>(k)) / n / n;
@@ -547,7 +561,7 @@ hipError_t launch_route_grad(const float *logits, const int32_t *idx, const floa
                              const int32_t *counts, const int32_t *live, int64_t T, int64_t seg,
                              int E, int k, float *dlogits, hipStream_t stream)
 {
-    const bool vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) |
+    const bool vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(counts) |
                                      reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
     const dim3 grid(static_cast<unsigned>(route_grad_blocks(seg, E)), layout_chunks(T, seg));
 #define MOE_ROUTE_GRAD(L, NE, V)                                                               \
