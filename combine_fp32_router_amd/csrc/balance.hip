@@ -20,10 +20,10 @@
 // the order in which blocks or atomics ran.  A segment that fits one block
 // needs no second launch.
 //
-// HBM-bound from about 10^7 logits on: 131072 tokens of 512 experts take 51 us
-// (5.3 TB/s) and 11 for the join, the gradient 107 (5.0 TB/s, half of it
-// written); 16384 of 256 in four segments 7 + 6 and 10.5, latency; 256 of 8
-// 4.5 and 3.6.
+// HBM-bound from about 10^7 logits on: 131072 tokens of 512 experts take 49 us
+// (5.5 TB/s) and 8 for the join, the gradient 92 (5.8 TB/s, half of it
+// written); 16384 of 256 in four segments 7.6 + 6.4 and 8.4, latency; 256 of 8
+// 4.4 and 3.8.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -352,8 +352,8 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float *__restr
 // side; the last ones first, for if the balance loss has just read the logits,
 // what the last-level cache still has of them is their end.  So that it stays
 // there, the gradient is written past it, and the logits are read for the last
-// time.  131072 tokens of 512 experts, both calls: 170 us, 192 front to back
-// with ordinary loads and stores; 131072 of 256: 97 and 112.
+// time.  Front to back with ordinary loads and stores both calls took 22 us longer
+// for 131072 tokens of 512 experts (now 154 us), 15 for 256 (now 80).
 constexpr int kGradTokens = 2;
 
 template <int L, int NE, bool VEC>
@@ -472,8 +472,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
     }
 }
 
-// Blocks of a segment and their tokens: about 1024 blocks over the batch,
-// none under 32 tokens.  Short segments have one block each, and no join, if
+// Blocks of a segment and their tokens: about 512 blocks over the batch (1024
+// leave the join twice the rows: 131072 tokens of 256 experts 84 us instead of
+// 79), none under 32 tokens.  Short segments have one block each, and no join, if
 // they are many or of few logits (256 tokens of 8 experts: 4.4 us; 16 segments of
 // 256 tokens of 256: 10.3, 11.7 with a join; but five of 235 tokens of 995: 57, 19
 // with a join).
@@ -482,7 +483,7 @@ struct BalanceTiling {
 };
 BalanceTiling balance_tiling(int64_t T, int64_t seg, int E)
 {
-    int64_t tpb = (T + 1023) / 1024;
+    int64_t tpb = (T + 511) / 512;
     tpb = tpb < 32 ? 32 : (tpb + 15) / 16 * 16;
     if (tpb > seg || (seg <= 256 && (T >= (E <= 256 ? 16 : 128) * seg || seg * E <= 32768)))
         tpb = seg > 0 ? seg : 1;
@@ -526,7 +527,7 @@ hipError_t launch_balance_loss(const float *logits, const int32_t *idx, const ui
     const BalanceOut out{loss, counts, prob_sums, live};
     const bool vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
     const bool one = bt.blocks == 1;
-    const int threads = one && E <= 256 ? 1024 : 256;
+    const int threads = one && E <= 256 ? 1024 : E <= 512 ? 512 : 256;
     const size_t lds = (static_cast<size_t>(threads / kWave) * E + E + 1) * 4;
     const dim3 grid(bt.blocks, S);
 #define MOE_BALANCE(L, NE, V)                                                                  \
