@@ -16,10 +16,13 @@
 // 8 slots: gates alone (read) 149 us, 7.1 TB/s; rows alone (write) 183, 5.8;
 // both in one kernel 376, since reads and writes then take turns in HBM
 // throughout, and in two launches, first all reads, 332.  With rows of one
-// byte or less that saves nothing (int8: 286 against 289).  Rows that the
-// last-level cache holds are written with ordinary stores (2048 tokens: 81 us
-// against 97; 4096 of 2048 int8: 36 against 43) and in one launch (81 against
-// 84); past it streaming stores are faster (376 against 405).
+// byte or less that saves nothing (int8: 286 against 289).
+// Few rows are written with ordinary stores and in one launch, many with
+// streaming stores, which do not push other data out of the last-level cache
+// (in turn over four sets of buffers, ordinary / streaming: 67 MB of rows
+// 28.0 / 28.4 us, 34 MB 21.8 / 23.2, 134 MB int8 46.5 / 43.4, 117 MB 53.6 / 46.4,
+// 235 MB 104 / 88; over one set, which the cache holds, ordinary ones take 36
+// instead of 43 for the 134).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -27,7 +30,7 @@ namespace moe {
 namespace {
 
 constexpr int kSlotGroup = 4;  // slots whose row loads are in flight together
-constexpr int64_t kLastLevelBytes = 256 << 20;  // the cache behind the eight L2s
+constexpr int64_t kManyBytes = 100 << 20;  // of written rows: streaming stores
 
 __device__ __forceinline__ float wave_sum(float v)
 {
@@ -157,7 +160,7 @@ void launch_format(const void *d_out, const void *rows, const float *scales, con
     const int G = H / 8;
     const RowTiling rt = row_tiling(G);
     const dim3 grid(static_cast<unsigned>(T)), block(rt.threads);
-    const bool large = T * k * H * 2 > kLastLevelBytes;
+    const bool large = T * k * H * 2 > kManyBytes;
 #define MOE_CG(V, R, W, S)                                                                     \
     combine_grad_kernel<Q, V, R, W, S><<<grid, block, 0, stream>>>(                            \
         static_cast<const u32x4 *>(d_out), rows, scales, pos, w, G, k,                         \
