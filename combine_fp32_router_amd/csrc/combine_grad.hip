@@ -30,6 +30,7 @@ namespace moe {
 namespace {
 
 constexpr int kSlotGroup = 4;  // slots whose row loads are in flight together
+constexpr int kNarrowTokens = 4;  // of a block, short rows
 constexpr int64_t kManyBytes = 100 << 20;  // of written rows: streaming stores
 
 __device__ __forceinline__ float wave_sum(float v)
@@ -152,15 +153,91 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
     }
 }
 
+// Short rows, of at most LG <= 16 groups of eight elements: a wave has one
+// token, and each LG of its lanes a slot.  16 slots of 32 elements int8, 26560
+// tokens: 26 us, 50 with a block a token; 8 of 64 bf16, 16000 tokens: 10 and 19; 8
+// of 128 int4, 30000: 28 and 35.  (LG = 32, 8 of 256 int8, 30000: 60 and 45.)
+template <int Q, int LG, bool ROWS, bool GATES>
+__global__ __launch_bounds__(kNarrowTokens *kWave) void combine_grad_narrow_kernel(
+    const u32x4 *__restrict__ d_out, const void *__restrict__ rows_,
+    const float *__restrict__ scales, const int32_t *__restrict__ pos,
+    const float *__restrict__ w, int64_t T, int G, int k, bool stream, u32x4 *__restrict__ d_rows,
+    float *__restrict__ d_w)
+{
+    typedef RowVec<Q> RV;
+    constexpr int kSlots = kWave / LG;
+    const typename RV::vec *rows = static_cast<const typename RV::vec *>(rows_);
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kNarrowTokens + threadIdx.x / kWave;
+    if (t >= T)
+        return;
+    const int g = lane_id() % LG, sub = lane_id() / LG;
+    float d[8];
+    unpack8(g < G ? d_out[t * G + g] : u32x4{0, 0, 0, 0}, d);
+#pragma unroll 4
+    for (int j0 = 0; j0 < k; j0 += kSlots) {
+        const int j = j0 + sub;
+        const int32_t p = j < k ? pos[t * k + j] : -1;
+        const bool in = p >= 0 && g < G;
+        typename RV::vec v{};
+        float scale = 1.0f;
+        if (GATES && in) {
+            v = __builtin_nontemporal_load(rows + static_cast<int64_t>(p) * G + g);
+            if (Q != 0)
+                scale = scales[p];
+        }
+        if (ROWS && in) {
+            const float wj = w[t * k + j];
+            float f[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                f[c] = wj * d[c];
+            u32x4 *at_row = d_rows + static_cast<int64_t>(p) * G + g;
+            if (stream)
+                __builtin_nontemporal_store(pack8(f), at_row);
+            else
+                *at_row = pack8(f);
+        }
+        if (GATES) {
+            float f[8], dot = 0.0f;
+            RV::get(v, f);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                dot = fmaf(d[c], f[c], dot);
+#pragma unroll
+            for (int o = LG / 2; o > 0; o >>= 1)
+                dot += __shfl_xor(dot, o);
+            if (g == 0 && j < k)
+                d_w[t * k + j] = p < 0 ? 0.0f : Q != 0 ? dot * scale : dot;
+        }
+    }
+}
+
 template <int Q>
 void launch_format(const void *d_out, const void *rows, const float *scales, const int32_t *pos,
                    const float *w, int64_t T, int H, int k, void *d_rows, float *d_w,
                    hipStream_t stream)
 {
     const int G = H / 8;
+    const bool large = T * k * H * 2 > kManyBytes;
+    if (G <= 16) {
+        const dim3 blocks(static_cast<unsigned>((T + kNarrowTokens - 1) / kNarrowTokens));
+#define MOE_CG_NARROW(LG, R, W)                                                                \
+    combine_grad_narrow_kernel<Q, LG, R, W><<<blocks, kNarrowTokens * kWave, 0, stream>>>(     \
+        static_cast<const u32x4 *>(d_out), rows, scales, pos, w, T, G, k, large,               \
+        static_cast<u32x4 *>(d_rows), d_w)
+#define MOE_CG_NARROW_PARTS(LG)                                                                \
+    if (d_rows && d_w) { MOE_CG_NARROW(LG, true, true); }                                      \
+    else if (d_rows) { MOE_CG_NARROW(LG, true, false); }                                       \
+    else { MOE_CG_NARROW(LG, false, true); }
+        if (G <= 2) { MOE_CG_NARROW_PARTS(2) }
+        else if (G <= 8) { MOE_CG_NARROW_PARTS(8) }
+        else { MOE_CG_NARROW_PARTS(16) }
+#undef MOE_CG_NARROW_PARTS
+#undef MOE_CG_NARROW
+        return;
+    }
     const RowTiling rt = row_tiling(G);
     const dim3 grid(static_cast<unsigned>(T)), block(rt.threads);
-    const bool large = T * k * H * 2 > kManyBytes;
 #define MOE_CG(V, R, W, S)                                                                     \
     combine_grad_kernel<Q, V, R, W, S><<<grid, block, 0, stream>>>(                            \
         static_cast<const u32x4 *>(d_out), rows, scales, pos, w, G, k,                         \

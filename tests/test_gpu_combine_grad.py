@@ -77,6 +77,14 @@ def test_combine_grad(T, H, k, quant, dropped, parts):
 
 
 @pytest.mark.parametrize("parts", ["both", "rows", "gates"])
+@pytest.mark.parametrize("T,H,k,quant,dropped", [(1, 16, 16, 0, 0.0), (4097, 16, 10, 1, 0.5), (333, 32, 16, 2, 0.1), (50, 64, 7, 3, 0.2),
+                                                 (1001, 48, 9, 0, 0.1), (77, 96, 12, 1, 0.1), (6, 256, 3, 2, 0.3), (500, 240, 16, 0, 0.0),
+                                                 (30, 272, 5, 1, 0.1), (30000, 256, 8, 0, 0.1), (30000, 256, 8, 3, 0.1)])
+def test_short_rows(T, H, k, quant, dropped, parts):
+    test_combine_grad(T, H, k, quant, dropped, parts)
+
+
+@pytest.mark.parametrize("parts", ["both", "rows", "gates"])
 @pytest.mark.parametrize("quant", range(4))
 def test_rows_past_the_last_level_cache(quant, parts):
     """More than 256 MiB of gradient rows."""
