@@ -51,34 +51,32 @@ __device__ __forceinline__ float sigmoid(float z)
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
 }
 
-// Q(z) = erfc(z / sqrt 2) / 2 for z >= 0, the normal distribution's upper
-// tail: with x = z / sqrt 2 and t = 1 / (1 + x/2), erfc(x) = t exp(-x^2 + p(t)),
-// p a polynomial fitted to log(erfc(x) exp(x^2) / t) on [0, 9.6] (off by
-// 5e-8).  In fp32 good to 2e-6 of the result for z < 5.6, 4e-7 absolute.
-// `gauss` gets exp(-z^2 / 2).
-__device__ __forceinline__ float normal_tail(float z, float &gauss)
+// The normal distribution function, branchless, from its tail Q(z) = erfc(z /
+// sqrt 2) / 2 for z >= 0: with x = z / sqrt 2 and t = 1 / (1 + x/2), erfc(x) = t
+// exp(-x^2 + r(t)), r a polynomial fitted to log(erfc(x) exp(x^2) / t) on [0,
+// 9.6] (off by 5e-8); p has it in base 2, with the half.  In fp32 Q is good to
+// 1.3e-6 of itself for z < 5.6, 1.3e-7 absolute.
+__device__ __forceinline__ float normal_below(float z)
 {
-    const float x = z * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.5f, x, 1.0f));
-    float p = 0.14144114f;
-    p = fmaf(p, t, -0.6617397f);
-    p = fmaf(p, t, 1.1115944f);
-    p = fmaf(p, t, -0.6358495f);
-    p = fmaf(p, t, -0.13053308f);
-    p = fmaf(p, t, 0.028138269f);
-    p = fmaf(p, t, 0.025399053f);
-    p = fmaf(p, t, 0.3885812f);
-    p = fmaf(p, t, 0.99840486f);
-    p = fmaf(p, t, -1.2654366f);
-    gauss = __builtin_amdgcn_exp2f(x * x * -1.44269504088896341f);
-    return 0.5f * t * (gauss * __builtin_amdgcn_exp2f(p * 1.44269504088896341f));
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.35355339f, 1.0f));
+    float p = 0.20405643f;
+    p = fmaf(p, t, -0.95468861f);
+    p = fmaf(p, t, 1.6036917f);
+    p = fmaf(p, t, -0.91733694f);
+    p = fmaf(p, t, -0.18831943f);
+    p = fmaf(p, t, 0.040594943f);
+    p = fmaf(p, t, 0.036643088f);
+    p = fmaf(p, t, 0.56060416f);
+    p = fmaf(p, t, 1.4403937f);
+    p = fmaf(p, t, -2.8256390f);
+    const float q = t * __builtin_amdgcn_exp2f(fmaf(z * z, -0.72134752f, p));
+    return z < 0.0f ? q : 1.0f - q;
 }
 
-// The normal distribution function, branchless; `gauss` as above.
-__device__ __forceinline__ float normal_below(float z, float &gauss)
+// Its density.
+__device__ __forceinline__ float normal_density(float z)
 {
-    const float q = normal_tail(fabsf(z), gauss);
-    return z < 0.0f ? q : 1.0f - q;
+    return __builtin_amdgcn_exp2f(fmaf(z * z, -0.72134752f, -1.3257480f));
 }
 
 // v[i][j] = act(v[i][j]) for the activations of one value.
@@ -95,10 +93,8 @@ __device__ __forceinline__ void apply_act(V (&v)[N], int act)
             v[i / 4][i % 4] *= sigmoid(v[i / 4][i % 4]);
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 4 * N; ++i) {
-            float gauss;
-            v[i / 4][i % 4] *= normal_below(v[i / 4][i % 4], gauss);
-        }
+        for (int i = 0; i < 4 * N; ++i)
+            v[i / 4][i % 4] *= normal_below(v[i / 4][i % 4]);
     }
 }
 
@@ -120,9 +116,7 @@ __device__ __forceinline__ void apply_slope(V (&v)[N], const V (&z)[N], int act)
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i) {
             const float x = z[i / 4][i % 4];
-            float gauss;
-            const float below = normal_below(x, gauss);
-            v[i / 4][i % 4] *= below + x * (gauss * 0.39894228040143268f);
+            v[i / 4][i % 4] *= fmaf(x, normal_density(x), normal_below(x));
         }
     }
 }
