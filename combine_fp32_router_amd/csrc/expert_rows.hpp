@@ -79,14 +79,15 @@ __device__ __forceinline__ float normal_density(float z)
     return __builtin_amdgcn_exp2f(fmaf(z * z, -0.72134752f, -1.3257480f));
 }
 
-// v[i][j] = act(v[i][j]) for the activations of one value.
+// v[i][j] = act(v[i][j]) for the activations of one value.  A NaN stays one
+// (a maximum with 0 would make it 0).
 template <int N, typename V>
 __device__ __forceinline__ void apply_act(V (&v)[N], int act)
 {
     if (act == MOE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i)
-            v[i / 4][i % 4] = fmaxf(v[i / 4][i % 4], 0.0f);
+            v[i / 4][i % 4] = v[i / 4][i % 4] <= 0.0f ? 0.0f : v[i / 4][i % 4];
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i)
@@ -98,14 +99,15 @@ __device__ __forceinline__ void apply_act(V (&v)[N], int act)
     }
 }
 
-// v[i][j] *= act'(z[i][j]).
+// v[i][j] *= act'(z[i][j]).  ReLU stops a gradient where z <= 0, so not at a
+// NaN.
 template <int N, typename V>
 __device__ __forceinline__ void apply_slope(V (&v)[N], const V (&z)[N], int act)
 {
     if (act == MOE_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i)
-            v[i / 4][i % 4] = z[i / 4][i % 4] > 0.0f ? v[i / 4][i % 4] : 0.0f;
+            v[i / 4][i % 4] = z[i / 4][i % 4] <= 0.0f ? 0.0f : v[i / 4][i % 4];
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
         for (int i = 0; i < 4 * N; ++i) {

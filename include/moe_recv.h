@@ -117,7 +117,7 @@ int moe_recv_ungroup(const void *grouped, const float *grouped_scales, int64_t m
 
 /* Activations of the experts' products. */
 #define MOE_ACT_NONE 0   /* z                                                */
-#define MOE_ACT_RELU 1   /* max(z, 0); slope 0 at 0                          */
+#define MOE_ACT_RELU 1   /* 0 where z <= 0 (slope 0), else z: NaN stays NaN  */
 #define MOE_ACT_SILU 2   /* z / (1 + exp(-z))                                */
 #define MOE_ACT_GELU 3   /* z (1 + erf(z / sqrt 2)) / 2                      */
 #define MOE_ACT_SWIGLU 4 /* silu(z_gate) * z_up: two columns of z per output */
