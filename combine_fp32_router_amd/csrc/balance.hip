@@ -414,9 +414,10 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
             for (int q = 0; q < NE; ++q)
                 dot = fmaf(c[q], d[u][q], dot);
             dot = group_sum<L>(dot);
+            const float by = live[u] ? scale : 0.0f;  // a masked row's 0 times an infinite scale would be NaN
 #pragma unroll
             for (int q = 0; q < NE; ++q)
-                d[u][q] = d[u][q] * (c[q] - dot) * scale;
+                d[u][q] = d[u][q] * (c[q] - dot) * by;
         }
     } else {
 #pragma unroll

@@ -447,7 +447,8 @@ int moe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t
  *                 occurs twice gets both contributions, one outside [0, E)
  *                 none.  Not used when d_topk_w is NULL.               (in)
  *   d_topk_w      [T, k] fp32 gradient of the gate weights, or NULL.   (in)
- *   d_loss        [S] fp32 gradient of each segment's loss, or NULL.   (in)
+ *   d_loss        [S] fp32 gradient of each segment's loss, or NULL; the value
+ *                 of a segment without live tokens may be anything.    (in)
  *   expert_counts, seg_live   from moe_balance_loss.                   (in)
  *   d_logits      [T, E] fp32; may be logits itself.                  (out)
  *

@@ -53,3 +53,29 @@ def test_gradient_passes_a_nan_of_relu(rows, K, N):
     want, = torch.autograd.grad(torch.relu(zz), zz, want)
     assert want[1, 5] != 0 and want[2, 2] == 0
     R.inside(dx, want, tol, "dx")
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (64, 4), (66, 2), (300, 3), (1024, 8)])
+def test_masked_rows_stay_zero_for_any_loss_gradient(E, k):
+    """A segment without live tokens may carry an infinite weight (one over its
+    tokens, say): its rows, and a masked token's of any segment, are zeros."""
+    T, seg = 70, 16
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    idx = logits.topk(k, 1).indices.int()
+    w, d_w = torch.rand(T, k, generator=g, device="cuda"), torch.randn(T, k, generator=g, device="cuda")
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.6).to(torch.uint8)
+    mask[16:32] = 0
+    mask[32:34] = torch.tensor([1, 0])
+    bal = B.moe_balance_loss(logits, idx, mask, B.alloc_balance(T, seg, E, k, "cuda"))
+    plain, odd = torch.tensor([0.5, 0.0, 2.0, 1.0, 3.0], device="cuda"), torch.empty(5, device="cuda")
+    odd.copy_(plain)
+    odd[1], odd[2], odd[4] = float("inf"), float("nan"), -float("inf")
+    for weights in (d_w, None):
+        want, got = torch.empty_like(logits), torch.empty_like(logits)
+        gates = w if weights is not None else None
+        B.moe_route_grad(logits, idx, gates, weights, mask, plain, bal, want)
+        B.moe_route_grad(logits, idx, gates, weights, mask, odd, bal, got)
+        assert not want[mask == 0].any() and not got[mask == 0].any()
+        assert torch.equal(got[:16], want[:16]) and torch.equal(got[48:64], want[48:64])
+        assert not torch.isfinite(got[32:48][mask[32:48] != 0]).all(1).any()
