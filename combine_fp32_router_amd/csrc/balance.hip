@@ -358,10 +358,10 @@ constexpr int kGradTokens = 2;
 
 template <int L, int NE, bool VEC>
 __global__ __launch_bounds__(256) void route_grad_kernel(
-    const float *__restrict__ logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
+    const float *logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
     const float *__restrict__ dw, const uint8_t *__restrict__ mask, const float *__restrict__ dloss,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ live_tokens, int64_t T,
-    int64_t seg, int E, int k, float *__restrict__ dlogits)
+    int64_t seg, int E, int k, float *dlogits)  // dlogits may be logits
 {
     constexpr int G = 256 / L, kRow = L * NE;  // tokens at a time; experts a row has room for
     __shared__ __align__(16) float rows[G * kRow];

@@ -79,3 +79,19 @@ def test_masked_rows_stay_zero_for_any_loss_gradient(E, k):
         assert not want[mask == 0].any() and not got[mask == 0].any()
         assert torch.equal(got[:16], want[:16]) and torch.equal(got[48:64], want[48:64])
         assert not torch.isfinite(got[32:48][mask[32:48] != 0]).all(1).any()
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (33, 4), (64, 4), (256, 8), (300, 3), (515, 5), (1024, 8)])
+def test_router_gradient_over_its_own_logits(E, k):
+    """d_logits may be logits: the same bits as apart from them."""
+    T, seg = 1001, 400
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    idx = logits.topk(k, 1).indices.int()
+    w, d_w = torch.rand(T, k, generator=g, device="cuda"), torch.randn(T, k, generator=g, device="cuda")
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.8).to(torch.uint8)
+    bal = B.moe_balance_loss(logits, idx, mask, B.alloc_balance(T, seg, E, k, "cuda"))
+    d_loss, apart = torch.randn(3, generator=g, device="cuda") * T, torch.empty_like(logits)
+    B.moe_route_grad(logits, idx, w, d_w, mask, d_loss, bal, apart)
+    B.moe_route_grad(logits, idx, w, d_w, mask, d_loss, bal, logits)
+    assert torch.equal(apart, logits)
