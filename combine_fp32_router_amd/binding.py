@@ -35,6 +35,7 @@ EXPORTS = ("moe_route_topk", "moe_dispatch_layout", "moe_dispatch_layout_chunks"
 
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = range(5)
 MOE_GRAD_FP32, MOE_GRAD_BF16, MOE_GRAD_ACCUMULATE = 0, 1, 0x100
+MOE_ROUTE_MASKED_GATES = 0x100  # OR into the k of moe_route_grad's entry point
 
 _lib = None
 
@@ -589,10 +590,12 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor,
 def moe_route_grad(logits: torch.Tensor | None, topk_idx: torch.Tensor,
                    topk_w: torch.Tensor | None, d_topk_w: torch.Tensor | None,
                    token_mask: torch.Tensor | None, d_loss: torch.Tensor | None,
-                   balance: Balance | None, d_logits: torch.Tensor, stream=None) -> torch.Tensor:
+                   balance: Balance | None, d_logits: torch.Tensor, stream=None,
+                   masked_gates: bool = False) -> torch.Tensor:
     """Gradient of the router's logits [T, E] from that of the gate weights
     (d_topk_w [T, k] or None) and of the balance loss (d_loss [S] with the
-    forward call's Balance, or None for both)."""
+    forward call's Balance, or None for both).  A masked token's row is zero;
+    with masked_gates it keeps the part through the gate weights."""
     _want(d_logits, torch.float32, "d_logits")
     _want(topk_idx, torch.int32, "topk_idx")
     T, E = d_logits.shape
@@ -621,7 +624,7 @@ def moe_route_grad(logits: torch.Tensor | None, topk_idx: torch.Tensor,
     live = balance.tokens if d_loss is not None else None
     seg = balance.seg_tokens if d_loss is not None else max(T, 1)
     _call("moe_route_grad", stream, logits, topk_idx, topk_w, d_topk_w, token_mask, d_loss, counts,
-          live, T, seg, E, k, d_logits)
+          live, T, seg, E, k | MOE_ROUTE_MASKED_GATES if masked_gates else k, d_logits)
     return d_logits
 
 

@@ -428,6 +428,9 @@ int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *to
                    const int32_t *expert_counts, const int32_t *seg_live, int64_t T,
                    int64_t seg_tokens, int E, int k, float *d_logits, hipStream_t stream)
 {
+    const bool masked_gates = k >= 0 && (k & MOE_ROUTE_MASKED_GATES) != 0;
+    if (masked_gates)
+        k &= ~MOE_ROUTE_MASKED_GATES;
     if (check_segments(T, seg_tokens, E, k) != MOE_OK ||
         !grid_fits(route_grad_blocks(seg_tokens, E), kRouteThreads))
         return MOE_ERR_SHAPE;
@@ -441,8 +444,8 @@ int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *to
         !aligned(seg_live, 4) || !aligned(d_logits, 4))
         return MOE_ERR_ALIGN;
     return hip_status(moe::launch_route_grad(logits, topk_idx, topk_w, d_topk_w, token_mask, d_loss,
-                                             expert_counts, seg_live, T, seg_tokens, E, k, d_logits,
-                                             stream));
+                                             expert_counts, seg_live, T, seg_tokens, E, k,
+                                             masked_gates, d_logits, stream));
 }
 
 int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv_scales, int quant,

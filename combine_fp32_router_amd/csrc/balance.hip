@@ -361,7 +361,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
     const float *logits, const int32_t *__restrict__ idx, const float *__restrict__ w,
     const float *__restrict__ dw, const uint8_t *__restrict__ mask, const float *__restrict__ dloss,
     const int32_t *__restrict__ counts, const int32_t *__restrict__ live_tokens, int64_t T,
-    int64_t seg, int E, int k, float *dlogits)  // dlogits may be logits
+    int64_t seg, int E, int k, bool masked_gates, float *dlogits)  // dlogits may be logits
 {
     constexpr int G = 256 / L, kRow = L * NE;  // tokens at a time; experts a row has room for
     __shared__ __align__(16) float rows[G * kRow];
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(
         if (dloss)
             load_row<L, NE, VEC, true>(logits + t * E, E, sub, live[u], d[u]);
         // lane j of the token holds slot j
-        const bool slot = dw && sub < k && live[u];
+        const bool slot = dw && sub < k && (masked_gates ? t < end : live[u]);
         e[u] = slot ? idx[t * k + sub] : -1;
         wj[u] = slot ? w[t * k + sub] : 0.0f;
         dwj[u] = slot ? dw[t * k + sub] : 0.0f;
@@ -561,14 +561,14 @@ int64_t route_grad_blocks(int64_t seg, int E)
 hipError_t launch_route_grad(const float *logits, const int32_t *idx, const float *w,
                              const float *dw, const uint8_t *mask, const float *dloss,
                              const int32_t *counts, const int32_t *live, int64_t T, int64_t seg,
-                             int E, int k, float *dlogits, hipStream_t stream)
+                             int E, int k, bool masked_gates, float *dlogits, hipStream_t stream)
 {
     const bool vec = E % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(counts) |
                                      reinterpret_cast<uintptr_t>(dlogits)) & 15) == 0;
     const dim3 grid(static_cast<unsigned>(route_grad_blocks(seg, E)), layout_chunks(T, seg));
 #define MOE_ROUTE_GRAD(L, NE, V)                                                               \
-    route_grad_kernel<L, NE, V><<<grid, 256, 0, stream>>>(logits, idx, w, dw, mask, dloss,     \
-                                                          counts, live, T, seg, E, k, dlogits)
+    route_grad_kernel<L, NE, V><<<grid, 256, 0, stream>>>(                                     \
+        logits, idx, w, dw, mask, dloss, counts, live, T, seg, E, k, masked_gates, dlogits)
     MOE_ROUTER_SHAPE(E, vec, MOE_ROUTE_GRAD)
 #undef MOE_ROUTE_GRAD
     return hipGetLastError();

@@ -106,7 +106,7 @@ int64_t route_grad_blocks(int64_t seg, int E);  // of a segment, of kRouteThread
 hipError_t launch_route_grad(const float *logits, const int32_t *idx, const float *w,
                              const float *dw, const uint8_t *mask, const float *dloss,
                              const int32_t *counts, const int32_t *live, int64_t T, int64_t seg,
-                             int E, int k, float *dlogits, hipStream_t stream);
+                             int E, int k, bool masked_gates, float *dlogits, hipStream_t stream);
 
 // Gradient of the combine; d_rows or d_w may be null.
 hipError_t launch_combine_grad(const void *d_out, const void *rows, const float *scales, int quant,

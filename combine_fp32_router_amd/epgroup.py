@@ -216,13 +216,17 @@ class EPGroup:
     @_group_device
     def backward(self, d_out: torch.Tensor, d_x: torch.Tensor | None, d_logits: torch.Tensor,
                  grads: ExpertGrads | None = None, d_loss: torch.Tensor | None = None,
-                 accumulate: bool = False, timer: KernelTimer | None = None):
+                 accumulate: bool = False, timer: KernelTimer | None = None,
+                 masked_gates: bool = False):
         """Gradients of the last run() from that of its output (d_out bf16
         [T, H]) and of its balance loss (d_loss fp32, one value per segment,
         or None): d_x bf16 [T, H] or None, d_logits fp32 [T, E], the experts'
         grads or None.  The run's logits, mask, Balance and this group's
         buffers must still hold what the run left in them.  Tokens that
-        token_mask leaves out get no logit gradient."""
+        token_mask leaves out get no logit gradient, as suits padding, whose
+        d_out is 0; where they only leave the balance loss and their d_out
+        counts, masked_gates gives them that of their gate weights, and
+        d_logits is the run's derivative for every d_out."""
         if self.experts is None or not self.experts.train:
             raise ValueError("backward needs experts with train=True")
         if self._last is None:
@@ -244,7 +248,8 @@ class EPGroup:
                     self.views[s].pos, self.w[t0:t1], t1 - t0, H, k,
                     self.d_send[s * so:(s + 1) * so], self.d_w[t0:t1], st))
         timed("route_grad", lambda: B.moe_route_grad(
-            logits, self.idx[:T], self.w[:T], self.d_w[:T], mask, d_loss, balance, d_logits, st))
+            logits, self.idx[:T], self.w[:T], self.d_w[:T], mask, d_loss, balance, d_logits, st,
+            masked_gates))
         if d_x is None and grads is None:
             return
         timed("exchange", lambda: self._exchange(self.d_send, None, self.d_recv, None, 0, False,

@@ -430,6 +430,10 @@ int moe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t
                      int32_t *expert_counts, float *prob_sums, int32_t *seg_live,
                      void *workspace, size_t *workspace_bytes, hipStream_t stream);
 
+/* OR into k of moe_route_grad: masked tokens keep the gradient of their gate
+ * weights. */
+#define MOE_ROUTE_MASKED_GATES 0x100
+
 /*
  * moe_route_grad -- gradient of the router's logits.
  *     d_logits[t, e] =  sum_{j: topk_idx[t, j] = e} w_j (d_j - sum_i w_i d_i)
@@ -438,7 +442,10 @@ int moe_balance_loss(const float *logits, const int32_t *topk_idx, const uint8_t
  * token's segment, its live tokens and its counts: the first line through
  * the renormalised gate weights of moe_route_topk, the second through
  * moe_balance_loss (whose counts are constants).  Either part may be left
- * out.  The whole row is written; a masked token's row is zero.
+ * out.  The whole row is written; a masked token's row is zero, through the
+ * gate weights too: for padding, whose d is 0 anyway.  Where masked tokens
+ * only leave the balance loss and their output counts, OR
+ * MOE_ROUTE_MASKED_GATES into k: their rows then have the first line.
  *
  *   logits, token_mask, T, seg_tokens, E, k   as moe_balance_loss; logits,
  *                 expert_counts and seg_live are not used when d_loss is

@@ -6,6 +6,8 @@ import torch
 
 import training_ref as R
 from combine_fp32_router_amd import binding as B
+from combine_fp32_router_amd.epgroup import EPGroup
+from combine_fp32_router_amd.experts import ExpertMLP
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +97,59 @@ def test_router_gradient_over_its_own_logits(E, k):
     B.moe_route_grad(logits, idx, w, d_w, mask, d_loss, bal, apart)
     B.moe_route_grad(logits, idx, w, d_w, mask, d_loss, bal, logits)
     assert torch.equal(apart, logits)
+
+
+@pytest.mark.parametrize("E,k", [(8, 2), (33, 4), (256, 8), (300, 3)])
+def test_masked_tokens_keep_their_gates_if_asked(E, k):
+    """masked_gates: a masked row has the gate weights' part alone, a live one
+    the same bits as without."""
+    T, seg = 333, 100
+    g = torch.Generator(device="cuda").manual_seed(E)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    idx = logits.topk(k, 1).indices.int()
+    w, d_w = torch.rand(T, k, generator=g, device="cuda"), torch.randn(T, k, generator=g, device="cuda")
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.7).to(torch.uint8)
+    logits[mask == 0] = float("nan")  # not in the loss: not read
+    bal = B.moe_balance_loss(logits, idx, mask, B.alloc_balance(T, seg, E, k, "cuda"))
+    d_loss = torch.tensor([1.0, 20.0, -3.0, 4.0], device="cuda")
+    plain, gates, got, only = (torch.empty_like(logits) for _ in range(4))
+    B.moe_route_grad(logits, idx, w, d_w, mask, d_loss, bal, plain)
+    B.moe_route_grad(None, idx, w, d_w, None, None, None, gates)
+    B.moe_route_grad(logits, idx, w, d_w, mask, d_loss, bal, got, masked_gates=True)
+    B.moe_route_grad(None, idx, w, d_w, mask, None, None, only, masked_gates=True)
+    want, tol = R.route_grad(np.zeros((T, E)), idx.cpu().numpy(), w.cpu().numpy(), d_w.cpu().numpy(), np.ones(T, bool),
+                             None, None, None, T, E, k, 0.0)
+    R.inside(gates.cpu(), want, tol, "gates")
+    off = mask == 0
+    assert torch.equal(got[~off], plain[~off]) and torch.equal(only, gates)
+    assert torch.equal(got[off], gates[off]) and gates[off].any() and not plain[off].any()
+
+
+def test_a_layer_gives_masked_tokens_their_gates_if_asked():
+    """With masked_gates the logits' gradient of a layer is that of its output
+    for every token, and of the balance loss for the live ones."""
+    T, H, E, k = 200, 64, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(9)
+    mlp = ExpertMLP(normal(g, E, 96, H, scale=H ** -0.5), normal(g, E, H, 48, scale=0.15), SWIGLU, max_rows=400, train=True)
+    group = EPGroup(T, H, E, k, 4, experts=mlp)
+    logits, x, d_out = torch.randn(T, E, generator=g, device="cuda"), normal(g, T, H), normal(g, T, H)
+    mask = (torch.rand(T, generator=g, device="cuda") < 0.7).to(torch.uint8)
+    bal, d_loss = B.alloc_balance(T, T, E, k, "cuda"), torch.full((1,), 50.0, device="cuda")
+    out, plain, got, alone = torch.empty_like(x), *(torch.empty_like(logits) for _ in range(3))
+    group.run(logits, x, out, balance=bal, token_mask=mask)
+    group.backward(d_out, None, plain, d_loss=d_loss)
+    group.backward(d_out, None, got, d_loss=d_loss, masked_gates=True)
+    group.run(logits, x, out)
+    group.backward(d_out, None, alone)
+    off = mask == 0
+    assert torch.equal(got[~off], plain[~off]) and torch.equal(got[off], alone[off]) and not plain[off].any()
+    # the gates' part, from the returned rows: <d_out, d out / d logits>
+    rows = torch.zeros(T, k, H, dtype=torch.float64, device="cuda")
+    for s, (a, b) in enumerate(group.bounds):
+        at = group.views[s].pos[:(b - a) * k].long()
+        rows[a:b] = group.send_rows(s, 0).view(torch.bfloat16).view(-1, H)[at].double().view(b - a, k, H)
+    z = logits.double().requires_grad_()
+    gate = z.gather(1, group.idx[:T].long()).softmax(1)
+    want, = torch.autograd.grad(((gate[..., None] * rows).sum(1) * d_out.double()).sum(), z)
+    size = (rows * d_out.double()[:, None]).abs().sum(2).sum(1, keepdim=True).expand_as(want)
+    R.inside(alone, want, size * (H + k + 24) * 2 * R.U32, "gates")
