@@ -100,6 +100,7 @@ class EPGroup:
                 self.d_send, self.d_recv, self.d_rows = rows16(), rows16(), rows16()
                 self.d_w = torch.empty((max(T, 1), k), dtype=torch.float32, device=dev)
                 self._last = None  # what backward needs to know of the last run
+                self._forward = None  # the experts' call of that run
 
     def _source_caps(self, factor):
         key = str(factor)
@@ -158,6 +159,7 @@ class EPGroup:
             self._run_experts(quant, timed, st)
             if self.experts.train:
                 self._last = (logits, quant, balance, token_mask)
+                self._forward = self.experts.forwards
         else:
             self._run_grouped(quant, timed, st)
         timed("exchange_back", lambda: self._exchange(self.send, self.send_scales, self.recv,
@@ -222,7 +224,8 @@ class EPGroup:
         [T, H]) and of its balance loss (d_loss fp32, one value per segment,
         or None): d_x bf16 [T, H] or None, d_logits fp32 [T, E], the experts'
         grads or None.  The run's logits, mask, Balance and this group's
-        buffers must still hold what the run left in them.  Tokens that
+        buffers must still hold what the run left in them; d_x and grads are
+        refused if the experts have run for another call since.  Tokens that
         token_mask leaves out get no logit gradient, as suits padding, whose
         d_out is 0; where they only leave the balance loss and their d_out
         counts, masked_gates gives them that of their gate weights, and
@@ -238,6 +241,8 @@ class EPGroup:
                 B._want_bf16(t, (T, H), name)
         if d_loss is not None and balance is None:
             raise ValueError("d_loss needs a run with a Balance")
+        if (d_x is not None or grads is not None) and self._forward != self.experts.forwards:
+            raise ValueError("the experts have run again since this group's run")
         st = torch.cuda.current_stream(self.device)
         timed = self._timed(timer, st)
         so = self.source_rows
@@ -258,7 +263,7 @@ class EPGroup:
                                                     self.d_rows, None, st))
         timed("experts_grad", lambda: self.experts.backward(
             self.d_rows, self.expert_in, rl.group_offsets, None if d_x is None else self.d_rows,
-            grads, accumulate, st))
+            grads, accumulate, st, self._forward))
         if d_x is None:
             return
         timed("ungroup", lambda: B.moe_recv_ungroup(self.d_rows, None, M, H, 0, rl.group_pos,

@@ -30,7 +30,12 @@ class ExpertGrads(NamedTuple):
 class ExpertMLP:
     """w_up bf16 [E, I, H] (MOE_ACT_SWIGLU: [E, 2I, H], an expert's I gate
     rows, then its I up rows), w_down bf16 [E, H, I], biases fp32 or None;
-    buffers for max_rows rows."""
+    buffers for max_rows rows.
+
+    The buffers hold one forward call: every other one, of another batch or
+    layer too, takes their place.  `forwards` counts the calls, so that a
+    backward call can say which one it belongs to.  (A replayed graph counts
+    nothing.)"""
 
     def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, act: int,
                  b_up: torch.Tensor | None = None, b_down: torch.Tensor | None = None,
@@ -57,6 +62,8 @@ class ExpertMLP:
         self.hidden = rows(self.I)
         self.preact = rows(self.wide * self.I) if train else None
         self.d_preact = rows(self.wide * self.I) if train else None
+        self.forwards = 0
+        self._kept = None  # rows of the forward call that the buffers hold
 
     def _rows(self, t: torch.Tensor, name: str) -> int:
         if t.dim() != 2 or t.shape[1] != self.H:
@@ -71,10 +78,14 @@ class ExpertMLP:
         [rows, H]; rows of no run are not written."""
         n = self._rows(x, "x")
         hidden = self.hidden[:n]
+        self.forwards += 1
+        self._kept = None
         B.moe_expert_matmul(x, offsets, self.w_up, self.b_up, self.act, None, hidden,
                             self.preact[:n] if self.train else None, stream)
-        return B.moe_expert_matmul(hidden, offsets, self.w_down, self.b_down, B.MOE_ACT_NONE,
-                                   residual, out, None, stream)
+        B.moe_expert_matmul(hidden, offsets, self.w_down, self.b_down, B.MOE_ACT_NONE, residual,
+                            out, None, stream)
+        self._kept = n
+        return out
 
     def alloc_grads(self, dtype=torch.float32) -> ExpertGrads:
         def f32(b):
@@ -86,14 +97,21 @@ class ExpertMLP:
 
     def backward(self, d_out: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
                  d_x: torch.Tensor | None, grads: ExpertGrads | None, accumulate: bool = False,
-                 stream=None) -> None:
+                 stream=None, forward: int | None = None) -> None:
         """Gradients of the last forward(x, offsets, ...) from d_out bf16
         [rows, H]: d_x bf16 [rows, H] (may be d_out itself; None: not
         wanted) and grads (None: not wanted), which `accumulate` adds to.
-        (A residual's gradient is d_out itself.)"""
+        (A residual's gradient is d_out itself.)  `forward`, what `forwards`
+        was after the call meant, refuses if another has run since."""
         if not self.train:
             raise ValueError("backward needs train=True")
         n = self._rows(x, "x")
+        if self._kept is None:
+            raise ValueError("backward before a whole forward")
+        if self._kept != n:
+            raise ValueError(f"backward of {n} rows, the last forward had {self._kept}")
+        if forward is not None and forward != self.forwards:
+            raise ValueError("the experts have run again since that forward")
         hidden, dz = self.hidden[:n], self.d_preact[:n]
         B.moe_expert_matmul_dx(d_out, offsets, self.w_down, self.act, self.preact[:n], dz, stream)
         if grads is not None:

@@ -6,6 +6,9 @@ import pytest
 import torch
 
 from combine_fp32_router_amd import binding as B
+from combine_fp32_router_amd import epgroup
+from combine_fp32_router_amd.epgroup import EPGroup
+from combine_fp32_router_amd.experts import ExpertMLP
 
 OK, NULL, SHAPE, ALIGN, WORKSPACE, HIP, ALIAS = range(7)
 F = ctypes.c_void_p(0x10000)  # aligned, never dereferenced
@@ -27,3 +30,78 @@ def test_the_flag_of_masked_gates_is_no_size(lib):
     assert f(2 | flag, T=0) == OK
     assert lib.moe_balance_loss(None, None, None, 10, 5, 8, 2 | flag, None, None, None, None, None,
                                 ctypes.byref(ctypes.c_size_t(0)), None) == SHAPE
+
+
+def bf16(*s):
+    return torch.zeros(*s, dtype=torch.bfloat16)
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """Every launch of a layer replaced by its name in a list."""
+    calls = []
+    for module, names in ((B, B.EXPORTS), (epgroup.HN, ("moe_exchange_blocks",))):
+        for name in names:
+            if hasattr(module, name) and name not in ("moe_status_string", "moe_row_bytes"):
+                monkeypatch.setattr(module, name, lambda *a, _name=name, **kw: calls.append(_name))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    return calls
+
+
+def experts(E=4, H=32, I=16, max_rows=64):
+    return ExpertMLP(bf16(E, I, H), bf16(E, H, I), B.MOE_ACT_SILU, max_rows=max_rows, train=True)
+
+
+def test_experts_refuse_a_backward_of_another_forward(launches):
+    m, off, x = experts(), torch.zeros(5, dtype=torch.int32), bf16(8, 32)
+    with pytest.raises(ValueError, match="before"):
+        m.backward(x, x, off, None, None)
+    assert m.forward(x, off, x) is x
+    first = m.forwards
+    m.backward(x, x, off, None, None)
+    m.backward(x, x, off, None, None, forward=first)
+    with pytest.raises(ValueError, match="9 rows"):
+        m.backward(bf16(9, 32), bf16(9, 32), off, None, None)
+    m.forward(x, off, x)
+    launches.clear()
+    with pytest.raises(ValueError, match="again"):
+        m.backward(x, x, off, None, None, forward=first)
+    assert not launches
+    m.backward(x, x, off, None, None)
+
+
+def test_a_forward_that_fails_half_way_keeps_nothing(launches, monkeypatch):
+    m, off, x = experts(), torch.zeros(5, dtype=torch.int32), bf16(8, 32)
+    m.forward(x, off, x)
+
+    def fail(*a, **kw):
+        raise B.MoeError("moe_expert_matmul", HIP)
+
+    monkeypatch.setattr(B, "moe_expert_matmul", fail)
+    with pytest.raises(B.MoeError):
+        m.forward(x, off, x)
+    with pytest.raises(ValueError, match="before"):
+        m.backward(x, x, off, None, None)
+
+
+def test_groups_that_share_their_experts(launches):
+    """A group's backward is refused once the experts ran for another group or
+    call; what needs no experts (the logits' gradient) still goes."""
+    m = experts()
+    one, two = (EPGroup(16, 32, 4, 2, 2, device="cpu", experts=m) for _ in range(2))
+    z, x = torch.zeros(16, 4), bf16(16, 32)
+    one.run(z, x, x)
+    one.backward(x, x, z)
+    two.run(z, x, x)
+    two.backward(x, x, z, m.alloc_grads())
+    for kw in (dict(d_x=x), dict(d_x=None, grads=m.alloc_grads())):
+        launches.clear()
+        with pytest.raises(ValueError, match="again"):
+            one.backward(x, d_logits=z, **kw)
+        assert not launches
+    one.backward(x, None, z)
+    m.forward(bf16(8, 32), torch.zeros(5, dtype=torch.int32), bf16(8, 32))
+    with pytest.raises(ValueError, match="again"):
+        two.backward(x, x, z)
+    two.run(z, x, x)
+    two.backward(x, x, z)
