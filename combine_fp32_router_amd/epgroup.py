@@ -85,6 +85,8 @@ class EPGroup:
         self.send_scales, self.recv_scales, self.grouped_scales = scales(), scales(), scales()
         self.ret_scales = scales() if standin else None
         self._caps = {}
+        self._last = None  # what backward needs to know of the last whole run
+        self._forward = None  # the experts' call of that run
         if experts is not None:
             if (experts.E, experts.H) != (E, H):
                 raise ValueError(f"experts [{experts.E}, {experts.H}] in a group of [{E}, {H}]")
@@ -99,8 +101,6 @@ class EPGroup:
             if experts.train:
                 self.d_send, self.d_recv, self.d_rows = rows16(), rows16(), rows16()
                 self.d_w = torch.empty((max(T, 1), k), dtype=torch.float32, device=dev)
-                self._last = None  # what backward needs to know of the last run
-                self._forward = None  # the experts' call of that run
 
     def _source_caps(self, factor):
         key = str(factor)
@@ -135,6 +135,7 @@ class EPGroup:
         T, H, E, k, R = self.T, self.H, self.E, self.k, self.R
         if logits.shape != (T, E) or x.shape[0] != T or out.shape[0] != T:
             raise ValueError("logits/x/out shapes do not match the group")
+        self._last = None  # the buffers are overwritten from here on
         st = torch.cuda.current_stream(self.device)
         M = self.max_rows
         timed = self._timed(timer, st)
@@ -157,9 +158,6 @@ class EPGroup:
                                                  self.recv_scales, quant, False, st))
         if self.experts is not None:
             self._run_experts(quant, timed, st)
-            if self.experts.train:
-                self._last = (logits, quant, balance, token_mask)
-                self._forward = self.experts.forwards
         else:
             self._run_grouped(quant, timed, st)
         timed("exchange_back", lambda: self._exchange(self.send, self.send_scales, self.recv,
@@ -169,6 +167,9 @@ class EPGroup:
                 timed("combine", lambda: B.moe_combine(
                     self.send_rows(s, quant), self.send_scales_of(s), quant, self.views[s].pos,
                     self.w[t0:t1], t1 - t0, H, k, out[t0:t1], st))
+        if self.experts is not None and self.experts.train:
+            self._last = (logits, quant, balance, token_mask)
+            self._forward = self.experts.forwards
         return out
 
     @staticmethod

@@ -105,3 +105,23 @@ def test_groups_that_share_their_experts(launches):
         two.backward(x, x, z)
     two.run(z, x, x)
     two.backward(x, x, z)
+
+
+@pytest.mark.parametrize("name", ["moe_recv_layout", "moe_recv_ungroup", "moe_combine"])
+def test_a_run_that_fails_half_way_is_not_gone_back_through(launches, monkeypatch, name):
+    m = experts()
+    group, z, x = EPGroup(16, 32, 4, 2, 2, device="cpu", experts=m), torch.zeros(16, 4), bf16(16, 32)
+    group.run(z, x, x)
+    group.backward(x, x, z)
+
+    def fail(*a, **kw):
+        raise B.MoeError(name, HIP)
+
+    with monkeypatch.context() as patch:
+        patch.setattr(B, name, fail)
+        with pytest.raises(B.MoeError):
+            group.run(z, x, x)
+    with pytest.raises(ValueError, match="before run"):
+        group.backward(x, x, z)
+    group.run(z, x, x)
+    group.backward(x, x, z)
