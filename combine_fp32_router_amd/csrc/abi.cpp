@@ -39,10 +39,13 @@ int check_segments(int64_t T, int64_t &seg_tokens, int E, int k)
     return moe::layout_chunks(T, seg_tokens) > 65535 ? MOE_ERR_SHAPE : MOE_OK;  // grid y dimension
 }
 
-// Sizes of an experts' product: N may count both halves of a gated one.
+// Sizes of an experts' product: N may count both halves of a gated one.  The
+// kernels round a run's rows up to whole tiles (of at most 256) and look two
+// stages (128 rows) past its end in 32 bits.
+constexpr int64_t kMaxProductRows = kMaxSlots - 256;
 int check_product(int E, int64_t max_rows, int K, int N, int most)
 {
-    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows >= kMaxSlots || K < 16 ||
+    if (E < 1 || E > MOE_MAX_EXPERTS || max_rows < 0 || max_rows > kMaxProductRows || K < 16 ||
         K > MOE_MAX_HIDDEN || (K % 16) != 0 || N < 16 || N > most || (N % 16) != 0)
         return MOE_ERR_SHAPE;
     return MOE_OK;

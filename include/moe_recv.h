@@ -140,9 +140,9 @@ int moe_recv_ungroup(const void *grouped, const float *grouped_scales, int64_t m
  *   bias       [E, N] fp32 (MOE_ACT_SWIGLU: [E, 2N]), or NULL.        (in)
  *   act        MOE_ACT_*.
  *   residual   [max_rows, N] bf16 bits, or NULL; may be out itself.   (in)
- *   E, max_rows, K, N   1 <= E <= MOE_MAX_EXPERTS; 0 <= max_rows < 2^31, at
- *              least the rows of all runs (a run is cut at max_rows: nothing
- *              is read or written past it); K and N multiples of 16 in [16,
+ *   E, max_rows, K, N   1 <= E <= MOE_MAX_EXPERTS; 0 <= max_rows <= 2^31 -
+ *              256, at least the rows of all runs (a run is cut at max_rows:
+ *              nothing is read or written past it); K and N multiples of 16 in [16,
  *              MOE_MAX_HIDDEN].  A call whose outputs make 2^30 tiles of 256 x
  *              128 or more returns MOE_ERR_SHAPE.
  *   out        [max_rows, N] bf16 bits; rows of no run are not written. (out)

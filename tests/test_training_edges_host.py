@@ -125,3 +125,16 @@ def test_a_run_that_fails_half_way_is_not_gone_back_through(launches, monkeypatc
         group.backward(x, x, z)
     group.run(z, x, x)
     group.backward(x, x, z)
+
+
+def test_most_rows_of_a_product(lib):
+    """Up to 2^31 - 256 rows: beyond, a run rounded up to whole tiles, or two
+    stages past its end, would pass 32 bits."""
+    none, n = [None] * 3, ctypes.c_size_t(0)
+    calls = (lambda rows: lib.moe_expert_matmul(*none, None, 0, None, 1, rows, 16, 16, None, None, None, ctypes.byref(n), None),
+             lambda rows: lib.moe_expert_matmul_dx(*none, 0, None, 1, rows, 16, 16, None, None, ctypes.byref(n), None),
+             lambda rows: lib.moe_expert_matmul_dw(*none, 1, rows, 16, 16, 0, None, None, None, ctypes.byref(n), None))
+    for call in calls:
+        assert call(2 ** 31 - 256) == OK
+        for rows in (2 ** 31 - 255, 2 ** 31 - 1, 2 ** 31, 2 ** 62):
+            assert call(rows) == SHAPE
