@@ -92,12 +92,12 @@ struct Stream {
         }
     }
     // Multiplies the chunk at `rd` (this wave's oldest loads) and refills the
-    // image behind it.
+    // chunk before it, once the last step's reads of that are done.
     __device__ __forceinline__ void step(const MOE_LDS char *__restrict__ rd, MOE_LDS char *__restrict__ wr, int k0)
     {
         asm volatile("" ::: "memory");
         constexpr int left = (kDepth - 2) * kLoads;  // younger loads
-        __builtin_amdgcn_s_waitcnt(0x0f70 | (left & 15) | (left >> 4) << 14);
+        __builtin_amdgcn_s_waitcnt(0x0070 | (left & 15) | (left >> 4) << 14);
         asm volatile("" ::: "memory");
         const int lane = lane_id();
         bf16x8 f[kImages][2];
