@@ -153,3 +153,26 @@ def test_a_layer_gives_masked_tokens_their_gates_if_asked():
     want, = torch.autograd.grad(((gate[..., None] * rows).sum(1) * d_out.double()).sum(), z)
     size = (rows * d_out.double()[:, None]).abs().sum(2).sum(1, keepdim=True).expand_as(want)
     R.inside(alone, want, size * (H + k + 24) * 2 * R.U32, "gates")
+
+
+@pytest.mark.parametrize("T,E,seg", [((1 << 20) + 77, 16, 1 << 21), (1 << 19, 64, 1 << 18), (300001, 256, 150001),
+                                     (200003, 300, 200003), (60001, 1024, 60001), (5000, 8, 250)])
+def test_probability_sums_of_long_segments(T, E, seg):
+    """The bound of a sum of probabilities by what a lane adds: a block has the
+    batch's 512th part, in 16s, at least 32 tokens, or a short segment, and
+    shares it over its waves and, up to 256 experts, their four groups of lanes."""
+    seg = min(seg, T)
+    tokens = min(max(32, -(-T // 512) + 15 & ~15), seg)
+    if seg <= 256 and (T >= (16 if E <= 256 else 128) * seg or seg * E <= 32768):
+        tokens = seg
+    waves = (16 if tokens == seg and E <= 256 else 8 if E <= 512 else 4) * (4 if E <= 256 else 1)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    idx = torch.randint(0, E, (T, 2), generator=g, device="cuda").int()
+    out = B.moe_balance_loss(logits, idx, None, B.alloc_balance(T, seg, E, 2, "cuda"))
+    S = -(-T // seg)
+    sums = torch.stack([logits[s * seg:(s + 1) * seg].double().softmax(1).sum(0) for s in range(S)])
+    spread = (logits.amax() - logits.amin()).item()
+    rel = (spread + E / 16 + 12 + 2 * -(-tokens // (2 * waves)) + 1) * 2 * R.U32  # R.softmax_rel_bound's terms
+    R.inside(out.prob_sums, sums, sums * rel, "prob_sums")
+    assert torch.equal(out.expert_counts.sum(1), 2 * out.tokens) and out.tokens.sum() == T
