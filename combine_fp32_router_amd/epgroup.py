@@ -58,7 +58,8 @@ class EPGroup:
     def __init__(self, T: int, H: int, E: int, k: int, R: int, standin: bool = True,
                  device="cuda", experts: ExpertMLP | None = None):
         self.T, self.H, self.E, self.k, self.R = T, H, E, k, R
-        self.device = torch.device(device)
+        # `cuda` is the device that is current now, whichever is in a later call
+        self.device = torch.empty(0, device=device).device
         self.experts = experts
         self.standin = standin = standin and experts is None
         self.bounds = chunk_ranges(T, R)

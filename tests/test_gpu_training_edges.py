@@ -176,3 +176,10 @@ def test_probability_sums_of_long_segments(T, E, seg):
     rel = (spread + E / 16 + 12 + 2 * -(-tokens // (2 * waves)) + 1) * 2 * R.U32  # R.softmax_rel_bound's terms
     R.inside(out.prob_sums, sums, sums * rel, "prob_sums")
     assert torch.equal(out.expert_counts.sum(1), 2 * out.tokens) and out.tokens.sum() == T
+
+
+def test_a_group_keeps_the_device_it_was_made_on():
+    """`cuda` names the device that is current when the group is made, not
+    whichever is current when it runs."""
+    group = EPGroup(16, 32, 4, 2, 2, device="cuda")
+    assert group.device == group.idx.device == torch.device("cuda", torch.cuda.current_device())
