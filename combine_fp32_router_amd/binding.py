@@ -512,10 +512,13 @@ def _call(name: str, stream, *args) -> None:
         _check(name, status)
 
 
+_BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)  # values, or their bits
+
+
 def _want_bf16(t: torch.Tensor, shape, name: str):
     """bf16 values (or their int16/uint16 bits) of exactly `shape`."""
-    if t.element_size() != 2:
-        raise ValueError(f"{name} must hold bf16 bits")
+    if t.dtype not in _BF16_TYPES:
+        raise ValueError(f"{name} must hold bf16 values or their bits, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
 

@@ -138,3 +138,30 @@ def test_most_rows_of_a_product(lib):
         assert call(2 ** 31 - 256) == OK
         for rows in (2 ** 31 - 255, 2 ** 31 - 1, 2 ** 31, 2 ** 62):
             assert call(rows) == SHAPE
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32, torch.uint8, torch.int32])
+def test_rows_of_another_type_are_refused(dtype):
+    """Two bytes do not make bf16: float16 is refused like the rest."""
+    off, w, x, y = torch.zeros(3, dtype=torch.int32), bf16(2, 48, 32), bf16(4, 32), bf16(4, 48)
+    other = lambda t: torch.zeros(t.shape, dtype=dtype)  # noqa: E731
+    for a in ((other(x), off, w, None, 0, None, y), (x, off, other(w), None, 0, None, y), (x, off, w, None, 0, other(y), y),
+              (x, off, w, None, 0, None, other(y)), (x, off, w, None, 0, None, y, other(y))):
+        with pytest.raises(ValueError, match="bf16"):
+            B.moe_expert_matmul(*a, stream=0)
+    for a in ((other(y), off, w, 1, x, x), (y, off, other(w), 1, x, x), (y, off, w, 1, other(x), x), (y, off, w, 1, x, other(x))):
+        with pytest.raises(ValueError, match="bf16"):
+            B.moe_expert_matmul_dx(*a, stream=0)
+    for a in ((other(y), x, off), (y, other(x), off)):
+        with pytest.raises(ValueError, match="bf16"):
+            B.moe_expert_matmul_dw(*a, torch.zeros(2, 48, 32), stream=0)
+    with pytest.raises(ValueError, match="bf16"):
+        ExpertMLP(other(w), bf16(2, 32, 48), B.MOE_ACT_SILU)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.int16, torch.uint16])
+def test_bits_of_bf16_are_taken(dtype):
+    """Past the types; the host's tensors are refused further in."""
+    x, off, w = torch.zeros(4, 32).to(dtype), torch.zeros(3, dtype=torch.int32), torch.zeros(2, 48, 32).to(dtype)
+    with pytest.raises(ValueError, match="device tensor"):
+        B.moe_expert_matmul(x, off, w, None, 0, None, torch.zeros(4, 48).to(dtype), stream=0)
