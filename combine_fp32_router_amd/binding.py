@@ -635,10 +635,18 @@ def moe_combine_grad(d_out: torch.Tensor, recv: torch.Tensor | None,
                      recv_scales: torch.Tensor | None, quant: int, pos: torch.Tensor,
                      topk_w: torch.Tensor, T: int, H: int, k: int, d_recv: torch.Tensor | None,
                      d_topk_w: torch.Tensor | None, stream=None) -> None:
-    """Gradient of moe_combine: d_out bf16 [T, H] -> d_recv (bf16 rows) and
-    d_topk_w fp32 [T*k]; either output may be None."""
-    if d_out.element_size() != 2 or d_out.numel() < T * H:
+    """Gradient of moe_combine: d_out bf16 [T, H] -> d_recv (bf16 rows, as
+    [rows, H] or as the bytes of a bf16 payload) and d_topk_w fp32 [T*k];
+    either output may be None.  d_recv has fewer than T*k rows only where its
+    shape says that they are whole ones."""
+    if d_out.dtype not in _BF16_TYPES or d_out.numel() < T * H:
         raise ValueError("d_out must hold T*H bf16 values")
+    if d_recv is not None:
+        if d_recv.dtype not in _BF16_TYPES and d_recv.dtype != torch.uint8:
+            raise ValueError(f"d_recv takes rows of bf16, not {d_recv.dtype}")
+        if d_recv.nbytes < T * k * H * 2 and (
+                d_recv.dim() != 2 or d_recv.shape[1] * d_recv.element_size() != 2 * H):
+            raise ValueError("d_recv must hold rows of 2*H bytes, whatever the payload of recv")
     _want(pos, torch.int32, "pos")
     _want(topk_w, torch.float32, "topk_w")
     if pos.numel() < T * k or topk_w.numel() < T * k:
@@ -647,6 +655,10 @@ def moe_combine_grad(d_out: torch.Tensor, recv: torch.Tensor | None,
         _want(d_topk_w, torch.float32, "d_topk_w")
         if d_topk_w.numel() < T * k:
             raise ValueError("d_topk_w must hold T*k values")
+        if recv is None:
+            raise ValueError("d_topk_w needs recv")
+        if recv.element_size() > (2 if quant == MOE_QUANT_BF16 else 1):
+            raise ValueError(f"recv: {recv.dtype} does not hold rows of this payload")
         _want_scales(recv_scales, 0, quant, "recv_scales")
     _call("moe_combine_grad", stream, d_out, recv, recv_scales, quant, pos, topk_w, T, H, k, d_recv,
           d_topk_w)

@@ -483,7 +483,8 @@ int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *to
  *   recv, recv_scales, quant, pos, topk_w, T, H, k   as moe_combine;
  *                recv and recv_scales are not used when d_topk_w is NULL. (in)
  *   d_recv       bf16 row buffer (rows of 2*H bytes), 16-byte aligned, not
- *                overlapping d_out or recv; or NULL.                  (out)
+ *                overlapping d_out or recv; or NULL.  As for a pack, no two
+ *                slots share a row.                                   (out)
  *   d_topk_w     [T*k] fp32, or NULL.                                 (out)
  *
  * Errors: as moe_combine; MOE_ERR_NULL also when both outputs are NULL;

@@ -165,3 +165,31 @@ def test_bits_of_bf16_are_taken(dtype):
     x, off, w = torch.zeros(4, 32).to(dtype), torch.zeros(3, dtype=torch.int32), torch.zeros(2, 48, 32).to(dtype)
     with pytest.raises(ValueError, match="device tensor"):
         B.moe_expert_matmul(x, off, w, None, 0, None, torch.zeros(4, 48).to(dtype), stream=0)
+
+
+def test_rows_of_the_combine_gradient():
+    """d_recv takes rows of 2 H bytes: a payload's own buffer, or another type,
+    would be written past its end or left as garbage."""
+    T, H, k = 4, 32, 2
+    pos, w, d_out = torch.zeros(8, dtype=torch.int32), torch.zeros(4, 2), bf16(T, H)
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+
+    def call(d_recv, d_out=d_out, recv=None, quant=0, scales=None, d_w=None):
+        with pytest.raises(ValueError) as e:
+            B.moe_combine_grad(d_out, recv, scales, quant, pos, w, T, H, k, d_recv, d_w, stream=0)
+        return "device tensor" not in str(e.value)  # else past the rows' checks
+
+    for bad in (torch.zeros(8, H), torch.zeros(8, H, dtype=torch.float16), torch.zeros(8, H, dtype=torch.int8), u8(8, H), u8(8 * H),
+                u8(8, H // 2), bf16(8, H // 2), bf16(7 * H), u8(7 * 2 * H), bf16(8, H - 16)):
+        assert call(bad), bad.shape
+    for good in (bf16(8, H), bf16(5, H), bf16(8 * H), bf16(20, H), u8(8, 2 * H), u8(3, 2 * H), u8(8 * 2 * H), bf16(8, H).view(torch.int16),
+                 u8(16, H)):
+        assert not call(good), good.shape
+    assert call(bf16(8, H), d_out=torch.zeros(T, H, dtype=torch.float16))
+    d_w, scales = torch.zeros(T, k), torch.zeros(8)
+    assert call(None, d_w=d_w)  # no recv
+    assert call(None, recv=torch.zeros(8, H), d_w=d_w)
+    assert call(None, recv=bf16(8, H), quant=1, scales=scales, d_w=d_w)
+    assert call(None, recv=torch.zeros(8, H, dtype=torch.int8), quant=1, d_w=d_w)  # no scales
+    assert not call(None, recv=torch.zeros(8, H, dtype=torch.int8), quant=1, scales=scales, d_w=d_w)
+    assert not call(None, recv=u8(8, 2 * H), d_w=d_w) and not call(None, recv=bf16(8, H), d_w=d_w)
