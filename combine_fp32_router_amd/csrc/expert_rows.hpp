@@ -44,8 +44,8 @@ __device__ __forceinline__ TileAt grouped_order(int id, int row_tiles, int col_t
 }
 
 // exp and the reciprocal in single instructions, good to 1 ulp each, behind a
-// rounded product: off by about (|z| + 2) 2^-24 of the result, against the
-// 2^-9 of the bf16 that is stored.  Past +-88 they give 0 and 1.
+// rounded product: off by at most (1.25 |z| + 5) 2^-24 of the result, against
+// the 2^-8 of the bf16 that is stored.  Past +-88 they give 0 and 1.
 __device__ __forceinline__ float sigmoid(float z)
 {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
@@ -53,9 +53,10 @@ __device__ __forceinline__ float sigmoid(float z)
 
 // The normal distribution function, branchless, from its tail Q(z) = erfc(z /
 // sqrt 2) / 2 for z >= 0: with x = z / sqrt 2 and t = 1 / (1 + x/2), erfc(x) = t
-// exp(-x^2 + r(t)), r a polynomial fitted to log(erfc(x) exp(x^2) / t) on [0,
-// 9.6] (off by 5e-8); p has it in base 2, with the half.  In fp32 Q is good to
-// 1.3e-6 of itself for z < 5.6, 1.3e-7 absolute.
+// exp(-x^2 + r(t)) (the form of Press et al., Numerical Recipes, 6.2), r a
+// polynomial of our own, fitted to log(erfc(x) exp(x^2) / t) on [0, 9.6] (off by
+// 5e-8); p has it in base 2, with the half.  In fp32, with instructions off by 1
+// ulp, Q is good to 2e-6 of itself for z < 5.6 and the result to 3.5e-7.
 __device__ __forceinline__ float normal_below(float z)
 {
     const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.35355339f, 1.0f));
