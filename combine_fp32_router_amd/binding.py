@@ -655,9 +655,7 @@ def moe_combine_grad(d_out: torch.Tensor, recv: torch.Tensor | None,
         _want(d_topk_w, torch.float32, "d_topk_w")
         if d_topk_w.numel() < T * k:
             raise ValueError("d_topk_w must hold T*k values")
-        if recv is None:
-            raise ValueError("d_topk_w needs recv")
-        if recv.element_size() > (2 if quant == MOE_QUANT_BF16 else 1):
+        if recv is not None and recv.element_size() > (2 if quant == MOE_QUANT_BF16 else 1):
             raise ValueError(f"recv: {recv.dtype} does not hold rows of this payload")
         _want_scales(recv_scales, 0, quant, "recv_scales")
     _call("moe_combine_grad", stream, d_out, recv, recv_scales, quant, pos, topk_w, T, H, k, d_recv,

@@ -187,7 +187,6 @@ def test_rows_of_the_combine_gradient():
         assert not call(good), good.shape
     assert call(bf16(8, H), d_out=torch.zeros(T, H, dtype=torch.float16))
     d_w, scales = torch.zeros(T, k), torch.zeros(8)
-    assert call(None, d_w=d_w)  # no recv
     assert call(None, recv=torch.zeros(8, H), d_w=d_w)
     assert call(None, recv=bf16(8, H), quant=1, scales=scales, d_w=d_w)
     assert call(None, recv=torch.zeros(8, H, dtype=torch.int8), quant=1, d_w=d_w)  # no scales
