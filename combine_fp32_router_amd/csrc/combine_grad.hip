@@ -16,7 +16,7 @@
 // 8 slots: gates alone (read) 149 us, 7.1 TB/s; rows alone (write) 183, 5.8;
 // both in one kernel 376, since reads and writes then take turns in HBM
 // throughout, and in two launches, first all reads, 332.  With rows of one
-// byte or less that saves nothing (int8: 286 against 289).
+// byte or less that saves nothing (int8: 286 against 289; E4M3 285, int4 239).
 // Few rows are written with ordinary stores and in one launch, many with
 // streaming stores, which do not push other data out of the last-level cache
 // (in turn over four sets of buffers, ordinary / streaming: 67 MB of rows
@@ -156,7 +156,8 @@ __global__ __launch_bounds__(1024) void combine_grad_kernel(
 // Short rows, of at most LG <= 16 groups of eight elements: a wave has one
 // token, and each LG of its lanes a slot.  16 slots of 32 elements int8, 26560
 // tokens: 26 us, 50 with a block a token; 8 of 64 bf16, 16000 tokens: 10 and 19; 8
-// of 128 int4, 30000: 28 and 35.  (LG = 32, 8 of 256 int8, 30000: 60 and 45.)
+// of 128 int4, 30000: 28 and 35; their bytes alone 7, 5.5 and 13.  (LG = 32, 8 of
+// 256 int8, 30000: 60 and 45.)
 template <int Q, int LG, bool ROWS, bool GATES>
 __global__ __launch_bounds__(kNarrowTokens *kWave) void combine_grad_narrow_kernel(
     const u32x4 *__restrict__ d_out, const void *__restrict__ rows_,

@@ -228,8 +228,10 @@ static int few_height(int E, int64_t max_rows)
 // for every 16 columns at 17 TB/s, or 6.2 where they are more than the L2s hold,
 // 2, and 0.8 for each round of the workgroups that fit the card.  The tiles: 8
 // for each round of them and 0.75 for 64 of K (in parts: 12, and 0.45 for 64 of
-// a part's), or the weights and 5 if that is longer.  Measured (here / tiles): 1 token of 8 experts above 78 / 80; 64 rows
-// of 1 expert, K = N = 4096 11 / 30; 256 rows of it 37 / 28; 128 rows of each of
+// a part's), or the weights and 5 if that is longer.  They are rough: 64 rows of
+// 1 expert, K = N = 4096, go in parts where a workspace allows it, 19, though 11
+// are enough here.  Measured (here / tiles): 1 token of 8 experts above 78 / 80; 64
+// rows of 1 expert, K = N = 4096 11 / 30; 256 rows of it 37 / 28; 128 rows of each of
 // 8, K = 2048, N = 768 gated 27 / 23; 64 rows of each of 8, K = 7168, N = 2048
 // gated 126 / 113; 2 rows of each of 64, K = 1024, N = 4096 108 / 95; 1 row of each
 // of 8, K = 2048, N = 7168 52 / 37; 4 of each of 32, K = 2048, N = 1024 32 / 24.
