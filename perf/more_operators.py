@@ -1,10 +1,10 @@
 """Cases for measuring the layer's operators around E4M3 rows: the residual's addition with the root-mean-square norm
 and its gradient, rows and weights in E4M3 codes with a scale for each block of 128, the experts' products of such
-rows and weights, and the gradient of a product's rows.
+rows and weights (alone, and two with the codes of the rows between them), and the gradient of their rows.
 
 Each case runs either in plain torch operations (`own` false) or through the package's calls (`own` true) on the same
-inputs.  A block's scale is its largest size / 448, a code is E4M3(value / scale).  Codes are returned as E4M3 values
-(torch's float8_e4m3fn), with their fp32 scales beside them."""
+inputs.  A block's scale is its largest size / 448, a code is E4M3(value / scale).  The norm's and the quantisers' codes are
+returned as E4M3 values (torch's float8_e4m3fn), with their fp32 scales beside them; a product's codes go into the next."""
 import math
 import random
 
@@ -33,21 +33,22 @@ def listed():
         dict(name="codes of rows 4099x7168", op="quant_rows", rows=4099, hidden=7168, halves=1),
         # after a training step: the gated up projections of eight experts, for the product and for its gradient
         dict(name="codes of weights 8x4096x7168", op="quant_weights", experts=8, outer=2048, inner=7168, halves=2),
-        # serving: one token at its eight experts, one row each, of the 32 a GPU holds, rows as a payload brought them
-        dict(name="product 1 token", op="product", rows=8, experts=32, inner=7168, outer=2048, act="swiglu", bias=False,
-             residual=False, keep=False, scales="row", result="codes", spread="single"),
+        # serving: one token at its eight experts, one row each, of the 32 a GPU holds, rows as a payload brought them;
+        # the gated up projection, and the down projection of its codes
+        dict(name="products 1 token", op="product", rows=8, experts=32, inner=7168, outer=2048, act="swiglu", bias=False,
+             residual=False, keep=False, scales="row", then=7168, spread="single"),
         # an uneven batch over many experts: down projection with bias and residual
         dict(name="product 4099 rows of 64", op="product", rows=4099, experts=64, inner=1024, outer=4096, act="none",
-             bias=True, residual=True, keep=False, scales="block", result="bf16", spread="uneven"),
-        # training: gated up projection of a large batch, pre-activations kept, hidden rows in bf16 and in codes
-        dict(name="product 16384x7168", op="product", rows=16384, experts=8, inner=7168, outer=2048, act="swiglu",
-             bias=False, residual=False, keep=True, scales="block", result="both", spread="uneven"),
+             bias=True, residual=True, keep=False, scales="block", then=0, spread="uneven"),
+        # training: both projections of a large batch, pre-activations kept
+        dict(name="products 16384x7168", op="product", rows=16384, experts=8, inner=7168, outer=2048, act="swiglu",
+             bias=False, residual=False, keep=True, scales="block", then=7168, spread="uneven"),
         # a short odd batch through the gradient of a small product
         dict(name="gradient 515x272", op="gradient", rows=515, experts=8, inner=272, outer=512, act="gelu", halves=1,
-             codes=False, spread="uneven"),
-        # gradient of the down projection's rows for a large batch, through the gate
-        dict(name="gradient 16384x2048", op="gradient", rows=16384, experts=8, inner=2048, outer=7168, act="swiglu",
-             halves=1, codes=True, spread="uneven"),
+             then=0, spread="uneven"),
+        # gradients of a large batch's rows through the down projection and the gate, and on through the up projection
+        dict(name="gradients 16384x2048", op="gradient", rows=16384, experts=8, inner=2048, outer=7168, act="swiglu",
+             halves=1, then=7168, spread="uneven"),
     ]
 
 
@@ -77,16 +78,20 @@ def draw(rng):
         return dict(op=op, experts=experts, outer=outer, inner=inner, halves=halves)
     act, rows = rng.choice(ACTS), _log_int(rng, 1, 16384)
     halves = rng.choice((1, 2)) if op == "gradient" and act == "none" else 1
-    wide = 2 if op == "product" and act == "swiglu" else halves
-    while rows * inner * outer * wide > 16384 * 7168 * 2048 * 2 or experts * inner * outer * wide > 32 * 7168 * 2048 * 2:
+    wide = 2 if act == "swiglu" else halves
+    then = _log_int(rng, 32, 8192, 16) if rng.random() < 0.4 else 0
+    if op == "product":
+        cost = inner * outer * wide + outer * then
+    else:
+        cost = inner * outer * halves + inner * then * (2 if act == "swiglu" else 1)
+    while rows * cost > 16384 * 7168 * 2048 * 3 or experts * cost > 32 * 7168 * 2048 * 3:
         rows, experts = (rows + 1) // 2, (experts + 1) // 2
     spread = "uneven" if rows > experts or rng.random() < 0.5 else "single"
+    more = dict(then=then, spread=spread)
     if op == "gradient":
-        return dict(op=op, rows=rows, experts=experts, inner=inner, outer=outer, act=act, halves=halves,
-                    codes=rng.random() < 0.5, spread=spread)
+        return dict(op=op, rows=rows, experts=experts, inner=inner, outer=outer, act=act, halves=halves, **more)
     return dict(op=op, rows=rows, experts=experts, inner=inner, outer=outer, act=act, bias=rng.random() < 0.5,
-                residual=rng.random() < 0.5, keep=rng.random() < 0.5, scales=rng.choice(("block", "row")),
-                result=rng.choice(("bf16", "codes", "both")), spread=spread)
+                residual=rng.random() < 0.5, keep=rng.random() < 0.5, scales=rng.choice(("block", "row")), **more)
 
 
 def _row_counts(case, seed):
@@ -119,6 +124,18 @@ def _coded(x, rows, cols):
     return codes[..., :R, :C].contiguous(), scales
 
 
+def _coded_weights(normal, experts, halves, outer, inner, turned=False):
+    """Codes [experts, halves * outer, inner] with a scale for each 128 x 128 of a half; turned: [experts, outer, halves *
+    inner], as a gradient's product reads them."""
+    codes, scales = [], []
+    for _ in range(experts):
+        c, v = _coded(normal(halves, outer, inner, scale=(halves * inner) ** -0.5).float(), BLOCK, BLOCK)
+        c = c.view(torch.uint8)
+        codes.append(c.transpose(0, 1).reshape(outer, -1) if turned else c.view(halves * outer, inner))
+        scales.append(v.transpose(0, 1) if turned else v)
+    return torch.stack(codes).view(torch.float8_e4m3fn), torch.stack(scales).contiguous()
+
+
 def prepare(case, seed):
     dev = torch.device("cuda")
     g = torch.Generator(device=dev).manual_seed(seed)
@@ -141,7 +158,8 @@ def prepare(case, seed):
         s["codes"] = s["scales"] = None
         if case["codes"] != "none":
             s["codes"] = room(T, H, dtype=torch.uint8).view(torch.float8_e4m3fn)
-            s["scales"] = room(T, _blocks(H), dtype=torch.float32) if case["codes"] == "block" else room(T, dtype=torch.float32)
+            shape = (T, _blocks(H)) if case["codes"] == "block" else (T,)
+            s["scales"] = room(*shape, dtype=torch.float32)
     elif case["op"] == "norm_grad":
         T, H = case["tokens"], case["hidden"]
         s["sum"], s["d_y"] = normal(T, H, scale=2.0), normal(T, H, scale=1e-2)
@@ -171,33 +189,29 @@ def prepare(case, seed):
             s["x"], s["x_scales"] = _coded(normal(rows, K).float(), 1, K if case["scales"] == "row" else BLOCK)
             if case["scales"] == "row":
                 s["x_scales"] = s["x_scales"][:, 0].contiguous()
-            w = [_coded(normal(wide, N, K, scale=K ** -0.5).float(), BLOCK, BLOCK) for _ in range(E)]
-            s["w"] = torch.stack([c.view(torch.uint8).view(wide * N, K) for c, _ in w]).view(torch.float8_e4m3fn)
-            s["w_scales"] = torch.stack([v for _, v in w])
+            s["w"], s["w_scales"] = _coded_weights(normal, E, wide, N, K)
             s["bias"] = normal(E, wide * N, scale=0.1, dtype=torch.float32) if case["bias"] else None
-            s["residual"] = normal(rows, N) if case["residual"] else None
             s["preact"] = room(rows, wide * N) if case["keep"] else None
-            s["out"] = room(rows, N) if case["result"] != "codes" else None
-            coded, made = case["result"] != "bf16", N
+            s["out"] = room(rows, case["then"] or N)
+            s["residual"] = normal(rows, case["then"] or N) if case["residual"] else None
+            if case["then"]:
+                s["w2"], s["w2_scales"] = _coded_weights(normal, E, 1, case["then"], N)
+                s["codes"] = room(rows, N, dtype=torch.uint8).view(torch.float8_e4m3fn)
+                s["scales"] = room(rows, _blocks(N), dtype=torch.float32)
         else:
             h = case["halves"]
             s["dy"], s["dy_scales"] = _coded(normal(rows * h, N, scale=1e-2).float(), 1, BLOCK)
             s["dy"] = s["dy"].view(rows, h * N)
             s["dy_scales"] = s["dy_scales"].view(rows, h, _blocks(N)) if h == 2 else s["dy_scales"]
-            # the transposed weights [K, halves, N], one block of 128 x 128 a scale
-            w = [_coded(normal(h, K, N, scale=K ** -0.5).float(), BLOCK, BLOCK) for _ in range(E)]
-            s["w_t"] = torch.stack([c.view(torch.uint8).transpose(0, 1).reshape(K, h * N) for c, _ in w])
-            s["w_t"] = s["w_t"].view(torch.float8_e4m3fn)
-            s["w_t_scales"] = torch.stack([v.transpose(0, 1) for _, v in w]).contiguous()
+            s["w_t"], s["w_t_scales"] = _coded_weights(normal, E, h, K, N, turned=True)
             s["preact"] = normal(rows, wide * K) if case["act"] != "none" else None
-            s["out"] = room(rows, wide * K)
-            coded, made = case["codes"], K
-        s["codes"] = s["scales"] = None
-        if coded:
-            halves = wide if case["op"] == "gradient" else 1
-            s["codes"] = room(rows, halves * made, dtype=torch.uint8).view(torch.float8_e4m3fn)
-            s["scales"] = room(rows, _blocks(made), dtype=torch.float32) if halves == 1 else \
-                room(rows, 2, _blocks(made), dtype=torch.float32)
+            s["dx"] = room(rows, wide * K)
+            if case["then"]:
+                s["w2_t"], s["w2_t_scales"] = _coded_weights(normal, E, wide, case["then"], K, turned=True)
+                s["codes"] = room(rows, wide * K, dtype=torch.uint8).view(torch.float8_e4m3fn)
+                s["scales"] = room(rows, _blocks(K), dtype=torch.float32) if wide == 1 else \
+                    room(rows, 2, _blocks(K), dtype=torch.float32)
+                s["out"] = room(rows, case["then"])
     return s
 
 
@@ -241,17 +255,28 @@ def _own_quant_weights(s):
 def _own_product(s):
     from combine_fp32_router_amd import binding as B
 
-    B.moe_expert_matmul_fp8(s["x"], s["x_scales"], s["offsets"], s["w"], s["w_scales"], s["bias"],
-                            ACTS.index(s["case"]["act"]), s["residual"], s["out"], s["codes"], s["scales"], s["preact"])
-    return {k: s[k] for k in ("out", "codes", "scales", "preact")}
+    act = ACTS.index(s["case"]["act"])
+    if s["case"]["then"]:
+        B.moe_expert_matmul_fp8(s["x"], s["x_scales"], s["offsets"], s["w"], s["w_scales"], s["bias"], act, None, None,
+                                s["codes"], s["scales"], s["preact"])
+        B.moe_expert_matmul_fp8(s["codes"], s["scales"], s["offsets"], s["w2"], s["w2_scales"], None, B.MOE_ACT_NONE,
+                                s["residual"], s["out"])
+    else:
+        B.moe_expert_matmul_fp8(s["x"], s["x_scales"], s["offsets"], s["w"], s["w_scales"], s["bias"], act, s["residual"],
+                                s["out"], preact=s["preact"])
+    return {k: s[k] for k in ("out", "preact")}
 
 
 def _own_gradient(s):
     from combine_fp32_router_amd import binding as B
 
+    codes = (s["codes"], s["scales"]) if s["case"]["then"] else (None, None)
     B.moe_expert_matmul_fp8_dx(s["dy"], s["dy_scales"], s["offsets"], s["w_t"], s["w_t_scales"],
-                               ACTS.index(s["case"]["act"]), s["preact"], s["out"], s["codes"], s["scales"])
-    return {k: s[k] for k in ("out", "codes", "scales")}
+                               ACTS.index(s["case"]["act"]), s["preact"], s["dx"], *codes)
+    if not s["case"]["then"]:
+        return dict(dx=s["dx"])
+    B.moe_expert_matmul_fp8_dx(*codes, s["offsets"], s["w2_t"], s["w2_t_scales"], B.MOE_ACT_NONE, None, s["out"])
+    return dict(dx=s["dx"], out=s["out"])
 
 
 # ---- the plain forms, in 32 bits, rounded once
@@ -333,43 +358,58 @@ def _act_gradient(z, g, act):
     return g
 
 
+def _plain_rows(x, scales, w, w_scales, counts, halves, outer, inner):
+    """fp32 rows [rows, inner] by their experts' weights [halves * outer, inner]."""
+    x = x.float() * (scales[:, None] if scales.dim() == 1 else _spread(scales, len(x), inner, 1))
+    parts = []
+    for e, rows in enumerate(x.split(counts)):
+        if len(rows):
+            m = w[e].float().view(halves, outer, inner) * _spread(w_scales[e], outer, inner, BLOCK)
+            parts.append(rows @ m.view(halves * outer, inner).t())
+    return torch.cat(parts)
+
+
 def _plain_product(s):
     c = s["case"]
     E, K, N, wide = c["experts"], c["inner"], c["outer"], 2 if c["act"] == "swiglu" else 1
-    x = s["x"].float() * (s["x_scales"][:, None] if c["scales"] == "row" else _spread(s["x_scales"], c["rows"], K, 1))
-    parts = []
-    for e, rows in enumerate(x.split(s["counts"])):
-        if len(rows):
-            w = s["w"][e].float().view(wide, N, K) * _spread(s["w_scales"][e], N, K, BLOCK)
-            z = rows @ w.view(wide * N, K).t()
-            parts.append(z if s["bias"] is None else z + s["bias"][e])
-    z = torch.cat(parts)
+    z = _plain_rows(s["x"], s["x_scales"], s["w"], s["w_scales"], s["counts"], wide, N, K)
+    if s["bias"] is not None:
+        at = torch.repeat_interleave(torch.arange(E, device=z.device), s["offsets"].diff(), output_size=len(z))
+        z = z + s["bias"][at]
     y = _act(z, c["act"])
+    if c["then"]:
+        codes, scales = _coded(y, 1, BLOCK)
+        y = _plain_rows(codes, scales, s["w2"], s["w2_scales"], s["counts"], 1, c["then"], N)
     if s["residual"] is not None:
         y = y + s["residual"].float()
-    codes, scales = _coded(y, 1, BLOCK) if s["codes"] is not None else (None, None)
-    return dict(out=None if s["out"] is None else y.bfloat16(), codes=codes, scales=scales,
-                preact=None if s["preact"] is None else z.bfloat16())
+    return dict(out=y.bfloat16(), preact=None if s["preact"] is None else z.bfloat16())
+
+
+def _plain_back(dy, scales, w_t, w_t_scales, counts, halves, outer, inner):
+    """fp32 rows [rows, halves * inner] by the transposed weights [outer, halves * inner]."""
+    rows = len(dy)
+    dy = dy.float().view(rows, halves, inner) * _spread(scales.view(rows, halves, -1), halves, inner, 1)
+    parts = []
+    for e, d in enumerate(dy.split(counts)):
+        if len(d):
+            m = w_t[e].float().view(outer, halves, inner).transpose(0, 1)
+            m = m * _spread(w_t_scales[e].transpose(0, 1), outer, inner, BLOCK)
+            parts.append(d.reshape(-1, halves * inner) @ m.transpose(0, 1).reshape(outer, halves * inner).t())
+    return torch.cat(parts)
 
 
 def _plain_gradient(s):
     c = s["case"]
-    K, N, h, rows = c["inner"], c["outer"], c["halves"], c["rows"]
-    dy = s["dy"].float().view(rows, h, N) * _spread(s["dy_scales"].view(rows, h, -1), h, N, 1)
-    parts = []
-    for e, d in enumerate(dy.split(s["counts"])):
-        if len(d):
-            scales = s["w_t_scales"][e].transpose(0, 1)  # [halves, blocks of K, blocks of N]
-            w = s["w_t"][e].float().view(K, h, N) * _spread(scales, K, N, BLOCK).transpose(0, 1)
-            parts.append(d.reshape(-1, h * N) @ w.reshape(K, h * N).t())
-    g = torch.cat(parts)
+    wide = 2 if c["act"] == "swiglu" else 1
+    g = _plain_back(s["dy"], s["dy_scales"], s["w_t"], s["w_t_scales"], s["counts"], c["halves"], c["inner"], c["outer"])
     if s["preact"] is not None:
         g = _act_gradient(s["preact"].float(), g, c["act"])
-    codes = scales = None
-    if s["codes"] is not None:
-        codes, scales = _coded(g.view(-1, K), 1, BLOCK)
-        codes, scales = codes.view(rows, -1), scales.view(s["scales"].shape)
-    return dict(out=g.bfloat16(), codes=codes, scales=scales)
+    if not c["then"]:
+        return dict(dx=g.bfloat16())
+    codes, scales = _coded(g.view(-1, c["inner"]), 1, BLOCK)
+    out = _plain_back(codes.view(c["rows"], -1), scales, s["w2_t"], s["w2_t_scales"], s["counts"], wide, c["then"],
+                      c["inner"])
+    return dict(dx=g.bfloat16(), out=out.bfloat16())
 
 
 _own = dict(norm=_own_norm, norm_grad=_own_norm_grad, quant_rows=_own_quant_rows, quant_weights=_own_quant_weights,
@@ -382,6 +422,7 @@ _plain = dict(norm=_plain_norm, norm_grad=_plain_norm_grad, quant_rows=_plain_qu
 
 
 def work(case):
+    op = case["op"]
     if case["op"] == "norm":
         n, T = case["tokens"] * case["hidden"], case["tokens"]
         moved = n * (2 + 4 * case["residual"] + 2 * case["y"] + (case["codes"] != "none")) + 4 * case["hidden"]
@@ -398,17 +439,16 @@ def work(case):
                     flops=2 * n)
     E, K, N, rows = case["experts"], case["inner"], case["outer"], case["rows"]
     wide = 2 if case["act"] == "swiglu" else 1
-    if case["op"] == "product":
-        weights = min(E, rows) * wide * (K * N + 4 * _blocks(K) * _blocks(N))
-        taken = rows * (K + 4 * (_blocks(K) if case["scales"] == "block" else 1) + 2 * N * case["residual"])
-        made = rows * (2 * N * (case["result"] != "codes") + 2 * wide * N * case["keep"])
-        if case["result"] != "bf16":
-            made += rows * (N + 4 * _blocks(N))
-        return dict(bytes=weights + taken + made, flops=2 * rows * K * N * wide)
+    then = case["then"]
+    if op == "product":
+        weights = wide * (K * N + 4 * _blocks(K) * _blocks(N)) + then * N + 4 * _blocks(then) * _blocks(N)
+        taken = K + 4 * (_blocks(K) if case["scales"] == "block" else 1) + 2 * (then or N) * case["residual"]
+        made = 2 * (then or N) + 2 * wide * N * case["keep"]
+        return dict(bytes=min(E, rows) * weights + rows * (taken + made), flops=2 * rows * (K * N * wide + N * then))
     h = case["halves"]
-    weights = min(E, rows) * h * (K * N + 4 * _blocks(K) * _blocks(N))
-    moved = rows * (h * (N + 4 * _blocks(N)) + 2 * wide * K * (1 if case["act"] == "none" else 2))
-    return dict(bytes=weights + moved + rows * wide * (K + 4 * _blocks(K)) * case["codes"], flops=2 * rows * K * N * h)
+    weights = h * (K * N + 4 * _blocks(K) * _blocks(N)) + wide * (then * K + 4 * _blocks(then) * _blocks(K))
+    moved = h * (N + 4 * _blocks(N)) + 2 * wide * K * (1 if case["act"] == "none" else 2) + 2 * then
+    return dict(bytes=min(E, rows) * weights + rows * moved, flops=2 * rows * (K * N * h + K * then * wide))
 
 
 # ---- the same from the definitions, in 64 bits (a code's value before its rounding)
@@ -486,6 +526,15 @@ def _exact_weights(codes, scales):
     return codes.double() * scales.double()[at[0]][:, at[1]]
 
 
+def _exact_rounded(v):
+    """The coded rows v [rows, n] in 64 bits: each value over its scale rounded to the nearest E4M3 number (three bits behind
+    the first, steps of 2^-9 below 2^-6; ties to even)."""
+    q, scales = _exact_codes(v, BLOCK)
+    step = torch.exp2(torch.floor(torch.log2(q.abs().clamp(min=2.0 ** -6))) - 3)
+    at = torch.arange(v.shape[1], device=v.device) // BLOCK
+    return torch.round(q / step) * step * scales[:, at]
+
+
 def _exact_product(s, case):
     K, N, gated = case["inner"], case["outer"], case["act"] == "swiglu"
     scales = s["x_scales"].double().view(case["rows"], -1)
@@ -504,16 +553,23 @@ def _exact_product(s, case):
     else:
         y = dict(none=lambda v: v, relu=torch.relu, silu=torch.nn.functional.silu,
                  gelu=torch.nn.functional.gelu)[case["act"]](z)
+    if case["then"]:
+        h = _exact_rounded(y)
+        y = torch.zeros(case["rows"], case["then"], dtype=torch.float64, device=x.device)
+        for e, n in enumerate(s["counts"]):
+            if n:
+                a = sum(s["counts"][:e])
+                y[a:a + n] = h[a:a + n] @ _exact_weights(s["w2"][e], s["w2_scales"][e][0]).T
     if s["residual"] is not None:
         y = y + s["residual"].double()
-    codes, scales = _exact_codes(y, BLOCK) if s["codes"] is not None else (None, None)
-    return dict(out=None if s["out"] is None else y, codes=codes, scales=scales, preact=None if s["preact"] is None else z)
+    return dict(out=y, preact=None if s["preact"] is None else z)
 
 
 def _exact_gradient(s, case):
-    K, N, h = case["inner"], case["outer"], case["halves"]
-    g = torch.zeros(case["rows"], K, dtype=torch.float64, device=s["dy"].device)
-    at = torch.arange(N, device=g.device) // BLOCK
+    K, N, h, then = case["inner"], case["outer"], case["halves"], case["then"]
+    dev = s["dy"].device
+    g = torch.zeros(case["rows"], K, dtype=torch.float64, device=dev)
+    at = torch.arange(N, device=dev) // BLOCK
     for half in range(h):
         cols = slice(half * N, (half + 1) * N)
         scales = s["dy_scales"].view(case["rows"], h, -1)[:, half].double()
@@ -530,12 +586,16 @@ def _exact_gradient(s, case):
             else:
                 y = dict(relu=torch.relu, silu=torch.nn.functional.silu, gelu=torch.nn.functional.gelu)[case["act"]](z)
             g, = torch.autograd.grad(y, z, g)
-    codes = scales = None
-    if s["codes"] is not None:
-        parts = [_exact_codes(v, BLOCK) for v in g.split(K, dim=1)]
-        codes = torch.cat([c for c, _ in parts], 1)
-        scales = parts[0][1] if len(parts) == 1 else torch.stack([v for _, v in parts], 1)
-    return dict(out=g, codes=codes, scales=scales)
+    if not then:
+        return dict(dx=g)
+    out = torch.zeros(case["rows"], then, dtype=torch.float64, device=dev)
+    for half, v in enumerate(g.split(K, dim=1)):
+        v, cols = _exact_rounded(v), slice(half * K, (half + 1) * K)
+        for e, n in enumerate(s["counts"]):
+            if n:
+                a = sum(s["counts"][:e])
+                out[a:a + n] += v[a:a + n] @ _exact_weights(s["w2_t"][e][:, cols], s["w2_t_scales"][e][:, half]).T
+    return dict(dx=g, out=out)
 
 
 _exact = dict(norm=_exact_norm, norm_grad=_exact_norm_grad, quant_rows=_exact_quant_rows,
