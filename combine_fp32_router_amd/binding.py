@@ -31,10 +31,13 @@ EXPORTS = ("moe_route_topk", "moe_dispatch_layout", "moe_dispatch_layout_chunks"
            "moe_dispatch_pack", "moe_combine", "moe_combine_pack", "moe_status_string",
            "moe_row_bytes", "moe_recv_layout", "moe_recv_regroup", "moe_recv_ungroup",
            "moe_balance_loss", "moe_route_grad", "moe_combine_grad", "moe_expert_matmul",
-           "moe_expert_matmul_dx", "moe_expert_matmul_dw")
+           "moe_expert_matmul_dx", "moe_expert_matmul_dw", "moe_add_norm", "moe_add_norm_grad",
+           "moe_quant_rows", "moe_quant_weights", "moe_expert_matmul_fp8",
+           "moe_expert_matmul_fp8_dx")
 
 MOE_ACT_NONE, MOE_ACT_RELU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_SWIGLU = range(5)
 MOE_GRAD_FP32, MOE_GRAD_BF16, MOE_GRAD_ACCUMULATE = 0, 1, 0x100
+MOE_BLOCK_ROW, MOE_BLOCK_128 = 0, 128  # what a scale of E4M3 codes stands for
 MOE_ROUTE_MASKED_GATES = 0x100  # OR into the k of moe_route_grad's entry point
 
 _lib = None
@@ -79,6 +82,16 @@ def load() -> ctypes.CDLL:
                                          ctypes.POINTER(sz), P]
     lib.moe_expert_matmul_dw.argtypes = [P, P, P, i32, i64, i32, i32, i32, P, P, P,
                                          ctypes.POINTER(sz), P]
+    f32 = ctypes.c_float
+    lib.moe_add_norm.argtypes = [P, P, P, f32, i64, i32, P, P, i32, P, P, P]
+    lib.moe_add_norm_grad.argtypes = [P, P, P, P, f32, i64, i32, P, P, i32, P, ctypes.POINTER(sz),
+                                      P]
+    lib.moe_quant_rows.argtypes = [P, P, i32, i64, i32, i32, P, P, P]
+    lib.moe_quant_weights.argtypes = [P, i32, i32, i32, i32, P, P, P, P, P]
+    lib.moe_expert_matmul_fp8.argtypes = [P, P, i32, P, P, P, P, i32, P, i32, i64, i32, i32, P, P,
+                                          P, P, P, ctypes.POINTER(sz), P]
+    lib.moe_expert_matmul_fp8_dx.argtypes = [P, P, P, P, P, i32, i32, P, i32, i64, i32, i32, P, P,
+                                             P, P, ctypes.POINTER(sz), P]
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_row_bytes.argtypes = [i32, i32]
@@ -692,7 +705,13 @@ def _call_sharing(name: str, stream, workspace: torch.Tensor | None, sizes: tupl
                   like: torch.Tensor, *args) -> None:
     """A product's call with its workspace: `workspace`, or one allocated for the
     call (torch's allocator, in the stream's order) when the sizes want one."""
-    need = expert_workspace_bytes(name, *sizes)
+    _call_with_room(name, stream, workspace, expert_workspace_bytes(name, *sizes), like, *args)
+
+
+def _call_with_room(name: str, stream, workspace: torch.Tensor | None, need: int,
+                    like: torch.Tensor, *args) -> None:
+    """A call with its workspace of `need` bytes, `workspace` or one allocated
+    for the call."""
     if not need:
         _call(name, stream, *args, None, None)
         return
@@ -789,3 +808,226 @@ def moe_expert_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tenso
     _call_sharing("moe_expert_matmul_dw", stream, workspace, (E, rows, K, N), dy, dy, x, offsets,
                   E, rows, K, N, flags, dw, dbias)
     return dw
+
+
+# ---- the norm in front of a layer, E4M3 codes and their products
+
+_CODE_TYPES = (torch.float8_e4m3fn, torch.uint8)  # E4M3 values, or their bits
+
+
+def code_blocks(n: int) -> int:
+    """Blocks of 128 values with a scale each."""
+    return -(-n // MOE_BLOCK_128)
+
+
+def _want_codes(t: torch.Tensor, shape, name: str):
+    if t.dtype not in _CODE_TYPES:
+        raise ValueError(f"{name} must hold E4M3 codes, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _want_floats(t: torch.Tensor, shapes, name: str):
+    """fp32 of one of `shapes`."""
+    _want(t, torch.float32, name)
+    if tuple(t.shape) not in shapes:
+        raise ValueError(f"{name}: expected shape {shapes[0]}, got {tuple(t.shape)}")
+
+
+def _want_coded(codes: torch.Tensor | None, scales: torch.Tensor | None, rows: int, n: int,
+                halves: int, name: str = "codes"):
+    """Codes [rows, halves * n] with their scales [rows, halves, blocks of n] (one
+    half: [rows, blocks] too), or neither."""
+    if (codes is None) != (scales is None):
+        raise ValueError(f"{name} and their scales come together")
+    if codes is not None:
+        _want_codes(codes, (rows, halves * n), name)
+        flat = ((rows, code_blocks(n)),) if halves == 1 else ()
+        _want_floats(scales, ((rows, halves, code_blocks(n)),) + flat, f"the scales of {name}")
+
+
+def moe_add_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor | None,
+                 eps: float, sum: torch.Tensor | None, y: torch.Tensor | None,
+                 codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """s = x + residual (bf16 [T, H] each; residual may be None) and its
+    root-mean-square norm by weight fp32 [H] -> sum and y bf16 [T, H], codes
+    E4M3 [T, H] with scales fp32 [T] (one a row) or [T, ceil(H / 128)]; any output
+    may be None, but not both y and codes."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    for t, name in ((x, "x"), (residual, "residual"), (sum, "sum"), (y, "y")):
+        if t is not None:
+            _want_bf16(t, (T, H), name)
+    if weight is not None:
+        _want_floats(weight, ((H,),), "weight")
+    if (codes is None) != (scales is None):
+        raise ValueError("codes and scales come together")
+    if codes is not None:
+        _want_codes(codes, (T, H), "codes")
+        _want_floats(scales, ((T, code_blocks(H)), (T,)), "scales")
+    block = MOE_BLOCK_ROW if scales is None or scales.dim() == 1 else MOE_BLOCK_128
+    _call("moe_add_norm", stream, x, residual, weight, float(eps), T, H, sum, y, block, codes, scales)
+
+
+@functools.lru_cache(maxsize=4096)
+def add_norm_grad_workspace_bytes(T: int, H: int) -> int:
+    """Workspace of moe_add_norm_grad with d_weight."""
+    n = ctypes.c_size_t(0)
+    _check("moe_add_norm_grad",
+           load().moe_add_norm_grad(None, None, None, None, 0.0, T, H, None, None, 0, None,
+                                    ctypes.byref(n), None))
+    return int(n.value)
+
+
+def moe_add_norm_grad(d_y: torch.Tensor, d_sum: torch.Tensor | None, sum: torch.Tensor,
+                      weight: torch.Tensor | None, eps: float, d_x: torch.Tensor,
+                      d_weight: torch.Tensor | None = None, accumulate: bool = False, stream=None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of moe_add_norm at `sum` bf16 [T, H] from those of y (d_y) and of
+    the sum (d_sum or None): d_x bf16 [T, H], of x and of the residual, and
+    d_weight fp32 [H] (which accumulate adds to) or None.  workspace: scratch of
+    add_norm_grad_workspace_bytes, else allocated where wanted."""
+    if d_y.dim() != 2:
+        raise ValueError("d_y must be [T, H]")
+    T, H = d_y.shape
+    for t, name in ((d_y, "d_y"), (d_sum, "d_sum"), (sum, "sum"), (d_x, "d_x")):
+        if t is not None:
+            _want_bf16(t, (T, H), name)
+    for t, name in ((weight, "weight"), (d_weight, "d_weight")):
+        if t is not None:
+            _want_floats(t, ((H,),), name)
+    need = 0 if d_weight is None else add_norm_grad_workspace_bytes(T, H)
+    _call_with_room("moe_add_norm_grad", stream, workspace, need, d_y, d_y, d_sum, sum, weight,
+                    float(eps), T, H, d_x, d_weight, int(accumulate))
+    return d_x
+
+
+def moe_quant_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                   offsets: torch.Tensor | None = None, halves: int = 1, stream=None) -> None:
+    """bf16 x [rows, H] -> E4M3 codes [rows, H] and scales fp32 [rows, ceil(H / 128)]
+    (halves 2: [rows, 2, ceil(H / 2 / 128)]); with offsets int32 [E+1] of the rows of
+    runs alone."""
+    if x.dim() != 2 or halves not in (1, 2) or x.shape[1] % halves:
+        raise ValueError("x must be [rows, H], in 1 or 2 halves")
+    rows, H = x.shape
+    _want_bf16(x, (rows, H), "x")
+    _want_coded(codes, scales, rows, H // halves, halves)
+    E = 0
+    if offsets is not None:
+        _want(offsets, torch.int32, "offsets")
+        E = offsets.numel() - 1
+        if E < 1:
+            raise ValueError("offsets must hold E+1 int32")
+    _call("moe_quant_rows", stream, x, offsets, E, rows, H, halves, codes, scales)
+
+
+def moe_quant_weights(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                      codes_t: torch.Tensor | None = None, scales_t: torch.Tensor | None = None,
+                      halves: int = 1, stream=None) -> None:
+    """bf16 w [E, halves * N, K] -> E4M3 codes of its shape with scales fp32 [E, halves,
+    ceil(N / 128), ceil(K / 128)], and codes_t [E, K, halves * N] with scales_t [E, ceil(K /
+    128), halves, ceil(N / 128)] (or None)."""
+    if w.dim() != 3 or halves not in (1, 2) or w.shape[1] % halves:
+        raise ValueError("w must be [E, N, K], in 1 or 2 halves of N")
+    E, wide_n, K = w.shape
+    N = wide_n // halves
+    nbn, nbk = code_blocks(N), code_blocks(K)
+    _want_bf16(w, (E, wide_n, K), "w")
+    _want_codes(codes, (E, wide_n, K), "codes")
+    _want_floats(scales, ((E, halves, nbn, nbk),) + (((E, nbn, nbk),) if halves == 1 else ()), "scales")
+    if (codes_t is None) != (scales_t is None):
+        raise ValueError("codes_t and scales_t come together")
+    if codes_t is not None:
+        _want_codes(codes_t, (E, K, wide_n), "codes_t")
+        _want_floats(scales_t, ((E, nbk, halves, nbn),) + (((E, nbk, nbn),) if halves == 1 else ()),
+                     "scales_t")
+    _call("moe_quant_weights", stream, w, E, N, K, halves, codes, scales, codes_t, scales_t)
+
+
+@functools.lru_cache(maxsize=4096)
+def expert_fp8_workspace_bytes(name: str, E: int, rows: int, K: int, N: int,
+                               act: int = MOE_ACT_NONE, halves: int = 1) -> int:
+    """Workspace of moe_expert_matmul_fp8 or _fp8_dx (`name`) for these sizes."""
+    n, i, none = ctypes.c_size_t(0), ctypes.byref, None
+    if name == "moe_expert_matmul_fp8":
+        status = load().moe_expert_matmul_fp8(none, none, 1, none, none, none, none, act, none, E,
+                                              rows, K, N, none, none, none, none, none, i(n), none)
+    else:
+        status = load().moe_expert_matmul_fp8_dx(none, none, none, none, none, halves, act, none, E,
+                                                 rows, K, N, none, none, none, none, i(n), none)
+    _check(name, status)
+    return int(n.value)
+
+
+def moe_expert_matmul_fp8(x: torch.Tensor, x_scales: torch.Tensor, offsets: torch.Tensor,
+                          w: torch.Tensor, w_scales: torch.Tensor, bias: torch.Tensor | None,
+                          act: int, residual: torch.Tensor | None, out: torch.Tensor | None,
+                          codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                          preact: torch.Tensor | None = None, stream=None,
+                          workspace: torch.Tensor | None = None) -> None:
+    """moe_expert_matmul of E4M3 x [rows, K] with x_scales fp32 [rows, ceil(K / 128)]
+    or [rows] (one a row) and w E4M3 [E, N, K] with w_scales [E, ceil(N / 128), ceil(K /
+    128)] (MOE_ACT_SWIGLU: [E, 2N, K], [E, 2, ...]) -> out bf16 [rows, N], codes [rows,
+    N] with scales [rows, ceil(N / 128)], or both; preact as there."""
+    _want_weights(w, offsets)
+    E, wide_n, K = w.shape
+    wide = 2 if act == MOE_ACT_SWIGLU else 1
+    if wide_n % wide:
+        raise ValueError("MOE_ACT_SWIGLU takes an even number of weight rows")
+    rows, N = x.shape[0], wide_n // wide
+    nbn, nbk = code_blocks(N), code_blocks(K)
+    _want_codes(w, (E, wide_n, K), "w")
+    _want_floats(w_scales, ((E, wide, nbn, nbk),) + (((E, nbn, nbk),) if wide == 1 else ()), "w_scales")
+    _want_codes(x, (rows, K), "x")
+    _want_floats(x_scales, ((rows, nbk), (rows,), (rows, 1)), "x_scales")
+    _want_coded(codes, scales, rows, N, 1)
+    for t, n, name in ((out, N, "out"), (residual, N, "residual"), (preact, wide_n, "preact")):
+        if t is not None:
+            _want_bf16(t, (rows, n), name)
+    if bias is not None:
+        _want(bias, torch.float32, "bias")
+        if bias.numel() != E * wide_n:
+            raise ValueError("bias must hold one value per weight row")
+    name = "moe_expert_matmul_fp8"
+    _call_with_room(name, stream, workspace, expert_fp8_workspace_bytes(name, E, rows, K, N, act), x,
+                    x, x_scales, 1 if x_scales.dim() == 1 else x_scales.shape[1], offsets, w,
+                    w_scales, bias, act, residual, E, rows, K, N, out, codes, scales, preact)
+
+
+def moe_expert_matmul_fp8_dx(dy: torch.Tensor, dy_scales: torch.Tensor, offsets: torch.Tensor,
+                             w_t: torch.Tensor, w_t_scales: torch.Tensor, act: int,
+                             preact: torch.Tensor | None, dx: torch.Tensor | None,
+                             codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                             stream=None, workspace: torch.Tensor | None = None) -> None:
+    """moe_expert_matmul_dx of E4M3 dy [rows, N] with dy_scales fp32 [rows, ceil(N /
+    128)] (two halves: [rows, 2N], [rows, 2, ceil(N / 128)]) and moe_quant_weights' codes_t
+    and scales_t -> dx bf16 [rows, K] ([rows, 2K] for MOE_ACT_SWIGLU), its codes with scales
+    [rows, ceil(K / 128)] ([rows, 2, ceil(K / 128)]), or both."""
+    if w_t.dim() != 3:
+        raise ValueError("w_t must be [E, K, N]")
+    _want_weights(w_t, offsets)
+    E, K, wide_n = w_t.shape
+    halves = dy_scales.shape[1] if dy_scales.dim() == 3 else 1
+    if halves not in (1, 2) or wide_n % halves:
+        raise ValueError("dy comes in 1 or 2 halves")
+    rows, N, wide = dy.shape[0], wide_n // halves, 2 if act == MOE_ACT_SWIGLU else 1
+    nbn, nbk = code_blocks(N), code_blocks(K)
+    _want_codes(w_t, (E, K, wide_n), "w_t")
+    _want_floats(w_t_scales, ((E, nbk, halves, nbn),) + (((E, nbk, nbn),) if halves == 1 else ()),
+                 "w_t_scales")
+    _want_coded(dy, dy_scales, rows, N, halves, "dy")
+    _want_coded(codes, scales, rows, K, wide)
+    if dx is not None:
+        _want_bf16(dx, (rows, wide * K), "dx")
+    if act == MOE_ACT_NONE:
+        preact = None
+    elif preact is None:
+        raise ValueError("an activation's gradient needs preact")
+    else:
+        _want_bf16(preact, (rows, wide * K), "preact")
+    name = "moe_expert_matmul_fp8_dx"
+    _call_with_room(name, stream, workspace,
+                    expert_fp8_workspace_bytes(name, E, rows, K, N, act, halves), dy, dy, dy_scales,
+                    offsets, w_t, w_t_scales, halves, act, preact, E, rows, K, N, dx, codes, scales)

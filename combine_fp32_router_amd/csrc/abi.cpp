@@ -51,6 +51,19 @@ int check_product(int E, int64_t max_rows, int K, int N, int most)
     return MOE_OK;
 }
 
+// Rows and eps of the norm (eps >= 0; NaN is none).
+int check_norm(int64_t T, int H, float eps)
+{
+    return T < 0 || T >= kMaxSlots || H < 16 || H > MOE_MAX_HIDDEN || H % 16 != 0 || !(eps >= 0.0f) ? MOE_ERR_SHAPE
+                                                                                                  : MOE_OK;
+}
+
+// The 8-bit products' grids and lists count tiles of 64 x 128 in 32 bits.
+bool fp8_tiles_fit(int E, int64_t max_rows, int cols)
+{
+    return max_row_tiles(max_rows, E, 64) * code_blocks(cols) < (int64_t(1) << 24) - 1;
+}
+
 bool known_act(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_SWIGLU; }
 
 }  // namespace
@@ -562,6 +575,150 @@ int moe_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, 
     return hip_status(
         moe::launch_expert_matmul_dw(dy, x, offsets, E, max_rows, K, N, flags, dw, dbias, workspace,
                                      stream));
+}
+
+int moe_add_norm(const void *x, const void *residual, const float *weight, float eps, int64_t T, int H,
+                 void *sum, void *y, int block, void *codes, float *scales, hipStream_t stream)
+{
+    if (check_norm(T, H, eps) != MOE_OK || (codes && block != MOE_BLOCK_ROW && block != MOE_BLOCK_128))
+        return MOE_ERR_SHAPE;
+    if (T == 0)
+        return MOE_OK;
+    if (!x || (!y && !codes) || (codes && !scales))
+        return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) || !aligned(y, 16) ||
+        !aligned(codes, 16) || (codes && !aligned(scales, 4)))
+        return MOE_ERR_ALIGN;
+    if (y && y == sum)
+        return MOE_ERR_ALIAS;
+    if (codes && (codes == x || codes == residual || codes == sum || codes == y))
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_add_norm(x, residual, weight, eps, T, H, sum, y, block == MOE_BLOCK_128, codes,
+                                           scales, stream));
+}
+
+int moe_add_norm_grad(const void *d_y, const void *d_sum, const void *sum, const float *weight, float eps, int64_t T,
+                      int H, void *d_x, float *d_weight, int accumulate, void *workspace, size_t *workspace_bytes,
+                      hipStream_t stream)
+{
+    if (check_norm(T, H, eps) != MOE_OK || (accumulate != 0 && accumulate != 1))
+        return MOE_ERR_SHAPE;
+    const size_t need = moe::norm_grad_workspace_bytes(T, H);
+    if (!workspace && workspace_bytes) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
+    if (d_weight && (!workspace_bytes || *workspace_bytes < need) && T > 0)
+        return MOE_ERR_WORKSPACE;
+    if (T == 0 && (!d_weight || accumulate))
+        return MOE_OK;
+    if (T > 0 && (!d_y || !sum || !d_x))
+        return MOE_ERR_NULL;
+    if (!aligned(d_y, 16) || !aligned(d_sum, 16) || !aligned(sum, 16) || !aligned(weight, 16) || !aligned(d_x, 16) ||
+        !aligned(d_weight, 16) || !aligned(workspace, 256))
+        return MOE_ERR_ALIGN;
+    return hip_status(moe::launch_add_norm_grad(d_y, d_sum, sum, weight, eps, T, H, d_x, d_weight, accumulate != 0,
+                                                workspace, stream));
+}
+
+int moe_quant_rows(const void *x, const int32_t *offsets, int E, int64_t max_rows, int H, int halves, void *codes,
+                   float *scales, hipStream_t stream)
+{
+    if ((halves != 1 && halves != 2) || H < 16 * halves || H > halves * MOE_MAX_HIDDEN || H % (16 * halves) != 0 ||
+        max_rows < 0 || max_rows > kMaxProductRows || (offsets && (E < 1 || E > MOE_MAX_EXPERTS)))
+        return MOE_ERR_SHAPE;
+    if (max_rows == 0)
+        return MOE_OK;
+    if (!x || !codes || !scales)
+        return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(offsets, 4) || !aligned(codes, 16) || !aligned(scales, 4))
+        return MOE_ERR_ALIGN;
+    if (codes == x)
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_quant_rows(x, offsets, E, max_rows, H / halves, halves, codes, scales, stream));
+}
+
+int moe_quant_weights(const void *w, int E, int N, int K, int halves, void *codes, float *scales, void *codes_t,
+                      float *scales_t, hipStream_t stream)
+{
+    if ((halves != 1 && halves != 2) || check_product(E, 0, K, N, MOE_MAX_HIDDEN) != MOE_OK ||
+        !grid_fits(moe::quant_weights_groups(E, N, K, halves), kRouteThreads))
+        return MOE_ERR_SHAPE;
+    if (!w || !codes || !scales || (codes_t != nullptr) != (scales_t != nullptr))
+        return MOE_ERR_NULL;
+    if (!aligned(w, 16) || !aligned(codes, 16) || !aligned(scales, 4) || !aligned(codes_t, 16) || !aligned(scales_t, 4))
+        return MOE_ERR_ALIGN;
+    if (codes == w || codes_t == w || codes_t == codes || scales_t == scales)
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_quant_weights(w, E, N, K, halves, codes, scales, codes_t, scales_t, stream));
+}
+
+int moe_expert_matmul_fp8(const void *x, const float *x_scales, int x_scale_cols, const int32_t *offsets,
+                          const void *w, const float *w_scales, const float *bias, int act, const void *residual,
+                          int E, int64_t max_rows, int K, int N, void *out, void *codes, float *scales, void *preact,
+                          void *workspace, size_t *workspace_bytes, hipStream_t stream)
+{
+    if (check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK || !known_act(act) ||
+        !fp8_tiles_fit(E, max_rows, act == MOE_ACT_SWIGLU ? 2 * N : N) ||
+        (x_scale_cols != 1 && x_scale_cols != code_blocks(K)))
+        return MOE_ERR_SHAPE;
+    const size_t need = 0;
+    if (!workspace && workspace_bytes) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
+    if (max_rows == 0)
+        return MOE_OK;
+    if (workspace && (!workspace_bytes || *workspace_bytes < need))
+        return MOE_ERR_WORKSPACE;
+    if (!x || !x_scales || !offsets || !w || !w_scales || (!out && !codes) || (codes && !scales))
+        return MOE_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(x_scales, 4) || !aligned(offsets, 4) || !aligned(w, 16) || !aligned(w_scales, 4) ||
+        !aligned(bias, 16) || !aligned(residual, 16) || !aligned(out, 16) || !aligned(codes, 16) ||
+        (codes && !aligned(scales, 4)) || !aligned(preact, 16) || !aligned(workspace, 256))
+        return MOE_ERR_ALIGN;
+    const void *made[] = {out, codes, preact}, *taken[] = {x, w};
+    for (const void *m : made)
+        for (const void *t : taken)
+            if (m && m == t)
+                return MOE_ERR_ALIAS;
+    if ((out && (out == codes || out == preact)) || (codes && (codes == preact || codes == residual)) ||
+        (preact && preact == residual) || (codes && (scales == x_scales || scales == w_scales)))
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_expert_fp8(x, x_scales, x_scale_cols, offsets, w, w_scales, bias, act, residual, E,
+                                             max_rows, K, N, out, codes, scales, preact, stream));
+}
+
+int moe_expert_matmul_fp8_dx(const void *dy, const float *dy_scales, const int32_t *offsets, const void *w_t,
+                             const float *w_t_scales, int halves, int act, const void *preact, int E,
+                             int64_t max_rows, int K, int N, void *dx, void *codes, float *scales, void *workspace,
+                             size_t *workspace_bytes, hipStream_t stream)
+{
+    if ((halves != 1 && halves != 2) || check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK ||
+        !known_act(act) || !fp8_tiles_fit(E, max_rows, K))
+        return MOE_ERR_SHAPE;
+    const size_t need = 0;
+    if (!workspace && workspace_bytes) {
+        *workspace_bytes = need;
+        return MOE_OK;
+    }
+    if (max_rows == 0)
+        return MOE_OK;
+    if (workspace && (!workspace_bytes || *workspace_bytes < need))
+        return MOE_ERR_WORKSPACE;
+    if (!dy || !dy_scales || !offsets || !w_t || !w_t_scales || (!dx && !codes) || (codes && !scales) ||
+        (act != MOE_ACT_NONE && !preact))
+        return MOE_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(dy_scales, 4) || !aligned(offsets, 4) || !aligned(w_t, 16) ||
+        !aligned(w_t_scales, 4) || !aligned(preact, 16) || !aligned(dx, 16) || !aligned(codes, 16) ||
+        (codes && !aligned(scales, 4)) || !aligned(workspace, 256))
+        return MOE_ERR_ALIGN;
+    if ((dx && (dx == dy || dx == w_t || dx == codes)) ||
+        (codes && (codes == dy || codes == w_t || (act != MOE_ACT_NONE && codes == preact) || scales == dy_scales ||
+                   scales == w_t_scales)))
+        return MOE_ERR_ALIAS;
+    return hip_status(moe::launch_expert_fp8_dx(dy, dy_scales, offsets, w_t, w_t_scales, halves, act, preact, E,
+                                                max_rows, K, N, dx, codes, scales, stream));
 }
 
 }  // extern "C"

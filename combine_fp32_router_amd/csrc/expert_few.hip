@@ -34,32 +34,6 @@ struct Few {
     int act, E, max_rows, K, N;
 };
 
-// The index-th tile of `height` rows over all runs in expert order (a run's
-// last tile is short); n == 0 past the last.
-struct RowTile {
-    int e, first, n;
-};
-__device__ __forceinline__ RowTile find_row_tile(const int32_t *__restrict__ offsets, int E, int max_rows,
-                                                 int height, int index)
-{
-    int before = 0;  // tiles of the experts below e0
-    for (int e0 = 0; e0 < E; e0 += kWave) {
-        const int e = min(e0 + lane_id(), E);
-        const int first = run_start(offsets, e, max_rows);
-        const int n = max(run_start(offsets, min(e + 1, E), max_rows) - first, 0);
-        const int tiles = (n + height - 1) / height;
-        const int upto = before + wave_inclusive_scan(tiles);
-        const uint64_t hit = __ballot(upto > index);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            const int in_run = (index - (lane_value(upto, l) - lane_value(tiles, l))) * height;
-            return {e0 + l, lane_value(first, l) + in_run, min(height, lane_value(n, l) - in_run)};
-        }
-        before = lane_value(upto, kWave - 1);
-    }
-    return {0, 0, 0};
-}
-
 // One wave's stream: 16 weight rows (GATED: 16 gate and 16 up) and 16 MB rows
 // of x, 64 of K a chunk, through a ring of kDepth chunks in its own LDS.  An
 // image is 16 rows of 128 bytes, piece c of row i at c ^ (i / 2) % 8.

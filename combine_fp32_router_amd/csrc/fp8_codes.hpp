@@ -1,0 +1,47 @@
+// E4M3 codes with one fp32 scale for a block of values: scale = max|v| / 448,
+// code = E4M3(v / scale), the payload's rule (a block of zeros: scale 0, codes
+// 0).  The largest size is taken over the values' bits, where a NaN is above an
+// infinity: a block that holds either gets it as its scale, and whoever
+// multiplies by that reads NaN.
+#pragma once
+
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace moe {
+
+__device__ __forceinline__ uint32_t size_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Largest of a 16-lane row, in every lane of it.
+__device__ __forceinline__ uint32_t row_umax(uint32_t v)
+{
+    v = umax(v, dpp32<0xB1>(v));
+    v = umax(v, dpp32<0x4E>(v));
+    v = umax(v, dpp32<0x141>(v));
+    return umax(v, dpp32<0x140>(v));
+}
+
+// A subnormal scale is rounded up, so that no quotient is above 448 by more than
+// its last bit (the conversion makes NaN of what rounds past 448).
+__device__ __forceinline__ float scale_of(uint32_t top)
+{
+    const float s = __uint_as_float(top) / 448.0f;
+    return __float_as_uint(s) < 0x00800000u && top ? __uint_as_float(__float_as_uint(s) + 1u) : s;
+}
+
+// Four codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float scale)
+{
+    if (scale == 0.0f)
+        return 0u;
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a / scale, b / scale, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c / scale, d / scale, w, true);
+    return static_cast<uint32_t>(w);
+}
+__device__ __forceinline__ u32x2 codes8(const float (&f)[8], float scale)
+{
+    return u32x2{codes4(f[0], f[1], f[2], f[3], scale), codes4(f[4], f[5], f[6], f[7], scale)};
+}
+
+}  // namespace moe

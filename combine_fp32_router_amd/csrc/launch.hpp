@@ -113,6 +113,32 @@ hipError_t launch_combine_grad(const void *d_out, const void *rows, const float 
                                const int32_t *pos, const float *w, int64_t T, int H, int k,
                                void *d_rows, float *d_w, hipStream_t stream);
 
+// Blocks of values with one scale, along a row.
+constexpr int kCodeBlock = 128;
+constexpr int code_blocks(int n) { return (n + kCodeBlock - 1) / kCodeBlock; }
+
+// The residual's addition with the norm, and its gradient; codes and scales of
+// rows and of weights.
+hipError_t launch_add_norm(const void *x, const void *residual, const float *weight, float eps, int64_t T, int H,
+                           void *sum, void *y, bool blocks, void *codes, float *scales, hipStream_t stream);
+size_t norm_grad_workspace_bytes(int64_t T, int H);
+hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *sum, const float *weight, float eps,
+                                int64_t T, int H, void *d_x, float *d_weight, bool accumulate, void *workspace,
+                                hipStream_t stream);
+hipError_t launch_quant_rows(const void *x, const int32_t *offsets, int E, int64_t max_rows, int n, int halves,
+                             void *codes, float *scales, hipStream_t stream);
+int64_t quant_weights_groups(int E, int N, int K, int halves);  // of kRouteThreads threads
+hipError_t launch_quant_weights(const void *w, int E, int N, int K, int halves, void *codes, float *scales,
+                                void *codes_t, float *scales_t, hipStream_t stream);
+
+// The experts' products of E4M3 rows and weights, and the gradient of their rows.
+hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const int32_t *offsets, const void *w,
+                             const float *ws, const float *bias, int act, const void *residual, int E, int64_t max_rows,
+                             int K, int N, void *out, void *codes, float *scales, void *preact, hipStream_t stream);
+hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
+                                const float *wts, int halves, int act, const void *z, int E, int64_t max_rows, int K,
+                                int N, void *dx, void *codes, float *scales, hipStream_t stream);
+
 // The experts' products over their runs of rows, and their gradients.
 hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const void *w,
                                 const float *bias, int act, const void *residual, int E,

@@ -1,0 +1,384 @@
+// The residual's addition with the root-mean-square norm, and its gradient.
+//
+//   s = x + r,   y = s R w,   R = (mean(s^2) + eps)^(-1/2)
+//   d_x = d_s + R g - s R^3 mean(g s),  g = d_y w;   d_w = sum over rows of d_y s R
+//
+// A row is read once and held in registers (THREADS threads, VPT 16-byte vectors
+// each) between its sums and its results.  Sixteen lanes hold the 128 values of a
+// block of codes, a row of the DPP moves.  The gradient of w stays in registers
+// over all rows of a workgroup; the workgroups' sums meet in a second kernel, in a
+// fixed order.
+#include "fp8_codes.hpp"
+#include "launch.hpp"
+
+namespace moe {
+namespace {
+
+struct Norm {
+    const uint16_t *x, *residual;
+    const float *weight;
+    float eps;
+    int64_t T;
+    int H;
+    uint16_t *sum, *y;
+    uint8_t *codes;
+    float *scales;
+    bool blocks;  // a scale for each block of 128, else for the row
+};
+
+__device__ __forceinline__ float wave_sum(float v)
+{
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1)
+        v += __shfl_xor(v, o);
+    return v;
+}
+
+// N sums over the row's threads (THREADS of them, one wave or the workgroup);
+// `red` holds 2 * N * 16 floats.  `turn` alternates between its halves, so that one
+// barrier a row is enough.
+template <int THREADS, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float *red, int turn)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = wave_sum(v[i]);
+    if (THREADS == kWave)
+        return;
+    float *mine = red + turn * N * 16;
+    if (lane_id() == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            mine[i * 16 + threadIdx.x / kWave] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        v[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < THREADS / kWave; ++w)
+            v[i] += mine[i * 16 + w];
+    }
+}
+
+template <int THREADS>
+__device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *red, int turn)
+{
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1)
+        v = umax(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o)));
+    if (THREADS == kWave)
+        return v;
+    uint32_t *mine = red + turn * 16;
+    if (lane_id() == 0)
+        mine[threadIdx.x / kWave] = v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / kWave; ++w)
+        v = umax(v, mine[w]);
+    return v;
+}
+
+// Rows of a workgroup at once, and its threads.
+constexpr int rows_of(int threads) { return threads == kWave ? 4 : 1; }
+constexpr int group_of(int threads) { return threads == kWave ? 4 * kWave : threads; }
+
+// A row's bytes; a row past the last is empty.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void *p, int64_t t, int bytes, bool live)
+{
+    return row_rsrc(const_cast<char *>(static_cast<const char *>(p)) + t * bytes, p && live ? bytes : 0);
+}
+
+template <int THREADS, int VPT>
+__global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
+{
+    constexpr int kRows = rows_of(THREADS);
+    __shared__ float red[2 * 16];
+    __shared__ uint32_t tops[2 * 16];
+    const int l = THREADS == kWave ? lane_id() : static_cast<int>(threadIdx.x);
+    const int first = THREADS == kWave ? static_cast<int>(uniform(threadIdx.x / kWave)) : 0;
+    const int nb = code_blocks(a.H);
+    float w[VPT][8];
+    {
+        const __amdgpu_buffer_rsrc_t r = row_of(a.weight, 0, a.H * 4, true);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 v = load_cached(r, (l + i * THREADS) * 32 + h * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[i][h * 4 + j] = a.weight ? __uint_as_float(v[j]) : 1.0f;
+            }
+    }
+    int turn = 0;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t t = t0 + first;
+        const bool live = t < a.T;
+        const __amdgpu_buffer_rsrc_t xr = row_of(a.x, t, a.H * 2, live), rr = row_of(a.residual, t, a.H * 2, live);
+        u32x4 v[VPT], u[VPT];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            v[i] = load_cached(xr, (l + i * THREADS) * 16);
+            u[i] = load_cached(rr, (l + i * THREADS) * 16);
+        }
+        float s[VPT][8], ss[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float f[8];
+            unpack8(v[i], s[i]);
+            unpack8(u[i], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (a.residual)
+                    s[i][j] += f[j];
+                ss[0] = fmaf(s[i][j], s[i][j], ss[0]);
+            }
+        }
+        if (a.sum) {
+            const __amdgpu_buffer_rsrc_t to = row_of(a.sum, t, a.H * 2, live);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(s[i]), to, (l + i * THREADS) * 16, 0, 0);
+        }
+        row_sums<THREADS, 1>(ss, red, turn);
+        const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.H) + a.eps);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s[i][j] = s[i][j] * r * w[i][j];
+        if (a.y) {
+            const __amdgpu_buffer_rsrc_t to = row_of(a.y, t, a.H * 2, live);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+                __builtin_amdgcn_raw_buffer_store_b128(pack8(s[i]), to, (l + i * THREADS) * 16, 0, 0);
+        }
+        if (a.codes) {
+            const __amdgpu_buffer_rsrc_t to = row_of(a.codes, t, a.H, live);
+            uint32_t top[VPT], all = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                top[i] = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)  // (past the row w has zeros, but an infinite r would make them NaN)
+                    top[i] = umax(top[i], (l + i * THREADS) * 8 < a.H ? size_bits(s[i][j]) : 0u);
+                all = umax(all, top[i]);
+            }
+            if (!a.blocks) {
+                all = row_top<THREADS>(all, tops, turn);
+                if (l == 0 && live)
+                    a.scales[t] = scale_of(all);
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = l + i * THREADS;
+                const float scale = scale_of(a.blocks ? row_umax(top[i]) : all);
+                if (a.blocks && c % 16 == 0 && c * 8 < a.H && live)
+                    a.scales[t * nb + c / 16] = scale;
+                __builtin_amdgcn_raw_buffer_store_b64(codes8(s[i], scale), to, c * 8, 0, 0);
+            }
+        }
+        turn ^= 1;
+    }
+}
+
+struct NormGrad {
+    const uint16_t *dy, *dsum, *sum;
+    const float *weight;
+    float eps;
+    int64_t T;
+    int H;
+    uint16_t *dx;
+    float *part;  // [workgroups * rows at once][H], or null
+};
+
+// HOLD: a row stays in registers between its sums and its results; else it is
+// read again (from cache: 128 KiB at the longest).
+template <int THREADS, int VPT, bool HOLD>
+__global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGrad a)
+{
+    constexpr int kRows = rows_of(THREADS), kHeld = HOLD ? VPT : 1;
+    __shared__ float red[2 * 2 * 16];
+    const int l = THREADS == kWave ? lane_id() : static_cast<int>(threadIdx.x);
+    const int first = THREADS == kWave ? static_cast<int>(uniform(threadIdx.x / kWave)) : 0;
+    const __amdgpu_buffer_rsrc_t wr = row_of(a.weight, 0, a.H * 4, true);
+    auto weights = [&](int i, float(&w)[8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const u32x4 v = load_cached(wr, (l + i * THREADS) * 32 + h * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[h * 4 + j] = a.weight ? __uint_as_float(v[j]) : 1.0f;
+        }
+    };
+    float dw[VPT][8] = {};
+    int turn = 0;
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t t = t0 + first;
+        const bool live = t < a.T;
+        const __amdgpu_buffer_rsrc_t sr = row_of(a.sum, t, a.H * 2, live), yr = row_of(a.dy, t, a.H * 2, live);
+        const __amdgpu_buffer_rsrc_t dr = row_of(a.dsum, t, a.H * 2, live), to = row_of(a.dx, t, a.H * 2, live);
+        u32x4 sv[kHeld], yv[kHeld];
+        float sums[2] = {0.0f, 0.0f};  // of s^2 and of g s
+        if (HOLD)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                sv[HOLD ? i : 0] = load_cached(sr, (l + i * THREADS) * 16);
+                yv[HOLD ? i : 0] = load_cached(yr, (l + i * THREADS) * 16);
+            }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float s[8], g[8], w[8];
+            unpack8(HOLD ? sv[HOLD ? i : 0] : load_cached(sr, (l + i * THREADS) * 16), s);
+            unpack8(HOLD ? yv[HOLD ? i : 0] : load_cached(yr, (l + i * THREADS) * 16), g);
+            weights(i, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sums[0] = fmaf(s[j], s[j], sums[0]);
+                sums[1] = fmaf(g[j] * w[j], s[j], sums[1]);
+            }
+        }
+        row_sums<THREADS, 2>(sums, red, turn);
+        const float n = static_cast<float>(a.H), r = 1.0f / sqrtf(sums[0] / n + a.eps);
+        const float back = r * r * (sums[1] / n);  // of s R
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float s[8], g[8], w[8], d[8];
+            unpack8(HOLD ? sv[HOLD ? i : 0] : load_cached(sr, (l + i * THREADS) * 16), s);
+            unpack8(HOLD ? yv[HOLD ? i : 0] : load_cached(yr, (l + i * THREADS) * 16), g);
+            unpack8(load_cached(dr, (l + i * THREADS) * 16), d);
+            weights(i, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float x = s[j] * r;
+                dw[i][j] = live ? fmaf(g[j], x, dw[i][j]) : dw[i][j];  // (of a missing row r may be infinite)
+                const float v = fmaf(g[j] * w[j], r, -x * back);
+                d[j] = a.dsum ? d[j] + v : v;
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(pack8(d), to, (l + i * THREADS) * 16, 0, 0);
+        }
+        turn ^= 1;
+    }
+    if (a.part) {
+        const __amdgpu_buffer_rsrc_t to = row_of(a.part, static_cast<int64_t>(blockIdx.x) * kRows + first, a.H * 4, true);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = __float_as_uint(dw[i][h * 4 + j]);
+                __builtin_amdgcn_raw_buffer_store_b128(v, to, (l + i * THREADS) * 32 + h * 16, 0, 0);
+            }
+    }
+}
+
+// d_w from the workgroups' sums: 32 columns a workgroup, its 32 groups of threads
+// every 32nd part each.
+__global__ __launch_bounds__(1024) void norm_weight_kernel(const float *__restrict__ part, int parts, int H,
+                                                           bool accumulate, float *__restrict__ dw)
+{
+    __shared__ float sums[32][33];
+    const int x = threadIdx.x % 32, y = threadIdx.x / 32, c = blockIdx.x * 32 + x;
+    float sum = 0.0f;
+    if (c < H)
+        for (int p = y; p < parts; p += 32)
+            sum += part[static_cast<int64_t>(p) * H + c];
+    sums[y][x] = sum;
+    __syncthreads();
+    if (y == 0 && c < H) {
+        float all = accumulate ? dw[c] : 0.0f;
+        for (int i = 0; i < 32; ++i)
+            all += sums[i][x];
+        dw[c] = all;
+    }
+}
+
+// Threads and vectors of a row.
+struct NormTiling {
+    int threads, vpt;
+};
+NormTiling norm_tiling(int64_t T, int H)
+{
+    const int vecs = H / 8;
+    NormTiling n{kWave, 1};
+    if (vecs > 4 * kWave)
+        n.threads = vecs > 4 * 256 ? 1024 : 256;
+    while (n.threads * n.vpt < vecs)
+        n.vpt *= 2;
+    return n;
+}
+int norm_groups(int64_t T, int rows, int most)
+{
+    const int64_t n = (T + rows - 1) / rows;
+    return static_cast<int>(n < most ? n : most);
+}
+// Workgroups of the gradient's first kernel.
+int grad_groups(int64_t T, const NormTiling &n) { return norm_groups(T, rows_of(n.threads), n.threads == 1024 ? kCus : 4 * kCus); }
+
+}  // namespace
+
+size_t norm_grad_workspace_bytes(int64_t T, int H)
+{
+    const NormTiling n = norm_tiling(T, H);
+    return static_cast<size_t>(grad_groups(T, n)) * rows_of(n.threads) * H * 4;
+}
+
+#define MOE_NORM(THREADS, VPT)                                                                          \
+    if (n.threads == THREADS && n.vpt == VPT)                                                           \
+    add_norm_kernel<THREADS, VPT><<<dim3(norm_groups(T, rows_of(THREADS), THREADS == 1024 ? 2 * kCus : 8 * kCus)), group_of(THREADS), 0, stream>>>(a)
+
+hipError_t launch_add_norm(const void *x, const void *residual, const float *weight, float eps, int64_t T, int H,
+                           void *sum, void *y, bool blocks, void *codes, float *scales, hipStream_t stream)
+{
+    Norm a{};
+    a.x = static_cast<const uint16_t *>(x), a.residual = static_cast<const uint16_t *>(residual);
+    a.weight = weight, a.eps = eps, a.T = T, a.H = H;
+    a.sum = static_cast<uint16_t *>(sum), a.y = static_cast<uint16_t *>(y);
+    a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.blocks = blocks;
+    const NormTiling n = norm_tiling(T, H);
+    MOE_NORM(64, 1);
+    MOE_NORM(64, 2);
+    MOE_NORM(64, 4);
+    MOE_NORM(256, 2);
+    MOE_NORM(256, 4);
+    MOE_NORM(1024, 2);
+    MOE_NORM(1024, 4);
+    MOE_NORM(1024, 8);
+    return hipGetLastError();
+}
+
+#define MOE_NORM_GRAD(THREADS, VPT)                                                                     \
+    if (n.threads == THREADS && n.vpt == VPT)                                                           \
+    add_norm_grad_kernel<THREADS, VPT, (VPT < 8)><<<dim3(groups), group_of(THREADS), 0, stream>>>(a)
+
+hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *sum, const float *weight, float eps,
+                                int64_t T, int H, void *d_x, float *d_weight, bool accumulate, void *workspace,
+                                hipStream_t stream)
+{
+    NormGrad a{};
+    a.dy = static_cast<const uint16_t *>(d_y), a.dsum = static_cast<const uint16_t *>(d_sum);
+    a.sum = static_cast<const uint16_t *>(sum), a.weight = weight, a.eps = eps, a.T = T, a.H = H;
+    a.dx = static_cast<uint16_t *>(d_x), a.part = d_weight ? static_cast<float *>(workspace) : nullptr;
+    const NormTiling n = norm_tiling(T, H);
+    const int groups = grad_groups(T, n);
+    if (T > 0) {
+        MOE_NORM_GRAD(64, 1);
+        MOE_NORM_GRAD(64, 2);
+        MOE_NORM_GRAD(64, 4);
+        MOE_NORM_GRAD(256, 2);
+        MOE_NORM_GRAD(256, 4);
+        MOE_NORM_GRAD(1024, 2);
+        MOE_NORM_GRAD(1024, 4);
+        MOE_NORM_GRAD(1024, 8);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess)
+            return err;
+    }
+    if (d_weight)
+        norm_weight_kernel<<<dim3((H + 31) / 32), 1024, 0, stream>>>(a.part, groups * rows_of(n.threads), H, accumulate, d_weight);
+    return hipGetLastError();
+}
+
+}  // namespace moe

@@ -229,6 +229,114 @@ int moe_expert_matmul_dw(const void *dy, const void *x, const int32_t *offsets, 
                          int64_t max_rows, int K, int N, int flags, void *dw, float *dbias,
                          void *workspace, size_t *workspace_bytes, hipStream_t stream);
 
+/*
+ * moe_quant_rows -- bf16 rows in E4M3 codes with a scale for each 128 values
+ * (MOE_BLOCK_128, moe_route.h), as the 8-bit products take them.
+ *
+ *   x          [max_rows, H] bf16 bits.                               (in)
+ *   offsets    NULL: all rows; or [E+1] int32, device, as moe_expert_matmul's:
+ *              rows of no run are not written.                        (in)
+ *   E, max_rows  1 <= E <= MOE_MAX_EXPERTS (with offsets), 0 <= max_rows <= 2^31 -
+ *              256.
+ *   halves     1, or 2: a row is two halves with blocks of their own (the gradient
+ *              of a gated product's pre-activations).
+ *   H          a multiple of 16 halves in [16 halves, halves * MOE_MAX_HIDDEN].
+ *   codes      [max_rows, H] E4M3.                                    (out)
+ *   scales     [max_rows, halves, ceil(H / halves / 128)] fp32.       (out)
+ *
+ * Arrays 16-byte aligned (offsets and scales 4), not overlapping.  Errors:
+ * MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN, MOE_ERR_ALIAS (codes start where x does).
+ * max_rows == 0: MOE_OK, nothing launched.
+ */
+int moe_quant_rows(const void *x, const int32_t *offsets, int E, int64_t max_rows, int H,
+                   int halves, void *codes, float *scales, hipStream_t stream);
+
+/*
+ * moe_quant_weights -- weights in E4M3 codes with a scale for each 128 x 128,
+ * and the same codes transposed, for the product and for its gradient.
+ *
+ *   w          [E, halves * N, K] bf16 bits.                          (in)
+ *   E, N, K    as moe_expert_matmul.
+ *   halves     1, or 2: N gate rows, then N up rows (MOE_ACT_SWIGLU), each half
+ *              with blocks of its own.
+ *   codes      [E, halves * N, K] E4M3.                               (out)
+ *   scales     [E, halves, ceil(N / 128), ceil(K / 128)] fp32.        (out)
+ *   codes_t    [E, K, halves * N] E4M3, or NULL with scales_t.        (out)
+ *   scales_t   [E, ceil(K / 128), halves, ceil(N / 128)] fp32.        (out)
+ *
+ * Arrays 16-byte aligned (scales 4), not overlapping.  Errors: MOE_ERR_NULL,
+ * MOE_ERR_SHAPE (also 2^24 blocks of 128 x 128 or more), MOE_ERR_ALIGN,
+ * MOE_ERR_ALIAS (two of the arrays of codes and w, or both scales, at one place).
+ */
+int moe_quant_weights(const void *w, int E, int N, int K, int halves, void *codes, float *scales,
+                      void *codes_t, float *scales_t, hipStream_t stream);
+
+/*
+ * moe_expert_matmul_fp8 -- moe_expert_matmul of E4M3 rows and weights:
+ *     z[p, n] = sum over blocks b of 128 of
+ *               x_scales[p, b] w_scales[n / 128, b] sum_{k in b} x[p, k] w[n, k]  + bias[n]
+ *     y[p, n] = act(z[p, n]) + residual[p, n]
+ * A block's products are summed by the matrix cores and scaled in fp32.  y leaves
+ * in bf16 (out), in codes with a scale for each 128 values, or in both, each
+ * rounded once from fp32; the codes are the next product's rows.
+ *
+ *   x          [max_rows, K] E4M3.                                    (in)
+ *   x_scales   [max_rows, x_scale_cols] fp32: x_scale_cols is ceil(K / 128), or 1:
+ *              one scale a row, the rows of a MOE_QUANT_FP8 payload as
+ *              moe_recv_regroup leaves them.                          (in)
+ *   offsets, E, max_rows, K, N, act, bias, residual, preact
+ *              as moe_expert_matmul (residual may be out itself).     (in, out)
+ *   w          [E, N, K] E4M3 (MOE_ACT_SWIGLU: [E, 2N, K], an expert's N gate
+ *              rows, then its N up rows).                             (in)
+ *   w_scales   [E, ceil(N / 128), ceil(K / 128)] fp32 (MOE_ACT_SWIGLU: [E, 2, ...],
+ *              each half with blocks of its own): moe_quant_weights.  (in)
+ *   out        [max_rows, N] bf16 bits, or NULL.                      (out)
+ *   codes, scales   [max_rows, N] E4M3 and [max_rows, ceil(N / 128)] fp32, or
+ *              NULL; not both out and codes NULL.                     (out)
+ *   workspace, workspace_bytes   as moe_expert_matmul.
+ *
+ * Rows of no run are not written.  Arrays 16-byte aligned (offsets and scales 4);
+ * outputs overlap neither each other nor the inputs, but for out == residual.
+ * Errors: as moe_expert_matmul (here 2^24 tiles of 64 x 128 are too many);
+ * MOE_ERR_ALIAS when an output starts where an input or another output does.
+ */
+int moe_expert_matmul_fp8(const void *x, const float *x_scales, int x_scale_cols,
+                          const int32_t *offsets, const void *w, const float *w_scales,
+                          const float *bias, int act, const void *residual, int E,
+                          int64_t max_rows, int K, int N, void *out, void *codes, float *scales,
+                          void *preact, void *workspace, size_t *workspace_bytes,
+                          hipStream_t stream);
+
+/*
+ * moe_expert_matmul_fp8_dx -- moe_expert_matmul_dx of a gradient in codes and
+ * the transposed weights' codes.  For z = x W_e^T and the codes dy of z's gradient:
+ *     g[p, k] = sum over blocks b of 128 of
+ *               dy_scales[p, b] w_t_scales[k / 128, b] sum_{n in b} dy[p, n] w_t[k, n]
+ * carried through the activation as there; the quantisation of x, of W and of the
+ * gradient counts as the identity.  (The weights' gradient is moe_expert_matmul_dw,
+ * of bf16 rows.)
+ *
+ *   dy, dy_scales   [max_rows, halves * N] E4M3 and [max_rows, halves, ceil(N /
+ *              128)] fp32: moe_quant_rows.                            (in)
+ *   w_t, w_t_scales  [E, K, halves * N] and [E, ceil(K / 128), halves, ceil(N /
+ *              128)]: moe_quant_weights' codes_t and scales_t.        (in)
+ *   halves     2 for the gradient of a MOE_ACT_SWIGLU product, else 1.
+ *   offsets, act, preact, E, max_rows   as moe_expert_matmul_dx.      (in)
+ *   K, N       multiples of 16 in [16, MOE_MAX_HIDDEN]; N counts one half.
+ *   dx         as moe_expert_matmul_dx (may be preact itself), or NULL. (out)
+ *   codes, scales   dx in codes: [max_rows, K] and [max_rows, ceil(K / 128)]
+ *              (MOE_ACT_SWIGLU: [max_rows, 2K] and [max_rows, 2, ceil(K / 128)]), or
+ *              NULL; not both dx and codes NULL.                      (out)
+ *   workspace, workspace_bytes   as moe_expert_matmul.
+ *
+ * Errors: as moe_expert_matmul_fp8.
+ */
+int moe_expert_matmul_fp8_dx(const void *dy, const float *dy_scales, const int32_t *offsets,
+                             const void *w_t, const float *w_t_scales, int halves, int act,
+                             const void *preact, int E, int64_t max_rows, int K, int N, void *dx,
+                             void *codes, float *scales, void *workspace,
+                             size_t *workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

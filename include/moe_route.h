@@ -32,6 +32,9 @@
  * combine for the rows and the gate weights).  The pack's gradient is
  * moe_combine with weights of 1: a token's gradient is the sum of its rows'.
  *
+ * In front of a layer: moe_add_norm (the residual's addition and the norm, in
+ * bf16 and in E4M3 codes) and its gradient, moe_add_norm_grad.
+ *
  * Conventions shared by every call
  *   - All array arguments are DEVICE pointers owned by the caller; the
  *     library allocates nothing and keeps no global state, so calls are
@@ -494,6 +497,73 @@ int moe_route_grad(const float *logits, const int32_t *topk_idx, const float *to
 int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv_scales, int quant,
                      const int32_t *pos, const float *topk_w, int64_t T, int H, int k,
                      void *d_recv, float *d_topk_w, hipStream_t stream);
+
+/* What a scale of E4M3 codes stands for: a whole row (as in a payload of
+ * MOE_QUANT_FP8), or each 128 values of it, the last block as long as the row
+ * lasts.  A block's scale and codes follow the payload's rule: scale = max|v| /
+ * 448, code = E4M3(v / scale), zeros for zeros; a block that holds a NaN or an
+ * infinity has it as its scale, and its values read NaN. */
+#define MOE_BLOCK_ROW 0
+#define MOE_BLOCK_128 128
+
+/*
+ * moe_add_norm -- what stands in front of a layer: the residual's addition and
+ * the root-mean-square norm, in bf16, in E4M3 codes for 8-bit products
+ * (moe_expert_matmul_fp8, moe_recv.h), or both:
+ *     s[t, h] = x[t, h] + residual[t, h]
+ *     y[t, h] = s[t, h] * (mean_h s[t, h]^2 + eps)^(-1/2) * weight[h]
+ * s stays in fp32 between the two lines; sum, y and codes are rounded once each.
+ * A row whose squares leave fp32 (|s| above 1e19) is not normed.
+ *
+ *   x          [T, H] bf16 bits.                                      (in)
+ *   residual   [T, H] bf16 bits, or NULL: s = x.                      (in)
+ *   weight     [H] fp32, or NULL: 1.                                  (in)
+ *   eps        >= 0.
+ *   T, H       0 <= T < 2^31; H a multiple of 16 in [16, MOE_MAX_HIDDEN].
+ *   sum        [T, H] bf16 bits of s, or NULL; may be x or residual.  (out)
+ *   y          [T, H] bf16 bits, or NULL; may be x or residual, not sum. (out)
+ *   block      MOE_BLOCK_ROW or MOE_BLOCK_128; not used without codes.
+ *   codes      [T, H] E4M3, or NULL; not both y and codes NULL.       (out)
+ *   scales     [T] fp32 (MOE_BLOCK_ROW) or [T, ceil(H / 128)]; with codes. (out)
+ *
+ * Arrays 16-byte aligned (scales 4), not overlapping but for the whole arrays
+ * named above.  Errors: MOE_ERR_NULL, MOE_ERR_SHAPE (also eps < 0 or NaN, an unknown
+ * block), MOE_ERR_ALIGN, MOE_ERR_ALIAS (y starts where sum does, or codes where
+ * any other array).  T == 0: MOE_OK, nothing launched.
+ */
+int moe_add_norm(const void *x, const void *residual, const float *weight, float eps, int64_t T,
+                 int H, void *sum, void *y, int block, void *codes, float *scales,
+                 hipStream_t stream);
+
+/*
+ * moe_add_norm_grad -- gradient of moe_add_norm at the sum that it stored: for the
+ * gradients d_y of y and d_sum of s,
+ *     R = (mean_h s^2 + eps)^(-1/2),  g = d_y * weight
+ *     d_x[t, h]   = d_sum + R g - s R^3 mean_h(g s)   (of x and of residual alike)
+ *     d_weight[h] = sum_t d_y s R
+ * fp32 sums in a fixed order; d_x is rounded once.  Codes of y count as y.
+ *
+ *   d_y        [T, H] bf16 bits.                                      (in)
+ *   d_sum      [T, H] bf16 bits, or NULL: 0.                          (in)
+ *   sum        [T, H] bf16 bits: moe_add_norm's sum (without a residual, its
+ *              x).                                                    (in)
+ *   weight, eps, T, H   as moe_add_norm.                              (in)
+ *   d_x        [T, H] bf16 bits; may be d_y, d_sum or sum.            (out)
+ *   d_weight   [H] fp32, or NULL.                                     (out)
+ *   accumulate 0, or 1: add to d_weight.
+ *   workspace  device scratch of *workspace_bytes bytes, 256-byte aligned, for
+ *              d_weight (not used without it).  Calls that may run at once need
+ *              one each.
+ *   workspace_bytes  host pointer; with workspace NULL the size needed is written
+ *              and nothing launched.
+ *
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN (16 bytes), MOE_ERR_WORKSPACE
+ * when d_weight's workspace is missing or too small.  T == 0: d_weight gets zeros
+ * (accumulate: keeps what is there).
+ */
+int moe_add_norm_grad(const void *d_y, const void *d_sum, const void *sum, const float *weight,
+                      float eps, int64_t T, int H, void *d_x, float *d_weight, int accumulate,
+                      void *workspace, size_t *workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
