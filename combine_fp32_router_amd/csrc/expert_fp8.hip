@@ -3,182 +3,311 @@
 //   forward   z = sum over blocks b of 128 of  xs[p, b] ws[n / 128, b] (xc wc)_b + bias,  y = act(z) + residual
 //   dx        g = the same of dy's codes and the transposed weights',  dx = act'(z_prev) g
 //
-// A block's codes are multiplied in one matrix instruction (16 x 16 x 128) and
-// its sums scaled into fp32 accumulators.  The results leave in bf16, in codes, or
-// both.
-#include "expert_rows.hpp"
-#include "fp8_codes.hpp"
+// The results leave in bf16, in codes with a scale for each 128, or both.
+#include "fp8_tile.hpp"
 #include "launch.hpp"
 
 namespace moe {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kOutside = static_cast<int>(0x80000000u);
-
 struct Fp8 {
-    const uint8_t *w, *x;   // [E][wide][C][steps' length], [max_rows][...]
+    const uint8_t *w, *q;   // weights and rows, of `segments` times R bytes
     const float *ws, *xs;
-    int xs_cols;            // scales of a row: 1, or one a step
+    int xs_cols;            // scales of a row: 1, or one a block
     const int32_t *offsets;
     int E, max_rows;
-    int R, segments;        // reduced length: `segments` of R
+    int R, segments;
     int C, act;             // output columns (of one half)
     const float *bias;
     const uint16_t *residual, *z;
-    uint16_t *out, *preact;
+    void *out;
+    uint16_t *preact;
     uint8_t *codes;
     float *scales;
+    int height;             // rows of a tile
 };
 
-// Largest size of this lane's values of a row's block and of the three lanes' that
-// hold the rest of it.
-__device__ __forceinline__ uint32_t block_top(const f32x4 (&v)[8], int inside)
+// Largest size of a lane's values of a row and of the three lanes' that hold the
+// rest of them.
+template <int BLOCKS>
+__device__ __forceinline__ uint32_t row_top(const f32x4 (&v)[BLOCKS])
 {
     uint32_t top = 0;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c * 16 < inside)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                top = umax(top, size_bits(v[c][j]));
+    for (int i = 0; i < 4 * BLOCKS; ++i)
+        top = umax(top, size_bits(v[i / 4][i % 4]));
     top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
     return umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
 }
 
-__device__ __forceinline__ void store4(uint16_t *p, f32x4 f)
+// Codes of 16 rows of a wave's columns, through LDS into whole pieces.
+template <int BLOCKS>
+__device__ __forceinline__ void store_codes(MOE_LDS char *__restrict__ lds, const f32x4 (&v)[BLOCKS], float scale,
+                                            const Pieces<BLOCKS> &to, int row)
 {
-    *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w)};
-}
-__device__ __forceinline__ f32x4 load4(const uint16_t *p)
-{
-    const u32x2 s = *reinterpret_cast<const u32x2 *>(p);
-    return f32x4{bf16_lo(s.x), bf16_hi(s.x), bf16_lo(s.y), bf16_hi(s.y)};
-}
-
-// Stores 128 columns of one row a lane (block `half` of `halves`): v[c] has columns
-// c0 + 16 c + 4 (lane / 16) .. + 3.
-__device__ __forceinline__ void store_block(const Fp8 &a, const f32x4 (&v)[8], int64_t row, bool live, int c0,
-                                            int halves, int half)
-{
-    const int inside = a.C - c0, at = lane_id() / 16 * 4;
-    const int64_t line = (row * halves + half) * a.C + c0 + at;
-    const uint32_t top = block_top(v, inside);
-    if (!live)
-        return;
-    const float scale = scale_of(top);
+    const int lane = lane_id(), r = lane % 16;
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (c * 16 < inside) {
-            if (a.out)
-                store4(a.out + line + c * 16, v[c]);
-            if (a.codes)
-                *reinterpret_cast<uint32_t *>(a.codes + line + c * 16) = codes4(v[c][0], v[c][1], v[c][2], v[c][3], scale);
-        }
-    if (a.codes && at == 0)
-        a.scales[(row * halves + half) * code_blocks(a.C) + c0 / kCodeBlock] = scale;
+    for (int c = 0; c < BLOCKS; ++c)
+        *reinterpret_cast<MOE_LDS uint32_t *>(lds + r * 256 + (c ^ r) * 16 + lane / 16 * 4) =
+            codes4(v[c][0], v[c][1], v[c][2], v[c][3], scale);
+#pragma unroll
+    for (int j = 0; j < BLOCKS / 4; ++j)
+        to.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<BLOCKS>(j)));
 }
 
-// One wave for 16 rows of a tile by 128 columns; GATED: of both halves.
-template <bool DX, bool GATED>
-__global__ __launch_bounds__(256) void expert_fp8_kernel(Fp8 a)
+// Where a tile's results go: its rows first .. first + n - 1, this wave's columns
+// from c on, `inside` of them (or more) the array's.
+struct Where {
+    int e, first, n, c, inside;
+};
+
+// The scale of the block that this wave's columns begin, of the 16 rows from `row`.
+__device__ __forceinline__ void store_scale(const Fp8 &a, const Where &at, int row, int halves, int half, float scale)
 {
-    constexpr int wide = GATED ? 2 : 1;
-    const int lane = lane_id(), w = static_cast<int>(uniform(threadIdx.x / kWave));
-    const int col_tiles = code_blocks(a.C);
-    const RowTile t = find_row_tile(a.offsets, a.E, a.max_rows, 64, blockIdx.x / col_tiles);
-    const int n = t.n - 16 * w;
-    if (n <= 0)
-        return;
-    const int cb = blockIdx.x % col_tiles, c0 = cb * kCodeBlock, inside = a.C - c0;
-    const int nb = code_blocks(a.R), steps = nb * a.segments, pitch = a.R * a.segments;
-    const int64_t first = t.first + 16 * w;
-    const __amdgpu_buffer_rsrc_t xr = row_rsrc(const_cast<uint8_t *>(a.x) + first * pitch, min(n, 16) * pitch);
-    const float *xs = a.xs + (first + min(lane % 16, n - 1)) * a.xs_cols;
-    f32x4 acc[wide][8] = {};
-    for (int k = 0; k < steps; ++k) {
-        const int r0 = k / nb * a.R + k % nb * kCodeBlock, end = (k / nb + 1) * a.R, r = r0 + lane / 16 * 32;
-        auto fragment = [&](const __amdgpu_buffer_rsrc_t &rsrc, int row) {
-            const u32x4 lo = load_cached(rsrc, r < end ? row * pitch + r : kOutside);
-            const u32x4 hi = load_cached(rsrc, r + 16 < end ? row * pitch + r + 16 : kOutside);
-            return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-        };
-        const i32x8 q = fragment(xr, lane % 16);
-        const float s = xs[a.xs_cols == 1 ? 0 : k];
+    const int r = row + lane_id() % 16;
+    if (lane_id() < 16 && r < at.n && at.inside > 0)
+        a.scales[((static_cast<int64_t>(at.first) + r) * halves + half) * code_blocks(a.C) + at.c / kCodeBlock] = scale;
+}
+
+// Loaded pieces of 16 rows, eight a row, into LDS: as the first or the second eight.
+__device__ __forceinline__ void put_pieces(MOE_LDS char *__restrict__ lds, const u32x4 (&in)[2], int second)
+{
 #pragma unroll
-        for (int g = 0; g < wide; ++g) {
-            const int64_t block = (static_cast<int64_t>(t.e) * wide + g) * col_tiles + cb;
-            const __amdgpu_buffer_rsrc_t wr = row_rsrc(
-                const_cast<uint8_t *>(a.w) + ((static_cast<int64_t>(t.e) * wide + g) * a.C + c0) * pitch, min(inside, 128) * pitch);
-            const float scale = s * a.ws[block * steps + k];
+    for (int j = 0; j < 2; ++j) {
+        const int row = 8 * j + lane_id() / 8;
+        *reinterpret_cast<MOE_LDS u32x4 *>(lds + row * 256 + ((lane_id() % 8 + 8 * second) ^ row) * 16) = in[j];
+    }
+}
+__device__ __forceinline__ f32x4 get_block(const MOE_LDS char *__restrict__ lds, int c)
+{
+    return widen4(*reinterpret_cast<const MOE_LDS u32x2 *>(lds + Place::half(c)));
+}
+
+// Forward: bias, pre-activations, activation, residual.  The accumulators are
+// changed in place, a block of 64 rows after the other: beside 128 of them there is
+// no room for copies.  GATED: blocks 0, 1, 4, 5 are the gate's, 2, 3, 6, 7 the up
+// half's.
+template <bool GATED>
+__device__ __forceinline__ void finish_forward(const Fp8 &a, CodeTile<GATED> &t, const Where &at, MOE_LDS char *lds)
+{
+    constexpr int kBlocks = GATED ? 4 : 8, P = 2 * kBlocks, wide = GATED ? 2 : 1;
+    MOE_LDS char *place = t.out_place(lds);
+    const Pieces<P> out(a.out, at.first, at.n, a.C, 2, at.c, at.inside), res(a.residual, at.first, at.n, a.C, 2, at.c, at.inside);
+    const Pieces<P> pre(a.preact, at.first, at.n, wide * a.C, 2, at.c, at.inside);
+    const Pieces<P> pre_up(a.preact, at.first, at.n, wide * a.C, 2, GATED ? at.c + a.C : at.c, at.inside);
+    const Pieces<kBlocks> codes(a.codes, at.first, at.n, a.C, 1, at.c, at.inside);
+    const float *bias = a.bias + static_cast<int64_t>(at.e) * wide * a.C + at.c + lane_id() / 16 * 4;
+    u32x4 ahead[P / 4];  // the residual's next 16 rows
+    auto load = [&](int row) {
+        if (a.residual)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const i32x8 p = fragment(wr, c * 16 + lane % 16);
-                const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, f32x4{}, 0, 0, 0, 0, 0, 0);
+            for (int j = 0; j < P / 4; ++j)
+                ahead[j] = res.load(row, j);
+    };
+    load(t.row0(0));
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[g][c][j] = fmaf(d[j], scale, acc[g][c][j]);
+    for (int b = 0; b < 4; ++b) {
+        if (b * 64 >= at.n)
+            break;
+        const int row = t.row0(b);
+        f32x4 g[kBlocks], u[GATED ? kBlocks : 1];
+#pragma unroll
+        for (int i = 0; i < kBlocks; ++i) {
+            g[i] = t.acc[GATED ? i / 2 * 4 + i % 2 : i][b];
+            if (GATED)
+                u[i] = t.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
+            if (a.bias && i * 16 < at.inside) {
+                g[i] += *reinterpret_cast<const f32x4 *>(bias + i * 16);
+                if (GATED)
+                    u[i] += *reinterpret_cast<const f32x4 *>(bias + a.C + i * 16);
             }
+        }
+        if (a.preact) {
+            store_blocks<P>(place, g, pre, row);
+            if constexpr (GATED)
+                store_blocks<P>(place, u, pre_up, row);
+        }
+        if (GATED) {
+#pragma unroll
+            for (int i = 0; i < 4 * kBlocks; ++i)
+                g[i / 4][i % 4] *= sigmoid(g[i / 4][i % 4]) * u[GATED ? i / 4 : 0][i % 4];
+        } else {
+            apply_act(g, a.act);
+        }
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < P / 4; ++j)
+                *reinterpret_cast<MOE_LDS u32x4 *>(place + Place::piece<P>(j)) = ahead[j];
+            load(t.row0(min(b + 1, 3)));  // in front of this block's stores: waiting for it is then not waiting for them
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
+                g[i] += get_block(place, i);
+        }
+        if (a.out)
+            store_blocks<P>(place, g, out, row);
+        if (a.codes) {
+            uint32_t top = row_top(g);
+            if (GATED)
+                top = t.both_halves(lds, b, top);
+            const float scale = scale_of(top);
+            store_codes(place, g, scale, codes, row);
+            if (!GATED || t.col0() == 0)
+                store_scale(a, at, row, 1, 0, scale);
         }
     }
-    const int64_t row = first + lane % 16;
-    const bool live = lane % 16 < n;
-    const int at = lane / 16 * 4;
-    if constexpr (DX) {
-        const bool gated = a.act == MOE_ACT_SWIGLU;
-        f32x4 up[8] = {};
+}
+
+// dx: through the activation that made the product's input, 64 columns at a time.
+__device__ __forceinline__ void finish_dx(const Fp8 &a, CodeTile<false> &t, const Where &at, MOE_LDS char *lds)
+{
+    MOE_LDS char *place = t.out_place(lds);
+    const bool gated = a.act == MOE_ACT_SWIGLU;
+    const int cols = gated ? 2 * a.C : a.C, up = gated ? at.c + a.C : at.c;
+    const Pieces<16> out(a.out, at.first, at.n, cols, 2, at.c, at.inside), out_up(a.out, at.first, at.n, cols, 2, up, at.inside);
+    const Pieces<8> codes(a.codes, at.first, at.n, cols, 1, at.c, at.inside), codes_up(a.codes, at.first, at.n, cols, 1, up, at.inside);
+    const Pieces<8> pre(a.z, at.first, at.n, cols, 2, at.c, at.inside), pre_r(a.z, at.first, at.n, cols, 2, at.c + 64, at.inside - 64);
+    const Pieces<8> pre_up(a.z, at.first, at.n, cols, 2, up, at.inside), pre_up_r(a.z, at.first, at.n, cols, 2, up + 64, at.inside - 64);
+    u32x4 ahead[2], ahead_up[2];
+    auto load = [&](int row, bool right) {
+        if (a.act != MOE_ACT_NONE)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            if (!live || c * 16 >= inside)
-                continue;
-            const int col = c0 + c * 16 + at;
-            if (gated) {
-                const f32x4 g = load4(a.z + row * 2 * a.C + col), u = load4(a.z + (row * 2 + 1) * a.C + col);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = acc[0][c][j], s = sigmoid(g[j]);
-                    acc[0][c][j] = x * u[j] * (s * (1.0f + g[j] * (1.0f - s)));
-                    up[c][j] = x * (g[j] * s);
-                }
-            } else if (a.act != MOE_ACT_NONE) {
-                const f32x4 z[1] = {load4(a.z + row * a.C + col)};
-                f32x4 v[1] = {acc[0][c]};
-                apply_slope(v, z, a.act);
-                acc[0][c] = v[0];
-            }
-        }
-        store_block(a, acc[0], row, live, c0, gated ? 2 : 1, 0);
+            for (int j = 0; j < 2; ++j)
+                ahead[j] = right ? pre_r.load(row, j) : pre.load(row, j);
         if (gated)
-            store_block(a, up, row, live, c0, 2, 1);
-    } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            if (!live || c * 16 >= inside)
-                continue;
-            const int col = c0 + c * 16 + at;
+            for (int j = 0; j < 2; ++j)
+                ahead_up[j] = right ? pre_up_r.load(row, j) : pre_up.load(row, j);
+    };
+    load(t.row0(0), false);
 #pragma unroll
-            for (int g = 0; g < wide; ++g) {
-                if (a.bias)
-                    acc[g][c] += *reinterpret_cast<const f32x4 *>(a.bias + (static_cast<int64_t>(t.e) * wide + g) * a.C + col);
-                if (a.preact)
-                    store4(a.preact + (row * wide + g) * a.C + col, acc[g][c]);
+    for (int b = 0; b < 4; ++b) {
+        if (b * 64 >= at.n)
+            break;
+        const int row = t.row0(b);
+        f32x4 v[8], u[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            v[c] = u[c] = t.acc[c][b];
+        if (a.act != MOE_ACT_NONE)
+#pragma unroll
+            for (int right = 0; right < 2; ++right) {
+                put_pieces(place, ahead, 0);
+                if (gated)
+                    put_pieces(place, ahead_up, 1);
+                load(right ? t.row0(min(b + 1, 3)) : row, !right);
+                if (gated) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const f32x4 z = get_block(place, c), zu = get_block(place, 4 + c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float g = z[j], x = v[right * 4 + c][j], s = sigmoid(g);
+                            v[right * 4 + c][j] = x * zu[j] * (s * (1.0f + g * (1.0f - s)));
+                            u[right * 4 + c][j] = x * (g * s);
+                        }
+                    }
+                } else {
+                    f32x4 z[4], w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        z[c] = get_block(place, c);
+                        w[c] = v[right * 4 + c];
+                    }
+                    apply_slope(w, z, a.act);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        v[right * 4 + c] = w[c];
+                }
             }
-            f32x4 y[1] = {acc[0][c]};
-            if (GATED) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    y[0][j] = y[0][j] * sigmoid(y[0][j]) * acc[wide - 1][c][j];
-            } else {
-                apply_act(y, a.act);
-            }
-            if (a.residual)
-                y[0] += load4(a.residual + row * a.C + col);
-            acc[0][c] = y[0];
+        if (a.out) {
+            store_blocks<16>(place, v, out, row);
+            if (gated)
+                store_blocks<16>(place, u, out_up, row);
         }
-        store_block(a, acc[0], row, live, c0, 1, 0);
+        if (a.codes) {
+            const float scale = scale_of(row_top(v));
+            store_codes(place, v, scale, codes, row);
+            store_scale(a, at, row, gated ? 2 : 1, 0, scale);
+            if (gated) {
+                const float scale_up = scale_of(row_top(u));
+                store_codes(place, u, scale_up, codes_up, row);
+                store_scale(a, at, row, 2, 1, scale_up);
+            }
+        }
     }
+}
+
+template <bool DX, bool GATED>
+__global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
+{
+    typedef CodeTile<GATED> T;
+    constexpr int kCols = GATED ? 128 : 256;  // output columns of a tile
+    typedef TileList<DX ? kDx : kForward, kCols, Fp8> List;
+    __shared__ __align__(1024) char shared[T::kLdsBytes + List::kBytes];
+    MOE_LDS char *lds = (MOE_LDS char *)shared;
+    List list;
+    list.build(a, reinterpret_cast<int32_t *>(shared + T::kLdsBytes));
+
+    T t;
+    auto start = [&](const Work &k) {  // the loads of a tile's first stages
+        const int nbc = code_blocks(a.C), pitch = a.R * a.segments;
+        const int64_t half = static_cast<int64_t>(k.e) * (GATED ? 2 : 1);
+        const uint8_t *w = a.w + (half * a.C + k.c0) * pitch;
+        t.init(w, w + static_cast<int64_t>(a.C) * pitch, min(kCols, a.C - k.c0), a.q + static_cast<int64_t>(k.first) * pitch,
+               k.n, a.xs + static_cast<int64_t>(k.first) * a.xs_cols, a.xs_cols, a.R, a.segments);
+        // (a wave past the last column takes the last block's)
+        const int block = min(k.c0 / kCodeBlock + (GATED ? 0 : t.wave() % 2), nbc - 1);
+#pragma unroll
+        for (int g = 0; g < (GATED ? 2 : 1); ++g)
+            t.ws[g] = (const MOE_SCALAR float *)(a.ws + ((half + g) * nbc + block) * t.steps);
+        t.start_rows(lds);
+    };
+
+    int i = 0;
+    Work k;
+    if (!list.next(a, i, k))
+        return;
+    start(k);
+    for (;;) {
+        t.run_rows(lds);
+        Work after = k;
+        ++i;
+        const bool more = list.next(a, i, after);
+        if (more)
+            start(after);  // runs beside the rest of this tile
+        const int c = k.c0 + t.col0() / (GATED ? 2 : 1);
+        const Where at{k.e, k.first, k.n, c, a.C - c};
+        if constexpr (DX)
+            finish_dx(a, t, at, lds);
+        else
+            finish_forward<GATED>(a, t, at, lds);
+        if (!more)
+            return;
+        k = after;
+    }
+}
+
+// Rows of a tile of 256 columns (128 of a gated product): the smallest of which
+// the call has no more than CUs.
+int tile_height(int E, int64_t max_rows, int col_tiles)
+{
+    for (int h = 64; h < 256; h *= 2)
+        if (max_row_tiles(max_rows, E, h) * col_tiles <= kCus)
+            return h;
+    return 256;
+}
+
+// As grid_for of the bf16 products.
+dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < kCus ? (n + 14) / 8 * 8 : kCus)); }
+
+template <bool DX, bool GATED>
+hipError_t launch(Fp8 &a, int64_t max_rows, hipStream_t stream)
+{
+    const int col_tiles = (a.C + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+    a.max_rows = static_cast<int>(max_rows);
+    a.height = tile_height(a.E, max_rows, col_tiles);
+    expert_fp8_kernel<DX, GATED><<<grid_for(max_row_tiles(max_rows, a.E, a.height) * col_tiles), 512, 0, stream>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -188,17 +317,11 @@ hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const 
                              int K, int N, void *out, void *codes, float *scales, void *preact, hipStream_t stream)
 {
     Fp8 a{};
-    a.x = static_cast<const uint8_t *>(x), a.xs = xs, a.xs_cols = xs_cols, a.offsets = offsets;
+    a.q = static_cast<const uint8_t *>(x), a.xs = xs, a.xs_cols = xs_cols, a.offsets = offsets;
     a.w = static_cast<const uint8_t *>(w), a.ws = ws, a.bias = bias, a.act = act;
-    a.residual = static_cast<const uint16_t *>(residual), a.E = E, a.max_rows = static_cast<int>(max_rows);
-    a.R = K, a.segments = 1, a.C = N, a.out = static_cast<uint16_t *>(out), a.codes = static_cast<uint8_t *>(codes);
-    a.scales = scales, a.preact = static_cast<uint16_t *>(preact);
-    const dim3 grid(static_cast<unsigned>(max_row_tiles(max_rows, E, 64) * code_blocks(N)));
-    if (act == MOE_ACT_SWIGLU)
-        expert_fp8_kernel<false, true><<<grid, 256, 0, stream>>>(a);
-    else
-        expert_fp8_kernel<false, false><<<grid, 256, 0, stream>>>(a);
-    return hipGetLastError();
+    a.residual = static_cast<const uint16_t *>(residual), a.E = E, a.R = K, a.segments = 1, a.C = N;
+    a.out = out, a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.preact = static_cast<uint16_t *>(preact);
+    return act == MOE_ACT_SWIGLU ? launch<false, true>(a, max_rows, stream) : launch<false, false>(a, max_rows, stream);
 }
 
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
@@ -206,13 +329,11 @@ hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t 
                                 int N, void *dx, void *codes, float *scales, hipStream_t stream)
 {
     Fp8 a{};
-    a.x = static_cast<const uint8_t *>(dy), a.xs = dys, a.xs_cols = halves * code_blocks(N), a.offsets = offsets;
+    a.q = static_cast<const uint8_t *>(dy), a.xs = dys, a.xs_cols = halves * code_blocks(N), a.offsets = offsets;
     a.w = static_cast<const uint8_t *>(wt), a.ws = wts, a.act = act, a.z = static_cast<const uint16_t *>(z);
-    a.E = E, a.max_rows = static_cast<int>(max_rows), a.R = N, a.segments = halves, a.C = K;
-    a.out = static_cast<uint16_t *>(dx), a.codes = static_cast<uint8_t *>(codes), a.scales = scales;
-    const dim3 grid(static_cast<unsigned>(max_row_tiles(max_rows, E, 64) * code_blocks(K)));
-    expert_fp8_kernel<true, false><<<grid, 256, 0, stream>>>(a);
-    return hipGetLastError();
+    a.E = E, a.R = N, a.segments = halves, a.C = K;
+    a.out = dx, a.codes = static_cast<uint8_t *>(codes), a.scales = scales;
+    return launch<true, false>(a, max_rows, stream);
 }
 
 }  // namespace moe

@@ -25,18 +25,14 @@
 // and the end of r need no other care.
 #pragma once
 
-#include "expert_rows.hpp"
+#include "expert_finish.hpp"
+#include "expert_list.hpp"
 
 namespace moe {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-#define MOE_LDS __attribute__((address_space(3)))
-
-constexpr int kOutside = static_cast<int>(0x80000000u);  // an offset past every descriptor
-constexpr int kStep = 64;       // r of a stage
 constexpr int kTileWaves = 4;
 
 // Image of W indices of an operand, kStep r a stage, staged by four waves.
