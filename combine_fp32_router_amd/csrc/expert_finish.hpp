@@ -39,21 +39,19 @@ __device__ __forceinline__ u32x2 round4(f32x4 f)
 struct Place {
     MOE_LDS char *base;
     // MFMA layout: four columns of block c, as bf16 or fp32 (c < 4)
-    static __device__ __forceinline__ int half(int c)
+    static __device__ __forceinline__ int half(int c, int lane = lane_id())
     {
-        const int lane = lane_id();
         return lane % 16 * 256 + ((c * 2 + lane / 32) ^ (lane % 16)) * 16 + lane / 16 % 2 * 8;
     }
-    static __device__ __forceinline__ int whole(int c)
+    static __device__ __forceinline__ int whole(int c, int lane = lane_id())
     {
-        const int lane = lane_id();
         return lane % 16 * 256 + ((c * 4 + lane / 16) ^ (lane % 16)) * 16;
     }
     // row layout: piece lane%P of row (64 / P) j + lane/P
     template <int P>
-    static __device__ __forceinline__ int piece(int j)
+    static __device__ __forceinline__ int piece(int j, int lane = lane_id())
     {
-        const int lane = lane_id(), row = 64 / P * j + lane / P;
+        const int row = 64 / P * j + lane / P;
         return row * 256 + ((lane % P) ^ row) * 16;
     }
 };
@@ -64,21 +62,23 @@ template <int P>
 struct Pieces {
     __amdgpu_buffer_rsrc_t rsrc;
     int pitch, col, n;  // bytes of a row, this lane's offset in a row (kOutside past the columns), rows
+    int lane;
 
     // Rows first .. first + n - 1 of `cols` columns of `size` bytes; the wave's
     // pieces start at column c, `inside` of its columns are the array's.
-    __device__ __forceinline__ Pieces(const void *p, int64_t first, int n_, int cols, int size, int c, int inside)
+    __device__ __forceinline__ Pieces(const void *p, int64_t first, int n_, int cols, int size, int c, int inside,
+                                     int lane_ = lane_id())
         : rsrc(row_rsrc(const_cast<char *>(static_cast<const char *>(p)) + first * cols * size, n_ * cols * size)),
-          pitch(cols * size), n(n_)
+          pitch(cols * size), n(n_), lane(lane_)
     {
-        const int in_wave = lane_id() % P * (16 / size);
+        const int in_wave = lane % P * (16 / size);
         col = in_wave < inside ? (c + in_wave) * size : kOutside;
     }
     static constexpr int kCount = P / 4;  // loads or stores for 16 rows
     // offset of the j-th of them, for the 16 rows from `row`
     __device__ __forceinline__ int at(int row, int j) const
     {
-        const int r = row + 64 / P * j + lane_id() / P;
+        const int r = row + 64 / P * j + lane / P;
         return r < n && col != kOutside ? r * pitch + col : kOutside;
     }
     __device__ __forceinline__ u32x4 load(int row, int j) const
@@ -109,10 +109,10 @@ __device__ __forceinline__ void store_blocks(MOE_LDS char *__restrict__ lds, con
 {
 #pragma unroll
     for (int c = 0; c < BLOCKS; ++c)
-        *reinterpret_cast<MOE_LDS u32x2 *>(lds + Place::half(c)) = round4(v[c]);
+        *reinterpret_cast<MOE_LDS u32x2 *>(lds + Place::half(c, out.lane)) = round4(v[c]);
 #pragma unroll
     for (int j = 0; j < P / 4; ++j)
-        out.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<P>(j)));
+        out.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<P>(j, out.lane)));
 }
 
 }  // namespace

@@ -4,6 +4,8 @@
 //   dx        g = the same of dy's codes and the transposed weights',  dx = act'(z_prev) g
 //
 // The results leave in bf16, in codes with a scale for each 128, or both.
+#include <type_traits>
+
 #include "fp8_tile.hpp"
 #include "launch.hpp"
 
@@ -45,58 +47,60 @@ template <int BLOCKS>
 __device__ __forceinline__ void store_codes(MOE_LDS char *__restrict__ lds, const f32x4 (&v)[BLOCKS], float scale,
                                             const Pieces<BLOCKS> &to, int row)
 {
-    const int lane = lane_id(), r = lane % 16;
+    const int lane = to.lane, r = lane % 16;
 #pragma unroll
     for (int c = 0; c < BLOCKS; ++c)
         *reinterpret_cast<MOE_LDS uint32_t *>(lds + r * 256 + (c ^ r) * 16 + lane / 16 * 4) =
             codes4(v[c][0], v[c][1], v[c][2], v[c][3], scale);
 #pragma unroll
     for (int j = 0; j < BLOCKS / 4; ++j)
-        to.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<BLOCKS>(j)));
+        to.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<BLOCKS>(j, lane)));
 }
 
 // Where a tile's results go: its rows first .. first + n - 1, this wave's columns
 // from c on, `inside` of them (or more) the array's.
 struct Where {
-    int e, first, n, c, inside;
+    int e, first, n, c, inside, lane;
 };
 
 // The scale of the block that this wave's columns begin, of the 16 rows from `row`.
 __device__ __forceinline__ void store_scale(const Fp8 &a, const Where &at, int row, int halves, int half, float scale)
 {
-    const int r = row + lane_id() % 16;
-    if (lane_id() < 16 && r < at.n && at.inside > 0)
+    const int r = row + at.lane % 16;
+    if (at.lane < 16 && r < at.n && at.inside > 0)
         a.scales[((static_cast<int64_t>(at.first) + r) * halves + half) * code_blocks(a.C) + at.c / kCodeBlock] = scale;
 }
 
 // Loaded pieces of 16 rows, eight a row, into LDS: as the first or the second eight.
-__device__ __forceinline__ void put_pieces(MOE_LDS char *__restrict__ lds, const u32x4 (&in)[2], int second)
+__device__ __forceinline__ void put_pieces(MOE_LDS char *__restrict__ lds, const u32x4 (&in)[2], int second, int lane)
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const int row = 8 * j + lane_id() / 8;
-        *reinterpret_cast<MOE_LDS u32x4 *>(lds + row * 256 + ((lane_id() % 8 + 8 * second) ^ row) * 16) = in[j];
+        const int row = 8 * j + lane / 8;
+        *reinterpret_cast<MOE_LDS u32x4 *>(lds + row * 256 + ((lane % 8 + 8 * second) ^ row) * 16) = in[j];
     }
 }
-__device__ __forceinline__ f32x4 get_block(const MOE_LDS char *__restrict__ lds, int c)
+__device__ __forceinline__ f32x4 get_block(const MOE_LDS char *__restrict__ lds, int c, int lane)
 {
-    return widen4(*reinterpret_cast<const MOE_LDS u32x2 *>(lds + Place::half(c)));
+    return widen4(*reinterpret_cast<const MOE_LDS u32x2 *>(lds + Place::half(c, lane)));
 }
 
 // Forward: bias, pre-activations, activation, residual.  The accumulators are
 // changed in place, a block of 64 rows after the other: beside 128 of them there is
 // no room for copies.  GATED: blocks 0, 1, 4, 5 are the gate's, 2, 3, 6, 7 the up
 // half's.
-template <bool GATED>
-__device__ __forceinline__ void finish_forward(const Fp8 &a, CodeTile<GATED> &t, const Where &at, MOE_LDS char *lds)
+template <bool GATED, int NB>
+__device__ __forceinline__ void finish_forward(const Fp8 &a, const CodeTile<GATED> &t,
+                                               const typename CodeTile<GATED>::template Regs<NB> &f, const Where &at,
+                                               MOE_LDS char *lds)
 {
     constexpr int kBlocks = GATED ? 4 : 8, P = 2 * kBlocks, wide = GATED ? 2 : 1;
     MOE_LDS char *place = t.out_place(lds);
-    const Pieces<P> out(a.out, at.first, at.n, a.C, 2, at.c, at.inside), res(a.residual, at.first, at.n, a.C, 2, at.c, at.inside);
-    const Pieces<P> pre(a.preact, at.first, at.n, wide * a.C, 2, at.c, at.inside);
-    const Pieces<P> pre_up(a.preact, at.first, at.n, wide * a.C, 2, GATED ? at.c + a.C : at.c, at.inside);
-    const Pieces<kBlocks> codes(a.codes, at.first, at.n, a.C, 1, at.c, at.inside);
-    const float *bias = a.bias + static_cast<int64_t>(at.e) * wide * a.C + at.c + lane_id() / 16 * 4;
+    const Pieces<P> out(a.out, at.first, at.n, a.C, 2, at.c, at.inside, at.lane), res(a.residual, at.first, at.n, a.C, 2, at.c, at.inside, at.lane);
+    const Pieces<P> pre(a.preact, at.first, at.n, wide * a.C, 2, at.c, at.inside, at.lane);
+    const Pieces<P> pre_up(a.preact, at.first, at.n, wide * a.C, 2, GATED ? at.c + a.C : at.c, at.inside, at.lane);
+    const Pieces<kBlocks> codes(a.codes, at.first, at.n, a.C, 1, at.c, at.inside, at.lane);
+    const float *bias = a.bias + static_cast<int64_t>(at.e) * wide * a.C + at.c + at.lane / 16 * 4;
     u32x4 ahead[P / 4];  // the residual's next 16 rows
     auto load = [&](int row) {
         if (a.residual)
@@ -106,16 +110,16 @@ __device__ __forceinline__ void finish_forward(const Fp8 &a, CodeTile<GATED> &t,
     };
     load(t.row0(0));
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < NB; ++b) {
         if (b * 64 >= at.n)
             break;
         const int row = t.row0(b);
         f32x4 g[kBlocks], u[GATED ? kBlocks : 1];
 #pragma unroll
         for (int i = 0; i < kBlocks; ++i) {
-            g[i] = t.acc[GATED ? i / 2 * 4 + i % 2 : i][b];
+            g[i] = f.acc[GATED ? i / 2 * 4 + i % 2 : i][b];
             if (GATED)
-                u[i] = t.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
+                u[i] = f.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
             if (a.bias && i * 16 < at.inside) {
                 g[i] += *reinterpret_cast<const f32x4 *>(bias + i * 16);
                 if (GATED)
@@ -137,18 +141,18 @@ __device__ __forceinline__ void finish_forward(const Fp8 &a, CodeTile<GATED> &t,
         if (a.residual) {
 #pragma unroll
             for (int j = 0; j < P / 4; ++j)
-                *reinterpret_cast<MOE_LDS u32x4 *>(place + Place::piece<P>(j)) = ahead[j];
-            load(t.row0(min(b + 1, 3)));  // in front of this block's stores: waiting for it is then not waiting for them
+                *reinterpret_cast<MOE_LDS u32x4 *>(place + Place::piece<P>(j, at.lane)) = ahead[j];
+            load(t.row0(min(b + 1, NB - 1)));  // in front of this block's stores: waiting for it is then not waiting for them
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i)
-                g[i] += get_block(place, i);
+                g[i] += get_block(place, i, at.lane);
         }
         if (a.out)
             store_blocks<P>(place, g, out, row);
         if (a.codes) {
             uint32_t top = row_top(g);
             if (GATED)
-                top = t.both_halves(lds, b, top);
+                top = t.both_halves(lds, b, top, at.lane);
             const float scale = scale_of(top);
             store_codes(place, g, scale, codes, row);
             if (!GATED || t.col0() == 0)
@@ -158,15 +162,17 @@ __device__ __forceinline__ void finish_forward(const Fp8 &a, CodeTile<GATED> &t,
 }
 
 // dx: through the activation that made the product's input, 64 columns at a time.
-__device__ __forceinline__ void finish_dx(const Fp8 &a, CodeTile<false> &t, const Where &at, MOE_LDS char *lds)
+template <int NB>
+__device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t, const CodeTile<false>::Regs<NB> &f,
+                                          const Where &at, MOE_LDS char *lds)
 {
     MOE_LDS char *place = t.out_place(lds);
     const bool gated = a.act == MOE_ACT_SWIGLU;
     const int cols = gated ? 2 * a.C : a.C, up = gated ? at.c + a.C : at.c;
-    const Pieces<16> out(a.out, at.first, at.n, cols, 2, at.c, at.inside), out_up(a.out, at.first, at.n, cols, 2, up, at.inside);
-    const Pieces<8> codes(a.codes, at.first, at.n, cols, 1, at.c, at.inside), codes_up(a.codes, at.first, at.n, cols, 1, up, at.inside);
-    const Pieces<8> pre(a.z, at.first, at.n, cols, 2, at.c, at.inside), pre_r(a.z, at.first, at.n, cols, 2, at.c + 64, at.inside - 64);
-    const Pieces<8> pre_up(a.z, at.first, at.n, cols, 2, up, at.inside), pre_up_r(a.z, at.first, at.n, cols, 2, up + 64, at.inside - 64);
+    const Pieces<16> out(a.out, at.first, at.n, cols, 2, at.c, at.inside, at.lane), out_up(a.out, at.first, at.n, cols, 2, up, at.inside, at.lane);
+    const Pieces<8> codes(a.codes, at.first, at.n, cols, 1, at.c, at.inside, at.lane), codes_up(a.codes, at.first, at.n, cols, 1, up, at.inside, at.lane);
+    const Pieces<8> pre(a.z, at.first, at.n, cols, 2, at.c, at.inside, at.lane), pre_r(a.z, at.first, at.n, cols, 2, at.c + 64, at.inside - 64, at.lane);
+    const Pieces<8> pre_up(a.z, at.first, at.n, cols, 2, up, at.inside, at.lane), pre_up_r(a.z, at.first, at.n, cols, 2, up + 64, at.inside - 64, at.lane);
     u32x4 ahead[2], ahead_up[2];
     auto load = [&](int row, bool right) {
         if (a.act != MOE_ACT_NONE)
@@ -180,25 +186,25 @@ __device__ __forceinline__ void finish_dx(const Fp8 &a, CodeTile<false> &t, cons
     };
     load(t.row0(0), false);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < NB; ++b) {
         if (b * 64 >= at.n)
             break;
         const int row = t.row0(b);
         f32x4 v[8], u[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-            v[c] = u[c] = t.acc[c][b];
+            v[c] = u[c] = f.acc[c][b];
         if (a.act != MOE_ACT_NONE)
 #pragma unroll
             for (int right = 0; right < 2; ++right) {
-                put_pieces(place, ahead, 0);
+                put_pieces(place, ahead, 0, at.lane);
                 if (gated)
-                    put_pieces(place, ahead_up, 1);
-                load(right ? t.row0(min(b + 1, 3)) : row, !right);
+                    put_pieces(place, ahead_up, 1, at.lane);
+                load(right ? t.row0(min(b + 1, NB - 1)) : row, !right);
                 if (gated) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const f32x4 z = get_block(place, c), zu = get_block(place, 4 + c);
+                        const f32x4 z = get_block(place, c, at.lane), zu = get_block(place, 4 + c, at.lane);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const float g = z[j], x = v[right * 4 + c][j], s = sigmoid(g);
@@ -210,7 +216,7 @@ __device__ __forceinline__ void finish_dx(const Fp8 &a, CodeTile<false> &t, cons
                     f32x4 z[4], w[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        z[c] = get_block(place, c);
+                        z[c] = get_block(place, c, at.lane);
                         w[c] = v[right * 4 + c];
                     }
                     apply_slope(w, z, a.act);
@@ -249,6 +255,8 @@ __global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
     list.build(a, reinterpret_cast<int32_t *>(shared + T::kLdsBytes));
 
     T t;
+    // blocks of 64 rows that a tile is run for
+    auto blocks_of = [](const Work &k) { return k.n <= 64 ? 1 : k.n <= 128 ? 2 : 4; };
     auto start = [&](const Work &k) {  // the loads of a tile's first stages
         const int nbc = code_blocks(a.C), pitch = a.R * a.segments;
         const int64_t half = static_cast<int64_t>(k.e) * (GATED ? 2 : 1);
@@ -260,30 +268,38 @@ __global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
 #pragma unroll
         for (int g = 0; g < (GATED ? 2 : 1); ++g)
             t.ws[g] = (const MOE_SCALAR float *)(a.ws + ((half + g) * nbc + block) * t.steps);
-        t.start_rows(lds);
+        t.start(lds, blocks_of(k));
     };
-
     int i = 0;
     Work k;
-    if (!list.next(a, i, k))
-        return;
-    start(k);
-    for (;;) {
-        t.run_rows(lds);
-        Work after = k;
-        ++i;
-        const bool more = list.next(a, i, after);
-        if (more)
-            start(after);  // runs beside the rest of this tile
+    bool more = list.next(a, i, k);
+    // A tile of at most NB blocks, from its first loads' arrival; the next one's
+    // loads run beside its results.
+    auto tile = [&](auto nb) {
+        constexpr int NB = decltype(nb)::value;
+        typename T::template Regs<NB> f;
+        t.run(f, lds);
         const int c = k.c0 + t.col0() / (GATED ? 2 : 1);
-        const Where at{k.e, k.first, k.n, c, a.C - c};
+        const Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
+        ++i;
+        more = list.next(a, i, k);
+        if (more)
+            start(k);
         if constexpr (DX)
-            finish_dx(a, t, at, lds);
+            finish_dx(a, t, f, at, lds);
         else
-            finish_forward<GATED>(a, t, at, lds);
-        if (!more)
-            return;
-        k = after;
+            finish_forward<GATED>(a, t, f, at, lds);
+    };
+    if (more)
+        start(k);
+    while (more) {
+        const int nb = blocks_of(k);
+        if (nb == 4)
+            tile(std::integral_constant<int, 4>());
+        else if (nb == 2)
+            tile(std::integral_constant<int, 2>());
+        else
+            tile(std::integral_constant<int, 1>());
     }
 }
 

@@ -26,11 +26,21 @@ namespace moe {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+// The lane, as a value of its own: what is worked out from it is not kept over the
+// tiles' loop, where there are no registers for it (the reloads of spilled ones waited
+// for every store of a tile's results: 30 us a tile).
+__device__ __forceinline__ int fresh_lane()
+{
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 #define MOE_SCALAR __attribute__((address_space(4)))
 
 template <bool GATED>
 struct CodeTile {
-    static constexpr int kWaves = 8, kFrags = 8, kBlocks = 4;  // blocks of 16 columns, of 64 rows
+    static constexpr int kWaves = 8, kFrags = 8;  // blocks of 16 columns of a wave
     static constexpr int kImage = 8192;                        // 64 indices of 128 bytes
     static constexpr int kStage = 8 * kImage, kQ = 4 * kImage;
     static constexpr int kScales = 2 * kStage;                 // the rows' scales: 4 x 64 a stage
@@ -44,7 +54,6 @@ struct CodeTile {
     int p_off, q_off, piece;             // of the first load
     int xs_off, xs_step, xs_bytes;
     const MOE_SCALAR float *ws[GATED ? 2 : 1];  // (uniform, and no kernel writes what it reads here)
-    f32x4 acc[kFrags][kBlocks];
 
     __device__ __forceinline__ int wave() const { return static_cast<int>(uniform(threadIdx.x / kWave)); }
     __device__ __forceinline__ int col0() const { return wave() % 2 * 128; }
@@ -64,7 +73,7 @@ struct CodeTile {
     __device__ __forceinline__ void init(const uint8_t *w, const uint8_t *w_up, int n_cols, const uint8_t *x, int n_rows,
                                          const float *x_scales, int xs_cols, int R_, int segments)
     {
-        const int v = wave(), lane = lane_id(), in64 = v * 8 + lane / 8;
+        const int v = wave(), lane = fresh_lane(), in64 = v * 8 + lane / 8;
         R = R_;
         pitch = R * segments;
         blocks = code_blocks(R);
@@ -143,6 +152,7 @@ struct CodeTile {
         f32x4 d[4];
         float xv[NB], s[GATED ? 2 : 1][NB];
         float wv[GATED ? 2 : 1];
+        f32x4 acc[kFrags][NB];
     };
     template <int NB>
     __device__ __forceinline__ void read_p(Regs<NB> &f, int c, const MOE_LDS char *__restrict__ stage) const
@@ -164,16 +174,16 @@ struct CodeTile {
     }
     __device__ __forceinline__ float scale_at(int g, int k) const { return ws[g][min(k, steps - 1)]; }
 
-    // The loads that a tile's first steps expect to be in flight.
-    template <int NB>
-    __device__ __forceinline__ void start(MOE_LDS char *lds) const
+    // The loads that a tile's first steps expect to be in flight: of `nb` blocks.
+    __device__ __forceinline__ void start(MOE_LDS char *lds, int nb) const
     {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             MOE_LDS char *stage = lds + k * kStage;
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-                load_q(stage, k, j);
+            for (int j = 0; j < 4; ++j)
+                if (j < nb)
+                    load_q(stage, k, j);
             load_p(stage, k, 0);
             load_p(stage, k, 2);
             load_scales(lds, k, k);
@@ -186,12 +196,12 @@ struct CodeTile {
 
     // The scaled addition that is due after MFMA m of a step (m - 3 of the ring).
     template <int NB>
-    __device__ __forceinline__ void add(const Regs<NB> &f, int m)
+    static __device__ __forceinline__ void add(Regs<NB> &f, int m)
     {
         const int c = m / NB, h = m % NB;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            acc[c][h][j] = fmaf(f.d[m % 4][j], f.s[GATED ? c / 2 % 2 : 0][h], acc[c][h][j]);
+            f.acc[c][h][j] = fmaf(f.d[m % 4][j], f.s[GATED ? c / 2 % 2 : 0][h], f.acc[c][h][j]);
     }
 
     // Step k, whose stage is at offset `cur`.  An image is refilled (rows and the
@@ -199,7 +209,7 @@ struct CodeTile {
     // join has shown that every wave has read it.
     template <int NB>
     __device__ __forceinline__ void step(Regs<NB> &f, const MOE_LDS char *__restrict__ rd, MOE_LDS char *__restrict__ wr,
-                                         int cur, int nxt, int k)
+                                         int cur, int nxt, int k) const
     {
         constexpr int A = Regs<NB>::kAhead, kSlots = 8 * NB;
         constexpr int kFirst = A == 2 ? 2 : 1;                     // column block at which the first join is
@@ -257,11 +267,11 @@ struct CodeTile {
         }
     }
 
-    // The product of a tile whose start<NB>() is under way.
+    // The product of a tile of at most NB blocks whose start(lds, NB) is under way, in
+    // f.acc.
     template <int NB>
-    __device__ __forceinline__ void run(MOE_LDS char *lds)
+    __device__ __forceinline__ void run(Regs<NB> &f, MOE_LDS char *lds) const
     {
-        Regs<NB> f;
 #pragma unroll
         for (int g = 0; g < (GATED ? 2 : 1); ++g) {
             f.wv[g] = scale_at(g, 0);
@@ -276,7 +286,7 @@ struct CodeTile {
         for (int c = 0; c < kFrags; ++c)
 #pragma unroll
             for (int h = 0; h < NB; ++h)
-                acc[c][h] = f32x4{};
+                f.acc[c][h] = f32x4{};
         join<2 + NB + 3>();  // all but the columns' second half
 #pragma unroll
         for (int h = 0; h < NB; ++h)
@@ -299,34 +309,11 @@ struct CodeTile {
         join<0>();
     }
 
-    __device__ __forceinline__ void start_rows(MOE_LDS char *lds) const
-    {
-        if (n <= 64)
-            start<1>(lds);
-        else if (n <= 128)
-            start<2>(lds);
-        else if (n <= 192)
-            start<3>(lds);
-        else
-            start<4>(lds);
-    }
-    __device__ __forceinline__ void run_rows(MOE_LDS char *lds)
-    {
-        if (n <= 64)
-            run<1>(lds);
-        else if (n <= 128)
-            run<2>(lds);
-        else if (n <= 192)
-            run<3>(lds);
-        else
-            run<4>(lds);
-    }
-
     // The largest of both column halves' sizes of this lane's row, of row block i.
-    __device__ __forceinline__ uint32_t both_halves(MOE_LDS char *lds, int i, uint32_t top) const
+    __device__ __forceinline__ uint32_t both_halves(MOE_LDS char *lds, int i, uint32_t top, int lane) const
     {
         MOE_LDS uint32_t *tops = reinterpret_cast<MOE_LDS uint32_t *>(lds + kTops) + i % 2 * 128;
-        const int at = wave() * 16 + lane_id() % 16;
+        const int at = wave() * 16 + lane % 16;
         tops[at] = top;  // (four lanes of a row, the same value)
         join<63>();
         return umax(top, tops[at ^ 16]);
