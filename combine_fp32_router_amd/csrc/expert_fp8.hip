@@ -4,8 +4,6 @@
 //   dx        g = the same of dy's codes and the transposed weights',  dx = act'(z_prev) g
 //
 // The results leave in bf16, in codes with a scale for each 128, or both.
-#include <type_traits>
-
 #include "fp8_tile.hpp"
 #include "launch.hpp"
 
@@ -243,21 +241,34 @@ __device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t
     }
 }
 
+// A workgroup's walk over its list of tiles.
 template <bool DX, bool GATED>
-__global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
-{
+struct Walk {
     typedef CodeTile<GATED> T;
-    constexpr int kCols = GATED ? 128 : 256;  // output columns of a tile
+    static constexpr int kCols = GATED ? 128 : 256;  // output columns of a tile
     typedef TileList<DX ? kDx : kForward, kCols, Fp8> List;
-    __shared__ __align__(1024) char shared[T::kLdsBytes + List::kBytes];
-    MOE_LDS char *lds = (MOE_LDS char *)shared;
+    const Fp8 &a;
+    MOE_LDS char *lds;
     List list;
-    list.build(a, reinterpret_cast<int32_t *>(shared + T::kLdsBytes));
-
     T t;
-    // blocks of 64 rows that a tile is run for
-    auto blocks_of = [](const Work &k) { return k.n <= 64 ? 1 : k.n <= 128 ? 2 : 4; };
-    auto start = [&](const Work &k) {  // the loads of a tile's first stages
+    int i;
+    Work k;
+    bool more;
+
+    // blocks of 64 rows that the tile is run for
+    __device__ __forceinline__ int blocks() const { return k.n <= 64 ? 1 : k.n <= 128 ? 2 : 4; }
+
+    // Goes to the next tile, if there is one, and starts its first loads.
+    __device__ __forceinline__ void next()
+    {
+        more = list.next(a, i, k);
+        ++i;
+        if (!more)
+            return;
+        T::keep_uniform(k.e);
+        T::keep_uniform(k.first);
+        T::keep_uniform(k.n);
+        T::keep_uniform(k.c0);
         const int nbc = code_blocks(a.C), pitch = a.R * a.segments;
         const int64_t half = static_cast<int64_t>(k.e) * (GATED ? 2 : 1);
         const uint8_t *w = a.w + (half * a.C + k.c0) * pitch;
@@ -268,38 +279,44 @@ __global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
 #pragma unroll
         for (int g = 0; g < (GATED ? 2 : 1); ++g)
             t.ws[g] = (const MOE_SCALAR float *)(a.ws + ((half + g) * nbc + block) * t.steps);
-        t.start(lds, blocks_of(k));
-    };
-    int i = 0;
-    Work k;
-    bool more = list.next(a, i, k);
+        t.start(lds, blocks());
+    }
+
     // A tile of at most NB blocks, from its first loads' arrival; the next one's
     // loads run beside its results.
-    auto tile = [&](auto nb) {
-        constexpr int NB = decltype(nb)::value;
+    template <int NB>
+    __device__ __forceinline__ void tile()
+    {
         typename T::template Regs<NB> f;
+        t.all_uniform();
         t.run(f, lds);
         const int c = k.c0 + t.col0() / (GATED ? 2 : 1);
         const Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
-        ++i;
-        more = list.next(a, i, k);
-        if (more)
-            start(k);
+        next();
         if constexpr (DX)
             finish_dx(a, t, f, at, lds);
         else
             finish_forward<GATED>(a, t, f, at, lds);
-    };
-    if (more)
-        start(k);
-    while (more) {
-        const int nb = blocks_of(k);
+    }
+};
+
+template <bool DX, bool GATED>
+__global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
+{
+    typedef Walk<DX, GATED> W;
+    __shared__ __align__(1024) char shared[W::T::kLdsBytes + W::List::kBytes];
+    W w{a, (MOE_LDS char *)shared};
+    w.list.build(a, reinterpret_cast<int32_t *>(shared + W::T::kLdsBytes));
+    w.i = 0;
+    w.next();
+    while (w.more) {
+        const int nb = w.blocks();
         if (nb == 4)
-            tile(std::integral_constant<int, 4>());
+            w.template tile<4>();
         else if (nb == 2)
-            tile(std::integral_constant<int, 2>());
+            w.template tile<2>();
         else
-            tile(std::integral_constant<int, 1>());
+            w.template tile<1>();
     }
 }
 

@@ -43,27 +43,27 @@ struct CodeTile {
     static constexpr int kWaves = 8, kFrags = 8;  // blocks of 16 columns of a wave
     static constexpr int kImage = 8192;                        // 64 indices of 128 bytes
     static constexpr int kStage = 8 * kImage, kQ = 4 * kImage;
-    static constexpr int kScales = 2 * kStage;                 // the rows' scales: 4 x 64 a stage
-    static constexpr int kMore = kScales + 2 * 1024, kOutBytes = 4096;
-    static constexpr int kTops = kMore + kWaves / 2 * kOutBytes;  // rows' largest sizes, which two waves put together
+    static constexpr int kScales = 2 * kStage;                 // the rows' scales: of 4 steps, and of the next 4
+    static constexpr int kOutBytes = 4096;
+    static constexpr int kTops = kScales + 2 * 4096;           // rows' largest sizes, which two waves put together
     static constexpr int kLdsBytes = kTops + 1024;
 
     // where the operands are, for this lane
     const char *p, *q, *xs;
     int pitch, pn, n, R, steps, blocks;  // bytes of a row; columns and rows inside; a segment's length; steps in all, of a segment
     int p_off, q_off, piece;             // of the first load
-    int xs_off, xs_step, xs_bytes;
+    int xs_off, xs_lane, xs_step, xs_bytes, xs_pitch;
     const MOE_SCALAR float *ws[GATED ? 2 : 1];  // (uniform, and no kernel writes what it reads here)
 
     __device__ __forceinline__ int wave() const { return static_cast<int>(uniform(threadIdx.x / kWave)); }
     __device__ __forceinline__ int col0() const { return wave() % 2 * 128; }
     __device__ __forceinline__ int row0(int block) const { return block * 64 + wave() / 2 * 16; }
-    // LDS of a wave's results: half of them behind the stages, half in what the
-    // next tile's second stage gets last.
+    // LDS of a wave's results, in what the next tile's second stage gets last: the
+    // columns' second half, and the rows from 128 on.
     __device__ __forceinline__ MOE_LDS char *out_place(MOE_LDS char *lds) const
     {
         const int w = wave();
-        return lds + (w < 4 ? kMore + w * kOutBytes : kStage + (w < 6 ? 1 : 3) * kImage + w % 2 * kOutBytes);
+        return lds + kStage + (w < 2 ? kImage : w < 4 ? 3 * kImage : kQ + w / 2 * kImage) + w % 2 * kOutBytes;
     }
 
     static __device__ __forceinline__ int place_of(int c, int i) { return c ^ (i / 2 % 8); }
@@ -88,7 +88,41 @@ struct CodeTile {
         xs = reinterpret_cast<const char *>(x_scales);
         xs_step = xs_cols == 1 ? 0 : 4;
         xs_bytes = n * xs_cols * 4;
-        xs_off = (lane / 16 * 64 + v / 2 * 16 + lane % 16) * xs_cols * 4;
+        xs_pitch = xs_cols * 4;
+        xs_off = (v / 2 * 16 + lane / 4) * xs_pitch + lane % 4 * xs_step;
+        xs_lane = lane % 4;
+    }
+
+    // Everything but the lane's own offsets is the same in all lanes.  If the compiler
+    // loses sight of that, every load gets a loop around it, so it is told again
+    // in front of a tile's product.
+    template <typename V>
+    static __device__ __forceinline__ void keep_uniform(V &v)
+    {
+        if constexpr (sizeof(V) == 8) {
+            const uint64_t u = (uint64_t)v;
+            v = (V)(static_cast<uint64_t>(uniform(static_cast<uint32_t>(u >> 32))) << 32 | uniform(static_cast<uint32_t>(u)));
+        } else {
+            v = static_cast<V>(uniform(static_cast<uint32_t>(v)));
+        }
+    }
+    __device__ __forceinline__ void all_uniform()
+    {
+        keep_uniform(p);
+        keep_uniform(q);
+        keep_uniform(xs);
+        keep_uniform(pitch);
+        keep_uniform(pn);
+        keep_uniform(n);
+        keep_uniform(R);
+        keep_uniform(steps);
+        keep_uniform(blocks);
+        keep_uniform(xs_step);
+        keep_uniform(xs_bytes);
+        keep_uniform(xs_pitch);
+#pragma unroll
+        for (int g = 0; g < (GATED ? 2 : 1); ++g)
+            keep_uniform(ws[g]);
     }
 
     // Bytes of a row in front of step k, and those of them that step has (<= 0 past
@@ -112,12 +146,17 @@ struct CodeTile {
                                                  (MOE_LDS void *)(stage + kQ + j * kImage + wave() * 1024), 16,
                                                  piece < live_of(k) ? q_off + j * 64 * pitch : kOutside, 0, 0, 0);
     }
-    // (both waves of a group of rows write the same scales to the same place)
-    __device__ __forceinline__ void load_scales(MOE_LDS char *__restrict__ lds, int which, int k) const
+    // The i-th load of the rows' scales: of 16 rows (of row block i % 4) for the four
+    // steps from i - i % 4, so that a row's line is asked for every fourth step: asked
+    // for in every step, for 64 rows, the scales were a third of the requests to L2.
+    // (Both waves of a group of rows write the same to the same place.)
+    __device__ __forceinline__ void load_scales(MOE_LDS char *__restrict__ lds, int i) const
     {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(const_cast<char *>(xs), xs_bytes),
-                                                 (MOE_LDS void *)(lds + kScales + which * 1024 + wave() / 2 * 256), 4,
-                                                 k < steps ? xs_off + k * xs_step : kOutside, 0, 0, 0);
+        const int k = i & ~3, h = i & 3;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            row_rsrc(const_cast<char *>(xs), xs_bytes),
+            (MOE_LDS void *)(lds + kScales + (i / 4 % 2) * 4096 + wave() / 2 * 1024 + h * 256), 4,
+            k + xs_lane < steps ? xs_off + h * 64 * xs_pitch + k * xs_step : kOutside, 0, 0, 0);
     }
 
     // As Tile::join.
@@ -143,11 +182,11 @@ struct CodeTile {
         return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     }
 
-    // NB: blocks of 64 rows that the tile has.  For few of them the columns'
+    // NB: blocks of 64 rows that the tile has (1, 2 or 4).  For few of them the columns'
     // fragments are read further ahead.
     template <int NB>
     struct Regs {
-        static constexpr int kAhead = NB >= 3 ? 2 : 4;
+        static constexpr int kBlocks = NB, kAhead = NB >= 3 ? 2 : 4;
         i32x8 pf[kAhead], qf[NB];
         f32x4 d[4];
         float xv[NB], s[GATED ? 2 : 1][NB];
@@ -165,33 +204,44 @@ struct CodeTile {
         f.qf[h] = frag(stage + kQ, row0(h));
     }
     template <int NB>
-    __device__ __forceinline__ void read_scales(Regs<NB> &f, const MOE_LDS char *__restrict__ lds, int which, int k) const
+    __device__ __forceinline__ void read_scales(Regs<NB> &f, const MOE_LDS char *__restrict__ lds, int k) const
     {
 #pragma unroll
         for (int h = 0; h < NB; ++h)
-            f.xv[h] = *reinterpret_cast<const MOE_LDS float *>(lds + kScales + which * 1024 + wave() / 2 * 256 +
-                                                               (h * 16 + lane_id() % 16) * 4);
+            f.xv[h] = *reinterpret_cast<const MOE_LDS float *>(lds + kScales + (k / 4 % 2) * 4096 + wave() / 2 * 1024 +
+                                                               h * 256 + lane_id() % 16 * 16 + k % 4 * 4);
     }
     __device__ __forceinline__ float scale_at(int g, int k) const { return ws[g][min(k, steps - 1)]; }
 
-    // The loads that a tile's first steps expect to be in flight: of `nb` blocks.
+    // The loads that a tile's first steps expect to be in flight, of `nb` blocks of
+    // rows; run() itself loads the second stage's rows from 128 on.
     __device__ __forceinline__ void start(MOE_LDS char *lds, int nb) const
     {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             MOE_LDS char *stage = lds + k * kStage;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < (k == 0 ? 4 : 2); ++j)
                 if (j < nb)
                     load_q(stage, k, j);
             load_p(stage, k, 0);
             load_p(stage, k, 2);
-            load_scales(lds, k, k);
+#pragma unroll
+            for (int i = 4 * k; i < 4 + k; ++i)
+                load_scales(lds, i);
             if (k == 0) {
                 load_p(stage, k, 1);
                 load_p(stage, k, 3);
             }
         }
+    }
+
+    template <int NB>
+    __device__ __forceinline__ void load_rest(const Regs<NB> &, MOE_LDS char *lds) const
+    {
+#pragma unroll
+        for (int j = 2; j < NB; ++j)
+            load_q(lds + kStage, 1, j);
     }
 
     // The scaled addition that is due after MFMA m of a step (m - 3 of the ring).
@@ -235,7 +285,7 @@ struct CodeTile {
             if (c == 7) {
                 read_q(f, h, rd + nxt);
                 if (h == NB - 1)
-                    read_scales(f, rd, nxt != 0, k + 1);
+                    read_scales(f, rd, k + 1);
             }
             const int t1 = m - kFirst * NB, t2 = m - 4 * NB;
             if (t1 >= 0 && t1 < T1)
@@ -252,7 +302,7 @@ struct CodeTile {
                     if (i < 2)
                         load_p(wr + cur, k + 2, 2 * i);
                     else
-                        load_scales(wr, cur != 0, k + 2);
+                        load_scales(wr, k + 5);
                 }
             // the scales of step k come into use with its first result
             if (m == 3) {
@@ -269,9 +319,10 @@ struct CodeTile {
 
     // The product of a tile of at most NB blocks whose start(lds, NB) is under way, in
     // f.acc.
-    template <int NB>
-    __device__ __forceinline__ void run(Regs<NB> &f, MOE_LDS char *lds) const
+    template <typename F>
+    __device__ __forceinline__ void run(F &f, MOE_LDS char *lds) const
     {
+        constexpr int NB = F::kBlocks;
 #pragma unroll
         for (int g = 0; g < (GATED ? 2 : 1); ++g) {
             f.wv[g] = scale_at(g, 0);
@@ -287,14 +338,15 @@ struct CodeTile {
 #pragma unroll
             for (int h = 0; h < NB; ++h)
                 f.acc[c][h] = f32x4{};
-        join<2 + NB + 3>();  // all but the columns' second half
+        join<2 + (NB > 2 ? 2 : NB) + 3>();  // all but the columns' second half
+        load_rest(f, lds);
 #pragma unroll
         for (int h = 0; h < NB; ++h)
             read_q(f, h, lds);
 #pragma unroll
         for (int c = 0; c < Regs<NB>::kAhead - 1; ++c)
             read_p(f, c, lds);
-        read_scales(f, lds, 0, 0);
+        read_scales(f, lds, 0);
         int cur = 0, nxt = kStage;
 #pragma unroll 1
         for (int k = 0; k < steps; ++k) {
