@@ -40,149 +40,200 @@ __device__ __forceinline__ uint32_t row_top(const f32x4 (&v)[BLOCKS])
     return umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
 }
 
-// Codes of 16 rows of a wave's columns, through LDS into whole pieces.
-template <int BLOCKS>
-__device__ __forceinline__ void store_codes(MOE_LDS char *__restrict__ lds, const f32x4 (&v)[BLOCKS], float scale,
-                                            const Pieces<BLOCKS> &to, int row)
-{
-    const int lane = to.lane, r = lane % 16;
-#pragma unroll
-    for (int c = 0; c < BLOCKS; ++c)
-        *reinterpret_cast<MOE_LDS uint32_t *>(lds + r * 256 + (c ^ r) * 16 + lane / 16 * 4) =
-            codes4(v[c][0], v[c][1], v[c][2], v[c][3], scale);
-#pragma unroll
-    for (int j = 0; j < BLOCKS / 4; ++j)
-        to.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<BLOCKS>(j, lane)));
-}
-
 // Where a tile's results go: its rows first .. first + n - 1, this wave's columns
 // from c on, `inside` of them (or more) the array's.
 struct Where {
     int e, first, n, c, inside, lane;
 };
 
-// The scale of the block that this wave's columns begin, of the 16 rows from `row`.
-__device__ __forceinline__ void store_scale(const Fp8 &a, const Where &at, int row, int halves, int half, float scale)
-{
-    const int r = row + at.lane % 16;
-    if (at.lane < 16 && r < at.n && at.inside > 0)
-        a.scales[((static_cast<int64_t>(at.first) + r) * halves + half) * code_blocks(a.C) + at.c / kCodeBlock] = scale;
-}
+// The results of 16 rows of a wave at a time, 64 columns of bf16 or all of the
+// codes, through LDS into 16-byte pieces of whole rows, P a row (expert_finish.hpp).
+// A lane's offsets into parts of arrays of one pitch are the same ones; the parts'
+// places are in their descriptors.
+struct Part {
+    __amdgpu_buffer_rsrc_t rsrc;
+    int pitch, inside;  // bytes of a row, from this part's column on
+    // The part of p [.., cols] from column c on, of the tile's rows.
+    __device__ __forceinline__ Part(const Where &at, const void *p, int cols, int size, int c, int inside_)
+        : rsrc(row_rsrc(const_cast<char *>(static_cast<const char *>(p)) + (static_cast<int64_t>(at.first) * cols + c) * size,
+                        p ? max(0, (at.n * cols - c) * size) : 0)),
+          pitch(cols * size), inside(inside_ * size)
+    {
+    }
+    template <int P>
+    __device__ __forceinline__ int offset(const Where &at, int row, int j, int lane) const
+    {
+        const int r = row + 64 / P * j + lane / P;
+        return r < at.n && lane % P * 16 < inside ? r * pitch + lane % P * 16 : kOutside;
+    }
+    template <int P>
+    __device__ __forceinline__ void load(const Where &at, int row, int lane, u32x4 (&v)[P / 4]) const
+    {
+#pragma unroll
+        for (int j = 0; j < P / 4; ++j)
+            v[j] = load_cached(rsrc, offset<P>(at, row, j, lane));
+    }
+    template <int P>
+    __device__ __forceinline__ void store(const Where &at, int row, int lane, const MOE_LDS char *__restrict__ place) const
+    {
+#pragma unroll
+        for (int j = 0; j < P / 4; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(*reinterpret_cast<const MOE_LDS u32x4 *>(place + Place::piece<P>(j, lane)),
+                                                   rsrc, offset<P>(at, row, j, lane), 0, 0);
+    }
+};
 
+__device__ __forceinline__ void put_bf16(MOE_LDS char *__restrict__ place, const f32x4 *v, int lane)
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<MOE_LDS u32x2 *>(place + Place::half(c, lane)) = round4(v[c]);
+}
+template <int BLOCKS>
+__device__ __forceinline__ void put_codes(MOE_LDS char *__restrict__ place, const f32x4 (&v)[BLOCKS], float scale, int lane)
+{
+    const int r = lane % 16;
+    const Coder coder(scale);
+#pragma unroll
+    for (int c = 0; c < BLOCKS; ++c)
+        *reinterpret_cast<MOE_LDS uint32_t *>(place + r * 256 + (c ^ r) * 16 + lane / 16 * 4) =
+            coder.codes4(v[c][0], v[c][1], v[c][2], v[c][3]);
+}
 // Loaded pieces of 16 rows, eight a row, into LDS: as the first or the second eight.
-__device__ __forceinline__ void put_pieces(MOE_LDS char *__restrict__ lds, const u32x4 (&in)[2], int second, int lane)
+__device__ __forceinline__ void put_pieces(MOE_LDS char *__restrict__ place, const u32x4 (&in)[2], int second, int lane)
 {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int row = 8 * j + lane / 8;
-        *reinterpret_cast<MOE_LDS u32x4 *>(lds + row * 256 + ((lane % 8 + 8 * second) ^ row) * 16) = in[j];
+        *reinterpret_cast<MOE_LDS u32x4 *>(place + row * 256 + ((lane % 8 + 8 * second) ^ row) * 16) = in[j];
     }
 }
-__device__ __forceinline__ f32x4 get_block(const MOE_LDS char *__restrict__ lds, int c, int lane)
+__device__ __forceinline__ f32x4 get_block(const MOE_LDS char *__restrict__ place, int c, int lane)
 {
-    return widen4(*reinterpret_cast<const MOE_LDS u32x2 *>(lds + Place::half(c, lane)));
+    return widen4(*reinterpret_cast<const MOE_LDS u32x2 *>(place + Place::half(c, lane)));
+}
+
+// The scale of the block that this wave's columns begin, of the 16 rows from `row`.
+__device__ __forceinline__ void store_scale(const Fp8 &a, const Where &at, int row, int halves, int half, float scale, int lane)
+{
+    const int r = row + lane % 16;
+    if (lane < 16 && r < at.n && at.inside > 0)
+        a.scales[((static_cast<int64_t>(at.first) + r) * halves + half) * code_blocks(a.C) + at.c / kCodeBlock] = scale;
 }
 
 // Forward: bias, pre-activations, activation, residual.  The accumulators are
 // changed in place, a block of 64 rows after the other: beside 128 of them there is
-// no room for copies.  GATED: blocks 0, 1, 4, 5 are the gate's, 2, 3, 6, 7 the up
-// half's.
+// no room for copies, nor for addresses kept from one 64 columns to the next (hence
+// the lane as a value of its own in each).  GATED: blocks 0, 1, 4, 5 are the gate's,
+// 2, 3, 6, 7 the up half's.
 template <bool GATED, int NB>
 __device__ __forceinline__ void finish_forward(const Fp8 &a, const CodeTile<GATED> &t,
                                                const typename CodeTile<GATED>::template Regs<NB> &f, const Where &at,
                                                MOE_LDS char *lds)
 {
-    constexpr int kBlocks = GATED ? 4 : 8, P = 2 * kBlocks, wide = GATED ? 2 : 1;
+    constexpr int kHalves = GATED ? 1 : 2, wide = GATED ? 2 : 1;  // of 64 columns
     MOE_LDS char *place = t.out_place(lds);
-    const Pieces<P> out(a.out, at.first, at.n, a.C, 2, at.c, at.inside, at.lane), res(a.residual, at.first, at.n, a.C, 2, at.c, at.inside, at.lane);
-    const Pieces<P> pre(a.preact, at.first, at.n, wide * a.C, 2, at.c, at.inside, at.lane);
-    const Pieces<P> pre_up(a.preact, at.first, at.n, wide * a.C, 2, GATED ? at.c + a.C : at.c, at.inside, at.lane);
-    const Pieces<kBlocks> codes(a.codes, at.first, at.n, a.C, 1, at.c, at.inside, at.lane);
-    const float *bias = a.bias + static_cast<int64_t>(at.e) * wide * a.C + at.c + at.lane / 16 * 4;
-    u32x4 ahead[P / 4];  // the residual's next 16 rows
-    auto load = [&](int row) {
+    int lane = at.lane;
+    u32x4 ahead[2];  // the residual's next 16 rows
+    auto load = [&](int row, int right) {
         if (a.residual)
-#pragma unroll
-            for (int j = 0; j < P / 4; ++j)
-                ahead[j] = res.load(row, j);
+            Part(at, a.residual, a.C, 2, at.c + 64 * right, at.inside - 64 * right).template load<8>(at, row, lane, ahead);
     };
-    load(t.row0(0));
+    load(t.row0(0), 0);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         if (b * 64 >= at.n)
             break;
         const int row = t.row0(b);
-        f32x4 g[kBlocks], u[GATED ? kBlocks : 1];
+        f32x4 y[4 * kHalves];
 #pragma unroll
-        for (int i = 0; i < kBlocks; ++i) {
-            g[i] = f.acc[GATED ? i / 2 * 4 + i % 2 : i][b];
-            if (GATED)
-                u[i] = f.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
-            if (a.bias && i * 16 < at.inside) {
-                g[i] += *reinterpret_cast<const f32x4 *>(bias + i * 16);
+        for (int right = 0; right < kHalves; ++right) {
+            asm volatile("" : "+v"(lane));
+            f32x4 g[4], u[GATED ? 4 : 1];
+            const float *bias = a.bias + static_cast<int64_t>(at.e) * wide * a.C + at.c + 64 * right + lane / 16 * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[i] = f.acc[GATED ? i / 2 * 4 + i % 2 : right * 4 + i][b];
                 if (GATED)
-                    u[i] += *reinterpret_cast<const f32x4 *>(bias + a.C + i * 16);
+                    u[i] = f.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
+                if (a.bias && right * 64 + i * 16 < at.inside) {
+                    g[i] += *reinterpret_cast<const f32x4 *>(bias + i * 16);
+                    if (GATED)
+                        u[i] += *reinterpret_cast<const f32x4 *>(bias + a.C + i * 16);
+                }
             }
-        }
-        if (a.preact) {
-            store_blocks<P>(place, g, pre, row);
-            if constexpr (GATED)
-                store_blocks<P>(place, u, pre_up, row);
-        }
-        if (GATED) {
+            if (a.preact) {
+                put_bf16(place, g, lane);
+                Part(at, a.preact, wide * a.C, 2, at.c + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
+                if (GATED) {
+                    put_bf16(place, u, lane);
+                    Part(at, a.preact, wide * a.C, 2, at.c + a.C, at.inside).template store<8>(at, row, lane, place);
+                }
+            }
+            if (GATED) {
 #pragma unroll
-            for (int i = 0; i < 4 * kBlocks; ++i)
-                g[i / 4][i % 4] *= sigmoid(g[i / 4][i % 4]) * u[GATED ? i / 4 : 0][i % 4];
-        } else {
-            apply_act(g, a.act);
-        }
-        if (a.residual) {
+                for (int i = 0; i < 16; ++i)
+                    g[i / 4][i % 4] *= sigmoid(g[i / 4][i % 4]) * u[GATED ? i / 4 : 0][i % 4];
+            } else {
+                apply_act(g, a.act);
+            }
+            if (a.residual) {
+                put_pieces(place, ahead, 0, lane);
+                // (in front of this block's stores: waiting for it is then not waiting for them)
+                load(right == kHalves - 1 ? t.row0(min(b + 1, NB - 1)) : row, (right + 1) % kHalves);
 #pragma unroll
-            for (int j = 0; j < P / 4; ++j)
-                *reinterpret_cast<MOE_LDS u32x4 *>(place + Place::piece<P>(j, at.lane)) = ahead[j];
-            load(t.row0(min(b + 1, NB - 1)));  // in front of this block's stores: waiting for it is then not waiting for them
+                for (int i = 0; i < 4; ++i)
+                    g[i] += get_block(place, i, lane);
+            }
+            if (a.out) {
+                put_bf16(place, g, lane);
+                Part(at, a.out, a.C, 2, at.c + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
+            }
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i)
-                g[i] += get_block(place, i, at.lane);
+            for (int i = 0; i < 4; ++i)
+                y[right * 4 + i] = g[i];
         }
-        if (a.out)
-            store_blocks<P>(place, g, out, row);
         if (a.codes) {
-            uint32_t top = row_top(g);
+            asm volatile("" : "+v"(lane));
+            uint32_t top = row_top(y);
             if (GATED)
-                top = t.both_halves(lds, b, top, at.lane);
+                top = t.both_halves(lds, b, top, lane);
             const float scale = scale_of(top);
-            store_codes(place, g, scale, codes, row);
+            put_codes(place, y, scale, lane);
+            Part(at, a.codes, a.C, 1, at.c, at.inside).template store<4 * kHalves>(at, row, lane, place);
             if (!GATED || t.col0() == 0)
-                store_scale(a, at, row, 1, 0, scale);
+                store_scale(a, at, row, 1, 0, scale, lane);
         }
     }
 }
 
-// dx: through the activation that made the product's input, 64 columns at a time.
-template <int NB>
+// dx: through the activation that made the product's input (SWIGLU: MOE_ACT_SWIGLU).
+template <bool SWIGLU, int NB>
 __device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t, const CodeTile<false>::Regs<NB> &f,
                                           const Where &at, MOE_LDS char *lds)
 {
     MOE_LDS char *place = t.out_place(lds);
-    const bool gated = a.act == MOE_ACT_SWIGLU;
-    const int cols = gated ? 2 * a.C : a.C, up = gated ? at.c + a.C : at.c;
-    const Pieces<16> out(a.out, at.first, at.n, cols, 2, at.c, at.inside, at.lane), out_up(a.out, at.first, at.n, cols, 2, up, at.inside, at.lane);
-    const Pieces<8> codes(a.codes, at.first, at.n, cols, 1, at.c, at.inside, at.lane), codes_up(a.codes, at.first, at.n, cols, 1, up, at.inside, at.lane);
-    const Pieces<8> pre(a.z, at.first, at.n, cols, 2, at.c, at.inside, at.lane), pre_r(a.z, at.first, at.n, cols, 2, at.c + 64, at.inside - 64, at.lane);
-    const Pieces<8> pre_up(a.z, at.first, at.n, cols, 2, up, at.inside, at.lane), pre_up_r(a.z, at.first, at.n, cols, 2, up + 64, at.inside - 64, at.lane);
+    const int cols = SWIGLU ? 2 * a.C : a.C;
+    int lane = at.lane;
     u32x4 ahead[2], ahead_up[2];
-    auto load = [&](int row, bool right) {
-        if (a.act != MOE_ACT_NONE)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                ahead[j] = right ? pre_r.load(row, j) : pre.load(row, j);
-        if (gated)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                ahead_up[j] = right ? pre_up_r.load(row, j) : pre_up.load(row, j);
+    auto load = [&](int row, int right) {
+        if (SWIGLU || a.act != MOE_ACT_NONE)
+            Part(at, a.z, cols, 2, at.c + 64 * right, at.inside - 64 * right).template load<8>(at, row, lane, ahead);
+        if (SWIGLU)
+            Part(at, a.z, cols, 2, at.c + a.C + 64 * right, at.inside - 64 * right).template load<8>(at, row, lane, ahead_up);
     };
-    load(t.row0(0), false);
+    auto store = [&](const f32x4 *v, int row, int right, int half) {
+        put_bf16(place, v, lane);
+        Part(at, a.out, cols, 2, at.c + half * a.C + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
+    };
+    auto store_coded = [&](const f32x4 (&v)[8], int row, int half) {
+        asm volatile("" : "+v"(lane));
+        const float scale = scale_of(row_top(v));
+        put_codes(place, v, scale, lane);
+        Part(at, a.codes, cols, 1, at.c + half * a.C, at.inside).template store<8>(at, row, lane, place);
+        store_scale(a, at, row, SWIGLU ? 2 : 1, half, scale, lane);
+    };
+    load(t.row0(0), 0);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         if (b * 64 >= at.n)
@@ -191,59 +242,55 @@ __device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t
         f32x4 v[8], u[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-            v[c] = u[c] = f.acc[c][b];
-        if (a.act != MOE_ACT_NONE)
+            v[c] = f.acc[c][b];
 #pragma unroll
-            for (int right = 0; right < 2; ++right) {
-                put_pieces(place, ahead, 0, at.lane);
-                if (gated)
-                    put_pieces(place, ahead_up, 1, at.lane);
+        for (int right = 0; right < 2; ++right) {
+            asm volatile("" : "+v"(lane));
+            if (SWIGLU || a.act != MOE_ACT_NONE) {
+                put_pieces(place, ahead, 0, lane);
+                if (SWIGLU)
+                    put_pieces(place, ahead_up, 1, lane);
                 load(right ? t.row0(min(b + 1, NB - 1)) : row, !right);
-                if (gated) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const f32x4 z = get_block(place, c, at.lane), zu = get_block(place, 4 + c, at.lane);
+                for (int c = 4 * right; c < 4 * right + 4; ++c) {
+                    const f32x4 z[1] = {get_block(place, c % 4, lane)};
+                    if constexpr (SWIGLU) {
+                        const f32x4 zu = get_block(place, 4 + c % 4, lane);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float g = z[j], x = v[right * 4 + c][j], s = sigmoid(g);
-                            v[right * 4 + c][j] = x * zu[j] * (s * (1.0f + g * (1.0f - s)));
-                            u[right * 4 + c][j] = x * (g * s);
+                            const float g = z[0][j], x = v[c][j], s = sigmoid(g);
+                            v[c][j] = x * zu[j] * (s * (1.0f + g * (1.0f - s)));
+                            u[c][j] = x * (g * s);
                         }
+                    } else {
+                        f32x4 w[1] = {v[c]};
+                        apply_slope(w, z, a.act);
+                        v[c] = w[0];
                     }
-                } else {
-                    f32x4 z[4], w[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        z[c] = get_block(place, c, at.lane);
-                        w[c] = v[right * 4 + c];
-                    }
-                    apply_slope(w, z, a.act);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        v[right * 4 + c] = w[c];
+                    __builtin_amdgcn_sched_barrier(0);  // (read together, the blocks take registers that are not there)
                 }
             }
-        if (a.out) {
-            store_blocks<16>(place, v, out, row);
-            if (gated)
-                store_blocks<16>(place, u, out_up, row);
+            if (a.out) {
+                store(v + 4 * right, row, right, 0);
+                if (SWIGLU)
+                    store(u + 4 * right, row, right, 1);
+            }
         }
         if (a.codes) {
-            const float scale = scale_of(row_top(v));
-            store_codes(place, v, scale, codes, row);
-            store_scale(a, at, row, gated ? 2 : 1, 0, scale);
-            if (gated) {
-                const float scale_up = scale_of(row_top(u));
-                store_codes(place, u, scale_up, codes_up, row);
-                store_scale(a, at, row, 2, 1, scale_up);
-            }
+            store_coded(v, row, 0);
+            if (SWIGLU)
+                store_coded(u, row, 1);
         }
     }
 }
 
+// Forward, of a gated product, dx, dx through SwiGLU.
+enum Kind { kPlain, kGated, kBack, kBackGated };
+
 // A workgroup's walk over its list of tiles.
-template <bool DX, bool GATED>
+template <Kind KIND>
 struct Walk {
+    static constexpr bool GATED = KIND == kGated, DX = KIND >= kBack;
     typedef CodeTile<GATED> T;
     static constexpr int kCols = GATED ? 128 : 256;  // output columns of a tile
     typedef TileList<DX ? kDx : kForward, kCols, Fp8> List;
@@ -294,16 +341,16 @@ struct Walk {
         const Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
         next();
         if constexpr (DX)
-            finish_dx(a, t, f, at, lds);
+            finish_dx<KIND == kBackGated>(a, t, f, at, lds);
         else
             finish_forward<GATED>(a, t, f, at, lds);
     }
 };
 
-template <bool DX, bool GATED>
+template <Kind KIND>
 __global__ __launch_bounds__(512) void expert_fp8_kernel(Fp8 a)
 {
-    typedef Walk<DX, GATED> W;
+    typedef Walk<KIND> W;
     __shared__ __align__(1024) char shared[W::T::kLdsBytes + W::List::kBytes];
     W w{a, (MOE_LDS char *)shared};
     w.list.build(a, reinterpret_cast<int32_t *>(shared + W::T::kLdsBytes));
@@ -333,13 +380,13 @@ int tile_height(int E, int64_t max_rows, int col_tiles)
 // As grid_for of the bf16 products.
 dim3 grid_for(int64_t n) { return dim3(static_cast<unsigned>(n + 14 < kCus ? (n + 14) / 8 * 8 : kCus)); }
 
-template <bool DX, bool GATED>
+template <Kind KIND>
 hipError_t launch(Fp8 &a, int64_t max_rows, hipStream_t stream)
 {
-    const int col_tiles = (a.C + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+    const int col_tiles = (a.C + Walk<KIND>::kCols - 1) / Walk<KIND>::kCols;
     a.max_rows = static_cast<int>(max_rows);
     a.height = tile_height(a.E, max_rows, col_tiles);
-    expert_fp8_kernel<DX, GATED><<<grid_for(max_row_tiles(max_rows, a.E, a.height) * col_tiles), 512, 0, stream>>>(a);
+    expert_fp8_kernel<KIND><<<grid_for(max_row_tiles(max_rows, a.E, a.height) * col_tiles), 512, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -354,7 +401,7 @@ hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const 
     a.w = static_cast<const uint8_t *>(w), a.ws = ws, a.bias = bias, a.act = act;
     a.residual = static_cast<const uint16_t *>(residual), a.E = E, a.R = K, a.segments = 1, a.C = N;
     a.out = out, a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.preact = static_cast<uint16_t *>(preact);
-    return act == MOE_ACT_SWIGLU ? launch<false, true>(a, max_rows, stream) : launch<false, false>(a, max_rows, stream);
+    return act == MOE_ACT_SWIGLU ? launch<kGated>(a, max_rows, stream) : launch<kPlain>(a, max_rows, stream);
 }
 
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
@@ -366,7 +413,7 @@ hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t 
     a.w = static_cast<const uint8_t *>(wt), a.ws = wts, a.act = act, a.z = static_cast<const uint16_t *>(z);
     a.E = E, a.R = N, a.segments = halves, a.C = K;
     a.out = dx, a.codes = static_cast<uint8_t *>(codes), a.scales = scales;
-    return launch<true, false>(a, max_rows, stream);
+    return act == MOE_ACT_SWIGLU ? launch<kBackGated>(a, max_rows, stream) : launch<kBack>(a, max_rows, stream);
 }
 
 }  // namespace moe

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
                 const float scale = scale_of(a.blocks ? row_umax(top[i]) : all);
                 if (a.blocks && c % 16 == 0 && c * 8 < a.H && live)
                     a.scales[t * nb + c / 16] = scale;
-                __builtin_amdgcn_raw_buffer_store_b64(codes8(s[i], scale), to, c * 8, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b64(Coder(scale).codes8(s[i]), to, c * 8, 0, 0);
             }
         }
         turn ^= 1;

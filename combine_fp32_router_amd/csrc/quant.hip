@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(QuantRows a)
                 top = umax(top, size_bits(f[j]));
             const float scale = scale_of(row_umax(top));
             if (c < vecs)
-                codes[c] = codes8(f, scale);
+                codes[c] = Coder(scale).codes8(f);
             if (c % 16 == 0)
                 a.scales[i * nb + c / 16] = scale;
         }
@@ -89,12 +89,13 @@ __global__ __launch_bounds__(kThreads) void quant_weights_kernel(QuantWeights a)
         if (a.codes_t)
             a.scales_t[((static_cast<int64_t>(e) * nbk + bk) * a.halves + half) * nbn + bn] = scale;
     }
+    const Coder coder(scale);
     u32x2 q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         float f[8];
         unpack8(v[i], f);
-        q[i] = codes8(f, scale);
+        q[i] = coder.codes8(f);
         if (n0 + i < a.N && k < a.K)
             *reinterpret_cast<u32x2 *>(a.codes + matrix + static_cast<int64_t>(n0 + i) * a.K + k) = q[i];
     }
