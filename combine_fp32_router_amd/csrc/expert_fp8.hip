@@ -338,8 +338,13 @@ struct Walk {
         t.all_uniform();
         t.run(f, lds);
         const int c = k.c0 + t.col0() / (GATED ? 2 : 1);
-        const Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
+        Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
         next();
+        T::keep_uniform(at.e);
+        T::keep_uniform(at.first);
+        T::keep_uniform(at.n);
+        T::keep_uniform(at.c);
+        T::keep_uniform(at.inside);
         if constexpr (DX)
             finish_dx<KIND == kBackGated>(a, t, f, at, lds);
         else

@@ -33,12 +33,12 @@ __device__ __forceinline__ float scale_of(uint32_t top)
 // Codes of values over one scale.  The quotients come from the scale's reciprocal
 // with one step of correction, q + (v - q s) / s, which is the correctly rounded
 // quotient but where v - q s is subnormal: three instructions a value where the
-// division takes ten (which cost 13 us a tile of the products' gradients).  A scale
-// whose reciprocal might not be finite takes the division.
+// division takes ten (which cost 13 us a tile of the products' gradients).  Where a
+// wave has a scale whose reciprocal might not be finite, it divides.
 struct Coder {
     float scale, inverse;
-    bool divide;
-    __device__ __forceinline__ explicit Coder(float s) : scale(s), inverse(1.0f / s), divide(s < 1e-37f) {}
+    bool divide;  // in any lane of the wave
+    __device__ __forceinline__ explicit Coder(float s) : scale(s), inverse(1.0f / s), divide(__any(s < 1e-37f)) {}
 
     __device__ __forceinline__ float over(float v) const
     {
@@ -49,9 +49,8 @@ struct Coder {
     __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) const
     {
         if (__builtin_expect(divide, false)) {
-            if (scale == 0.0f)
-                return 0u;
-            return pack(a / scale, b / scale, c / scale, d / scale);
+            const uint32_t w = pack(a / scale, b / scale, c / scale, d / scale);
+            return scale == 0.0f ? 0u : w;
         }
         return pack(over(a), over(b), over(c), over(d));
     }
