@@ -4,10 +4,10 @@
 //   d_x = d_s + R g - s R^3 mean(g s),  g = d_y w;   d_w = sum over rows of d_y s R
 //
 // A row is read once and held in registers (THREADS threads, VPT 16-byte vectors
-// each) between its sums and its results.  Sixteen lanes hold the 128 values of a
-// block of codes, a row of the DPP moves.  The gradient of w stays in registers
-// over all rows of a workgroup; the workgroups' sums meet in a second kernel, in a
-// fixed order.
+// each) between its sums and its results, and the next row's loads are in flight
+// meanwhile.  Sixteen lanes hold the 128 values of a block of codes, a row of the
+// DPP moves.  The gradient of w stays in registers over all rows of a workgroup; the
+// workgroups' sums meet in a second kernel, in a fixed order.
 #include "fp8_codes.hpp"
 #include "launch.hpp"
 
@@ -79,6 +79,7 @@ __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *red, int turn)
 }
 
 // Rows of a workgroup at once, and its threads.
+constexpr int64_t kCacheBytes = 256 << 20;  // of the last-level cache
 constexpr int rows_of(int threads) { return threads == kWave ? 4 : 1; }
 constexpr int group_of(int threads) { return threads == kWave ? 4 * kWave : threads; }
 
@@ -88,7 +89,39 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void *p, int64_t 
     return row_rsrc(const_cast<char *>(static_cast<const char *>(p)) + t * bytes, p && live ? bytes : 0);
 }
 
+// VPT vectors of a row from lane l on; STREAM: rows that no cache will keep.
+template <int THREADS, int VPT, bool STREAM>
+__device__ __forceinline__ void load_row(const __amdgpu_buffer_rsrc_t &r, int l, u32x4 (&v)[VPT])
+{
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+        v[i] = STREAM ? load_stream16(r, (l + i * THREADS) * 16) : load_cached(r, (l + i * THREADS) * 16);
+}
+template <bool STREAM, typename V>
+__device__ __forceinline__ void store_vector(const __amdgpu_buffer_rsrc_t &r, int offset, V v)
+{
+    constexpr int policy = STREAM ? kCpolStream : kCpolDefault;
+    if constexpr (sizeof(V) == 16)
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, offset, 0, policy);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(v, r, offset, 0, policy);
+}
+
+// This lane's weights (1 where there are none).
 template <int THREADS, int VPT>
+__device__ __forceinline__ void load_weights(const float *weight, int H, int l, float (&w)[VPT][8])
+{
+    const __amdgpu_buffer_rsrc_t r = row_of(weight, 0, H * 4, true);
+#pragma unroll
+    for (int i = 0; i < 2 * VPT; ++i) {
+        const u32x4 v = load_cached(r, (l + i / 2 * THREADS) * 32 + i % 2 * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[i / 2][i % 2 * 4 + j] = weight ? __uint_as_float(v[j]) : 1.0f;
+    }
+}
+
+template <int THREADS, int VPT, bool STREAM>
 __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
 {
     constexpr int kRows = rows_of(THREADS);
@@ -96,62 +129,64 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
     __shared__ uint32_t tops[2 * 16];
     const int l = THREADS == kWave ? lane_id() : static_cast<int>(threadIdx.x);
     const int first = THREADS == kWave ? static_cast<int>(uniform(threadIdx.x / kWave)) : 0;
+    constexpr bool kHold = THREADS < 1024;  // the weights, beside the row and the next one
     const int nb = code_blocks(a.H);
-    float w[VPT][8];
-    {
-        const __amdgpu_buffer_rsrc_t r = row_of(a.weight, 0, a.H * 4, true);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u32x4 v = load_cached(r, (l + i * THREADS) * 32 + h * 16);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i][h * 4 + j] = a.weight ? __uint_as_float(v[j]) : 1.0f;
-            }
+    float w[kHold ? VPT : 1][8];
+    u32x4 v[VPT], u[VPT];
+    auto load = [&](int64_t t) {
+        load_row<THREADS, VPT, STREAM>(row_of(a.x, t, a.H * 2, t < a.T), l, v);
+        if (a.residual)
+            load_row<THREADS, VPT, STREAM>(row_of(a.residual, t, a.H * 2, t < a.T), l, u);
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    if (kHold) {
+        load(static_cast<int64_t>(blockIdx.x) * kRows + first);
+        load_weights<THREADS, kHold ? VPT : 1>(a.weight, a.H, l, w);
     }
     int turn = 0;
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += step) {
         const int64_t t = t0 + first;
         const bool live = t < a.T;
-        const __amdgpu_buffer_rsrc_t xr = row_of(a.x, t, a.H * 2, live), rr = row_of(a.residual, t, a.H * 2, live);
-        u32x4 v[VPT], u[VPT];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            v[i] = load_cached(xr, (l + i * THREADS) * 16);
-            u[i] = load_cached(rr, (l + i * THREADS) * 16);
-        }
+        if (!kHold)
+            load(t);
         float s[VPT][8], ss[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float f[8];
             unpack8(v[i], s[i]);
-            unpack8(u[i], f);
+            if (a.residual) {
+                float f[8];
+                unpack8(u[i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (a.residual)
+                for (int j = 0; j < 8; ++j)
                     s[i][j] += f[j];
-                ss[0] = fmaf(s[i][j], s[i][j], ss[0]);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ss[0] = fmaf(s[i][j], s[i][j], ss[0]);
         }
+        if (kHold)
+            load(t + step);
         if (a.sum) {
             const __amdgpu_buffer_rsrc_t to = row_of(a.sum, t, a.H * 2, live);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                __builtin_amdgcn_raw_buffer_store_b128(pack8(s[i]), to, (l + i * THREADS) * 16, 0, 0);
+                store_vector<STREAM>(to, (l + i * THREADS) * 16, pack8(s[i]));
         }
         row_sums<THREADS, 1>(ss, red, turn);
         const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.H) + a.eps);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < VPT; ++i) {
+            if (!kHold)
+                load_weights<THREADS, 1>(a.weight, a.H, l + i * THREADS, reinterpret_cast<float(&)[1][8]>(w[0]));
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                s[i][j] = s[i][j] * r * w[i][j];
+                s[i][j] = s[i][j] * r * w[kHold ? i : 0][j];
+        }
         if (a.y) {
             const __amdgpu_buffer_rsrc_t to = row_of(a.y, t, a.H * 2, live);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                __builtin_amdgcn_raw_buffer_store_b128(pack8(s[i]), to, (l + i * THREADS) * 16, 0, 0);
+                store_vector<STREAM>(to, (l + i * THREADS) * 16, pack8(s[i]));
         }
         if (a.codes) {
             const __amdgpu_buffer_rsrc_t to = row_of(a.codes, t, a.H, live);
@@ -175,7 +210,7 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
                 const float scale = scale_of(a.blocks ? row_umax(top[i]) : all);
                 if (a.blocks && c % 16 == 0 && c * 8 < a.H && live)
                     a.scales[t * nb + c / 16] = scale;
-                __builtin_amdgcn_raw_buffer_store_b64(Coder(scale).codes8(s[i]), to, c * 8, 0, 0);
+                store_vector<STREAM>(to, c * 8, Coder(scale).codes8(s[i]));
             }
         }
         turn ^= 1;
@@ -189,64 +224,83 @@ struct NormGrad {
     int64_t T;
     int H;
     uint16_t *dx;
-    float *part;  // [workgroups * rows at once][H], or null
+    float *part;  // [workgroups][H], or null
 };
 
-// HOLD: a row stays in registers between its sums and its results; else it is
-// read again (from cache: 128 KiB at the longest).
-template <int THREADS, int VPT, bool HOLD>
+// HOLD: a row stays in registers between its sums and its results, beside the
+// weights and the next row; else it is read again (from cache: 128 KiB at the longest).
+template <int THREADS, int VPT, bool STREAM>
 __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGrad a)
 {
+    constexpr bool HOLD = THREADS < 1024;
     constexpr int kRows = rows_of(THREADS), kHeld = HOLD ? VPT : 1;
     __shared__ float red[2 * 2 * 16];
     const int l = THREADS == kWave ? lane_id() : static_cast<int>(threadIdx.x);
     const int first = THREADS == kWave ? static_cast<int>(uniform(threadIdx.x / kWave)) : 0;
-    const __amdgpu_buffer_rsrc_t wr = row_of(a.weight, 0, a.H * 4, true);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+    auto rows_at = [&](const uint16_t *p, int64_t t) { return row_of(p, t, a.H * 2, t < a.T); };
+    float held[kHeld][8], dw[VPT][8] = {};
+    u32x4 sv[kHeld], yv[kHeld], dv[kHeld], sn[kHeld], yn[kHeld], dn[kHeld];
+    auto load_next = [&](int64_t t) {
+        load_row<THREADS, kHeld, STREAM>(rows_at(a.sum, t), l, sn);
+        load_row<THREADS, kHeld, STREAM>(rows_at(a.dy, t), l, yn);
+        if (a.dsum)
+            load_row<THREADS, kHeld, STREAM>(rows_at(a.dsum, t), l, dn);
+    };
+    if (HOLD) {
+        load_next(static_cast<int64_t>(blockIdx.x) * kRows + first);
+        load_weights<THREADS, kHeld>(a.weight, a.H, l, held);
+    }
+    // vector i of an array of the row, and of the weights
+    auto vector = [&](const u32x4 (&kept)[kHeld], const __amdgpu_buffer_rsrc_t &r, int i) {
+        return HOLD ? kept[HOLD ? i : 0] : load_cached(r, (l + i * THREADS) * 16);
+    };
     auto weights = [&](int i, float(&w)[8]) {
+        if constexpr (HOLD) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const u32x4 v = load_cached(wr, (l + i * THREADS) * 32 + h * 16);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[h * 4 + j] = a.weight ? __uint_as_float(v[j]) : 1.0f;
+            for (int j = 0; j < 8; ++j)
+                w[j] = held[i][j];
+        } else {
+            load_weights<THREADS, 1>(a.weight, a.H, l + i * THREADS, reinterpret_cast<float(&)[1][8]>(w));
         }
     };
-    float dw[VPT][8] = {};
     int turn = 0;
-    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += static_cast<int64_t>(gridDim.x) * kRows) {
+    for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += step) {
         const int64_t t = t0 + first;
         const bool live = t < a.T;
-        const __amdgpu_buffer_rsrc_t sr = row_of(a.sum, t, a.H * 2, live), yr = row_of(a.dy, t, a.H * 2, live);
-        const __amdgpu_buffer_rsrc_t dr = row_of(a.dsum, t, a.H * 2, live), to = row_of(a.dx, t, a.H * 2, live);
-        u32x4 sv[kHeld], yv[kHeld];
-        float sums[2] = {0.0f, 0.0f};  // of s^2 and of g s
-        if (HOLD)
+        const __amdgpu_buffer_rsrc_t sr = rows_at(a.sum, t), yr = rows_at(a.dy, t), dr = rows_at(a.dsum, t);
+        if (HOLD) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                sv[HOLD ? i : 0] = load_cached(sr, (l + i * THREADS) * 16);
-                yv[HOLD ? i : 0] = load_cached(yr, (l + i * THREADS) * 16);
-            }
+            for (int i = 0; i < kHeld; ++i)
+                sv[i] = sn[i], yv[i] = yn[i], dv[i] = dn[i];
+            load_next(t + step);
+        }
+        float sums[2] = {0.0f, 0.0f};  // of s^2 and of g s
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float s[8], g[8], w[8];
-            unpack8(HOLD ? sv[HOLD ? i : 0] : load_cached(sr, (l + i * THREADS) * 16), s);
-            unpack8(HOLD ? yv[HOLD ? i : 0] : load_cached(yr, (l + i * THREADS) * 16), g);
+            unpack8(vector(sv, sr, i), s);
+            unpack8(vector(yv, yr, i), g);
             weights(i, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 sums[0] = fmaf(s[j], s[j], sums[0]);
                 sums[1] = fmaf(g[j] * w[j], s[j], sums[1]);
             }
+            if (!HOLD)
+                __builtin_amdgcn_sched_barrier(0);  // (all vectors at once would not fit)
         }
         row_sums<THREADS, 2>(sums, red, turn);
         const float n = static_cast<float>(a.H), r = 1.0f / sqrtf(sums[0] / n + a.eps);
         const float back = r * r * (sums[1] / n);  // of s R
+        const __amdgpu_buffer_rsrc_t to = rows_at(a.dx, t);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float s[8], g[8], w[8], d[8];
-            unpack8(HOLD ? sv[HOLD ? i : 0] : load_cached(sr, (l + i * THREADS) * 16), s);
-            unpack8(HOLD ? yv[HOLD ? i : 0] : load_cached(yr, (l + i * THREADS) * 16), g);
-            unpack8(load_cached(dr, (l + i * THREADS) * 16), d);
+            unpack8(vector(sv, sr, i), s);
+            unpack8(vector(yv, yr, i), g);
+            if (a.dsum)
+                unpack8(vector(dv, dr, i), d);
             weights(i, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -255,22 +309,37 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGr
                 const float v = fmaf(g[j] * w[j], r, -x * back);
                 d[j] = a.dsum ? d[j] + v : v;
             }
-            __builtin_amdgcn_raw_buffer_store_b128(pack8(d), to, (l + i * THREADS) * 16, 0, 0);
+            store_vector<STREAM>(to, (l + i * THREADS) * 16, pack8(d));
+            if (!HOLD)
+                __builtin_amdgcn_sched_barrier(0);
         }
         turn ^= 1;
     }
-    if (a.part) {
-        const __amdgpu_buffer_rsrc_t to = row_of(a.part, static_cast<int64_t>(blockIdx.x) * kRows + first, a.H * 4, true);
+    if (!a.part)
+        return;
+    if constexpr (kRows > 1) {  // the waves' sums, wave 0's first, in its registers
+        __shared__ float sums[kRows - 1][VPT][8][kWave];
+        if (first > 0)
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT * 8; ++i)
+                sums[first - 1][i / 8][i % 8][l] = dw[i / 8][i % 8];
+        __syncthreads();
+        if (first > 0)
+            return;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 v;
+        for (int w = 0; w < kRows - 1; ++w)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = __float_as_uint(dw[i][h * 4 + j]);
-                __builtin_amdgcn_raw_buffer_store_b128(v, to, (l + i * THREADS) * 32 + h * 16, 0, 0);
-            }
+            for (int i = 0; i < VPT * 8; ++i)
+                dw[i / 8][i % 8] += sums[w][i / 8][i % 8][l];
+    }
+    const __amdgpu_buffer_rsrc_t to = row_of(a.part, blockIdx.x, a.H * 4, true);
+#pragma unroll
+    for (int i = 0; i < 2 * VPT; ++i) {
+        u32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = __float_as_uint(dw[i / 2][i % 2 * 4 + j]);
+        __builtin_amdgcn_raw_buffer_store_b128(v, to, (l + i / 2 * THREADS) * 32 + i % 2 * 16, 0, 0);
     }
 }
 
@@ -299,12 +368,12 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(const float *__restri
 struct NormTiling {
     int threads, vpt;
 };
-NormTiling norm_tiling(int64_t T, int H)
+NormTiling norm_tiling(int H)
 {
     const int vecs = H / 8;
     NormTiling n{kWave, 1};
     if (vecs > 4 * kWave)
-        n.threads = vecs > 4 * 256 ? 1024 : 256;
+        n.threads = vecs > 4 * 512 ? 1024 : vecs > 4 * 256 ? 512 : 256;
     while (n.threads * n.vpt < vecs)
         n.vpt *= 2;
     return n;
@@ -315,19 +384,32 @@ int norm_groups(int64_t T, int rows, int most)
     return static_cast<int>(n < most ? n : most);
 }
 // Workgroups of the gradient's first kernel.
-int grad_groups(int64_t T, const NormTiling &n) { return norm_groups(T, rows_of(n.threads), n.threads == 1024 ? kCus : 4 * kCus); }
+// One a CU, whose next row is on its way while it works on one, is enough, and more
+// leave more sums to the second kernel (16384 x 7168: 162 us; 173 with two, 177 with
+// four); rows of a wave, four at once, take two (65536 x 1024: 112 us against 116).
+int grad_groups(int64_t T, const NormTiling &n) { return norm_groups(T, rows_of(n.threads), n.threads == kWave ? 2 * kCus : kCus); }
 
 }  // namespace
 
 size_t norm_grad_workspace_bytes(int64_t T, int H)
 {
-    const NormTiling n = norm_tiling(T, H);
-    return static_cast<size_t>(grad_groups(T, n)) * rows_of(n.threads) * H * 4;
+    const NormTiling n = norm_tiling(H);
+    return static_cast<size_t>(grad_groups(T, n)) * H * 4;
 }
 
+// Whether a call's arrays, `bytes` a value, are more than the last-level cache
+// keeps for whoever reads them next: its rows then pass the caches by (16384 x 7168,
+// all outputs: 192 us, 5.5 TB/s, against 206; its gradient 162, 5.8 TB/s, against 191).
+static bool streams(int64_t T, int H, int bytes) { return T * H * bytes > kCacheBytes; }
+
 #define MOE_NORM(THREADS, VPT)                                                                          \
-    if (n.threads == THREADS && n.vpt == VPT)                                                           \
-    add_norm_kernel<THREADS, VPT><<<dim3(norm_groups(T, rows_of(THREADS), THREADS == 1024 ? 2 * kCus : 8 * kCus)), group_of(THREADS), 0, stream>>>(a)
+    if (n.threads == THREADS && n.vpt == VPT) {                                                         \
+        const dim3 grid(norm_groups(T, rows_of(THREADS), THREADS == 1024 ? 2 * kCus : 16 * kCus));       \
+        if (stream_rows)                                                                                \
+            add_norm_kernel<THREADS, VPT, true><<<grid, group_of(THREADS), 0, stream>>>(a);             \
+        else                                                                                            \
+            add_norm_kernel<THREADS, VPT, false><<<grid, group_of(THREADS), 0, stream>>>(a);            \
+    }
 
 hipError_t launch_add_norm(const void *x, const void *residual, const float *weight, float eps, int64_t T, int H,
                            void *sum, void *y, bool blocks, void *codes, float *scales, hipStream_t stream)
@@ -337,21 +419,26 @@ hipError_t launch_add_norm(const void *x, const void *residual, const float *wei
     a.weight = weight, a.eps = eps, a.T = T, a.H = H;
     a.sum = static_cast<uint16_t *>(sum), a.y = static_cast<uint16_t *>(y);
     a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.blocks = blocks;
-    const NormTiling n = norm_tiling(T, H);
-    MOE_NORM(64, 1);
-    MOE_NORM(64, 2);
-    MOE_NORM(64, 4);
-    MOE_NORM(256, 2);
-    MOE_NORM(256, 4);
-    MOE_NORM(1024, 2);
-    MOE_NORM(1024, 4);
-    MOE_NORM(1024, 8);
+    const NormTiling n = norm_tiling(H);
+    const bool stream_rows = streams(T, H, 2 + (residual ? 2 : 0) + (sum ? 2 : 0) + (y ? 2 : 0) + (codes ? 1 : 0));
+    MOE_NORM(64, 1)
+    MOE_NORM(64, 2)
+    MOE_NORM(64, 4)
+    MOE_NORM(256, 2)
+    MOE_NORM(256, 4)
+    MOE_NORM(512, 4)
+    MOE_NORM(1024, 4)
+    MOE_NORM(1024, 8)
     return hipGetLastError();
 }
 
 #define MOE_NORM_GRAD(THREADS, VPT)                                                                     \
-    if (n.threads == THREADS && n.vpt == VPT)                                                           \
-    add_norm_grad_kernel<THREADS, VPT, (VPT < 8)><<<dim3(groups), group_of(THREADS), 0, stream>>>(a)
+    if (n.threads == THREADS && n.vpt == VPT) {                                                         \
+        if (stream_rows)                                                                                \
+            add_norm_grad_kernel<THREADS, VPT, true><<<dim3(groups), group_of(THREADS), 0, stream>>>(a); \
+        else                                                                                            \
+            add_norm_grad_kernel<THREADS, VPT, false><<<dim3(groups), group_of(THREADS), 0, stream>>>(a); \
+    }
 
 hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *sum, const float *weight, float eps,
                                 int64_t T, int H, void *d_x, float *d_weight, bool accumulate, void *workspace,
@@ -361,23 +448,24 @@ hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *
     a.dy = static_cast<const uint16_t *>(d_y), a.dsum = static_cast<const uint16_t *>(d_sum);
     a.sum = static_cast<const uint16_t *>(sum), a.weight = weight, a.eps = eps, a.T = T, a.H = H;
     a.dx = static_cast<uint16_t *>(d_x), a.part = d_weight ? static_cast<float *>(workspace) : nullptr;
-    const NormTiling n = norm_tiling(T, H);
+    const NormTiling n = norm_tiling(H);
     const int groups = grad_groups(T, n);
+    const bool stream_rows = streams(T, H, d_sum ? 8 : 6);
     if (T > 0) {
-        MOE_NORM_GRAD(64, 1);
-        MOE_NORM_GRAD(64, 2);
-        MOE_NORM_GRAD(64, 4);
-        MOE_NORM_GRAD(256, 2);
-        MOE_NORM_GRAD(256, 4);
-        MOE_NORM_GRAD(1024, 2);
-        MOE_NORM_GRAD(1024, 4);
-        MOE_NORM_GRAD(1024, 8);
+        MOE_NORM_GRAD(64, 1)
+        MOE_NORM_GRAD(64, 2)
+        MOE_NORM_GRAD(64, 4)
+        MOE_NORM_GRAD(256, 2)
+        MOE_NORM_GRAD(256, 4)
+        MOE_NORM_GRAD(512, 4)
+        MOE_NORM_GRAD(1024, 4)
+        MOE_NORM_GRAD(1024, 8)
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess)
             return err;
     }
     if (d_weight)
-        norm_weight_kernel<<<dim3((H + 31) / 32), 1024, 0, stream>>>(a.part, groups * rows_of(n.threads), H, accumulate, d_weight);
+        norm_weight_kernel<<<dim3((H + 31) / 32), 1024, 0, stream>>>(a.part, groups, H, accumulate, d_weight);
     return hipGetLastError();
 }
 
