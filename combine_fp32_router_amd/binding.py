@@ -990,10 +990,11 @@ def moe_expert_matmul_fp8(x: torch.Tensor, x_scales: torch.Tensor, offsets: torc
         _want(bias, torch.float32, "bias")
         if bias.numel() != E * wide_n:
             raise ValueError("bias must hold one value per weight row")
-    name = "moe_expert_matmul_fp8"
-    _call_with_room(name, stream, workspace, expert_fp8_workspace_bytes(name, E, rows, K, N, act), x,
-                    x, x_scales, 1 if x_scales.dim() == 1 else x_scales.shape[1], offsets, w,
-                    w_scales, bias, act, residual, E, rows, K, N, out, codes, scales, preact)
+    name = "moe_expert_matmul_fp8"  # whose workspace is for coded results
+    need = 0 if codes is None else expert_fp8_workspace_bytes(name, E, rows, K, N, act)
+    cols = 1 if x_scales.dim() == 1 else x_scales.shape[1]
+    _call_with_room(name, stream, workspace, need, x, x, x_scales, cols, offsets, w, w_scales, bias,
+                    act, residual, E, rows, K, N, out, codes, scales, preact)
 
 
 def moe_expert_matmul_fp8_dx(dy: torch.Tensor, dy_scales: torch.Tensor, offsets: torch.Tensor,

@@ -662,7 +662,7 @@ int moe_expert_matmul_fp8(const void *x, const float *x_scales, int x_scale_cols
         !fp8_tiles_fit(E, max_rows, act == MOE_ACT_SWIGLU ? 2 * N : N) ||
         (x_scale_cols != 1 && x_scale_cols != code_blocks(K)))
         return MOE_ERR_SHAPE;
-    const size_t need = 0;
+    const size_t need = moe::expert_fp8_workspace_bytes(act, E, max_rows, K, N);
     if (!workspace && workspace_bytes) {
         *workspace_bytes = need;
         return MOE_OK;
@@ -686,7 +686,7 @@ int moe_expert_matmul_fp8(const void *x, const float *x_scales, int x_scale_cols
         (preact && preact == residual) || (codes && (scales == x_scales || scales == w_scales)))
         return MOE_ERR_ALIAS;
     return hip_status(moe::launch_expert_fp8(x, x_scales, x_scale_cols, offsets, w, w_scales, bias, act, residual, E,
-                                             max_rows, K, N, out, codes, scales, preact, stream));
+                                             max_rows, K, N, out, codes, scales, preact, workspace, stream));
 }
 
 int moe_expert_matmul_fp8_dx(const void *dy, const float *dy_scales, const int32_t *offsets, const void *w_t,

@@ -4,41 +4,12 @@
 //   dx        g = the same of dy's codes and the transposed weights',  dx = act'(z_prev) g
 //
 // The results leave in bf16, in codes with a scale for each 128, or both.
+#include "fp8_args.hpp"
 #include "fp8_tile.hpp"
 #include "launch.hpp"
 
 namespace moe {
 namespace {
-
-struct Fp8 {
-    const uint8_t *w, *q;   // weights and rows, of `segments` times R bytes
-    const float *ws, *xs;
-    int xs_cols;            // scales of a row: 1, or one a block
-    const int32_t *offsets;
-    int E, max_rows;
-    int R, segments;
-    int C, act;             // output columns (of one half)
-    const float *bias;
-    const uint16_t *residual, *z;
-    void *out;
-    uint16_t *preact;
-    uint8_t *codes;
-    float *scales;
-    int height;             // rows of a tile
-};
-
-// Largest size of a lane's values of a row and of the three lanes' that hold the
-// rest of them.
-template <int BLOCKS>
-__device__ __forceinline__ uint32_t row_top(const f32x4 (&v)[BLOCKS])
-{
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4 * BLOCKS; ++i)
-        top = umax(top, size_bits(v[i / 4][i % 4]));
-    top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-    return umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
-}
 
 // Where a tile's results go: its rows first .. first + n - 1, this wave's columns
 // from c on, `inside` of them (or more) the array's.
@@ -399,14 +370,22 @@ hipError_t launch(Fp8 &a, int64_t max_rows, hipStream_t stream)
 
 hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const int32_t *offsets, const void *w,
                              const float *ws, const float *bias, int act, const void *residual, int E, int64_t max_rows,
-                             int K, int N, void *out, void *codes, float *scales, void *preact, hipStream_t stream)
+                             int K, int N, void *out, void *codes, float *scales, void *preact, void *workspace,
+                             hipStream_t stream)
 {
     Fp8 a{};
     a.q = static_cast<const uint8_t *>(x), a.xs = xs, a.xs_cols = xs_cols, a.offsets = offsets;
     a.w = static_cast<const uint8_t *>(w), a.ws = ws, a.bias = bias, a.act = act;
     a.residual = static_cast<const uint16_t *>(residual), a.E = E, a.R = K, a.segments = 1, a.C = N;
     a.out = out, a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.preact = static_cast<uint16_t *>(preact);
+    if (few_fp8_pay(act, E, max_rows, K, N))
+        return launch_fp8_few(a, max_rows, workspace, stream);
     return act == MOE_ACT_SWIGLU ? launch<kGated>(a, max_rows, stream) : launch<kPlain>(a, max_rows, stream);
+}
+
+size_t expert_fp8_workspace_bytes(int act, int E, int64_t max_rows, int K, int N)
+{
+    return max_rows > 0 && few_fp8_pay(act, E, max_rows, K, N) ? static_cast<size_t>(few_fp8_bytes(E, max_rows, N)) : 0;
 }
 
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,

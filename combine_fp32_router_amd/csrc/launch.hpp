@@ -127,6 +127,8 @@ hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *
                                 hipStream_t stream);
 hipError_t launch_quant_rows(const void *x, const int32_t *offsets, int E, int64_t max_rows, int n, int halves,
                              void *codes, float *scales, hipStream_t stream);
+hipError_t launch_quant_wide_rows(const float *x, const int32_t *offsets, int E, int64_t max_rows, int n, void *codes,
+                                  float *scales, hipStream_t stream);  // of fp32 values
 int64_t quant_weights_groups(int E, int N, int K, int halves);  // of kRouteThreads threads
 hipError_t launch_quant_weights(const void *w, int E, int N, int K, int halves, void *codes, float *scales,
                                 void *codes_t, float *scales_t, hipStream_t stream);
@@ -134,7 +136,12 @@ hipError_t launch_quant_weights(const void *w, int E, int N, int K, int halves, 
 // The experts' products of E4M3 rows and weights, and the gradient of their rows.
 hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const int32_t *offsets, const void *w,
                              const float *ws, const float *bias, int act, const void *residual, int E, int64_t max_rows,
-                             int K, int N, void *out, void *codes, float *scales, void *preact, hipStream_t stream);
+                             int K, int N, void *out, void *codes, float *scales, void *preact, void *workspace,
+                             hipStream_t stream);
+size_t expert_fp8_workspace_bytes(int act, int E, int64_t max_rows, int K, int N);
+// Few rows an expert: whether their kernel pays, and what its coded results need.
+bool few_fp8_pay(int act, int E, int64_t max_rows, int K, int N);
+int64_t few_fp8_bytes(int E, int64_t max_rows, int N);
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
                                 const float *wts, int halves, int act, const void *z, int E, int64_t max_rows, int K,
                                 int N, void *dx, void *codes, float *scales, hipStream_t stream);
@@ -176,6 +183,7 @@ inline int64_t max_row_tiles(int64_t max_rows, int E, int height)
 }
 
 constexpr int kCus = 256;  // of the card
+constexpr int64_t kCacheBytes = 256 << 20;  // of its last-level cache
 
 // Rows and columns of the tiles of a product whose outputs have C columns,
 // `unit` of which make 128 of a tile.  256 x 256 has the best rate; smaller ones

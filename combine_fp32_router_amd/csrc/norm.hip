@@ -79,7 +79,6 @@ __device__ __forceinline__ uint32_t row_top(uint32_t v, uint32_t *red, int turn)
 }
 
 // Rows of a workgroup at once, and its threads.
-constexpr int64_t kCacheBytes = 256 << 20;  // of the last-level cache
 constexpr int rows_of(int threads) { return threads == kWave ? 4 : 1; }
 constexpr int group_of(int threads) { return threads == kWave ? 4 * kWave : threads; }
 
@@ -207,6 +206,8 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int c = l + i * THREADS;
+                if (c / 16 >= nb)  // (zeros; the Coder would take them for scales to divide by)
+                    continue;
                 const float scale = scale_of(a.blocks ? row_umax(top[i]) : all);
                 if (a.blocks && c % 16 == 0 && c * 8 < a.H && live)
                     a.scales[t * nb + c / 16] = scale;

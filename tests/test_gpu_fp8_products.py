@@ -232,3 +232,15 @@ def test_sums_of_near_codes(lengths, K, N, act):
     B.moe_expert_matmul_fp8(x, xs, off, w, ws, None, act, None, out, codes_out, scales[:, 0])
     R.inside(out, y, F.bf16(y, dy), "out")
     F.check_codes(codes_out, scales[:, 0], y, dy, "out")
+
+
+# few rows an expert: with a workspace their coded results take another way
+@pytest.mark.parametrize("lengths,K,N,act", [([1], 400, 144, SILU), ([1, 0, 3, 16, 1], 1040, 272, SWIGLU), ([2] * 9, 272, 2064, NONE),
+                                             ([1] * 8 + [0] * 24, 2064, 768, SWIGLU)])
+def test_few_coded_rows_without_a_workspace(lengths, K, N, act):
+    x, xs, off, w, ws, b, res, out, codes, scales, _ = check_product(lengths, K, N, act, True, True, False, False)
+    rows, E = x.shape[0], len(lengths)
+    assert B.expert_fp8_workspace_bytes("moe_expert_matmul_fp8", E, rows, K, N, act) == rows * N * 4
+    _, c, s = rooms(rows, N)
+    B._call("moe_expert_matmul_fp8", None, x, xs, xs.shape[1], off, w, ws, b, act, res, E, rows, K, N, None, c, s, None, None, None)
+    assert torch.equal(c, codes) and torch.equal(s, scales)
