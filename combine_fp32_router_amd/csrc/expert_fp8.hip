@@ -227,12 +227,7 @@ __device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t
                     const f32x4 z[1] = {get_block(place, c % 4, lane)};
                     if constexpr (SWIGLU) {
                         const f32x4 zu = get_block(place, 4 + c % 4, lane);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float g = z[0][j], x = v[c][j], s = sigmoid(g);
-                            v[c][j] = x * zu[j] * (s * (1.0f + g * (1.0f - s)));
-                            u[c][j] = x * (g * s);
-                        }
+                        swiglu_slopes(v[c], u[c], z[0], zu);
                     } else {
                         f32x4 w[1] = {v[c]};
                         apply_slope(w, z, a.act);
@@ -254,9 +249,6 @@ __device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t
         }
     }
 }
-
-// Forward, of a gated product, dx, dx through SwiGLU.
-enum Kind { kPlain, kGated, kBack, kBackGated };
 
 // A workgroup's walk over its list of tiles.
 template <Kind KIND>
@@ -378,14 +370,15 @@ hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const 
     a.w = static_cast<const uint8_t *>(w), a.ws = ws, a.bias = bias, a.act = act;
     a.residual = static_cast<const uint16_t *>(residual), a.E = E, a.R = K, a.segments = 1, a.C = N;
     a.out = out, a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.preact = static_cast<uint16_t *>(preact);
-    if (few_fp8_pay(act, E, max_rows, K, N))
-        return launch_fp8_few(a, max_rows, workspace, stream);
+    const Kind kind = act == MOE_ACT_SWIGLU ? kGated : kPlain;
+    if (few_fp8_pay(kind == kGated ? 2 : 1, E, max_rows, K, N, false))
+        return launch_fp8_few(kind, a, max_rows, workspace, stream);
     return act == MOE_ACT_SWIGLU ? launch<kGated>(a, max_rows, stream) : launch<kPlain>(a, max_rows, stream);
 }
 
 size_t expert_fp8_workspace_bytes(int act, int E, int64_t max_rows, int K, int N)
 {
-    return max_rows > 0 && few_fp8_pay(act, E, max_rows, K, N) ? static_cast<size_t>(few_fp8_bytes(E, max_rows, N)) : 0;
+    return max_rows > 0 && few_fp8_pay(act == MOE_ACT_SWIGLU ? 2 : 1, E, max_rows, K, N, false) ? static_cast<size_t>(few_fp8_bytes(E, max_rows, N)) : 0;
 }
 
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
@@ -397,6 +390,8 @@ hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t 
     a.w = static_cast<const uint8_t *>(wt), a.ws = wts, a.act = act, a.z = static_cast<const uint16_t *>(z);
     a.E = E, a.R = N, a.segments = halves, a.C = K;
     a.out = dx, a.codes = static_cast<uint8_t *>(codes), a.scales = scales;
+    if (few_fp8_pay(1, E, max_rows, halves * N, K, codes != nullptr))
+        return launch_fp8_few(act == MOE_ACT_SWIGLU ? kBackGated : kBack, a, max_rows, nullptr, stream);
     return act == MOE_ACT_SWIGLU ? launch<kBackGated>(a, max_rows, stream) : launch<kBack>(a, max_rows, stream);
 }
 

@@ -18,26 +18,28 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-template <bool GATED, int CW>
+template <Kind KIND, int CW>
 __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
 {
-    constexpr int wide = GATED ? 2 : 1, kDepth = 4;
-    __shared__ uint32_t tops[CW][16];
+    constexpr bool GATED = KIND == kGated, BOTH = KIND == kBackGated;
+    constexpr int wide = GATED ? 2 : 1, out = BOTH ? 2 : 1, kDepth = 4;  // halves of the weights, of the results
+    __shared__ uint32_t tops[out][CW][16];
     const int lane = lane_id(), w = static_cast<int>(uniform(threadIdx.x / kWave));
     const int groups = (a.C + 16 * CW - 1) / (16 * CW), nbc = code_blocks(a.C);
     const RowTile t = find_row_tile(a.offsets, a.E, a.max_rows, 16, blockIdx.x / groups);
     if (t.n <= 0)
         return;
-    const int c0 = blockIdx.x % groups * (16 * CW) + w * 16, steps = code_blocks(a.R);
+    const int c0 = blockIdx.x % groups * (16 * CW) + w * 16;
+    const int pitch = a.R * a.segments, blocks = code_blocks(a.R), steps = blocks * a.segments;
     const bool inside = c0 < a.C;  // of the array; a.C is a multiple of 16
     __amdgpu_buffer_rsrc_t wr[wide], wsr[wide];
 #pragma unroll
     for (int g = 0; g < wide; ++g) {
         const int64_t half = static_cast<int64_t>(t.e) * wide + g;
-        wr[g] = row_rsrc(const_cast<uint8_t *>(a.w) + (half * a.C + c0) * a.R, inside ? 16 * a.R : 0);
+        wr[g] = row_rsrc(const_cast<uint8_t *>(a.w) + (half * a.C + c0) * pitch, inside ? 16 * pitch : 0);
         wsr[g] = row_rsrc(const_cast<float *>(a.ws) + (half * nbc + c0 / kCodeBlock) * steps, inside ? steps * 4 : 0);
     }
-    const __amdgpu_buffer_rsrc_t xr = row_rsrc(const_cast<uint8_t *>(a.q) + static_cast<int64_t>(t.first) * a.R, t.n * a.R);
+    const __amdgpu_buffer_rsrc_t xr = row_rsrc(const_cast<uint8_t *>(a.q) + static_cast<int64_t>(t.first) * pitch, t.n * pitch);
     const __amdgpu_buffer_rsrc_t xsr =
         row_rsrc(const_cast<float *>(a.xs) + static_cast<int64_t>(t.first) * a.xs_cols, t.n * a.xs_cols * 4);
     const int row = lane % 16, at = lane / 16 * 16, xs_step = a.xs_cols == 1 ? 0 : 4;
@@ -48,10 +50,11 @@ __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
     };
     Block ring[kDepth];
     auto load = [&](Block &b, int k) {
-        const int r = k * kCodeBlock + at;
+        const int segment = k < blocks ? 0 : a.R;  // of at most two
+        const int r = (k < blocks ? k : k - blocks) * kCodeBlock + at;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int o = r + 64 * h < a.R ? row * a.R + r + 64 * h : kOutside;
+            const int o = k < steps && r + 64 * h < a.R ? row * pitch + segment + r + 64 * h : kOutside;
 #pragma unroll
             for (int g = 0; g < wide; ++g)
                 b.w[g][h] = load_cached(wr[g], o);  // (past the caches, the line's second half comes from memory again: 85 us)
@@ -89,66 +92,90 @@ __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
     const int c = c0 + lane / 16 * 4;
     const bool live = inside && row < t.n;
     const int64_t r = t.first + row;
+    auto load4 = [](const uint16_t *p) { return widen4(*reinterpret_cast<const u32x2 *>(p)); };
     auto store4 = [](uint16_t *p, f32x4 f) { *reinterpret_cast<u32x2 *>(p) = round4(f); };
-#pragma unroll
-    for (int g = 0; g < wide; ++g) {
-        if (a.bias && live)
-            acc[g] += *reinterpret_cast<const f32x4 *>(a.bias + (static_cast<int64_t>(t.e) * wide + g) * a.C + c);
-        if (a.preact && live)
-            store4(a.preact + (r * wide + g) * a.C + c, acc[g]);
-    }
-    f32x4 y[1] = {acc[0]};
-    if (GATED) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            y[0][j] *= sigmoid(y[0][j]) * acc[wide - 1][j];
+    f32x4 y[out][1] = {};
+    y[0][0] = acc[0];
+    if constexpr (KIND == kBack) {
+        if (a.act != MOE_ACT_NONE && live) {
+            const f32x4 z[1] = {load4(a.z + r * a.C + c)};
+            apply_slope(y[0], z, a.act);
+        }
+    } else if constexpr (BOTH) {
+        if (live) {
+            const f32x4 g = load4(a.z + r * 2 * a.C + c), u = load4(a.z + (r * 2 + 1) * a.C + c);
+            swiglu_slopes(y[0][0], y[1][0], g, u);
+        }
     } else {
-        apply_act(y, a.act);
-    }
-    if (a.residual && live)
-        y[0] += widen4(*reinterpret_cast<const u32x2 *>(a.residual + r * a.C + c));
-    if (a.out && live)
-        store4(static_cast<uint16_t *>(a.out) + r * a.C + c, y[0]);
-    if (a.wide_out && live)
-        *reinterpret_cast<f32x4 *>(a.wide_out + r * a.C + c) = y[0];
-    if constexpr (CW == 8) {
-        const uint32_t mine = row_top(y);
-        tops[w][row] = inside ? mine : 0u;  // (four lanes of a row, the same value)
-        __syncthreads();
-        uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < CW; ++i)
-            top = umax(top, tops[i][row]);
-        const float scale = scale_of(top);
-        const uint32_t q = Coder(scale).codes4(y[0][0], y[0][1], y[0][2], y[0][3]);
-        if (!live)
-            return;
-        *reinterpret_cast<uint32_t *>(a.codes + r * a.C + c) = q;
-        if (w == 0 && lane < 16)
-            a.scales[r * nbc + c0 / kCodeBlock] = scale;
+        for (int g = 0; g < wide; ++g) {
+            if (a.bias && live)
+                acc[g] += *reinterpret_cast<const f32x4 *>(a.bias + (static_cast<int64_t>(t.e) * wide + g) * a.C + c);
+            if (a.preact && live)
+                store4(a.preact + (r * wide + g) * a.C + c, acc[g]);
+        }
+        y[0][0] = acc[0];
+        if (GATED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[0][0][j] *= sigmoid(y[0][0][j]) * acc[wide - 1][j];
+        } else {
+            apply_act(y[0], a.act);
+        }
+        if (a.residual && live)
+            y[0][0] += load4(a.residual + r * a.C + c);
+        if (a.wide_out && live)
+            *reinterpret_cast<f32x4 *>(a.wide_out + r * a.C + c) = y[0][0];
+    }
+#pragma unroll
+    for (int o = 0; o < out; ++o)
+        if (a.out && live)
+            store4(static_cast<uint16_t *>(a.out) + (r * out + o) * a.C + c, y[o][0]);
+    if constexpr (CW == 8) {
+#pragma unroll
+        for (int o = 0; o < out; ++o) {
+            const uint32_t mine = row_top(y[o]);
+            tops[o][w][row] = live ? mine : 0u;  // (four lanes of a row, the same value)
+        }
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < out; ++o) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < CW; ++i)
+                top = umax(top, tops[o][i][row]);
+            const float scale = scale_of(top);
+            const uint32_t q = Coder(scale).codes4(y[o][0][0], y[o][0][1], y[o][0][2], y[o][0][3]);
+            if (!live)
+                continue;
+            *reinterpret_cast<uint32_t *>(a.codes + (r * out + o) * a.C + c) = q;
+            if (w == 0 && lane < 16)
+                a.scales[(r * out + o) * nbc + c0 / kCodeBlock] = scale;
+        }
     }
 }
 
-template <bool GATED, int CW>
+template <Kind KIND, int CW>
 void launch(const Fp8 &a, int64_t tiles, hipStream_t stream)
 {
-    fp8_few_kernel<GATED, CW><<<dim3(static_cast<unsigned>(tiles * ((a.C + 16 * CW - 1) / (16 * CW)))), 64 * CW, 0, stream>>>(a);
+    fp8_few_kernel<KIND, CW><<<dim3(static_cast<unsigned>(tiles * ((a.C + 16 * CW - 1) / (16 * CW)))), 64 * CW, 0, stream>>>(a);
 }
-template <bool GATED>
+template <Kind KIND>
 hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
 {
     const int64_t tiles = max_row_tiles(max_rows, a.E, 16);
     uint8_t *codes = a.codes;
+    a.max_rows = static_cast<int>(max_rows);
     if (codes && !(workspace && few_fp8_bytes(a.E, max_rows, a.C))) {
-        launch<GATED, 8>(a, tiles, stream);
+        launch<KIND, 8>(a, tiles, stream);
         return hipGetLastError();
     }
     a.codes = nullptr;
     a.wide_out = codes ? static_cast<float *>(workspace) : nullptr;
     if (tiles * ((a.C + 63) / 64) >= kCus)
-        launch<GATED, 4>(a, tiles, stream);
+        launch<KIND, 4>(a, tiles, stream);
     else
-        launch<GATED, 1>(a, tiles, stream);
+        launch<KIND, 1>(a, tiles, stream);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !codes)
         return err;
@@ -157,36 +184,45 @@ hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
 
 }  // namespace
 
-int64_t few_fp8_bytes(int E, int64_t max_rows, int N)
+int64_t few_fp8_bytes(int E, int64_t max_rows, int C)
 {
-    return max_row_tiles(max_rows, E, 16) * code_blocks(N) < kCus ? max_rows * N * 4 : 0;
+    return max_row_tiles(max_rows, E, 16) * code_blocks(C) < kCus ? max_rows * C * 4 : 0;
 }
 
 // Estimates in us.  Here: the weights once from memory at 6 TB/s, again for every
 // further 16 rows and the rows for every 16 columns from the caches at 11, and 3.  The
-// tiles: 4 and 0.75 a block of 128 for each round of them, or the weights at 5.6 TB/s
-// and 3 if that is longer.  Measured (here / tiles): one token of 8 experts above 44 /
+// tiles: 6, and 1 and 0.8 a block of 128 for each round of them, or the weights at 5.6
+// TB/s and 3 if that is longer.  Measured (here / tiles): one token of 8 experts above 44 /
 // 63; 4 rows of each of 32, 7168 -> 2048 gated 158 / 166, 2048 -> 7168 90 / 98; 16 rows
 // of each 119 / 99; 2 of each of 64, 1024 -> 4096 57 / 64; 1 or 16 rows of one, 4096 ->
-// 4096 9.5 / 28.
-bool few_fp8_pay(int act, int E, int64_t max_rows, int K, int N)
+// 4096 9.5 / 28.  Codes without a workspace (whole_blocks: dx) also take what a
+// workgroup's 128 columns do at 30 GB/s: 16 rows of one, 4096 <- 4096, 38 / 30.  dx else:
+// 515 rows of 8, 272 <- 512, 10 / 14; one token of 8, 7168 <- 2 x 2048, 58 / 61; 2 of
+// each of 64, 4096 <- 1024, 66 / 88; 16 of each of 32, 7168 <- 2 x 2048, 274 / 181.
+bool few_fp8_pay(int wide, int E, int64_t max_rows, int R, int C, bool whole_blocks)
 {
-    const int wide = act == MOE_ACT_SWIGLU ? 2 : 1;
     const int64_t live = max_rows < E ? max_rows : E, tiles = max_row_tiles(max_rows, E, 16);
-    if (!grid_fits(tiles * (N / 16), 64))
+    if (!grid_fits(tiles * code_blocks(C), 512))  // (the largest of its three)
         return false;
-    const double each = 1.0 * wide * N * K, weights = live * each;
-    const double here = weights / 6e6 + ((tiles - live) * each + (N / 16.0) * max_rows * K) / 11e6 + 3;
+    const double each = 1.0 * wide * C * R, weights = live * each;
+    double here = weights / 6e6 + ((tiles - live) * each + (C / 16.0) * max_rows * R) / 11e6 + 3;
+    const double group = R * 128.0 * (wide + (max_rows < 16 ? max_rows / 16.0 : 1)) / 3e4 + 3;  // of a workgroup
+    if (whole_blocks && here < group)
+        here = group;
     const int cols = 256 / wide;
-    const int64_t coarse = max_row_tiles(max_rows, E, 64) * ((N + cols - 1) / cols);
-    const double there = ((coarse + kCus - 1) / kCus) * (4 + code_blocks(K) * 0.75);
+    const int64_t coarse = max_row_tiles(max_rows, E, 64) * ((C + cols - 1) / cols);
+    const double there = ((coarse + kCus - 1) / kCus) * (1 + code_blocks(R) * 0.8) + 6;
     return here < (there > weights / 5.6e6 + 3 ? there : weights / 5.6e6 + 3);
 }
 
-hipError_t launch_fp8_few(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
+hipError_t launch_fp8_few(Kind kind, Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
 {
-    a.max_rows = static_cast<int>(max_rows);
-    return a.act == MOE_ACT_SWIGLU ? launch<true>(a, max_rows, workspace, stream) : launch<false>(a, max_rows, workspace, stream);
+    switch (kind) {
+    case kPlain: return launch<kPlain>(a, max_rows, workspace, stream);
+    case kGated: return launch<kGated>(a, max_rows, workspace, stream);
+    case kBack: return launch<kBack>(a, max_rows, nullptr, stream);
+    default: return launch<kBackGated>(a, max_rows, nullptr, stream);
+    }
 }
 
 }  // namespace moe

@@ -6,6 +6,9 @@
 
 namespace moe {
 
+// Forward, of a gated product, dx, dx through SwiGLU.
+enum Kind { kPlain, kGated, kBack, kBackGated };
+
 struct Fp8 {
     const uint8_t *w, *q;   // weights and rows, of `segments` times R bytes
     const float *ws, *xs;
@@ -24,8 +27,11 @@ struct Fp8 {
     float *wide_out;        // few rows: results in fp32, to be coded
 };
 
-// The products for few rows an expert; workspace: few_fp8_bytes, or null.
-hipError_t launch_fp8_few(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream);
+// The products for few rows an expert, and whether they pay: `wide` halves of
+// weights, C columns, sums over R in all; whole_blocks: codes are wanted, and there is
+// no workspace.  workspace: few_fp8_bytes, or null (dx: null).
+bool few_fp8_pay(int wide, int E, int64_t max_rows, int R, int C, bool whole_blocks);
+hipError_t launch_fp8_few(Kind kind, Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream);
 
 // Largest size of a lane's values of a row and of the three lanes' that hold the
 // rest of them.
@@ -38,6 +44,17 @@ __device__ __forceinline__ uint32_t row_top(const f32x4 (&v)[BLOCKS])
         top = umax(top, size_bits(v[i / 4][i % 4]));
     top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
     return umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+}
+
+// Gradients of silu(gate) * up: of the gate's inputs into d, of the up half's into du.
+__device__ __forceinline__ void swiglu_slopes(f32x4 &d, f32x4 &du, const f32x4 &gate, const f32x4 &up)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float g = gate[j], x = d[j], s = sigmoid(g);
+        d[j] = x * up[j] * (s * (1.0f + g * (1.0f - s)));
+        du[j] = x * (g * s);
+    }
 }
 
 }  // namespace moe

@@ -140,7 +140,6 @@ hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const 
                              hipStream_t stream);
 size_t expert_fp8_workspace_bytes(int act, int E, int64_t max_rows, int K, int N);
 // Few rows an expert: whether their kernel pays, and what its coded results need.
-bool few_fp8_pay(int act, int E, int64_t max_rows, int K, int N);
 int64_t few_fp8_bytes(int E, int64_t max_rows, int N);
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
                                 const float *wts, int halves, int act, const void *z, int E, int64_t max_rows, int K,
