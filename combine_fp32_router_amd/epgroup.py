@@ -15,7 +15,9 @@ through the reverse exchange, and every source combines its own tokens
 An ``ExpertMLP`` takes and gives bf16 rows.  Between it and a quantised
 payload the regroup dequantises in the same pass, as a combine of one slot of
 weight 1 over the row map (each row rounded once to bf16), and the ungroup
-quantises, as a pack of one slot.
+quantises, as a pack of one slot.  An ``ExpertMLP8`` takes the rows of an E4M3
+payload as they are: codes and their scales are regrouped, nothing is
+dequantised (but for the weights' gradients, if it trains).
 
 With ``train=True`` experts, ``backward`` runs the last ``run``'s layer the
 other way: the combine's gradient at every source, the exchange, the regroup,
@@ -39,7 +41,7 @@ import torch
 from . import binding as B
 from . import harness as HN
 from .driver import KernelTimer, chunk_capacity, chunk_ranges
-from .experts import ExpertGrads, ExpertMLP
+from .experts import ExpertGrads, ExpertMLP, ExpertMLP8
 
 
 def _group_device(call):
@@ -200,16 +202,25 @@ class EPGroup:
                                                     self.recv_scales, st))
 
     def _run_experts(self, quant, timed, st):
-        """Regroup to bf16, the experts, and ungroup to the payload's format."""
+        """Regroup to bf16 (E4M3 rows for experts of such: as they are), the
+        experts, and ungroup to the payload's format."""
         H, M, rl = self.H, self.max_rows, self.rl
-        x, y = self.expert_in, self.expert_out
+        x, y, coded = self.expert_in, self.expert_out, {}
+        rows8 = quant == B.MOE_QUANT_FP8 and isinstance(self.experts, ExpertMLP8)
+        if rows8:
+            timed("regroup", lambda: B.moe_recv_regroup(
+                self.recv, self.recv_scales, M, H, quant, rl.group_src, self.grouped,
+                self.grouped_scales, st))
         if quant == B.MOE_QUANT_BF16:
             timed("regroup", lambda: B.moe_recv_regroup(self.recv, None, M, H, quant, rl.group_src,
                                                         x, None, st))
-        else:
+        elif not rows8 or self.experts.train:
             timed("regroup", lambda: B.moe_combine(self.recv, self.recv_scales, quant,
                                                    rl.group_src, self.ones, M, H, 1, x, st))
-        timed("experts", lambda: self.experts.forward(x, rl.group_offsets, y, stream=st))
+        if rows8:
+            x = self.grouped.view(-1)[:M * H].view(torch.float8_e4m3fn).view(M, H)
+            coded["scales"] = self.grouped_scales[:M]
+        timed("experts", lambda: self.experts.forward(x, rl.group_offsets, y, stream=st, **coded))
         if quant == B.MOE_QUANT_BF16:
             timed("ungroup", lambda: B.moe_recv_ungroup(y, None, M, H, quant, rl.group_pos,
                                                         self.recv, None, st))

@@ -7,6 +7,7 @@ over one contiguous run of rows per expert (the receiver's grouped rows).
 bf16 rows and weights, fp32 sums; h and y are rounded once each.  With
 ``train`` the forward call also keeps z = x W_up^T + b_up (bf16), and
 ``backward`` gives the gradients of the rows, the weights and the biases.
+ExpertMLP8 is the same layer with its products in E4M3 codes.
 All arithmetic runs in the HIP library; this module allocates (torch) and
 orders launches.
 """
@@ -112,11 +113,94 @@ class ExpertMLP:
             raise ValueError(f"backward of {n} rows, the last forward had {self._kept}")
         if forward is not None and forward != self.forwards:
             raise ValueError("the experts have run again since that forward")
-        hidden, dz = self.hidden[:n], self.d_preact[:n]
-        B.moe_expert_matmul_dx(d_out, offsets, self.w_down, self.act, self.preact[:n], dz, stream)
+        self._through_down(d_out, offsets, n, grads is not None, d_x is not None, stream)
         if grads is not None:
-            B.moe_expert_matmul_dw(d_out, hidden, offsets, grads.w_down, grads.b_down, accumulate,
-                                   stream)
-            B.moe_expert_matmul_dw(dz, x, offsets, grads.w_up, grads.b_up, accumulate, stream)
+            B.moe_expert_matmul_dw(d_out, self.hidden[:n], offsets, grads.w_down, grads.b_down,
+                                   accumulate, stream)
+            B.moe_expert_matmul_dw(self.d_preact[:n], x, offsets, grads.w_up, grads.b_up,
+                                   accumulate, stream)
         if d_x is not None:
-            B.moe_expert_matmul_dx(dz, offsets, self.w_up, B.MOE_ACT_NONE, None, d_x, stream)
+            self._through_up(offsets, n, d_x, stream)
+
+    def _through_down(self, d_out, offsets, n, for_grads, for_x, stream):
+        """d_preact from d_out, for the parameters' gradients and for the rows'."""
+        B.moe_expert_matmul_dx(d_out, offsets, self.w_down, self.act, self.preact[:n],
+                               self.d_preact[:n], stream)
+
+    def _through_up(self, offsets, n, d_x, stream):
+        """d_x from d_preact."""
+        B.moe_expert_matmul_dx(self.d_preact[:n], offsets, self.w_up, B.MOE_ACT_NONE, None, d_x,
+                               stream)
+
+
+class ExpertMLP8(ExpertMLP):
+    """The experts with E4M3 rows and weights in the products of `forward` and of
+    the rows' gradients: a scale for each 1 x 128 of a row and 128 x 128 of a weight,
+    fp32 sums.  h goes from one product to the next as codes; the weights'
+    gradients are bf16 products, of bf16 rows, and a quantisation counts as the
+    identity.
+
+    The codes are those that the weights had when it was made: after a change
+    of w_up or w_down, `quantize` takes them again."""
+
+    def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, act: int,
+                 b_up: torch.Tensor | None = None, b_down: torch.Tensor | None = None,
+                 max_rows: int = 0, train: bool = False):
+        super().__init__(w_up, w_down, act, b_up, b_down, max_rows, train)
+        E, H, I, wide, dev = self.E, self.H, self.I, self.wide, self.device
+        nbh, nbi = B.code_blocks(H), B.code_blocks(I)
+
+        def coded(codes, scales):
+            return (torch.empty(codes, dtype=torch.float8_e4m3fn, device=dev),
+                    torch.empty(scales, dtype=torch.float32, device=dev))
+
+        self.up8 = coded((E, wide * I, H), (E, wide, nbi, nbh))
+        self.down8 = coded((E, H, I), (E, 1, nbh, nbi))
+        self.up8_t = coded((E, H, wide * I), (E, nbh, wide, nbi)) if train else (None, None)
+        self.down8_t = coded((E, I, H), (E, nbi, 1, nbh)) if train else (None, None)
+        self.x8 = coded((max_rows, H), (max_rows, nbh))  # d_out's, in a backward call
+        self.hidden8 = coded((max_rows, I), (max_rows, nbi))
+        self.d_preact8 = coded((max_rows, wide * I), (max_rows, wide, nbi)) if train else None
+        if not train:
+            self.hidden = None
+        if dev.type == "cuda":
+            self.quantize()
+
+    def quantize(self, stream=None) -> None:
+        """The weights' codes, from w_up and w_down as they are now."""
+        B.moe_quant_weights(self.w_up, *self.up8, *self.up8_t, self.wide, stream)
+        B.moe_quant_weights(self.w_down, *self.down8, *self.down8_t, 1, stream)
+
+    def forward(self, x: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor,
+                residual: torch.Tensor | None = None, stream=None,
+                scales: torch.Tensor | None = None) -> torch.Tensor:
+        """ExpertMLP.forward; with `scales` (fp32 [rows], one a row, or [rows, ceil(H /
+        128)]) x is E4M3 codes [rows, H]."""
+        n = self._rows(x, "x")
+        B._want_bf16(out, (n, self.H), "out")
+        h8, hs = self.hidden8[0][:n], self.hidden8[1][:n]
+        self.forwards += 1
+        self._kept = None
+        if scales is None:
+            bf16, (x, scales) = x, (t[:n] for t in self.x8)
+            B.moe_quant_rows(bf16, x, scales, offsets, 1, stream)
+        B.moe_expert_matmul_fp8(x, scales, offsets, *self.up8, self.b_up, self.act, None,
+                                self.hidden[:n] if self.train else None, h8, hs,
+                                self.preact[:n] if self.train else None, stream)
+        B.moe_expert_matmul_fp8(h8, hs, offsets, *self.down8, self.b_down, B.MOE_ACT_NONE,
+                                residual, out, stream=stream)
+        self._kept = n
+        return out
+
+    def _through_down(self, d_out, offsets, n, for_grads, for_x, stream):
+        if not (for_grads or for_x):
+            return
+        d8, dz8 = [t[:n] for t in self.x8], [t[:n] for t in self.d_preact8]
+        B.moe_quant_rows(d_out, *d8, offsets, 1, stream)
+        B.moe_expert_matmul_fp8_dx(*d8, offsets, *self.down8_t, self.act, self.preact[:n],
+                                   self.d_preact[:n] if for_grads else None,
+                                   *(dz8 if for_x else (None, None)), stream)
+
+    def _through_up(self, offsets, n, d_x, stream):
+        B.moe_expert_matmul_fp8_dx(*(t[:n] for t in self.d_preact8), offsets, *self.up8_t,
+                                   B.MOE_ACT_NONE, None, d_x, stream=stream)
