@@ -8,6 +8,8 @@
 #include "fp8_tile.hpp"
 #include "launch.hpp"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -92,163 +94,221 @@ __device__ __forceinline__ void store_scale(const Fp8 &a, const Where &at, int r
         a.scales[((static_cast<int64_t>(at.first) + r) * halves + half) * code_blocks(a.C) + at.c / kCodeBlock] = scale;
 }
 
+// What a tile's results take from memory, a piece of 16 rows by 64 columns (of one or
+// two arrays) after the other, kDepth of them ahead.  The first are asked for in
+// front of the next tile's first loads: behind them, they would come after them.
+template <int ARRAYS, int PIECES>
+struct Ahead {
+    static constexpr int kDepth = PIECES == 2 ? 2 : 1;  // (more blocks of rows leave no room for it)
+    u32x4 v[kDepth][ARRAYS][2];
+};
+
 // Forward: bias, pre-activations, activation, residual.  The accumulators are
 // changed in place, a block of 64 rows after the other: beside 128 of them there is
 // no room for copies, nor for addresses kept from one 64 columns to the next (hence
 // the lane as a value of its own in each).  GATED: blocks 0, 1, 4, 5 are the gate's,
 // 2, 3, 6, 7 the up half's.
 template <bool GATED, int NB>
-__device__ __forceinline__ void finish_forward(const Fp8 &a, const CodeTile<GATED> &t,
-                                               const typename CodeTile<GATED>::template Regs<NB> &f, const Where &at,
-                                               MOE_LDS char *lds)
-{
-    constexpr int kHalves = GATED ? 1 : 2, wide = GATED ? 2 : 1;  // of 64 columns
-    MOE_LDS char *place = t.out_place(lds);
-    int lane = at.lane;
-    u32x4 ahead[2];  // the residual's next 16 rows
-    auto load = [&](int row, int right) {
-        if (a.residual)
-            Part(at, a.residual, a.C, 2, at.c + 64 * right, at.inside - 64 * right).template load<8>(at, row, lane, ahead);
-    };
-    load(t.row0(0), 0);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        if (b * 64 >= at.n)
-            break;
-        const int row = t.row0(b);
-        f32x4 y[4 * kHalves];
-#pragma unroll
-        for (int right = 0; right < kHalves; ++right) {
-            asm volatile("" : "+v"(lane));
-            f32x4 g[4], u[GATED ? 4 : 1];
-            const float *bias = a.bias + static_cast<int64_t>(at.e) * wide * a.C + at.c + 64 * right + lane / 16 * 4;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                g[i] = f.acc[GATED ? i / 2 * 4 + i % 2 : right * 4 + i][b];
-                if (GATED)
-                    u[i] = f.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
-                if (a.bias && right * 64 + i * 16 < at.inside) {
-                    g[i] += *reinterpret_cast<const f32x4 *>(bias + i * 16);
-                    if (GATED)
-                        u[i] += *reinterpret_cast<const f32x4 *>(bias + a.C + i * 16);
-                }
-            }
-            if (a.preact) {
-                put_bf16(place, g, lane);
-                Part(at, a.preact, wide * a.C, 2, at.c + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
-                if (GATED) {
-                    put_bf16(place, u, lane);
-                    Part(at, a.preact, wide * a.C, 2, at.c + a.C, at.inside).template store<8>(at, row, lane, place);
-                }
-            }
-            if (GATED) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    g[i / 4][i % 4] *= sigmoid(g[i / 4][i % 4]) * u[GATED ? i / 4 : 0][i % 4];
-            } else {
-                apply_act(g, a.act);
-            }
-            if (a.residual) {
-                put_pieces(place, ahead, 0, lane);
-                // (in front of this block's stores: waiting for it is then not waiting for them)
-                load(right == kHalves - 1 ? t.row0(min(b + 1, NB - 1)) : row, (right + 1) % kHalves);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    g[i] += get_block(place, i, lane);
-            }
-            if (a.out) {
-                put_bf16(place, g, lane);
-                Part(at, a.out, a.C, 2, at.c + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                y[right * 4 + i] = g[i];
-        }
-        if (a.codes) {
-            asm volatile("" : "+v"(lane));
-            uint32_t top = row_top(y);
-            if (GATED)
-                top = t.both_halves(lds, b, top, lane);
-            const float scale = scale_of(top);
-            put_codes(place, y, scale, lane);
-            Part(at, a.codes, a.C, 1, at.c, at.inside).template store<4 * kHalves>(at, row, lane, place);
-            if (!GATED || t.col0() == 0)
-                store_scale(a, at, row, 1, 0, scale, lane);
+struct Forward {
+    static constexpr int kHalves = GATED ? 1 : 2, wide = GATED ? 2 : 1;  // of 64 columns
+    typedef CodeTile<GATED> T;
+    const Fp8 &a;
+    const T &t;
+    const Where &at;
+    Ahead<1, NB * kHalves> ahead;
+    static constexpr bool kKept = NB < 4;  // the bias, for all of the tile
+    f32x4 bias[kKept ? 8 : 1];
+
+    // Of 16 columns: block i of the wave's, or of the up half's after the gate's four.
+    __device__ __forceinline__ f32x4 bias_of(int i, int lane) const
+    {
+        const __amdgpu_buffer_rsrc_t r = row_rsrc(
+            const_cast<float *>(a.bias) + static_cast<int64_t>(at.e) * wide * a.C + at.c, max(0, at.inside + (wide - 1) * a.C) * 4);
+        const int c = (GATED ? i % 4 : i) * 16;
+        return __builtin_bit_cast(f32x4, load_cached(r, c < at.inside ? (c + lane / 16 * 4 + (GATED ? i / 4 * a.C : 0)) * 4 : kOutside));
+    }
+    __device__ __forceinline__ void load(int piece, int lane)
+    {
+        if (piece < NB * kHalves && a.residual) {
+            const int right = piece % kHalves;
+            Part(at, a.residual, a.C, 2, at.c + 64 * right, at.inside - 64 * right)
+                .template load<8>(at, t.row0(piece / kHalves), lane, ahead.v[piece % ahead.kDepth][0]);
         }
     }
-}
+    __device__ __forceinline__ void begin()
+    {
+#pragma unroll
+        for (int i = 0; i < ahead.kDepth; ++i)
+            load(i, at.lane);
+        if (kKept && a.bias)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                bias[kKept ? i : 0] = bias_of(i, at.lane);
+    }
+
+    __device__ __forceinline__ void finish(const typename T::template Regs<NB> &f, MOE_LDS char *lds)
+    {
+        MOE_LDS char *place = t.out_place(lds);
+        int lane = at.lane;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (b * 64 >= at.n)
+                break;
+            const int row = t.row0(b);
+            f32x4 y[4 * kHalves];
+#pragma unroll
+            for (int right = 0; right < kHalves; ++right) {
+                asm volatile("" : "+v"(lane));
+                f32x4 g[4], u[GATED ? 4 : 1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    g[i] = f.acc[GATED ? i / 2 * 4 + i % 2 : right * 4 + i][b];
+                    if (GATED)
+                        u[i] = f.acc[(i / 2 * 4 + i % 2 + 2) % 8][b];
+                    if (a.bias) {
+                        g[i] += kKept ? bias[kKept ? right * 4 + i : 0] : bias_of(right * 4 + i, lane);
+                        if (GATED)
+                            u[i] += kKept ? bias[kKept ? 4 + i : 0] : bias_of(4 + i, lane);
+                    }
+                }
+                if (a.preact) {
+                    put_bf16(place, g, lane);
+                    Part(at, a.preact, wide * a.C, 2, at.c + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
+                    if (GATED) {
+                        put_bf16(place, u, lane);
+                        Part(at, a.preact, wide * a.C, 2, at.c + a.C, at.inside).template store<8>(at, row, lane, place);
+                    }
+                }
+                if (GATED) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        g[i / 4][i % 4] *= sigmoid(g[i / 4][i % 4]) * u[GATED ? i / 4 : 0][i % 4];
+                } else {
+                    apply_act(g, a.act);
+                }
+                if (a.residual) {
+                    const int piece = b * kHalves + right;
+                    put_pieces(place, ahead.v[piece % ahead.kDepth][0], 0, lane);
+                    // (in front of this block's stores: waiting for it is then not waiting for them)
+                    load(piece + ahead.kDepth, lane);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        g[i] += get_block(place, i, lane);
+                }
+                if (a.out) {
+                    put_bf16(place, g, lane);
+                    Part(at, a.out, a.C, 2, at.c + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[right * 4 + i] = g[i];
+            }
+            if (a.codes) {
+                asm volatile("" : "+v"(lane));
+                uint32_t top = row_top(y);
+                if (GATED)
+                    top = t.both_halves(lds, b, top, lane);
+                const float scale = scale_of(top);
+                put_codes(place, y, scale, lane);
+                Part(at, a.codes, a.C, 1, at.c, at.inside).template store<4 * kHalves>(at, row, lane, place);
+                if (!GATED || t.col0() == 0)
+                    store_scale(a, at, row, 1, 0, scale, lane);
+            }
+        }
+    }
+};
 
 // dx: through the activation that made the product's input (SWIGLU: MOE_ACT_SWIGLU).
 template <bool SWIGLU, int NB>
-__device__ __forceinline__ void finish_dx(const Fp8 &a, const CodeTile<false> &t, const CodeTile<false>::Regs<NB> &f,
-                                          const Where &at, MOE_LDS char *lds)
-{
-    MOE_LDS char *place = t.out_place(lds);
-    const int cols = SWIGLU ? 2 * a.C : a.C;
-    int lane = at.lane;
-    u32x4 ahead[2], ahead_up[2];
-    auto load = [&](int row, int right) {
-        if (SWIGLU || a.act != MOE_ACT_NONE)
-            Part(at, a.z, cols, 2, at.c + 64 * right, at.inside - 64 * right).template load<8>(at, row, lane, ahead);
-        if (SWIGLU)
-            Part(at, a.z, cols, 2, at.c + a.C + 64 * right, at.inside - 64 * right).template load<8>(at, row, lane, ahead_up);
-    };
-    auto store = [&](const f32x4 *v, int row, int right, int half) {
-        put_bf16(place, v, lane);
-        Part(at, a.out, cols, 2, at.c + half * a.C + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
-    };
-    auto store_coded = [&](const f32x4 (&v)[8], int row, int half) {
-        asm volatile("" : "+v"(lane));
-        const float scale = scale_of(row_top(v));
-        put_codes(place, v, scale, lane);
-        Part(at, a.codes, cols, 1, at.c + half * a.C, at.inside).template store<8>(at, row, lane, place);
-        store_scale(a, at, row, SWIGLU ? 2 : 1, half, scale, lane);
-    };
-    load(t.row0(0), 0);
+struct Back {
+    typedef CodeTile<false> T;
+    static constexpr int halves = SWIGLU ? 2 : 1;
+    const Fp8 &a;
+    const T &t;
+    const Where &at;
+    Ahead<halves, 2 * NB> ahead;
+
+    __device__ __forceinline__ void load(int piece, int lane)
+    {
+        if (piece < 2 * NB && (SWIGLU || a.act != MOE_ACT_NONE)) {
+            const int right = piece % 2;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        if (b * 64 >= at.n)
-            break;
-        const int row = t.row0(b);
-        f32x4 v[8], u[8];
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            v[c] = f.acc[c][b];
-#pragma unroll
-        for (int right = 0; right < 2; ++right) {
-            asm volatile("" : "+v"(lane));
-            if (SWIGLU || a.act != MOE_ACT_NONE) {
-                put_pieces(place, ahead, 0, lane);
-                if (SWIGLU)
-                    put_pieces(place, ahead_up, 1, lane);
-                load(right ? t.row0(min(b + 1, NB - 1)) : row, !right);
-#pragma unroll
-                for (int c = 4 * right; c < 4 * right + 4; ++c) {
-                    const f32x4 z[1] = {get_block(place, c % 4, lane)};
-                    if constexpr (SWIGLU) {
-                        const f32x4 zu = get_block(place, 4 + c % 4, lane);
-                        swiglu_slopes(v[c], u[c], z[0], zu);
-                    } else {
-                        f32x4 w[1] = {v[c]};
-                        apply_slope(w, z, a.act);
-                        v[c] = w[0];
-                    }
-                    __builtin_amdgcn_sched_barrier(0);  // (read together, the blocks take registers that are not there)
-                }
-            }
-            if (a.out) {
-                store(v + 4 * right, row, right, 0);
-                if (SWIGLU)
-                    store(u + 4 * right, row, right, 1);
-            }
-        }
-        if (a.codes) {
-            store_coded(v, row, 0);
-            if (SWIGLU)
-                store_coded(u, row, 1);
+            for (int h = 0; h < halves; ++h)
+                Part(at, a.z, halves * a.C, 2, at.c + h * a.C + 64 * right, at.inside - 64 * right)
+                    .template load<8>(at, t.row0(piece / 2), lane, ahead.v[piece % ahead.kDepth][h]);
         }
     }
-}
+    __device__ __forceinline__ void begin()
+    {
+#pragma unroll
+        for (int i = 0; i < ahead.kDepth; ++i)
+            load(i, at.lane);
+    }
+    __device__ __forceinline__ void store(MOE_LDS char *place, const f32x4 *v, int row, int right, int half, int lane) const
+    {
+        put_bf16(place, v, lane);
+        Part(at, a.out, halves * a.C, 2, at.c + half * a.C + 64 * right, at.inside - 64 * right).template store<8>(at, row, lane, place);
+    }
+    __device__ __forceinline__ void store_coded(MOE_LDS char *place, const f32x4 (&v)[8], int row, int half, int lane) const
+    {
+        const float scale = scale_of(row_top(v));
+        put_codes(place, v, scale, lane);
+        Part(at, a.codes, halves * a.C, 1, at.c + half * a.C, at.inside).template store<8>(at, row, lane, place);
+        store_scale(a, at, row, halves, half, scale, lane);
+    }
+
+    __device__ __forceinline__ void finish(const typename T::template Regs<NB> &f, MOE_LDS char *lds)
+    {
+        MOE_LDS char *place = t.out_place(lds);
+        int lane = at.lane;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (b * 64 >= at.n)
+                break;
+            const int row = t.row0(b);
+            f32x4 v[8], u[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                v[c] = f.acc[c][b];
+#pragma unroll
+            for (int right = 0; right < 2; ++right) {
+                asm volatile("" : "+v"(lane));
+                if (SWIGLU || a.act != MOE_ACT_NONE) {
+                    const int piece = 2 * b + right;
+#pragma unroll
+                    for (int h = 0; h < halves; ++h)
+                        put_pieces(place, ahead.v[piece % ahead.kDepth][h], h, lane);
+                    load(piece + ahead.kDepth, lane);
+#pragma unroll
+                    for (int c = 4 * right; c < 4 * right + 4; ++c) {
+                        const f32x4 z[1] = {get_block(place, c % 4, lane)};
+                        if constexpr (SWIGLU) {
+                            swiglu_slopes(v[c], u[c], z[0], get_block(place, 4 + c % 4, lane));
+                        } else {
+                            f32x4 w[1] = {v[c]};
+                            apply_slope(w, z, a.act);
+                            v[c] = w[0];
+                        }
+                        __builtin_amdgcn_sched_barrier(0);  // (read together, the blocks take registers that are not there)
+                    }
+                }
+                if (a.out) {
+                    store(place, v + 4 * right, row, right, 0, lane);
+                    if (SWIGLU)
+                        store(place, u + 4 * right, row, right, 1, lane);
+                }
+            }
+            if (a.codes) {
+                asm volatile("" : "+v"(lane));
+                store_coded(place, v, row, 0, lane);
+                if (SWIGLU) {
+                    asm volatile("" : "+v"(lane));
+                    store_coded(place, u, row, 1, lane);
+                }
+            }
+        }
+    }
+};
 
 // A workgroup's walk over its list of tiles.
 template <Kind KIND>
@@ -302,16 +362,15 @@ struct Walk {
         t.run(f, lds);
         const int c = k.c0 + t.col0() / (GATED ? 2 : 1);
         Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
+        std::conditional_t<DX, Back<KIND == kBackGated, NB>, Forward<GATED, NB>> results{a, t, at};
+        results.begin();
         next();
         T::keep_uniform(at.e);
         T::keep_uniform(at.first);
         T::keep_uniform(at.n);
         T::keep_uniform(at.c);
         T::keep_uniform(at.inside);
-        if constexpr (DX)
-            finish_dx<KIND == kBackGated>(a, t, f, at, lds);
-        else
-            finish_forward<GATED>(a, t, f, at, lds);
+        results.finish(f, lds);
     }
 };
 

@@ -42,8 +42,11 @@ __device__ __forceinline__ uint32_t row_top(const f32x4 (&v)[BLOCKS])
 #pragma unroll
     for (int i = 0; i < 4 * BLOCKS; ++i)
         top = umax(top, size_bits(v[i / 4][i % 4]));
-    top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16)));
-    return umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32)));
+    // (of a row's four lanes, 16 apart: rows of 16 lanes 1, 3 change places with 0, 2, then halves)
+    const auto x = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+    top = umax(x[0], x[1]);
+    const auto y = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+    return umax(y[0], y[1]);
 }
 
 // Gradients of silu(gate) * up: of the gate's inputs into d, of the up half's into du.

@@ -128,6 +128,23 @@ def test_large_values_and_saturation():
         assert torch.isfinite(out[:340]).all() and torch.isfinite(pre[:340]).all()
 
 
+# some rows an expert, 64 of them a tile: runs around its blocks of 16, and columns that
+# end inside a group of 128
+SOME = [1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 0, 66, 127, 129, 130]
+
+
+@pytest.mark.parametrize("K,N,act", [(16, 4112, NONE), (528, 2064, SWIGLU), (640, 2048, SILU), (2064, 1040, SWIGLU), (1040, 4096, GELU)])
+@pytest.mark.parametrize("row", [False, True])
+def test_some_rows_an_expert(K, N, act, row):
+    check_product(SOME, K, N, act, True, True, True, row, base=3)
+
+
+@pytest.mark.parametrize("K,N,act,halves", [(4112, 16, NONE, 1), (2064, 528, SWIGLU, 1), (2048, 640, NONE, 2), (1040, 400, GELU, 1),
+                                            (4096, 1040, SWIGLU, 1), (2064, 528, NONE, 2)])
+def test_some_rows_dx(K, N, act, halves):
+    test_dx(SOME, K, N, act, halves)
+
+
 @pytest.mark.parametrize("n", [12, 400, 3000])
 def test_nan_stays_in_its_row(n):
     """A NaN code, or a NaN scale, of one row reaches no other row; NaN behind the
