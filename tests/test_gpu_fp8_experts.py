@@ -249,6 +249,22 @@ def test_group(T, H, I, E, k, Rn, act, quant, train):
     R.inside(grads.w_down, dw, tw + tie, "w_down")
 
 
+@pytest.mark.parametrize("quant", [0, 1, 3])
+def test_no_tokens(quant):
+    """Nothing to do but zero gradients."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    mlp = make(g, 4, 32, 16, SWIGLU, True, 0, True)
+    grp = EPGroup(0, 32, 4, 2, 2, experts=mlp)
+    x, logits = normal(g, 0, 32), normal(g, 0, 4, dtype=torch.float32)
+    grads = mlp.alloc_grads()
+    for t in grads:
+        t.fill_(3.0)
+    grp.run(logits, x, torch.empty_like(x), quant=quant)
+    grp.backward(x, torch.empty_like(x), torch.empty_like(logits), grads)
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in grads)
+
+
 def block(mlp, x, res, w1, w2, off, room):
     """norm -> codes -> experts with the residual -> norm, and all of it back from
     d_y: as a block of a network has them."""
