@@ -970,7 +970,8 @@ def moe_expert_matmul_fp8(x: torch.Tensor, x_scales: torch.Tensor, offsets: torc
     """moe_expert_matmul of E4M3 x [rows, K] with x_scales fp32 [rows, ceil(K / 128)]
     or [rows] (one a row) and w E4M3 [E, N, K] with w_scales [E, ceil(N / 128), ceil(K /
     128)] (MOE_ACT_SWIGLU: [E, 2N, K], [E, 2, ...]) -> out bf16 [rows, N], codes [rows,
-    N] with scales [rows, ceil(N / 128)], or both; preact as there."""
+    N] with scales [rows, ceil(N / 128)], or both; preact as there; workspace: for
+    codes, scratch of expert_fp8_workspace_bytes, else allocated where wanted."""
     _want_weights(w, offsets)
     E, wide_n, K = w.shape
     wide = 2 if act == MOE_ACT_SWIGLU else 1
