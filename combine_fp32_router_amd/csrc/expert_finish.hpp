@@ -62,23 +62,21 @@ template <int P>
 struct Pieces {
     __amdgpu_buffer_rsrc_t rsrc;
     int pitch, col, n;  // bytes of a row, this lane's offset in a row (kOutside past the columns), rows
-    int lane;
 
     // Rows first .. first + n - 1 of `cols` columns of `size` bytes; the wave's
     // pieces start at column c, `inside` of its columns are the array's.
-    __device__ __forceinline__ Pieces(const void *p, int64_t first, int n_, int cols, int size, int c, int inside,
-                                     int lane_ = lane_id())
+    __device__ __forceinline__ Pieces(const void *p, int64_t first, int n_, int cols, int size, int c, int inside)
         : rsrc(row_rsrc(const_cast<char *>(static_cast<const char *>(p)) + first * cols * size, n_ * cols * size)),
-          pitch(cols * size), n(n_), lane(lane_)
+          pitch(cols * size), n(n_)
     {
-        const int in_wave = lane % P * (16 / size);
+        const int in_wave = lane_id() % P * (16 / size);
         col = in_wave < inside ? (c + in_wave) * size : kOutside;
     }
     static constexpr int kCount = P / 4;  // loads or stores for 16 rows
     // offset of the j-th of them, for the 16 rows from `row`
     __device__ __forceinline__ int at(int row, int j) const
     {
-        const int r = row + 64 / P * j + lane / P;
+        const int r = row + 64 / P * j + lane_id() / P;
         return r < n && col != kOutside ? r * pitch + col : kOutside;
     }
     __device__ __forceinline__ u32x4 load(int row, int j) const
@@ -109,10 +107,10 @@ __device__ __forceinline__ void store_blocks(MOE_LDS char *__restrict__ lds, con
 {
 #pragma unroll
     for (int c = 0; c < BLOCKS; ++c)
-        *reinterpret_cast<MOE_LDS u32x2 *>(lds + Place::half(c, out.lane)) = round4(v[c]);
+        *reinterpret_cast<MOE_LDS u32x2 *>(lds + Place::half(c)) = round4(v[c]);
 #pragma unroll
     for (int j = 0; j < P / 4; ++j)
-        out.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<P>(j, out.lane)));
+        out.store(row, j, *reinterpret_cast<const MOE_LDS u32x4 *>(lds + Place::piece<P>(j)));
 }
 
 }  // namespace
