@@ -829,8 +829,9 @@ def _want_codes(t: torch.Tensor, shape, name: str):
 
 def _want_floats(t: torch.Tensor, shapes, name: str):
     """fp32 of one of `shapes`."""
-    _want(t, torch.float32, name)
-    if tuple(t.shape) not in shapes:
+    if t.dtype is not torch.float32:
+        _want(t, torch.float32, name)
+    if t.shape not in shapes:
         raise ValueError(f"{name}: expected shape {shapes[0]}, got {tuple(t.shape)}")
 
 
@@ -854,18 +855,23 @@ def moe_add_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.T
     root-mean-square norm by weight fp32 [H] -> sum and y bf16 [T, H], codes
     E4M3 [T, H] with scales fp32 [T] (one a row) or [T, ceil(H / 128)]; any output
     may be None, but not both y and codes."""
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    for t, name in ((x, "x"), (residual, "residual"), (sum, "sum"), (y, "y")):
-        if t is not None:
-            _want_bf16(t, (T, H), name)
+    T, H = shape
+    _want_bf16(x, shape, "x")
+    if residual is not None:
+        _want_bf16(residual, shape, "residual")
+    if sum is not None:
+        _want_bf16(sum, shape, "sum")
+    if y is not None:
+        _want_bf16(y, shape, "y")
     if weight is not None:
         _want_floats(weight, ((H,),), "weight")
     if (codes is None) != (scales is None):
         raise ValueError("codes and scales come together")
     if codes is not None:
-        _want_codes(codes, (T, H), "codes")
+        _want_codes(codes, shape, "codes")
         _want_floats(scales, ((T, code_blocks(H)), (T,)), "scales")
     block = MOE_BLOCK_ROW if scales is None or scales.dim() == 1 else MOE_BLOCK_128
     _call("moe_add_norm", stream, x, residual, weight, float(eps), T, H, sum, y, block, codes, scales)
@@ -889,15 +895,19 @@ def moe_add_norm_grad(d_y: torch.Tensor, d_sum: torch.Tensor | None, sum: torch.
     the sum (d_sum or None): d_x bf16 [T, H], of x and of the residual, and
     d_weight fp32 [H] (which accumulate adds to) or None.  workspace: scratch of
     add_norm_grad_workspace_bytes, else allocated where wanted."""
-    if d_y.dim() != 2:
+    shape = d_y.shape
+    if len(shape) != 2:
         raise ValueError("d_y must be [T, H]")
-    T, H = d_y.shape
-    for t, name in ((d_y, "d_y"), (d_sum, "d_sum"), (sum, "sum"), (d_x, "d_x")):
-        if t is not None:
-            _want_bf16(t, (T, H), name)
-    for t, name in ((weight, "weight"), (d_weight, "d_weight")):
-        if t is not None:
-            _want_floats(t, ((H,),), name)
+    T, H = shape
+    _want_bf16(d_y, shape, "d_y")
+    if d_sum is not None:
+        _want_bf16(d_sum, shape, "d_sum")
+    _want_bf16(sum, shape, "sum")
+    _want_bf16(d_x, shape, "d_x")
+    if weight is not None:
+        _want_floats(weight, ((H,),), "weight")
+    if d_weight is not None:
+        _want_floats(d_weight, ((H,),), "d_weight")
     need = 0 if d_weight is None else add_norm_grad_workspace_bytes(T, H)
     _call_with_room("moe_add_norm_grad", stream, workspace, need, d_y, d_y, d_sum, sum, weight,
                     float(eps), T, H, d_x, d_weight, int(accumulate))
