@@ -3,11 +3,13 @@
 // Every live expert's weights are read once and multiplied with up to 16 rows, so the
 // reading bounds it.  A wave has 16 output columns (GATED: 16 of both halves): two
 // loads of 16 bytes a lane are a matrix instruction's operand, 16 rows of one whole
-// line each, so they go straight to registers, four blocks of 128 ahead.
+// line each, so they go straight to registers, four blocks of 128 ahead (eight where
+// one wave a CU is all there is: 1 row, 4096 -> 4096, 9.8 us against 12.3).
 //
-// A CU takes some 30 GB/s, so all of them have to read: 64 columns a workgroup
-// where they make one for every CU, else 16.  (One token at 8 of 32 experts, 7168 ->
-// 2048 gated, 235 MB of weights: 44 us, 5.3 TB/s, in 256 workgroups; 66 in 128.)  But
+// A CU takes some 30 GB/s, so all of them have to read: 32 columns a workgroup
+// where 64 would make one for every CU, else 16.  (One token at 8 of 32 experts, 7168 ->
+// 2048 gated, 235 MB of weights: 44 us, 5.3 TB/s, in 512 workgroups or 256, 66 in 128;
+// 2048 -> 7168, 117 MB: 26 us in 1792 workgroups, 28 in 896 of twice the columns.)  But
 // the scale of a coded block goes by 128 columns: their workgroups have all of them, or,
 // with a workspace, leave the results there in fp32 for a second kernel to code.
 #include "fp8_args.hpp"
@@ -22,7 +24,8 @@ template <Kind KIND, int CW>
 __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
 {
     constexpr bool GATED = KIND == kGated, BOTH = KIND == kBackGated;
-    constexpr int wide = GATED ? 2 : 1, out = BOTH ? 2 : 1, kDepth = 4;  // halves of the weights, of the results
+    constexpr int wide = GATED ? 2 : 1, out = BOTH ? 2 : 1;  // halves of the weights, of the results
+    constexpr int kDepth = CW == 1 && !GATED ? 8 : 4;
     __shared__ uint32_t tops[out][CW][16];
     const int lane = lane_id(), w = static_cast<int>(uniform(threadIdx.x / kWave));
     const int groups = (a.C + 16 * CW - 1) / (16 * CW), nbc = code_blocks(a.C);
@@ -173,7 +176,7 @@ hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
     a.codes = nullptr;
     a.wide_out = codes ? static_cast<float *>(workspace) : nullptr;
     if (tiles * ((a.C + 63) / 64) >= kCus)
-        launch<KIND, 4>(a, tiles, stream);
+        launch<KIND, 2>(a, tiles, stream);
     else
         launch<KIND, 1>(a, tiles, stream);
     const hipError_t err = hipGetLastError();
