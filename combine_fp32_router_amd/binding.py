@@ -1016,7 +1016,7 @@ def moe_expert_matmul_fp8_dx(dy: torch.Tensor, dy_scales: torch.Tensor, offsets:
     """moe_expert_matmul_dx of E4M3 dy [rows, N] with dy_scales fp32 [rows, ceil(N /
     128)] (two halves: [rows, 2N], [rows, 2, ceil(N / 128)]) and moe_quant_weights' codes_t
     and scales_t -> dx bf16 [rows, K] ([rows, 2K] for MOE_ACT_SWIGLU), its codes with scales
-    [rows, ceil(K / 128)] ([rows, 2, ceil(K / 128)]), or both."""
+    [rows, ceil(K / 128)] ([rows, 2, ceil(K / 128)]), or both; workspace as there."""
     if w_t.dim() != 3:
         raise ValueError("w_t must be [E, K, N]")
     _want_weights(w_t, offsets)
@@ -1039,7 +1039,7 @@ def moe_expert_matmul_fp8_dx(dy: torch.Tensor, dy_scales: torch.Tensor, offsets:
         raise ValueError("an activation's gradient needs preact")
     else:
         _want_bf16(preact, (rows, wide * K), "preact")
-    name = "moe_expert_matmul_fp8_dx"
-    _call_with_room(name, stream, workspace,
-                    expert_fp8_workspace_bytes(name, E, rows, K, N, act, halves), dy, dy, dy_scales,
-                    offsets, w_t, w_t_scales, halves, act, preact, E, rows, K, N, dx, codes, scales)
+    name = "moe_expert_matmul_fp8_dx"  # whose workspace is for coded results
+    need = 0 if codes is None else expert_fp8_workspace_bytes(name, E, rows, K, N, act, halves)
+    _call_with_room(name, stream, workspace, need, dy, dy, dy_scales, offsets, w_t, w_t_scales,
+                    halves, act, preact, E, rows, K, N, dx, codes, scales)

@@ -697,7 +697,7 @@ int moe_expert_matmul_fp8_dx(const void *dy, const float *dy_scales, const int32
     if ((halves != 1 && halves != 2) || check_product(E, max_rows, K, N, MOE_MAX_HIDDEN) != MOE_OK ||
         !known_act(act) || !fp8_tiles_fit(E, max_rows, K))
         return MOE_ERR_SHAPE;
-    const size_t need = 0;
+    const size_t need = moe::expert_fp8_dx_workspace_bytes(halves, act, E, max_rows, K, N);
     if (!workspace && workspace_bytes) {
         *workspace_bytes = need;
         return MOE_OK;
@@ -718,7 +718,7 @@ int moe_expert_matmul_fp8_dx(const void *dy, const float *dy_scales, const int32
                    scales == w_t_scales)))
         return MOE_ERR_ALIAS;
     return hip_status(moe::launch_expert_fp8_dx(dy, dy_scales, offsets, w_t, w_t_scales, halves, act, preact, E,
-                                                max_rows, K, N, dx, codes, scales, stream));
+                                                max_rows, K, N, dx, codes, scales, workspace, stream));
 }
 
 }  // extern "C"

@@ -438,27 +438,38 @@ hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const 
     a.residual = static_cast<const uint16_t *>(residual), a.E = E, a.R = K, a.segments = 1, a.C = N;
     a.out = out, a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.preact = static_cast<uint16_t *>(preact);
     const Kind kind = act == MOE_ACT_SWIGLU ? kGated : kPlain;
-    if (few_fp8_pay(kind == kGated ? 2 : 1, E, max_rows, K, N, false))
+    const int wide = kind == kGated ? 2 : 1;
+    const bool room = workspace && few_fp8_bytes(wide, 1, E, max_rows, K, N);
+    if (few_fp8_pay(wide, E, max_rows, K, N, codes && !room))
         return launch_fp8_few(kind, a, max_rows, workspace, stream);
     return act == MOE_ACT_SWIGLU ? launch<kGated>(a, max_rows, stream) : launch<kPlain>(a, max_rows, stream);
 }
 
 size_t expert_fp8_workspace_bytes(int act, int E, int64_t max_rows, int K, int N)
 {
-    return max_rows > 0 && few_fp8_pay(act == MOE_ACT_SWIGLU ? 2 : 1, E, max_rows, K, N, false) ? static_cast<size_t>(few_fp8_bytes(E, max_rows, N)) : 0;
+    const int wide = act == MOE_ACT_SWIGLU ? 2 : 1;
+    const bool few = max_rows > 0 && few_fp8_pay(wide, E, max_rows, K, N, false);
+    return few ? static_cast<size_t>(few_fp8_bytes(wide, 1, E, max_rows, K, N)) : 0;
+}
+
+size_t expert_fp8_dx_workspace_bytes(int halves, int act, int E, int64_t max_rows, int K, int N)
+{
+    const bool few = max_rows > 0 && few_fp8_pay(1, E, max_rows, halves * N, K, false);
+    return few ? static_cast<size_t>(few_fp8_bytes(1, act == MOE_ACT_SWIGLU ? 2 : 1, E, max_rows, halves * N, K)) : 0;
 }
 
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
                                 const float *wts, int halves, int act, const void *z, int E, int64_t max_rows, int K,
-                                int N, void *dx, void *codes, float *scales, hipStream_t stream)
+                                int N, void *dx, void *codes, float *scales, void *workspace, hipStream_t stream)
 {
     Fp8 a{};
     a.q = static_cast<const uint8_t *>(dy), a.xs = dys, a.xs_cols = halves * code_blocks(N), a.offsets = offsets;
     a.w = static_cast<const uint8_t *>(wt), a.ws = wts, a.act = act, a.z = static_cast<const uint16_t *>(z);
     a.E = E, a.R = N, a.segments = halves, a.C = K;
     a.out = dx, a.codes = static_cast<uint8_t *>(codes), a.scales = scales;
-    if (few_fp8_pay(1, E, max_rows, halves * N, K, codes != nullptr))
-        return launch_fp8_few(act == MOE_ACT_SWIGLU ? kBackGated : kBack, a, max_rows, nullptr, stream);
+    const bool room = workspace && few_fp8_bytes(1, act == MOE_ACT_SWIGLU ? 2 : 1, E, max_rows, halves * N, K);
+    if (few_fp8_pay(1, E, max_rows, halves * N, K, codes && !room))
+        return launch_fp8_few(act == MOE_ACT_SWIGLU ? kBackGated : kBack, a, max_rows, workspace, stream);
     return act == MOE_ACT_SWIGLU ? launch<kBackGated>(a, max_rows, stream) : launch<kBack>(a, max_rows, stream);
 }
 

@@ -127,13 +127,14 @@ __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
         }
         if (a.residual && live)
             y[0][0] += load4(a.residual + r * a.C + c);
-        if (a.wide_out && live)
-            *reinterpret_cast<f32x4 *>(a.wide_out + r * a.C + c) = y[0][0];
     }
 #pragma unroll
-    for (int o = 0; o < out; ++o)
+    for (int o = 0; o < out; ++o) {
+        if (a.wide_out && live)
+            *reinterpret_cast<f32x4 *>(a.wide_out + (r * out + o) * a.C + c) = y[o][0];
         if (a.out && live)
             store4(static_cast<uint16_t *>(a.out) + (r * out + o) * a.C + c, y[o][0]);
+    }
     if constexpr (CW == 8) {
 #pragma unroll
         for (int o = 0; o < out; ++o) {
@@ -166,10 +167,11 @@ void launch(const Fp8 &a, int64_t tiles, hipStream_t stream)
 template <Kind KIND>
 hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
 {
+    constexpr int halves_in = KIND == kGated ? 2 : 1, out = KIND == kBackGated ? 2 : 1;
     const int64_t tiles = max_row_tiles(max_rows, a.E, 16);
     uint8_t *codes = a.codes;
     a.max_rows = static_cast<int>(max_rows);
-    if (codes && !(workspace && few_fp8_bytes(a.E, max_rows, a.C))) {
+    if (codes && !(workspace && few_fp8_bytes(halves_in, out, a.E, max_rows, a.R * a.segments, a.C))) {
         launch<KIND, 8>(a, tiles, stream);
         return hipGetLastError();
     }
@@ -182,15 +184,10 @@ hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || !codes)
         return err;
-    return launch_quant_wide_rows(a.wide_out, a.offsets, a.E, max_rows, a.C, codes, a.scales, stream);
+    return launch_quant_wide_rows(a.wide_out, a.offsets, a.E, max_rows, a.C, out, codes, a.scales, stream);
 }
 
 }  // namespace
-
-int64_t few_fp8_bytes(int E, int64_t max_rows, int C)
-{
-    return max_row_tiles(max_rows, E, 16) * code_blocks(C) < kCus ? max_rows * C * 4 : 0;
-}
 
 // Estimates in us.  Here: the weights once from memory at 6 TB/s, again for every
 // further 16 rows and the rows for every 16 columns from the caches at 11, and 3.  The
@@ -198,24 +195,38 @@ int64_t few_fp8_bytes(int E, int64_t max_rows, int C)
 // TB/s and 3 if that is longer.  Measured (here / tiles): one token of 8 experts above 44 /
 // 63; 4 rows of each of 32, 7168 -> 2048 gated 158 / 166, 2048 -> 7168 90 / 98; 16 rows
 // of each 119 / 99; 2 of each of 64, 1024 -> 4096 57 / 64; 1 or 16 rows of one, 4096 ->
-// 4096 9.5 / 28.  Codes without a workspace (whole_blocks: dx) also take what a
-// workgroup's 128 columns do at 30 GB/s: 16 rows of one, 4096 <- 4096, 38 / 30.  dx else:
+// 4096 9.5 / 28.  Coded by the workgroup itself (whole_blocks), a call also
+// takes what 128 columns do at 30 GB/s, so 16 rows of one, 4096 <- 4096, take 38 (30 in
+// tiles); over the workspace they take 15, but another kernel and 4 us more of any
+// call (8 of 65 rows, 272 <- 512 through SwiGLU: 15 against 11).  dx else:
 // 515 rows of 8, 272 <- 512, 10 / 14; one token of 8, 7168 <- 2 x 2048, 58 / 61; 2 of
 // each of 64, 4096 <- 1024, 66 / 88; 16 of each of 32, 7168 <- 2 x 2048, 274 / 181.
-bool few_fp8_pay(int wide, int E, int64_t max_rows, int R, int C, bool whole_blocks)
+static double few_us(int wide, int E, int64_t max_rows, int R, int C, bool whole_blocks)
 {
     const int64_t live = max_rows < E ? max_rows : E, tiles = max_row_tiles(max_rows, E, 16);
-    if (!grid_fits(tiles * code_blocks(C), 512))  // (the largest of its three)
-        return false;
-    const double each = 1.0 * wide * C * R, weights = live * each;
-    double here = weights / 6e6 + ((tiles - live) * each + (C / 16.0) * max_rows * R) / 11e6 + 3;
+    const double each = 1.0 * wide * C * R;
+    const double us = live * each / 6e6 + ((tiles - live) * each + (C / 16.0) * max_rows * R) / 11e6 + 3;
     const double group = R * 128.0 * (wide + (max_rows < 16 ? max_rows / 16.0 : 1)) / 3e4 + 3;  // of a workgroup
-    if (whole_blocks && here < group)
-        here = group;
+    return whole_blocks && us < group ? group : us;
+}
+
+bool few_fp8_pay(int wide, int E, int64_t max_rows, int R, int C, bool whole_blocks)
+{
+    if (!grid_fits(max_row_tiles(max_rows, E, 16) * code_blocks(C), 512))  // (the largest of its three)
+        return false;
+    const double weights = 1.0 * (max_rows < E ? max_rows : E) * wide * C * R;
     const int cols = 256 / wide;
     const int64_t coarse = max_row_tiles(max_rows, E, 64) * ((C + cols - 1) / cols);
     const double there = ((coarse + kCus - 1) / kCus) * (1 + code_blocks(R) * 0.8) + 6;
+    const double here = few_us(wide, E, max_rows, R, C, whole_blocks);
     return here < (there > weights / 5.6e6 + 3 ? there : weights / 5.6e6 + 3);
+}
+
+int64_t few_fp8_bytes(int wide, int halves, int E, int64_t max_rows, int R, int C)
+{
+    const bool pays = max_row_tiles(max_rows, E, 16) * code_blocks(C) < kCus &&
+                      few_us(wide, E, max_rows, R, C, true) > few_us(wide, E, max_rows, R, C, false) + 4;
+    return pays ? max_rows * halves * C * 4 : 0;
 }
 
 hipError_t launch_fp8_few(Kind kind, Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
@@ -223,8 +234,8 @@ hipError_t launch_fp8_few(Kind kind, Fp8 &a, int64_t max_rows, void *workspace, 
     switch (kind) {
     case kPlain: return launch<kPlain>(a, max_rows, workspace, stream);
     case kGated: return launch<kGated>(a, max_rows, workspace, stream);
-    case kBack: return launch<kBack>(a, max_rows, nullptr, stream);
-    default: return launch<kBackGated>(a, max_rows, nullptr, stream);
+    case kBack: return launch<kBack>(a, max_rows, workspace, stream);
+    default: return launch<kBackGated>(a, max_rows, workspace, stream);
     }
 }
 

@@ -24,13 +24,15 @@ struct Fp8 {
     uint8_t *codes;
     float *scales;
     int height;             // rows of a tile
-    float *wide_out;        // few rows: results in fp32, to be coded
+    float *wide_out;        // few rows: results in fp32, of both halves, to be coded
 };
 
 // The products for few rows an expert, and whether they pay: `wide` halves of
-// weights, C columns, sums over R in all; whole_blocks: codes are wanted, and there is
-// no workspace.  workspace: few_fp8_bytes, or null (dx: null).
+// weights, C columns, sums over R in all; whole_blocks: codes are wanted, and no
+// workspace is for them.  workspace: few_fp8_bytes (of `halves` of results; 0: none is
+// worth it), or null.
 bool few_fp8_pay(int wide, int E, int64_t max_rows, int R, int C, bool whole_blocks);
+int64_t few_fp8_bytes(int wide, int halves, int E, int64_t max_rows, int R, int C);
 hipError_t launch_fp8_few(Kind kind, Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream);
 
 // Largest size of a lane's values of a row and of the three lanes' that hold the

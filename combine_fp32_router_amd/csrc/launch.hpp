@@ -127,8 +127,8 @@ hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *
                                 hipStream_t stream);
 hipError_t launch_quant_rows(const void *x, const int32_t *offsets, int E, int64_t max_rows, int n, int halves,
                              void *codes, float *scales, hipStream_t stream);
-hipError_t launch_quant_wide_rows(const float *x, const int32_t *offsets, int E, int64_t max_rows, int n, void *codes,
-                                  float *scales, hipStream_t stream);  // of fp32 values
+hipError_t launch_quant_wide_rows(const float *x, const int32_t *offsets, int E, int64_t max_rows, int n, int halves,
+                                  void *codes, float *scales, hipStream_t stream);  // of fp32 values
 int64_t quant_weights_groups(int E, int N, int K, int halves);  // of kRouteThreads threads
 hipError_t launch_quant_weights(const void *w, int E, int N, int K, int halves, void *codes, float *scales,
                                 void *codes_t, float *scales_t, hipStream_t stream);
@@ -139,11 +139,10 @@ hipError_t launch_expert_fp8(const void *x, const float *xs, int xs_cols, const 
                              int K, int N, void *out, void *codes, float *scales, void *preact, void *workspace,
                              hipStream_t stream);
 size_t expert_fp8_workspace_bytes(int act, int E, int64_t max_rows, int K, int N);
-// Few rows an expert: whether their kernel pays, and what its coded results need.
-int64_t few_fp8_bytes(int E, int64_t max_rows, int N);
+size_t expert_fp8_dx_workspace_bytes(int halves, int act, int E, int64_t max_rows, int K, int N);
 hipError_t launch_expert_fp8_dx(const void *dy, const float *dys, const int32_t *offsets, const void *wt,
                                 const float *wts, int halves, int act, const void *z, int E, int64_t max_rows, int K,
-                                int N, void *dx, void *codes, float *scales, hipStream_t stream);
+                                int N, void *dx, void *codes, float *scales, void *workspace, hipStream_t stream);
 
 // The experts' products over their runs of rows, and their gradients.
 hipError_t launch_expert_matmul(const void *x, const int32_t *offsets, const void *w,

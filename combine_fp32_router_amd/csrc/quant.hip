@@ -194,10 +194,10 @@ hipError_t launch_quant_rows(const void *x, const int32_t *offsets, int E, int64
     return launch_rows(x, nullptr, offsets, E, max_rows, n, halves, codes, scales, stream);
 }
 
-hipError_t launch_quant_wide_rows(const float *x, const int32_t *offsets, int E, int64_t max_rows, int n, void *codes,
-                                  float *scales, hipStream_t stream)
+hipError_t launch_quant_wide_rows(const float *x, const int32_t *offsets, int E, int64_t max_rows, int n, int halves,
+                                  void *codes, float *scales, hipStream_t stream)
 {
-    return launch_rows(nullptr, x, offsets, E, max_rows, n, 1, codes, scales, stream);
+    return launch_rows(nullptr, x, offsets, E, max_rows, n, halves, codes, scales, stream);
 }
 
 int64_t quant_weights_groups(int E, int N, int K, int halves)

@@ -334,7 +334,7 @@ int moe_expert_matmul_fp8(const void *x, const float *x_scales, int x_scale_cols
  *   codes, scales   dx in codes: [max_rows, K] and [max_rows, ceil(K / 128)]
  *              (MOE_ACT_SWIGLU: [max_rows, 2K] and [max_rows, 2, ceil(K / 128)]), or
  *              NULL; not both dx and codes NULL.                      (out)
- *   workspace, workspace_bytes   as moe_expert_matmul_fp8 (no call needs one now).
+ *   workspace, workspace_bytes   as moe_expert_matmul_fp8.
  *
  * Errors: as moe_expert_matmul_fp8.
  */
