@@ -4,7 +4,8 @@
 // reading bounds it.  A wave has 16 output columns (GATED: 16 of both halves): two
 // loads of 16 bytes a lane are a matrix instruction's operand, 16 rows of one whole
 // line each, so they go straight to registers, four blocks of 128 ahead (eight where
-// one wave a CU is all there is: 1 row, 4096 -> 4096, 9.8 us against 12.3).
+// some wave or two a CU are all there is: 1 row, 4096 -> 4096, 9.8 us against 12.3; of
+// a short sum half of them would be loads of nothing: 515 rows, 272 <- 512, 5.9 against 5.4).
 //
 // A CU takes some 30 GB/s, so all of them have to read: 32 columns a workgroup
 // where 64 would make one for every CU, else 16.  (One token at 8 of 32 experts, 7168 ->
@@ -20,12 +21,11 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-template <Kind KIND, int CW>
+template <Kind KIND, int CW, int kDepth>
 __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
 {
     constexpr bool GATED = KIND == kGated, BOTH = KIND == kBackGated;
     constexpr int wide = GATED ? 2 : 1, out = BOTH ? 2 : 1;  // halves of the weights, of the results
-    constexpr int kDepth = CW == 1 && !GATED ? 8 : 4;
     __shared__ uint32_t tops[out][CW][16];
     const int lane = lane_id(), w = static_cast<int>(uniform(threadIdx.x / kWave));
     const int groups = (a.C + 16 * CW - 1) / (16 * CW), nbc = code_blocks(a.C);
@@ -159,10 +159,11 @@ __global__ __launch_bounds__(64 * CW) void fp8_few_kernel(Fp8 a)
     }
 }
 
-template <Kind KIND, int CW>
+template <Kind KIND, int CW, int DEPTH = 4>
 void launch(const Fp8 &a, int64_t tiles, hipStream_t stream)
 {
-    fp8_few_kernel<KIND, CW><<<dim3(static_cast<unsigned>(tiles * ((a.C + 16 * CW - 1) / (16 * CW)))), 64 * CW, 0, stream>>>(a);
+    fp8_few_kernel<KIND, CW, DEPTH>
+        <<<dim3(static_cast<unsigned>(tiles * ((a.C + 16 * CW - 1) / (16 * CW)))), 64 * CW, 0, stream>>>(a);
 }
 template <Kind KIND>
 hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
@@ -179,6 +180,8 @@ hipError_t launch(Fp8 &a, int64_t max_rows, void *workspace, hipStream_t stream)
     a.wide_out = codes ? static_cast<float *>(workspace) : nullptr;
     if (tiles * ((a.C + 63) / 64) >= kCus)
         launch<KIND, 2>(a, tiles, stream);
+    else if (KIND != kGated && a.R * a.segments > 8 * kCodeBlock)
+        launch<KIND, 1, KIND == kGated ? 4 : 8>(a, tiles, stream);
     else
         launch<KIND, 1>(a, tiles, stream);
     const hipError_t err = hipGetLastError();
