@@ -103,11 +103,12 @@ __device__ __forceinline__ void store_scale(const Fp8 &a, const Where &at, int r
 }
 
 // What a tile's results take from memory, a piece of 16 rows by 64 columns (of one or
-// two arrays) after the other, kDepth of them ahead.  The first are asked for in
-// front of the next tile's first loads: behind them, they would come after them.
+// two arrays) after the other.  All of it is there before the product where the tile
+// is short; beside 256 rows' accumulators there is room for one piece ahead, the first
+// asked for in front of the next tile's first loads: behind them, it would come after.
 template <int ARRAYS, int PIECES>
 struct Ahead {
-    static constexpr int kDepth = PIECES == 2 ? 2 : 1;  // (more blocks of rows leave no room for it)
+    static constexpr int kDepth = PIECES <= 4 ? PIECES : 1;
     u32x4 v[kDepth][ARRAYS][2];
 };
 
@@ -367,11 +368,14 @@ struct Walk {
     {
         typename T::template Regs<NB> f;
         t.all_uniform();
-        t.run(f, lds);
         const int c = k.c0 + t.col0() / (GATED ? 2 : 1);
         Where at{k.e, k.first, k.n, c, a.C - c, fresh_lane()};
         std::conditional_t<DX, Back<KIND == kBackGated, NB>, Forward<GATED, NB>> results{a, t, at};
-        results.begin();
+        if (NB < 4)
+            results.begin();
+        t.run(f, lds);
+        if (NB == 4)
+            results.begin();
         next();
         T::keep_uniform(at.e);
         T::keep_uniform(at.first);
