@@ -7,9 +7,9 @@
 //
 // Many rows an expert are bound by the matrix cores' power (fp8_tile.hpp) and by the
 // results, which leave from all CUs at once while no matrix core works: 16384 rows of 8,
-// 7168 -> 2048 gated with z kept, then 2048 -> 7168: 793 us, 1.8 PFLOP/s.  dx of 16384 rows,
-// 2048 <- 7168: 271 us, and through SwiGLU with its codes 374: 335 MB more.  Few and some rows
-// are bound by the weights: 64 rows of each of 64, 2048 -> 4096: 123 us, 4.7 TB/s.  (A kernel
+// 7168 -> 2048 gated with z kept, then 2048 -> 7168: 805 us, 1.8 PFLOP/s.  dx of 16384 rows,
+// 2048 <- 7168: 271 us, and through SwiGLU with its codes 374, 335 MB more (397 with its
+// inputs' lines asked for ahead of the product).  Few and some rows are bound by the weights: 64 rows of each of 64, 2048 -> 4096: 123 us, 4.7 TB/s.  (A kernel
 // that streams weights to registers past 64 rows in LDS, two workgroups a CU, took 120
 // there, but 191 against 173 for 32 x 64 rows, 7168 -> 2048 gated.)
 #include "fp8_args.hpp"
