@@ -137,8 +137,8 @@ class ExpertMLP8(ExpertMLP):
     """The experts with E4M3 rows and weights in the products of `forward` and of
     the rows' gradients: a scale for each 1 x 128 of a row and 128 x 128 of a weight,
     fp32 sums.  h goes from one product to the next as codes; the weights'
-    gradients are bf16 products, of bf16 rows, and a quantisation counts as the
-    identity.
+    gradients are bf16 products, of bf16 rows (`backward` takes x in bf16 also
+    where `forward` had it in codes), and a quantisation counts as the identity.
 
     The codes are those that the weights had when it was made: after a change
     of w_up or w_down, `quantize` takes them again."""
