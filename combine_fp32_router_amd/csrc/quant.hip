@@ -94,7 +94,8 @@ struct QuantWeights {
 };
 
 // One workgroup for 128 x 128: a thread has 8 x 8 of them, so that its codes turn
-// in registers and the transposed tile passes LDS in 8-byte pieces.
+// in registers and the transposed tile passes LDS in 8-byte pieces.  (256 x 256 and
+// 1024 threads, for longer pieces of rows: 183 us where this takes 175.)
 template <bool STREAM>
 __global__ __launch_bounds__(kThreads) void quant_weights_kernel(QuantWeights a)
 {
