@@ -295,7 +295,7 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGr
         }
         row_sums<THREADS, 2>(sums, red, turn);
         const float n = static_cast<float>(a.H), r = 1.0f / sqrtf(sums[0] / n + a.eps);
-        const float back = r * r * (sums[1] / n);  // of s R
+        const float back = r * (r * (sums[1] / n));  // of s R (r * r could leave fp32)
         const __amdgpu_buffer_rsrc_t to = rows_at(a.dx, t);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
