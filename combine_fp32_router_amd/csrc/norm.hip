@@ -22,6 +22,7 @@ struct Norm {
     float eps;
     int64_t T;
     int H;
+    float n, per_n;  // H, 1 / H
     uint16_t *sum, *y;
     uint8_t *codes;
     float *scales;
@@ -108,6 +109,19 @@ __device__ __forceinline__ void store_vector(const __amdgpu_buffer_rsrc_t &r, in
         __builtin_amdgcn_raw_buffer_store_b64(v, r, offset, 0, policy);
 }
 
+// A row's sums are taken of c s, c = 1 at first; where the mean of squares leaves fp32,
+// or is so small (2^-60) that squares do, once more with another power of two: R = c
+// (mean((c s)^2) + c^2 eps)^(-1/2).  The squares of c s are then 2^-106 .. 2^96 for all
+// values that bf16 has, 2^-133 .. 2^128, and a row's sum is below 2^117.
+constexpr float kUp = 0x1p80f, kDown = 0x1p-80f;
+constexpr uint32_t kLeastSquares = (127 - 60) << 23, kInfinity = 0x7f800000u;  // of fp32, as bits
+__device__ __forceinline__ bool in_range(uint32_t squares) { return squares - kLeastSquares < kInfinity - kLeastSquares; }
+
+constexpr int kNowhere = static_cast<int>(0x80000000u);  // an offset past every row
+
+// A value that all of a row's threads have, for branches that they take together.
+__device__ __forceinline__ uint32_t uniform_bits(float v) { return uniform(__float_as_uint(v)); }
+
 // This lane's weights (1 where there are none).
 template <int THREADS, int VPT>
 __device__ __forceinline__ void load_weights(const float *weight, int H, int l, float (&w)[VPT][8])
@@ -150,7 +164,7 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
         const bool live = t < a.T;
         if (!kHold)
             load(t);
-        float s[VPT][8], ss[1] = {0.0f};
+        float s[VPT][8], c = 1.0f, ss[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             unpack8(v[i], s[i]);
@@ -161,9 +175,10 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
                 for (int j = 0; j < 8; ++j)
                     s[i][j] += f[j];
             }
+            if (kHold)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                ss[0] = fmaf(s[i][j], s[i][j], ss[0]);
+                for (int j = 0; j < 8; ++j)
+                    ss[0] = fmaf(s[i][j], s[i][j], ss[0]);
         }
         if (kHold)
             load(t + step);
@@ -173,8 +188,27 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_kernel(Norm a)
             for (int i = 0; i < VPT; ++i)
                 store_vector<STREAM>(to, (l + i * THREADS) * 16, pack8(s[i]));
         }
-        row_sums<THREADS, 1>(ss, red, turn);
-        const float r = 1.0f / sqrtf(ss[0] / static_cast<float>(a.H) + a.eps);
+        for (bool sum = !kHold;; sum = true) {
+            if (sum) {
+                ss[0] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float f = s[i][j] * c;
+                        ss[0] = fmaf(f, f, ss[0]);
+                    }
+            }
+            row_sums<THREADS, 1>(ss, red, turn);
+            const uint32_t squares = uniform_bits(fmaf(ss[0], a.per_n, a.eps));
+            if (__builtin_expect(in_range(squares), true))
+                break;
+            if (c != 1.0f)
+                break;
+            c = squares < kLeastSquares ? kUp : kDown;
+            turn ^= 1;
+        }
+        const float r = 1.0f / sqrtf(ss[0] / a.n + a.eps * c * c) * c;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (!kHold)
@@ -226,6 +260,7 @@ struct NormGrad {
     float eps;
     int64_t T;
     int H;
+    float n, per_n;  // H, 1 / H
     uint16_t *dx;
     float *part;  // [workgroups][H], or null
 };
@@ -247,7 +282,9 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGr
     auto load_next = [&](int64_t t) {
         load_row<THREADS, kHeld, STREAM>(rows_at(a.sum, t), l, sn);
         load_row<THREADS, kHeld, STREAM>(rows_at(a.dy, t), l, yn);
-        if (a.dsum)
+        // (of a null array no memory is read; behind a branch a lone vector is waited for at
+        // once, 131072 x 512: 109 us instead of 95, but 16384 x 7168: 163 instead of 167)
+        if (VPT == 1 || a.dsum)
             load_row<THREADS, kHeld, STREAM>(rows_at(a.dsum, t), l, dn);
     };
     if (HOLD) {
@@ -267,6 +304,34 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGr
             load_weights<THREADS, 1>(a.weight, a.H, l + i * THREADS, reinterpret_cast<float(&)[1][8]>(w));
         }
     };
+    // the sums of (c s)^2 and of g c s
+    auto sum_up = [&](const u32x4 &sv, const u32x4 &yv, const float(&w)[8], float c, float(&sums)[2]) {
+        float s[8], g[8];
+        unpack8(sv, s);
+        unpack8(yv, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            s[j] *= c;
+            sums[0] = fmaf(s[j], s[j], sums[0]);
+            sums[1] = fmaf(g[j] * w[j], s[j], sums[1]);
+        }
+    };
+    // d_x, `back` of s R off it, and d_w's share if the row has one
+    auto gradient = [&](const u32x4 &sv, const u32x4 &yv, const u32x4 &dv, const float(&w)[8], float r, float back, bool add,
+                        float(&sum)[8]) {
+        float s[8], g[8], d[8];
+        unpack8(sv, s);
+        unpack8(yv, g);
+        unpack8(dv, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = s[j] * r;
+            sum[j] = add ? fmaf(g[j], x, sum[j]) : sum[j];  // (of a missing row r may be infinite)
+            const float v = fmaf(g[j] * w[j], r, -x * back);
+            d[j] = a.dsum ? d[j] + v : v;
+        }
+        return pack8(d);
+    };
     int turn = 0;
     for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < a.T; t0 += step) {
         const int64_t t = t0 + first;
@@ -281,42 +346,57 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGr
         float sums[2] = {0.0f, 0.0f};  // of s^2 and of g s
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float s[8], g[8], w[8];
-            unpack8(vector(sv, sr, i), s);
-            unpack8(vector(yv, yr, i), g);
+            float w[8];
             weights(i, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sums[0] = fmaf(s[j], s[j], sums[0]);
-                sums[1] = fmaf(g[j] * w[j], s[j], sums[1]);
-            }
+            sum_up(vector(sv, sr, i), vector(yv, yr, i), w, 1.0f, sums);
             if (!HOLD)
                 __builtin_amdgcn_sched_barrier(0);  // (all vectors at once would not fit)
         }
         row_sums<THREADS, 2>(sums, red, turn);
-        const float n = static_cast<float>(a.H), r = 1.0f / sqrtf(sums[0] / n + a.eps);
-        const float back = r * (r * (sums[1] / n));  // of s R (r * r could leave fp32)
+        turn ^= 1;
+        const uint32_t squares = __float_as_uint(fmaf(sums[0], a.per_n, a.eps));
+        const bool good = in_range(squares) & (__float_as_uint(fabsf(sums[1])) < kInfinity);
+        const float r = 1.0f / sqrtf(sums[0] / a.n + a.eps);
         const __amdgpu_buffer_rsrc_t to = rows_at(a.dx, t);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            float s[8], g[8], w[8], d[8];
-            unpack8(vector(sv, sr, i), s);
-            unpack8(vector(yv, yr, i), g);
-            if (a.dsum)
-                unpack8(vector(dv, dr, i), d);
+            float w[8];
             weights(i, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float x = s[j] * r;
-                dw[i][j] = live ? fmaf(g[j], x, dw[i][j]) : dw[i][j];  // (of a missing row r may be infinite)
-                const float v = fmaf(g[j] * w[j], r, -x * back);
-                d[j] = a.dsum ? d[j] + v : v;
-            }
-            store_vector<STREAM>(to, (l + i * THREADS) * 16, pack8(d));
+            const u32x4 d = a.dsum ? vector(dv, dr, i) : u32x4{};
+            const u32x4 dx = gradient(vector(sv, sr, i), vector(yv, yr, i), d, w, r, r * (r * (sums[1] / a.n)), live && good, dw[i]);
+            store_vector<STREAM>(to, good ? (l + i * THREADS) * 16 : kNowhere, dx);
             if (!HOLD)
                 __builtin_amdgcn_sched_barrier(0);
         }
-        turn ^= 1;
+        if (__builtin_expect(uniform(!good), false)) {
+            // nothing of the row is stored or counted yet; where g s alone is too large, a power
+            // of two brings s to some 2^-20
+            const float c = squares < kLeastSquares ? kUp
+                            : squares < kInfinity   ? __uint_as_float(__float_as_uint(r * 0x1p-20f) & kInfinity)
+                                                    : kDown;
+            sums[0] = sums[1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float w[8];
+                load_weights<THREADS, 1>(a.weight, a.H, l + i * THREADS, reinterpret_cast<float(&)[1][8]>(w));
+                const int at = (l + i * THREADS) * 16;
+                sum_up(load_cached(sr, at), load_cached(yr, at), w, c, sums);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            row_sums<THREADS, 2>(sums, red, turn);
+            turn ^= 1;
+            const float rc = 1.0f / sqrtf(sums[0] / a.n + a.eps * c * c);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                float w[8];
+                load_weights<THREADS, 1>(a.weight, a.H, l + i * THREADS, reinterpret_cast<float(&)[1][8]>(w));
+                const int at = (l + i * THREADS) * 16;
+                const u32x4 d = a.dsum ? load_cached(dr, at) : u32x4{};
+                store_vector<STREAM>(to, at, gradient(load_cached(sr, at), load_cached(yr, at), d, w, rc * c,
+                                                      rc * c * (rc * (sums[1] / a.n)), live, dw[i]));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
     if (!a.part)
         return;
@@ -419,7 +499,7 @@ hipError_t launch_add_norm(const void *x, const void *residual, const float *wei
 {
     Norm a{};
     a.x = static_cast<const uint16_t *>(x), a.residual = static_cast<const uint16_t *>(residual);
-    a.weight = weight, a.eps = eps, a.T = T, a.H = H;
+    a.weight = weight, a.eps = eps, a.T = T, a.H = H, a.n = static_cast<float>(H), a.per_n = 1.0f / a.n;
     a.sum = static_cast<uint16_t *>(sum), a.y = static_cast<uint16_t *>(y);
     a.codes = static_cast<uint8_t *>(codes), a.scales = scales, a.blocks = blocks;
     const NormTiling n = norm_tiling(H);
@@ -449,7 +529,7 @@ hipError_t launch_add_norm_grad(const void *d_y, const void *d_sum, const void *
 {
     NormGrad a{};
     a.dy = static_cast<const uint16_t *>(d_y), a.dsum = static_cast<const uint16_t *>(d_sum);
-    a.sum = static_cast<const uint16_t *>(sum), a.weight = weight, a.eps = eps, a.T = T, a.H = H;
+    a.sum = static_cast<const uint16_t *>(sum), a.weight = weight, a.eps = eps, a.T = T, a.H = H, a.n = static_cast<float>(H), a.per_n = 1.0f / a.n;
     a.dx = static_cast<uint16_t *>(d_x), a.part = d_weight ? static_cast<float *>(workspace) : nullptr;
     const NormTiling n = norm_tiling(H);
     const int groups = grad_groups(T, n);

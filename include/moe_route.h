@@ -513,7 +513,9 @@ int moe_combine_grad(const void *d_out_bf16, const void *recv, const float *recv
  *     s[t, h] = x[t, h] + residual[t, h]
  *     y[t, h] = s[t, h] * (mean_h s[t, h]^2 + eps)^(-1/2) * weight[h]
  * s stays in fp32 between the two lines; sum, y and codes are rounded once each.
- * A row whose squares leave fp32 (|s| above 1e19) is not normed.
+ * Rows of any finite s are normed, also where the squares or their sum leave fp32; only
+ * a root above fp32's largest number (without eps, a root mean square below 2^-128) is
+ * infinite.
  *
  *   x          [T, H] bf16 bits.                                      (in)
  *   residual   [T, H] bf16 bits, or NULL: s = x.                      (in)
@@ -541,7 +543,8 @@ int moe_add_norm(const void *x, const void *residual, const float *weight, float
  *     R = (mean_h s^2 + eps)^(-1/2),  g = d_y * weight
  *     d_x[t, h]   = d_sum + R g - s R^3 mean_h(g s)   (of x and of residual alike)
  *     d_weight[h] = sum_t d_y s R
- * fp32 sums in a fixed order; d_x is rounded once.  Codes of y count as y.
+ * fp32 sums in a fixed order; d_x is rounded once.  Codes of y count as y.  Rows of any
+ * size, as there.
  *
  *   d_y        [T, H] bf16 bits.                                      (in)
  *   d_sum      [T, H] bf16 bits, or NULL: 0.                          (in)
