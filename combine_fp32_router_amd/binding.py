@@ -525,6 +525,25 @@ def _call(name: str, stream, *args) -> None:
         _check(name, status)
 
 
+def stream_handle(stream, device: torch.device) -> int:
+    """The handle of `stream`: a torch stream, a handle, or None for the device's
+    current one."""
+    if stream is None:
+        return _raw_stream(device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def stream_of(stream, device: torch.device) -> torch.cuda.Stream:
+    """The same as torch's stream."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    handle = int(stream)
+    return (torch.cuda.ExternalStream(handle, device=device) if handle else
+            torch.cuda.default_stream(device))
+
+
 _BF16_TYPES = (torch.bfloat16, torch.int16, torch.uint16)  # values, or their bits
 
 
@@ -720,11 +739,8 @@ def _call_with_room(name: str, stream, workspace: torch.Tensor | None, need: int
         if stream is not None and workspace.is_cuda:
             # allocated in the current stream's order, used in this one's
             current = torch.cuda.current_stream(like.device)
-            handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-            if handle != current.cuda_stream:
-                user = (stream if isinstance(stream, torch.cuda.Stream) else
-                        torch.cuda.ExternalStream(handle, device=like.device) if handle else
-                        torch.cuda.default_stream(like.device))
+            if stream_handle(stream, like.device) != current.cuda_stream:
+                user = stream_of(stream, like.device)
                 user.wait_stream(current)
                 workspace.record_stream(user)
     n = ctypes.c_size_t(workspace.numel() * workspace.element_size())

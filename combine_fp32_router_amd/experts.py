@@ -133,6 +133,11 @@ class ExpertMLP:
                                stream)
 
 
+def _capturing(stream: torch.cuda.Stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class ExpertMLP8(ExpertMLP):
     """The experts with E4M3 rows and weights in the products of `forward` and of
     the rows' gradients: a scale for each 1 x 128 of a row and 128 x 128 of a weight,
@@ -141,11 +146,15 @@ class ExpertMLP8(ExpertMLP):
     where `forward` had it in codes), and a quantisation counts as the identity.
 
     The codes are those that the weights had when it was made: after a change
-    of w_up or w_down, `quantize` takes them again."""
+    of w_up or w_down, `quantize` takes them again.  Calls on other streams than
+    the codes were made on wait for them (but for calls captured into a graph,
+    whose replays the caller orders).  `quantize` itself waits for nothing: like any
+    other call it is the caller's to order behind calls on other streams."""
 
     def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, act: int,
                  b_up: torch.Tensor | None = None, b_down: torch.Tensor | None = None,
-                 max_rows: int = 0, train: bool = False):
+                 max_rows: int = 0, train: bool = False, stream=None):
+        """`stream`: where the codes are made (None: the current one)."""
         super().__init__(w_up, w_down, act, b_up, b_down, max_rows, train)
         E, H, I, wide, dev = self.E, self.H, self.I, self.wide, self.device
         nbh, nbi = B.code_blocks(H), B.code_blocks(I)
@@ -163,13 +172,27 @@ class ExpertMLP8(ExpertMLP):
         self.d_preact8 = coded((max_rows, wide * I), (max_rows, wide, nbi)) if train else None
         if not train:
             self.hidden = None
+        self._codes_made = None  # event behind the codes' making
+        self._behind = set()  # handles of the streams that are behind it
         if dev.type == "cuda":
-            self.quantize()
+            self.quantize(stream)
 
     def quantize(self, stream=None) -> None:
         """The weights' codes, from w_up and w_down as they are now."""
         B.moe_quant_weights(self.w_up, *self.up8, *self.up8_t, self.wide, stream)
         B.moe_quant_weights(self.w_down, *self.down8, *self.down8_t, 1, stream)
+        on = B.stream_of(stream, self.device)
+        if not _capturing(on):
+            self._codes_made, self._behind = on.record_event(), {on.cuda_stream}
+
+    def _behind_codes(self, stream) -> None:
+        """What `stream` is given next waits for the codes."""
+        if self._codes_made is None or B.stream_handle(stream, self.device) in self._behind:
+            return
+        on = B.stream_of(stream, self.device)
+        if not _capturing(on):
+            on.wait_event(self._codes_made)
+            self._behind.add(on.cuda_stream)
 
     def forward(self, x: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor,
                 residual: torch.Tensor | None = None, stream=None,
@@ -181,6 +204,7 @@ class ExpertMLP8(ExpertMLP):
         h8, hs = self.hidden8[0][:n], self.hidden8[1][:n]
         self.forwards += 1
         self._kept = None
+        self._behind_codes(stream)
         if scales is None:
             bf16, (x, scales) = x, (t[:n] for t in self.x8)
             B.moe_quant_rows(bf16, x, scales, offsets, 1, stream)
@@ -195,6 +219,7 @@ class ExpertMLP8(ExpertMLP):
     def _through_down(self, d_out, offsets, n, for_grads, for_x, stream):
         if not (for_grads or for_x):
             return
+        self._behind_codes(stream)
         d8, dz8 = [t[:n] for t in self.x8], [t[:n] for t in self.d_preact8]
         B.moe_quant_rows(d_out, *d8, offsets, 1, stream)
         B.moe_expert_matmul_fp8_dx(*d8, offsets, *self.down8_t, self.act, self.preact[:n],
