@@ -6,10 +6,11 @@
 // The results leave in bf16, in codes with a scale for each 128, or both.
 //
 // Many rows an expert are bound by the matrix cores' power (fp8_tile.hpp) and by the
-// results, which leave from all CUs at once while no matrix core works: 16384 rows of 8,
-// 7168 -> 2048 gated with z kept, then 2048 -> 7168: 805 us, 1.8 PFLOP/s.  dx of 16384 rows,
-// 2048 <- 7168: 271 us, and through SwiGLU with its codes 374, 335 MB more (397 with its
-// inputs' lines asked for ahead of the product).  Few and some rows are bound by the weights: 64 rows of each of 64, 2048 -> 4096: 123 us, 4.7 TB/s.  (A kernel
+// results, which leave from all CUs at once while no matrix core works (the next tile's
+// first loads are under way then, but stand in one count with the stores): 16384 rows of 8,
+// 7168 -> 2048 gated with z kept, then 2048 -> 7168: 802 us, 1.8 PFLOP/s.  dx of 16384 rows,
+// 2048 <- 7168: 267 us, and through SwiGLU with its codes 325, 335 MB in place of 67 (6%
+// more with its inputs' lines asked for ahead of the product).  Few and some rows are bound by the weights: 64 rows of each of 64, 2048 -> 4096: 123 us, 4.7 TB/s.  (A kernel
 // that streams weights to registers past 64 rows in LDS, two workgroups a CU, took 120
 // there, but 191 against 173 for 32 x 64 rows, 7168 -> 2048 gated.)
 #include "fp8_args.hpp"

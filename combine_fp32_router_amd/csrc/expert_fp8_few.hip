@@ -3,9 +3,11 @@
 // Every live expert's weights are read once and multiplied with up to 16 rows, so the
 // reading bounds it.  A wave has 16 output columns (GATED: 16 of both halves): two
 // loads of 16 bytes a lane are a matrix instruction's operand, 16 rows of one whole
-// line each, so they go straight to registers, four blocks of 128 ahead (eight where
-// some wave or two a CU are all there is: 1 row, 4096 -> 4096, 9.8 us against 12.3; of
-// a short sum half of them would be loads of nothing: 515 rows, 272 <- 512, 5.9 against 5.4).
+// line each, so they go straight to registers, four blocks of 128 ahead, or eight where
+// one to four waves a CU are all there is: 1 row, 4096 -> 4096 (one a CU), 9.3 us against
+// 12.5; -> 8192 (two) 13.7 against 17.3; -> 16320 (four) 21.9 against 24.4.  Of a short sum
+// half of them would be loads of nothing: 515 rows, 272 <- 512, 5.9 against 5.4, so sums up to
+// 1024 take four.  (With four waves a CU the two meet at 2048; 1040 -> 16320 is 7.4 against 6.7.)
 //
 // A CU takes some 30 GB/s, so all of them have to read: 32 columns a workgroup
 // where 64 would make one for every CU, else 16.  (One token at 8 of 32 experts, 7168 ->

@@ -33,7 +33,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 // The lane, as a value of its own: what is worked out from it is not kept over the
 // tiles' loop, where there are no registers for it (the reloads of spilled ones waited
-// for every store of a tile's results: 30 us a tile).
+// for every store of a tile's results: 30 us a tile.  One of the plain gradient's is still
+// spilled, and reloaded there).
 __device__ __forceinline__ int fresh_lane()
 {
     int lane = lane_id();

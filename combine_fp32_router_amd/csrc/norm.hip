@@ -5,11 +5,15 @@
 //
 // A row is read once and held in registers (THREADS threads, VPT 16-byte vectors
 // each) between its sums and its results, and the next row's loads are in flight
-// meanwhile.  Sixteen lanes hold the 128 values of a block of codes, a row of the
-// DPP moves.  The gradient of w stays in registers over all rows of a workgroup; the
-// workgroups' sums meet in a second kernel, in a fixed order.  Bound by memory (16384 x
-// 7168, all outputs: 192 us, 5.5 TB/s; the gradient 164, 5.7 TB/s), small calls by the launch
-// (1 x 7168: 4 us).
+// meanwhile; above 16384 columns neither the next row nor, in the gradient, this one is
+// held.  Sixteen lanes hold the 128 values of a block of codes, a row of the DPP moves.
+// The gradient of w stays in registers over all rows of a workgroup; the workgroups'
+// sums meet in a second kernel, in a fixed order.  Bound by memory (16384 x 7168, all
+// outputs: 191 us, 5.5 TB/s; the gradient 163, 5.8 TB/s), small calls by the launch (1 x 7168:
+// 4 us).  Wide rows lack registers: 4096 x 32768 215 us and 268 (4.0 TB/s); above
+// that some go to scratch, 27 a lane of the norm's and 233 of the gradient's (2048 x
+// 65536: 246 us, 4.9 TB/s, and 632, 1.7 TB/s), and 7 of the gradient's from 8208 to 16384
+// columns (4096 x 16384: 117 us and 101, 5.3 TB/s).
 #include "fp8_codes.hpp"
 #include "launch.hpp"
 
@@ -266,7 +270,8 @@ struct NormGrad {
 };
 
 // HOLD: a row stays in registers between its sums and its results, beside the
-// weights and the next row; else it is read again (from cache: 128 KiB at the longest).
+// weights and the next row; else it is read again (from cache: 128 KiB of each array at
+// the longest).
 template <int THREADS, int VPT, bool STREAM>
 __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGrad a)
 {
@@ -468,8 +473,11 @@ int norm_groups(int64_t T, int rows, int most)
 }
 // Workgroups of the gradient's first kernel.
 // One a CU, whose next row is on its way while it works on one, is enough, and more
-// leave more sums to the second kernel (16384 x 7168: 162 us; 173 with two, 177 with
-// four); rows of a wave, four at once, take two (65536 x 1024: 112 us against 116).
+// leave more sums to the second kernel (16384 x 7168: 163 us; 173 with two, 177 with
+// four; 4096 x 16384 101, 105 and 117); rows of a wave, four at once, take two (65536 x
+// 1024: 96 us; 113 with one, 108 with four; 131072 x 512 95, 135 and 103.  From 1040 to 2048
+// columns a wave's registers let one be on a CU at a time: 32768 x 2048 95 us, 90 with
+// one).
 int grad_groups(int64_t T, const NormTiling &n) { return norm_groups(T, rows_of(n.threads), n.threads == kWave ? 2 * kCus : kCus); }
 
 }  // namespace
@@ -482,7 +490,7 @@ size_t norm_grad_workspace_bytes(int64_t T, int H)
 
 // Whether a call's arrays, `bytes` a value, are more than the last-level cache
 // keeps for whoever reads them next: its rows then pass the caches by (16384 x 7168,
-// all outputs: 192 us, 5.5 TB/s, against 206; its gradient 162, 5.8 TB/s, against 191).
+// all outputs: 191 us against 198; its gradient 163 against 182).
 static bool streams(int64_t T, int H, int bytes) { return T * H * bytes > kCacheBytes; }
 
 #define MOE_NORM(THREADS, VPT)                                                                          \
