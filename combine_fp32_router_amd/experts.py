@@ -154,7 +154,8 @@ class ExpertMLP8(ExpertMLP):
     def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, act: int,
                  b_up: torch.Tensor | None = None, b_down: torch.Tensor | None = None,
                  max_rows: int = 0, train: bool = False, stream=None):
-        """`stream`: where the codes are made (None: the current one)."""
+        """`stream`: where the codes are made, behind the current stream's work
+        (None: on that itself)."""
         super().__init__(w_up, w_down, act, b_up, b_down, max_rows, train)
         E, H, I, wide, dev = self.E, self.H, self.I, self.wide, self.device
         nbh, nbi = B.code_blocks(H), B.code_blocks(I)
@@ -175,6 +176,8 @@ class ExpertMLP8(ExpertMLP):
         self._codes_made = None  # event behind the codes' making
         self._behind = set()  # handles of the streams that are behind it
         if dev.type == "cuda":
+            if stream is not None:  # the buffers are in the current one's order
+                B.stream_of(stream, dev).wait_stream(torch.cuda.current_stream(dev))
             self.quantize(stream)
 
     def quantize(self, stream=None) -> None:

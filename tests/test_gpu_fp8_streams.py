@@ -67,6 +67,24 @@ def test_calls_wait_for_codes_taken_again():
     assert torch.equal(out, want) and torch.equal(d_x, d_want)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_made_on_another_stream(handle):
+    """Behind what the current stream does with the weights and the buffers' memory."""
+    w, late, (x, off, d_out) = weights(1), weights(2), inputs()
+    want, d_want = alone(late, x, off, d_out)
+    maker, out, d_x = torch.cuda.Stream(), torch.zeros_like(x), torch.zeros_like(x)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(SPIN)
+    w[0].copy_(late[0]), w[1].copy_(late[1])
+    stream = maker.cuda_stream if handle else maker
+    mlp = ExpertMLP8(*w, SWIGLU, max_rows=ROWS, train=True, stream=stream)
+    mlp.forward(x, off, out, stream=stream)
+    mlp.backward(d_out, x, off, d_x, None, stream=stream)
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(d_x, d_want)
+
+
 def test_captured_with_codes_of_another_stream():
     w, (x, off, d_out) = weights(1), inputs()
     want, d_want = alone(w, x, off, d_out)
