@@ -374,8 +374,9 @@ __global__ __launch_bounds__(group_of(THREADS)) void add_norm_grad_kernel(NormGr
                 __builtin_amdgcn_sched_barrier(0);
         }
         if (__builtin_expect(uniform(!good), false)) {
-            // nothing of the row is stored or counted yet; where g s alone is too large, a power
-            // of two brings s to some 2^-20
+            // Nothing of the row is stored or counted yet.  (A branch in front of the results
+            // would hold back their loads: 4096 x 32768 281 us instead of 268.)  Where g s alone
+            // is too large, a power of two brings s to some 2^-20.
             const float c = squares < kLeastSquares ? kUp
                             : squares < kInfinity   ? __uint_as_float(__float_as_uint(r * 0x1p-20f) & kInfinity)
                                                     : kDown;
